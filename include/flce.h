@@ -358,6 +358,126 @@ flce_status_t flce_forward_noalloc(const flce_params_t* p, const void* x, const 
                                    const void* b, const int64_t* y, float* loss, float* lse,
                                    int32_t* dev_err, void* stream);
 
+/*
+ * Layer operators around the head: what a training or serving step runs right
+ * before the loss (a linear layer with its epilogue, a gated feed-forward
+ * projection) and right after it (the global gradient norm and clipping).
+ * The conventions at the top of this file hold for all of them. Operands are
+ * bf16, or fp16 with input_fp16; sums, activations and norms are fp32. The
+ * pages have no counterpart: these are additions next to the method.
+ *
+ * Row pitches (ld_*) are in elements, 0 meaning dense rows; a pitch is at
+ * least the row length. Features that a product reads (K everywhere, F of the
+ * gated projection) are multiples of 8, and the rows of x, W and the kept
+ * buffers start on 16-byte boundaries (FLCE_ERR_ALIGNMENT otherwise). Token
+ * counts are free, and so are a linear layer's output features N, residual
+ * and output pitches.
+ */
+typedef enum {
+  FLCE_ACT_NONE = 0,
+  FLCE_ACT_RELU = 1,
+  FLCE_ACT_GELU = 2,      /* z Phi(z), by erf */
+  FLCE_ACT_GELU_TANH = 3, /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  FLCE_ACT_SILU = 4,      /* z / (1 + exp(-z)) */
+  FLCE_ACT_SIGMOID = 5
+} flce_activation_t;
+
+/* y = a(z) + r, z = x W^T + b. */
+typedef struct {
+  int64_t M;              /* tokens (rows of x); 0 is a valid no-op */
+  int64_t K;              /* input features, a multiple of 8 */
+  int64_t N;              /* output features, > 0 */
+  int64_t ld_x, ld_res, ld_y; /* row pitches of x, of the residual, of y (backward: of dy) */
+  int32_t activation;     /* flce_activation_t */
+  int32_t has_bias;       /* 1: b is given ([N], 16-byte aligned) */
+  int32_t has_residual;   /* 1: the residual is given (forward) */
+  int32_t input_fp16;     /* 0: bf16 operands, 1: fp16 */
+  int32_t dW_fp32;        /* backward: 1 = dW in fp32, 0 = in the operands' type */
+  int32_t db_fp32;        /* backward: 1 = db in fp32, 0 = in the operands' type */
+} flce_linear_params_t;
+
+/* Workspace bytes: which = 0 forward, 1 backward. 0 for invalid parameters, for
+ * M == 0, and for calls that need none (workspace may then be NULL). */
+size_t flce_linear_workspace_size(const flce_linear_params_t* p, int which);
+
+/* Forward. W: [N, K] dense. y: [M, N]; it may be the residual's own buffer (with
+ * the same pitch), which it then replaces. pre: NULL, or a dense [M, N] buffer
+ * of the operands' type, 16-byte aligned, that receives z for the backward of
+ * a call with an activation. */
+flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, const void* W,
+                                  const void* b, const void* residual, void* y, void* pre,
+                                  void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                  void* stream);
+
+/* Backward: with dz = dy a'(z), dx = dz W ([M, K] dense), dW = dz^T x ([N, K]),
+ * db = column sums of dz ([N], with has_bias); the residual's gradient is dy
+ * itself. dz is rounded to the operands' type before the two products (it is
+ * exactly dy without an activation), not before the sums of db. pre: the
+ * forward's kept z (not read without an activation). Each of dx, dW, db
+ * may be NULL: it is then not computed. Written outputs are overwritten;
+ * with M == 0, dW and db are zeroed. dx and dW are 16-byte aligned. */
+flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy, const void* x,
+                                   const void* W, const void* pre, void* dx, void* dW, void* db,
+                                   void* workspace, size_t workspace_bytes, int32_t* dev_err,
+                                   void* stream);
+
+/* h = a(x Wg^T) * (x Wu^T): both projections, the activation and the product
+ * in one kernel. */
+typedef struct {
+  int64_t M;           /* tokens; 0 is a valid no-op */
+  int64_t K;           /* input features, a multiple of 8 */
+  int64_t F;           /* output features of each projection, a multiple of 8 */
+  int64_t ld_x, ld_h;  /* row pitches of x and of h (backward: of dh), ld_h a multiple of 8 */
+  int32_t activation;  /* flce_activation_t */
+  int32_t input_fp16;  /* 0: bf16 operands, 1: fp16 */
+  int32_t dW_fp32;     /* backward: 1 = dWg and dWu in fp32, 0 = in the operands' type */
+} flce_gated_params_t;
+
+size_t flce_gated_workspace_size(const flce_gated_params_t* p, int which);
+
+/* Forward. Wg, Wu: [F, K] dense. h: [M, F]. pre: NULL, or a dense [2, M, F] buffer of
+ * the operands' type that receives the two projections for the backward. h, pre:
+ * 16-byte aligned. */
+flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, const void* Wg,
+                                 const void* Wu, void* h, void* pre, void* workspace,
+                                 size_t workspace_bytes, int32_t* dev_err, void* stream);
+
+/* Backward: with g, u the forward's kept projections, dg = dh u a'(g) and
+ * du = dh a(g) (rounded to the operands' type), dx = dg Wg + du Wu ([M, K] dense,
+ * one fp32 sum), dWg = dg^T x and dWu = du^T x ([F, K]). dx, or both of dWg and
+ * dWu, may be NULL: not computed. Written outputs are overwritten; with
+ * M == 0 the weight gradients are zeroed. All outputs are 16-byte aligned. */
+flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, const void* x,
+                                  const void* Wg, const void* Wu, const void* pre, void* dx,
+                                  void* dWg, void* dWu, void* workspace, size_t workspace_bytes,
+                                  int32_t* dev_err, void* stream);
+
+/* One dense gradient tensor of any shape. */
+typedef enum { FLCE_DTYPE_BF16 = 0, FLCE_DTYPE_FP16 = 1, FLCE_DTYPE_FP32 = 2 } flce_dtype_t;
+
+/* The global norm sqrt(sum over all tensors of all squares) of `count` tensors into
+ * the device float *norm (0 for no elements). ptrs, numel and dtypes
+ * (flce_dtype_t) are HOST arrays that the call reads before it returns; pointers
+ * are aligned to their element size. Squares are summed in fp32 within a
+ * thread's share of 32 KiB and in fp64 beyond it, in a fixed
+ * order: the same tensors (at the same alignment) give the same bits. A NaN or infinity anywhere gives
+ * NaN or +inf, and so do squares beyond fp32's range (elements above 1.8e19). */
+size_t flce_grad_norm_workspace_size(int64_t count);
+flce_status_t flce_grad_norm(int64_t count, const void* const* ptrs, const int64_t* numel,
+                             const int32_t* dtypes, float* norm, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/* The same norm, then out[t] = c ptrs[t] with c = min(1, max_norm / (norm + eps))
+ * for every tensor, each product rounded once to the tensor's type. out: HOST array
+ * of destinations (an entry may equal its ptrs entry: in place; otherwise the two
+ * must not overlap), or NULL for all in place. With c = 1 in-place tensors
+ * are not touched. A NaN norm gives c = NaN, an infinite one c = 0, as the formula
+ * says. max_norm >= 0, eps >= 0. Nothing is read back to the host. */
+flce_status_t flce_clip_grads(int64_t count, const void* const* ptrs, void* const* out,
+                              const int64_t* numel, const int32_t* dtypes, float max_norm,
+                              float eps, float* norm, void* workspace, size_t workspace_bytes,
+                              void* stream);
+
 /* Failure-detection self-test: launches one kernel that waits, through the
  * same bounded mbarrier wait the GEMM pipelines use, on a barrier nothing
  * arrives on. After limit_cycles (1 .. 2^32 SM clock cycles) the wait gives

@@ -28,6 +28,10 @@ __all__ = [
     "FusedLinearCrossEntropyFunction", "FusedLinearCrossEntropyLoss",
     "fused_linear_cross_entropy", "FlceError", "params", "KernelTrace", "flce_saved_size",
     "GEMM_FORMS", "resolved_gemm_form", "flce_kept_size", "flce_keep_vocab_within",
+    "ACTIVATIONS", "flce_linear_forward", "flce_linear_backward", "flce_gated_forward",
+    "flce_gated_backward", "flce_grad_norm", "flce_clip_grads", "clip_grad_norm_",
+    "FusedLinearFunction", "GatedLinearFunction", "fused_linear", "gated_linear",
+    "GatedFeedForward",
 ]
 
 _err_words = {}
@@ -436,3 +440,9 @@ class FusedLinearCrossEntropyLoss(torch.nn.Module):
             x2, y2, weight, bias, self.ignore_index, self.label_smoothing,
             self.lse_square_scale, self.logit_scale, self.reduction, self.recompute, config,
             self.keep_block, self.keep_vocab)
+
+
+from .block import (ACTIVATIONS, FusedLinearFunction, GatedFeedForward,  # noqa: E402
+                    GatedLinearFunction, clip_grad_norm_, flce_clip_grads, flce_gated_backward,
+                    flce_gated_forward, flce_grad_norm, flce_linear_backward, flce_linear_forward,
+                    fused_linear, gated_linear)

@@ -47,6 +47,24 @@ class FlceParams(ctypes.Structure):
     ]
 
 
+# flce_activation_t and flce_dtype_t.
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "sigmoid": 5}
+DTYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
+
+
+class FlceLinearParams(ctypes.Structure):
+    """Mirror of flce_linear_params_t."""
+    _fields_ = [(f, ctypes.c_int64) for f in ("M", "K", "N", "ld_x", "ld_res", "ld_y")] + \
+        [(f, ctypes.c_int32) for f in ("activation", "has_bias", "has_residual", "input_fp16",
+                                       "dW_fp32", "db_fp32")]
+
+
+class FlceGatedParams(ctypes.Structure):
+    """Mirror of flce_gated_params_t."""
+    _fields_ = [(f, ctypes.c_int64) for f in ("M", "K", "F", "ld_x", "ld_h")] + \
+        [(f, ctypes.c_int32) for f in ("activation", "input_fp16", "dW_fp32")]
+
+
 class FlceTrace(ctypes.Structure):
     """Mirror of flce_trace_t."""
     _fields_ = [
@@ -132,6 +150,27 @@ def load() -> ctypes.CDLL:
     lib.flce_read_device_error.restype = ctypes.c_int
     lib.flce_resolved_gemm_form.argtypes = [P, ctypes.c_int32]
     lib.flce_resolved_gemm_form.restype = ctypes.c_int32
+    i64 = ctypes.c_int64
+    # Parameter structs and host arrays of the layer operators go in by address.
+    lib.flce_linear_workspace_size.argtypes = [vp, ctypes.c_int]
+    lib.flce_linear_workspace_size.restype = sz
+    lib.flce_linear_forward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.flce_linear_forward.restype = ctypes.c_int
+    lib.flce_linear_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.flce_linear_backward.restype = ctypes.c_int
+    lib.flce_gated_workspace_size.argtypes = [vp, ctypes.c_int]
+    lib.flce_gated_workspace_size.restype = sz
+    lib.flce_gated_forward.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.flce_gated_forward.restype = ctypes.c_int
+    lib.flce_gated_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
+    lib.flce_gated_backward.restype = ctypes.c_int
+    lib.flce_grad_norm_workspace_size.argtypes = [i64]
+    lib.flce_grad_norm_workspace_size.restype = sz
+    lib.flce_grad_norm.argtypes = [i64, vp, vp, vp, vp, vp, sz, vp]
+    lib.flce_grad_norm.restype = ctypes.c_int
+    lib.flce_clip_grads.argtypes = [i64, vp, vp, vp, vp, ctypes.c_float, ctypes.c_float, vp, vp,
+                                    sz, vp]
+    lib.flce_clip_grads.restype = ctypes.c_int
     lib.flce_status_string.argtypes = [ctypes.c_int]
     lib.flce_status_string.restype = ctypes.c_char_p
     lib.flce_version.argtypes = []

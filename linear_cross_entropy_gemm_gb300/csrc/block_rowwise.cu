@@ -1,0 +1,155 @@
+// Element-wise (HBM-bound) parts of the layer operators' backward passes:
+//   dz     : dz = dy a'(z) in the operands' type, with its fp32 column sums
+//            (the bias gradient's partials)
+//   gated  : dg = dh u a'(g), du = dh a(g)
+#include <cuda_runtime.h>
+
+#include "block_epilogues.cuh"
+#include "block_internal.h"
+
+namespace flce {
+
+__device__ __forceinline__ void unpack8(const uint4& u, bool f16, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    v[2 * e] = unpack_16(w[e] & 0xFFFFu, f16);
+    v[2 * e + 1] = unpack_16(w[e] >> 16, f16);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8], bool f16) {
+  uint4 u;
+  u.x = pack_16x2(v[0], v[1], f16);
+  u.y = pack_16x2(v[2], v[3], f16);
+  u.z = pack_16x2(v[4], v[5], f16);
+  u.w = pack_16x2(v[6], v[7], f16);
+  return u;
+}
+
+// A block takes 256 columns (32 threads x 8) of one part's rows, 8 rows at a
+// time; a thread keeps the fp32 sums of its columns, and the eight row groups
+// are added in a fixed order at the end. With rows off the 16-byte boundaries
+// a thread's columns are 32 apart instead of adjacent, so that a warp's
+// accesses stay contiguous.
+constexpr int kDzCols = 256, kDzRowGroups = 8;
+
+static int dz_rows_per_part(int64_t M, int64_t N) {
+  // About two waves of 8 blocks on each of 152 SMs.
+  const int64_t ct = (N + kDzCols - 1) / kDzCols;
+  int64_t parts = (2 * 8 * 152 + ct - 1) / ct;
+  int64_t rows = (M + parts - 1) / parts;
+  rows = (rows + kDzRowGroups - 1) / kDzRowGroups * kDzRowGroups;
+  return static_cast<int>(rows);
+}
+
+int dz_parts(int64_t M, int64_t N) {
+  const int64_t rows = dz_rows_per_part(M, N);
+  return static_cast<int>((M + rows - 1) / rows);
+}
+
+__global__ void __launch_bounds__(32 * kDzRowGroups) dz_kernel(const DzArgs a, int rows_per_part) {
+  __shared__ float s_sum[kDzRowGroups][kDzCols];
+  const int cg = threadIdx.x & 31, rg = threadIdx.x >> 5;
+  const bool f16 = a.fp16 != 0, vec = a.vec != 0;
+  const int col0 = blockIdx.x * kDzCols;
+  const int r_lo = blockIdx.y * rows_per_part;
+  const int r_hi = min(a.M, r_lo + rows_per_part);
+  float sum[8] = {};
+  const int vcol = col0 + cg * 8;
+  if (vec && vcol + 8 <= a.N) {
+    for (int r = r_lo + rg; r < r_hi; r += kDzRowGroups) {
+      float v[8];
+      unpack8(*reinterpret_cast<const uint4*>(a.dy + static_cast<size_t>(r) * a.ld_dy + vcol), f16,
+              v);
+      if (a.z) {
+        float z[8];
+        unpack8(__ldg(reinterpret_cast<const uint4*>(a.z + static_cast<size_t>(r) * a.N + vcol)),
+                f16, z);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          float val, slope;
+          act_value_slope(a.act, z[j], val, slope);
+          v[j] *= slope;
+        }
+      }
+      if (a.dz)
+        *reinterpret_cast<uint4*>(a.dz + static_cast<size_t>(r) * a.ld_dz + vcol) = pack8(v, f16);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum[j] += v[j];
+    }
+  } else {
+    const int first = vec ? vcol : col0 + cg, step = vec ? 1 : 32;
+    for (int r = r_lo + rg; r < r_hi; r += kDzRowGroups) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int c = first + j * step;
+        if (c >= a.N) continue;
+        float v = unpack_16(a.dy[static_cast<size_t>(r) * a.ld_dy + c], f16);
+        if (a.z) {
+          float val, slope;
+          act_value_slope(a.act, unpack_16(a.z[static_cast<size_t>(r) * a.N + c], f16), val, slope);
+          v *= slope;
+        }
+        if (a.dz) a.dz[static_cast<size_t>(r) * a.ld_dz + c] = to16(v, f16);
+        sum[j] += v;
+      }
+    }
+  }
+  if (!a.part) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s_sum[rg][vec ? cg * 8 + j : j * 32 + cg] = sum[j];
+  __syncthreads();
+  const int c = threadIdx.x;
+  if (col0 + c < a.N) {
+    float t = 0.f;
+#pragma unroll
+    for (int k = 0; k < kDzRowGroups; ++k) t += s_sum[k][c];
+    a.part[static_cast<size_t>(blockIdx.y) * a.N + col0 + c] = t;
+  }
+}
+
+cudaError_t launch_dz(const DzArgs& a, cudaStream_t st) {
+  const dim3 grid((a.N + kDzCols - 1) / kDzCols, dz_parts(a.M, a.N));
+  dz_kernel<<<grid, 32 * kDzRowGroups, 0, st>>>(a, dz_rows_per_part(a.M, a.N));
+  return cudaGetLastError();
+}
+
+// One thread takes 8 columns of one row: three 16-byte loads, two 16-byte
+// stores. Index: the 32- or 64-bit type that holds M F / 8.
+template <class Index>
+__global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradArgs a) {
+  const Index f8 = static_cast<Index>(a.F / 8);
+  const Index i = static_cast<Index>(blockIdx.x) * 256 + threadIdx.x;
+  if (i >= f8 * static_cast<Index>(a.M)) return;
+  const Index row = i / f8;
+  const size_t col = static_cast<size_t>(i - row * f8) * 8;
+  const size_t at = static_cast<size_t>(i) * 8;
+  const bool f16 = a.fp16 != 0;
+  float d[8], g[8], u[8];
+  unpack8(__ldg(reinterpret_cast<const uint4*>(a.dh + static_cast<size_t>(row) * a.ld_dh + col)),
+          f16, d);
+  unpack8(__ldg(reinterpret_cast<const uint4*>(a.g + at)), f16, g);
+  unpack8(__ldg(reinterpret_cast<const uint4*>(a.u + at)), f16, u);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    float val, slope;
+    act_value_slope(a.act, g[j], val, slope);
+    g[j] = d[j] * u[j] * slope;
+    u[j] = d[j] * val;
+  }
+  *reinterpret_cast<uint4*>(a.dg + at) = pack8(g, f16);
+  *reinterpret_cast<uint4*>(a.du + at) = pack8(u, f16);
+}
+
+cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t st) {
+  const uint64_t n = static_cast<uint64_t>(a.M) * (a.F / 8);
+  const uint64_t blocks = (n + 255) / 256;
+  if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+  if (n < (1ull << 32) - 256)
+    gated_grad_kernel<uint32_t><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a);
+  else
+    gated_grad_kernel<uint64_t><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace flce

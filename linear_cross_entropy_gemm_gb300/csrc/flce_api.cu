@@ -24,15 +24,13 @@
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
-#include <mutex>
 
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <cudaTypedefs.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include "../../include/flce.h"
 #include "epilogues.cuh"
+#include "flce_host.h"
 #include "flce_internal.h"
 
 using namespace flce;
@@ -45,59 +43,7 @@ namespace {
 // kMinVocabBlock.
 constexpr int64_t kDlBudgetBytes = 1LL << 30;
 constexpr int64_t kMinVocabBlock = 4096;
-constexpr size_t kAlign = 256;
 
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-std::once_flag g_encode_once;
-
-PFN_cuTensorMapEncodeTiled_v12000 encoder() {
-  std::call_once(g_encode_once, [] {
-    cudaDriverEntryPointQueryResult q;
-    void* fn = nullptr;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                         &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-  });
-  return g_encode;
-}
-
-// 2-D 16-bit tensor [outer, inner] (bf16, or fp16 when fp16) with row pitch
-// `pitch_bytes`, 128-B swizzled boxes of box_inner x box_outer elements;
-// out-of-range elements read as 0.
-bool encode_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer,
-               uint64_t pitch_bytes, uint32_t box_inner, uint32_t box_outer, bool fp16) {
-  auto fn = encoder();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {pitch_bytes};
-  cuuint32_t box[2] = {box_inner, box_outer};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
-            const_cast<void*>(base), dims, strides, box,
-            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// TMA store map of a row-major [outer, inner] output for the epilogues'
-// 32 x 32 blocks: fp32 with the 128-byte swizzle (128-byte box rows) or a
-// 16-bit type with the 64-byte swizzle (64-byte box rows), the staging layouts
-// of epilogues.cuh. Stores are clipped to [inner, outer].
-bool encode_store_2d(CUtensorMap* m, void* base, uint64_t inner, uint64_t outer,
-                     uint64_t pitch_bytes, bool fp32) {
-  auto fn = encoder();
-  if (!fn) return false;
-  cuuint64_t dims[2] = {inner, outer};
-  cuuint64_t strides[1] = {pitch_bytes};
-  cuuint32_t box[2] = {32, 32};
-  cuuint32_t estr[2] = {1, 1};
-  return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base,
-            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            fp32 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b); }
 
 // GEMM kernel form of a call: an explicit gemm_form decides; with the
 // default form, FLCE_GEMM_FORM=single|pair|wide in the environment overrides
@@ -130,21 +76,6 @@ GemmKind gemm_for(GemmKind kind, int64_t M, int64_t N, int64_t K) {
   if (kind != kGemmAuto) return kind;
   const int64_t wide_tiles = ((M + 255) / 256) * ((N + 511) / 512);
   return (K >= kWideMinK && wide_tiles >= kWideMinTiles) ? kGemmWide : kGemmPair;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// SM count and architecture of the current device.
-flce_status_t device_info(int* sms) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return FLCE_ERR_CUDA;
-  int major = 0, minor = 0;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return FLCE_ERR_CUDA;
-  if (major != 10 || minor != 3) return FLCE_ERR_UNSUPPORTED;
-  return FLCE_OK;
 }
 
 flce_status_t check_params(const flce_params_t* p) {
@@ -181,21 +112,6 @@ int64_t vocab_total(const flce_params_t* p) { return p->vocab_total > 0 ? p->voc
 bool whole_vocab(const flce_params_t* p) {
   return p->vocab_total == 0 || (p->vocab_total == p->V && p->vocab_start == 0);
 }
-
-struct Carver {
-  uintptr_t base, cur, end;
-  explicit Carver(void* b, size_t n)
-      : base(reinterpret_cast<uintptr_t>(b)),
-        cur((reinterpret_cast<uintptr_t>(b) + kAlign - 1) & ~(kAlign - 1)),
-        end(reinterpret_cast<uintptr_t>(b) + n) {}
-  template <class T>
-  T* take(size_t count) {
-    T* r = reinterpret_cast<T*>(cur);
-    cur = (cur + count * sizeof(T) + kAlign - 1) & ~(kAlign - 1);
-    return r;
-  }
-  size_t used() const { return cur - base; }
-};
 
 struct FwdWs {
   float *part_m, *part_d, *part_s, *zy;
@@ -315,20 +231,6 @@ flce_params_t whole_vocab_block(const flce_params_t* p) {
   return q;
 }
 
-GemmGeom geom(int M, int N, int K, bool fp16) {
-  GemmGeom g;
-  std::memset(&g, 0, sizeof(g));
-  g.ab_fp16 = fp16 ? 1 : 0;
-  g.M = M;
-  g.N = N;
-  g.K = K;
-  g.tiles_m = cdiv(M, kBM);
-  g.tiles_n = cdiv(N, kBN);
-  g.k_blocks = cdiv(K, kBK);
-  g.raster_m_inner = 1;
-  return g;
-}
-
 // Tile order. FLCE_RASTER=0 selects the plain orders (M inner for the
 // logits GEMMs, N inner for dW / dx); the default bands the reused operand so
 // its slice stays in L2 (bands of 16 pair-M-tiles = 4096 tokens of x for the
@@ -337,20 +239,6 @@ bool use_bands() {
   const char* e = std::getenv("FLCE_RASTER");
   return !(e && e[0] == '0');
 }
-
-int grid_for(const GemmGeom& g, int sms) {
-  const int tiles = g.tiles_m * g.tiles_n;
-  return tiles < sms ? tiles : sms;
-}
-
-// NVTX range over a scope (host timeline; free unless a profiler is attached),
-// so Nsight Systems shows each call and each backward vocabulary block.
-struct NvtxRange {
-  explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange&) = delete;
-  NvtxRange& operator=(const NvtxRange&) = delete;
-};
 
 // Records the caller's events around each launch (flce_trace_t in flce.h).
 struct Tracer {
