@@ -8,6 +8,7 @@
 // Gated   forward   one GEMM whose tiles hold both projections of the same outputs
 //         backward  dg and du in one element-wise pass, then dx as one GEMM whose sum
 //                   runs over both, and dWg and dWu as one GEMM over both
+#include <algorithm>
 #include <cstdint>
 #include <cstring>
 
@@ -74,14 +75,120 @@ bool out16(Out16* o, void* ptr, int64_t rows, int64_t cols, int64_t ld) {
                                         false);
 }
 
-// K-major operand [rows, k]: boxes of 64 x 128. MN-major operand, the transpose
-// of a row-major [k, rows] array: boxes of 64 x 64.
-bool k_major(CUtensorMap* m, const void* p, int64_t rows, int64_t k, int64_t ld, bool f16) {
-  return encode_2d(m, p, k, rows, static_cast<uint64_t>(ld) * 2, kBK, kBM, f16);
+// K-major operand [rows, k]: boxes of 64 x 128 (or fewer rows). MN-major operand, the
+// transpose of a row-major [k, rows] array: boxes of 64 x 128, or 64 x 64 for the
+// few-token kernel.
+bool k_major(CUtensorMap* m, const void* p, int64_t rows, int64_t k, int64_t ld, bool f16,
+             int box = kBM) {
+  return encode_2d(m, p, k, rows, static_cast<uint64_t>(ld) * 2, kBK, static_cast<uint32_t>(box),
+                   f16);
 }
-bool mn_major(CUtensorMap* m, const void* p, int64_t rows, int64_t k, int64_t ld, bool f16) {
-  return encode_2d(m, p, rows, k, static_cast<uint64_t>(ld) * 2, 64, kBK, f16);
+bool mn_major(CUtensorMap* m, const void* p, int64_t rows, int64_t k, int64_t ld, bool f16,
+              int box) {
+  return encode_2d(m, p, rows, k, static_cast<uint64_t>(ld) * 2, 64, static_cast<uint32_t>(box),
+                   f16);
 }
+
+// Products of at most this many tokens go to the few-token kernel.
+constexpr int64_t kSmallTokens = 128;
+
+int64_t small_most() { return kSmallTokens; }
+
+// The parts of a few-token product's arguments that do not depend on the operator.
+// x: [M, k] with pitch ld_x; the sum runs over `segments` times k.
+bool small_args(SmallArgs* a, const void* x, int64_t ld_x, int64_t M, int64_t k, int segments,
+                int64_t N, void* y, int64_t ld_y, bool f16, int32_t* dev_err) {
+  std::memset(a, 0, sizeof(*a));
+  a->y = static_cast<uint16_t*>(y);
+  a->ld_y = ld_y;
+  a->y_vec = aligned16(y) && ld_y % 8 == 0 ? 1 : 0;
+  a->fp16 = f16 ? 1 : 0;
+  a->M = static_cast<int>(M);
+  a->N = static_cast<int>(N);
+  a->k_split = cdiv(k, kBK);
+  a->k_blocks = segments * a->k_split;
+  a->slices = small_slices(M, N, a->k_blocks);
+  a->dev_err = reinterpret_cast<int*>(dev_err);
+  return encode_2d(&a->x, x, k, M, static_cast<uint64_t>(ld_x) * 2, kBK,
+                   static_cast<uint32_t>(small_tokens(M)), f16);
+}
+
+// ------------------------------------------------- tile width of a pair GEMM
+// A tile shape (pair_engine.cuh) and the ns it takes for 64 sum elements, measured on
+// one wave of tiles at 1.92 GHz with a K-major and with an MN-major B, whose boxes
+// are 64 columns wide, so that only widths in multiples of 128 load nothing twice.
+struct TileShape {
+  int halves, bn;
+  float ns, ns_mn;  // 0: not used with that B
+};
+constexpr TileShape kTileShapes[] = {
+    {1, 256, 296.f, 296.f}, {1, 224, 243.f, 0.f},   {1, 192, 222.f, 255.f}, {1, 160, 196.f, 0.f},
+    {1, 128, 215.f, 202.f}, {1, 64, 170.f, 193.f},  {2, 256, 0.f, 530.f},   {2, 192, 0.f, 405.f},
+};
+constexpr int kPairClusters = 76;    // two CTAs of 152
+constexpr float kSustained[] = {1.66e6f, 1.75e6f};  // flop/ns under the power cap, by halves
+
+// ns of a whole product: its waves of tiles, each as long as the sum or (where it
+// runs beside the next tile's sum) the epilogue; the last epilogue; and no less than
+// the padded flops take under the power cap. The two-half form, whose epilogue is not
+// overlapped, is kept to the weight and input gradients: at 8192 x 28672 x 4096 (gated)
+// it took 1213 us against 1133 us, for dW 4096 x 14336 x 8192 549 us against 579 us.
+float tile_ns(const TileShape& t, bool mn, int64_t tiles_m, int64_t N, int64_t k64, bool two_b,
+              float epi_ns) {
+  const int cols = pair_cols(two_b ? kTwoB : kOneEach, t.halves, t.bn);
+  const int64_t tiles = tiles_m * ((N + cols - 1) / cols);
+  const float waves = static_cast<float>((tiles + kPairClusters - 1) / kPairClusters);
+  const float sum = static_cast<float>(k64) * (mn ? t.ns_mn : t.ns), epi = epi_ns * cols;
+  const float busy = t.halves == 1 ? waves * std::max(sum, epi) + epi : waves * (sum + epi);
+  const float flops = 2.f * 256.f * 64.f * t.halves * t.bn * static_cast<float>(tiles) * k64;
+  return std::max(busy, flops / kSustained[t.halves - 1]);
+}
+
+const TileShape& best_tile(bool mn, int64_t M, int64_t N, int64_t k64, bool two_b, float epi_ns) {
+  const TileShape* best = nullptr;
+  float least = 0.f;
+  for (const TileShape& t : kTileShapes) {
+    if ((mn ? t.ns_mn : t.ns) == 0.f) continue;
+    const float ns = tile_ns(t, mn, (M + 255) / 256, N, k64, two_b, epi_ns);
+    if (!best || ns < least) {
+      best = &t;
+      least = ns;
+    }
+  }
+  return *best;
+}
+
+// ns that an epilogue takes per output column of a 256-row tile (measured: 1.5 us for
+// 256 stored columns, 6.5 us with gelu and a kept z).
+float epilogue_ns(int act, bool keep, bool two_b) {
+  const float a = act == FLCE_ACT_NONE || act == FLCE_ACT_RELU ? 0.f
+                  : act == FLCE_ACT_GELU                       ? 14.f
+                                                               : 8.f;
+  return 6.f + a + (keep ? (two_b ? 12.f : 6.f) : 0.f) + (two_b ? 2.f : 0.f);
+}
+
+// The geometry of a pair GEMM D[M, N] with a sum of K (`segments` of them): tile shape and
+// raster. Bands of 16 row tiles keep 4096 rows of A in L2 while B streams: at 8192 x
+// 4096 x 14336, 573 us against 596 us with bands of 8 column tiles.
+PairArgs pair_args(int M, int N, int K, int segments, bool mn, bool two_b, float epi_ns, bool f16,
+                   int32_t* dev_err) {
+  PairArgs g;
+  std::memset(&g, 0, sizeof(g));
+  const TileShape& t = best_tile(mn, M, N, static_cast<int64_t>(segments) * cdiv(K, 64), two_b,
+                                 epi_ns);
+  g.halves = t.halves;
+  g.bn = t.bn;
+  g.band_m = 16;
+  g.tiles_m = cdiv(M, 256);
+  g.tiles_n = cdiv(N, pair_cols(two_b ? kTwoB : kOneEach, g.halves, g.bn));
+  g.k_split = cdiv(K, pair_lk(g.halves));
+  g.k_stages = segments * g.k_split;
+  g.fp16 = f16 ? 1 : 0;
+  g.dev_err = reinterpret_cast<int*>(dev_err);
+  return g;
+}
+
+flce_status_t done(cudaError_t e) { return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA; }
 
 // Backward scratch of the linear layer: dz where it is not dy itself, and the
 // bias gradient's partial sums.
@@ -143,6 +250,19 @@ flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, 
   if ((st = device_info(&sms)) != FLCE_OK) return st;
   const bool f16 = p->input_fp16 != 0;
   const int M = static_cast<int>(p->M), K = static_cast<int>(p->K), N = static_cast<int>(p->N);
+  if (M <= small_most()) {
+    SmallArgs sa;
+    if (!small_args(&sa, x, pitch(p->ld_x, K), M, K, 1, N, y, pitch(p->ld_y, N), f16, dev_err) ||
+        !k_major(&sa.w, W, N, K, K, f16))
+      return FLCE_ERR_CUDA;
+    sa.bias = static_cast<const uint16_t*>(p->has_bias ? b : nullptr);
+    sa.res = static_cast<const uint16_t*>(p->has_residual ? residual : nullptr);
+    sa.ld_res = pitch(p->ld_res, N);
+    sa.res_vec = aligned16(residual) && sa.ld_res % 8 == 0 ? 1 : 0;
+    sa.keep = static_cast<uint16_t*>(pre);
+    sa.act = p->activation;
+    return done(launch_small(false, false, sa, static_cast<cudaStream_t>(stream)));
+  }
 
   LinearArgs ea;
   std::memset(&ea, 0, sizeof(ea));
@@ -155,15 +275,12 @@ flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, 
   ea.keep = pre ? 1 : 0;
   ea.M = M;
   ea.N = N;
-  CUtensorMap mx, mw;
+  PairArgs g = pair_args(M, N, K, 1, false, false,
+                         epilogue_ns(p->activation, pre != nullptr, false), f16, dev_err);
   if (!out16(&ea.y, y, M, N, pitch(p->ld_y, N)) || (pre && !out16(&ea.z, pre, M, N, N)) ||
-      !k_major(&mx, x, M, K, pitch(p->ld_x, K), f16) || !k_major(&mw, W, N, K, K, f16))
+      !k_major(&g.a, x, M, K, pitch(p->ld_x, K), f16) || !k_major(&g.b, W, N, K, K, f16, g.bn / 2))
     return FLCE_ERR_CUDA;
-  const GemmGeom g = geom(M, N, K, f16);
-  return launch_linear(kGemmPair, mx, mw, g, ea, reinterpret_cast<int*>(dev_err), sms,
-                       static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? FLCE_OK
-             : FLCE_ERR_CUDA;
+  return done(launch_linear(g, ea, sms, static_cast<cudaStream_t>(stream)));
 }
 
 flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy, const void* x,
@@ -195,7 +312,6 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
   if ((st = device_info(&sms)) != FLCE_OK) return st;
   const bool f16 = p->input_fp16 != 0;
   const int M = static_cast<int>(p->M), K = static_cast<int>(p->K), N = static_cast<int>(p->N);
-  int* derr = reinterpret_cast<int*>(dev_err);
 
   const int64_t ld_dy = pitch(p->ld_y, N);
   const bool dy_rows16 = aligned16(dy) && ld_dy % 8 == 0;
@@ -220,18 +336,20 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
   }
   const void* dz = copy ? static_cast<const void*>(w.dz) : dy;
   const int64_t ld_dz = copy ? w.ld_dz : ld_dy;
-  if (dx) {
+  if (dx && M <= small_most()) {
+    SmallArgs sa;
+    if (!small_args(&sa, dz, ld_dz, M, N, 1, K, dx, K, f16, dev_err) ||
+        !mn_major(&sa.w, W, K, N, K, f16, kBK) || launch_small(false, true, sa, s) != cudaSuccess)
+      return FLCE_ERR_CUDA;
+  } else if (dx) {
     GradXArgs ea;
     std::memset(&ea, 0, sizeof(ea));
     ea.fp16 = f16 ? 1 : 0;
     ea.M = M;
     ea.K = K;
-    CUtensorMap ma, mb;
-    if (!out16(&ea.dx, dx, M, K, K) || !k_major(&ma, dz, M, N, ld_dz, f16) ||
-        !mn_major(&mb, W, K, N, K, f16))
-      return FLCE_ERR_CUDA;
-    const GemmGeom g = geom(M, K, N, f16);
-    if (launch_grad_x(kGemmPair, false, ma, mb, g, ea, derr, sms, s) != cudaSuccess)
+    PairArgs g = pair_args(M, K, N, 1, true, false, 6.f, f16, dev_err);
+    if (!out16(&ea.dx, dx, M, K, K) || !k_major(&g.a, dz, M, N, ld_dz, f16) ||
+        !mn_major(&g.b, W, K, N, K, f16, pair_lk(g.halves)) || launch_grad_x(false, g, ea, sms, s) != cudaSuccess)
       return FLCE_ERR_CUDA;
   }
   if (dW) {
@@ -241,13 +359,11 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
     ea.fp16 = f16 ? 1 : 0;
     ea.N = N;
     ea.K = K;
-    CUtensorMap ma, mb;
+    PairArgs g = pair_args(N, K, M, 1, true, false, 6.f, f16, dev_err);
     if (!encode_store_2d(&ea.out, dW, K, N, static_cast<uint64_t>(K) * (p->dW_fp32 ? 4 : 2),
                          p->dW_fp32 != 0) ||
-        !mn_major(&ma, dz, N, M, ld_dz, f16) || !mn_major(&mb, x, K, M, pitch(p->ld_x, K), f16))
-      return FLCE_ERR_CUDA;
-    const GemmGeom g = geom(N, K, M, f16);
-    if (launch_grad_w(kGemmPair, false, ma, mb, g, ea, derr, sms, s) != cudaSuccess)
+        !mn_major(&g.a, dz, N, M, ld_dz, f16, pair_lk(g.halves)) || !mn_major(&g.b, x, K, M, pitch(p->ld_x, K), f16, pair_lk(g.halves)) ||
+        launch_grad_w(false, g, ea, sms, s) != cudaSuccess)
       return FLCE_ERR_CUDA;
   }
   return FLCE_OK;
@@ -275,6 +391,15 @@ flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, co
   if ((st = device_info(&sms)) != FLCE_OK) return st;
   const bool f16 = p->input_fp16 != 0;
   const int M = static_cast<int>(p->M), K = static_cast<int>(p->K), F = static_cast<int>(p->F);
+  if (M <= small_most()) {
+    SmallArgs sa;
+    if (!small_args(&sa, x, pitch(p->ld_x, K), M, K, 1, F, h, pitch(p->ld_h, F), f16, dev_err) ||
+        !k_major(&sa.w, Wg, F, K, K, f16) || !k_major(&sa.w2, Wu, F, K, K, f16))
+      return FLCE_ERR_CUDA;
+    sa.keep = static_cast<uint16_t*>(pre);
+    sa.act = p->activation;
+    return done(launch_small(true, false, sa, static_cast<cudaStream_t>(stream)));
+  }
 
   GatedArgs ea;
   std::memset(&ea, 0, sizeof(ea));
@@ -284,19 +409,15 @@ flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, co
   ea.M = M;
   ea.F = F;
   uint16_t* keep = static_cast<uint16_t*>(pre);
-  CUtensorMap mx, mg;
+  PairArgs g = pair_args(M, F, K, 1, false, true, epilogue_ns(p->activation, pre != nullptr, true),
+                         f16, dev_err);
   if (!out16(&ea.h, h, M, F, pitch(p->ld_h, F)) ||
       (pre && (!out16(&ea.g, keep, M, F, F) ||
                !out16(&ea.u, keep + static_cast<size_t>(M) * F, M, F, F))) ||
-      !k_major(&mx, x, M, K, pitch(p->ld_x, K), f16) || !k_major(&mg, Wg, F, K, K, f16) ||
-      !k_major(&ea.second.b2, Wu, F, K, K, f16))
+      !k_major(&g.a, x, M, K, pitch(p->ld_x, K), f16) || !k_major(&g.b, Wg, F, K, K, f16, g.bn / 2) ||
+      !k_major(&g.b2, Wu, F, K, K, f16, g.bn / 2))
     return FLCE_ERR_CUDA;
-  GemmGeom g = geom(M, F, K, f16);
-  g.tiles_n = cdiv(F, kBN / 2);  // a 256 x 256 pair tile holds 128 outputs
-  return launch_gated(kGemmPair, mx, mg, g, ea, reinterpret_cast<int*>(dev_err), sms,
-                      static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? FLCE_OK
-             : FLCE_ERR_CUDA;
+  return done(launch_gated(g, ea, sms, static_cast<cudaStream_t>(stream)));
 }
 
 flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, const void* x,
@@ -326,7 +447,6 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
   if ((st = device_info(&sms)) != FLCE_OK) return st;
   const bool f16 = p->input_fp16 != 0;
   const int M = static_cast<int>(p->M), K = static_cast<int>(p->K), F = static_cast<int>(p->F);
-  int* derr = reinterpret_cast<int*>(dev_err);
 
   GatedGradArgs ga;
   ga.dh = static_cast<const uint16_t*>(dh);
@@ -340,21 +460,24 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
   ga.act = p->activation;
   ga.fp16 = f16 ? 1 : 0;
   if (launch_gated_grad(ga, s) != cudaSuccess) return FLCE_ERR_CUDA;
-  if (dx) {
+  if (dx && M <= small_most()) {
+    SmallArgs sa;
+    if (!small_args(&sa, w.dg, F, M, F, 2, K, dx, K, f16, dev_err) ||
+        !encode_2d(&sa.x2, w.du, F, M, static_cast<uint64_t>(F) * 2, kBK,
+                   static_cast<uint32_t>(small_tokens(M)), f16) ||
+        !mn_major(&sa.w, Wg, K, F, K, f16, kBK) || !mn_major(&sa.w2, Wu, K, F, K, f16, kBK) ||
+        launch_small(false, true, sa, s) != cudaSuccess)
+      return FLCE_ERR_CUDA;
+  } else if (dx) {
     GradXArgs ea;
     std::memset(&ea, 0, sizeof(ea));
     ea.fp16 = f16 ? 1 : 0;
     ea.M = M;
     ea.K = K;
-    CUtensorMap ma, mb;
-    if (!out16(&ea.dx, dx, M, K, K) || !k_major(&ma, w.dg, M, F, F, f16) ||
-        !k_major(&ea.second.a2, w.du, M, F, F, f16) || !mn_major(&mb, Wg, K, F, K, f16) ||
-        !mn_major(&ea.second.b2, Wu, K, F, K, f16))
-      return FLCE_ERR_CUDA;
-    GemmGeom g = geom(M, K, F, f16);
-    ea.second.k_split = g.k_blocks;
-    g.k_blocks *= 2;
-    if (launch_grad_x(kGemmPair, true, ma, mb, g, ea, derr, sms, s) != cudaSuccess)
+    PairArgs g = pair_args(M, K, F, 2, true, false, 6.f, f16, dev_err);
+    if (!out16(&ea.dx, dx, M, K, K) || !k_major(&g.a, w.dg, M, F, F, f16) ||
+        !k_major(&g.a2, w.du, M, F, F, f16) || !mn_major(&g.b, Wg, K, F, K, f16, pair_lk(g.halves)) ||
+        !mn_major(&g.b2, Wu, K, F, K, f16, pair_lk(g.halves)) || launch_grad_x(true, g, ea, sms, s) != cudaSuccess)
       return FLCE_ERR_CUDA;
   }
   if (dWg) {
@@ -365,16 +488,13 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
     ea.N = F;
     ea.K = K;
     const uint64_t row = static_cast<uint64_t>(K) * (p->dW_fp32 ? 4 : 2);
-    CUtensorMap ma, mb;
+    PairArgs g = pair_args(2 * cdiv(F, 256) * 256, K, M, 1, true, false, 6.f, f16, dev_err);
+    g.m_split = g.tiles_m / 2;
     if (!encode_store_2d(&ea.out, dWg, K, F, row, p->dW_fp32 != 0) ||
         !encode_store_2d(&ea.out2, dWu, K, F, row, p->dW_fp32 != 0) ||
-        !mn_major(&ma, w.dg, F, M, F, f16) || !mn_major(&ea.second.a2, w.du, F, M, F, f16) ||
-        !mn_major(&mb, x, K, M, pitch(p->ld_x, K), f16))
-      return FLCE_ERR_CUDA;
-    GemmGeom g = geom(F, K, M, f16);
-    ea.second.m_split = cdiv(F, 2 * kBM);
-    g.tiles_m = 4 * ea.second.m_split;  // both gradients, in 128-row units
-    if (launch_grad_w(kGemmPair, true, ma, mb, g, ea, derr, sms, s) != cudaSuccess)
+        !mn_major(&g.a, w.dg, F, M, F, f16, pair_lk(g.halves)) || !mn_major(&g.a2, w.du, F, M, F, f16, pair_lk(g.halves)) ||
+        !mn_major(&g.b, x, K, M, pitch(p->ld_x, K), f16, pair_lk(g.halves)) ||
+        launch_grad_w(true, g, ea, sms, s) != cudaSuccess)
       return FLCE_ERR_CUDA;
   }
   return FLCE_OK;

@@ -10,8 +10,10 @@
 // and the forward's own output is computed from the unrounded values.
 #pragma once
 #include <cstdint>
+#include <type_traits>
 
 #include "epilogues.cuh"
+#include "pair_engine.cuh"
 
 namespace flce {
 
@@ -40,81 +42,85 @@ __device__ __forceinline__ float sigmoid_f(float z) {
 __device__ __forceinline__ float gelu_tanh_gate(float z) {
   return sigmoid_f(2.f * kGeluC * z * fmaf(kGeluC3 * z, z, 1.f));
 }
-__device__ __forceinline__ float gelu_cdf(float z) { return fmaf(0.5f, erff(z * kInvSqrt2), 0.5f); }
+// gelu: Phi(z) = 1 - Q(z) with, for x = |z| / sqrt(2), Q = erfc(x) / 2 and
+// erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2) + e, t = 1 / (1 + p x), |e| <= 1.5e-7
+// (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26, after
+// Hastings). A third of erff's instructions, no branch, and e^(-z^2 / 2) is the
+// density that the derivative needs. gauss: e^(-z^2 / 2).
+__device__ __forceinline__ float gelu_cdf(float z, float& gauss) {
+  const float t = __fdividef(1.f, fmaf(0.3275911f * kInvSqrt2, fabsf(z), 1.f));
+  gauss = fast_exp2(-0.5f * kLog2e * z * z);
+  float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
+  q = fmaf(t, q, 0.5f * 1.421413741f);
+  q = fmaf(t, q, 0.5f * -0.284496736f);
+  q = fmaf(t, q, 0.5f * 0.254829592f);
+  q *= t * gauss;
+  return z < 0.f ? q : 1.f - q;
+}
 
-__device__ __forceinline__ float act_value(int act, float z) {
-  switch (act) {
-    case kActRelu: return z < 0.f ? 0.f : z;  // a NaN stays one
-    case kActGelu: return z * gelu_cdf(z);
-    case kActGeluTanh: return z * gelu_tanh_gate(z);
-    case kActSilu: return z * sigmoid_f(z);
-    case kActSigmoid: return sigmoid_f(z);
-    default: return z;
+template <int ACT>
+__device__ __forceinline__ float act_value(float z) {
+  if constexpr (ACT == kActRelu) return z < 0.f ? 0.f : z;  // a NaN stays one
+  if constexpr (ACT == kActGelu) {
+    float gauss;
+    return z * gelu_cdf(z, gauss);
   }
+  if constexpr (ACT == kActGeluTanh) return z * gelu_tanh_gate(z);
+  if constexpr (ACT == kActSilu) return z * sigmoid_f(z);
+  if constexpr (ACT == kActSigmoid) return sigmoid_f(z);
+  return z;
 }
 
 // a(z) and a'(z).
-__device__ __forceinline__ void act_value_slope(int act, float z, float& val, float& slope) {
-  switch (act) {
-    case kActRelu:
-      val = z < 0.f ? 0.f : z;
-      slope = z > 0.f ? 1.f : 0.f;
-      return;
-    case kActGelu: {
-      const float c = gelu_cdf(z);
-      val = z * c;
-      slope = fmaf(z * kInvSqrt2Pi, fast_exp2(-0.5f * kLog2e * z * z), c);
-      return;
-    }
-    case kActGeluTanh: {
-      const float p = gelu_tanh_gate(z);
-      val = z * p;
-      // Beyond |z| = 64 p is 0 or 1 and the second term is 0; its polynomial must not overflow.
-      const float zc = fminf(fmaxf(z, -64.f), 64.f);
-      slope = fmaf(zc * p * (1.f - p), 2.f * kGeluC * fmaf(3.f * kGeluC3 * zc, zc, 1.f), p);
-      return;
-    }
-    case kActSilu: {
-      const float p = sigmoid_f(z);
-      val = z * p;
-      slope = fmaf(val, 1.f - p, p);
-      return;
-    }
-    case kActSigmoid: {
-      val = sigmoid_f(z);
-      slope = val * (1.f - val);
-      return;
-    }
-    default:
-      val = z;
-      slope = 1.f;
+template <int ACT>
+__device__ __forceinline__ void act_value_slope(float z, float& val, float& slope) {
+  if constexpr (ACT == kActRelu) {
+    val = z < 0.f ? 0.f : z;
+    slope = z > 0.f ? 1.f : 0.f;
+  } else if constexpr (ACT == kActGelu) {
+    float gauss;
+    const float c = gelu_cdf(z, gauss);
+    val = z * c;
+    slope = fmaf(z * kInvSqrt2Pi, gauss, c);
+  } else if constexpr (ACT == kActGeluTanh) {
+    const float p = gelu_tanh_gate(z);
+    val = z * p;
+    // Beyond |z| = 64 p is 0 or 1 and the second term is 0; its polynomial must not overflow.
+    const float zc = fminf(fmaxf(z, -64.f), 64.f);
+    slope = fmaf(zc * p * (1.f - p), 2.f * kGeluC * fmaf(3.f * kGeluC3 * zc, zc, 1.f), p);
+  } else if constexpr (ACT == kActSilu) {
+    const float p = sigmoid_f(z);
+    val = z * p;
+    slope = fmaf(val, 1.f - p, p);
+  } else if constexpr (ACT == kActSigmoid) {
+    val = sigmoid_f(z);
+    slope = val * (1.f - val);
+  } else {
+    val = z;
+    slope = 1.f;
   }
 }
 
-// The activation of 32 values: one branch for the chunk, not one per value.
-__device__ __forceinline__ void act_32(int act, float (&v)[32]) {
+// Calls f with the activation as a compile-time constant: one branch around a
+// loop over values, none inside it.
+template <class Fn>
+__device__ __forceinline__ void with_act(int act, Fn f) {
   switch (act) {
-    case kActNone: return;
-    case kActRelu:
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = act_value(kActRelu, v[j]);
-      return;
-    case kActGelu:
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = act_value(kActGelu, v[j]);
-      return;
-    case kActGeluTanh:
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = act_value(kActGeluTanh, v[j]);
-      return;
-    case kActSilu:
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = act_value(kActSilu, v[j]);
-      return;
-    default:
-#pragma unroll
-      for (int j = 0; j < 32; ++j) v[j] = act_value(kActSigmoid, v[j]);
+    case kActRelu: f(std::integral_constant<int, kActRelu>()); return;
+    case kActGelu: f(std::integral_constant<int, kActGelu>()); return;
+    case kActGeluTanh: f(std::integral_constant<int, kActGeluTanh>()); return;
+    case kActSilu: f(std::integral_constant<int, kActSilu>()); return;
+    case kActSigmoid: f(std::integral_constant<int, kActSigmoid>()); return;
+    default: f(std::integral_constant<int, kActNone>());
   }
+}
+
+template <int N>
+__device__ __forceinline__ void act_all(int act, float (&v)[N]) {
+  with_act(act, [&](auto a) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
+  });
 }
 
 // A 16-bit [rows, cols] output: through a TMA store map of 32 x 32 boxes where
@@ -126,14 +132,43 @@ struct Out16 {
   int use_map;
 };
 
+// As tma_block_16 (epilogues.cuh: the box and its swizzle), through the two buffers
+// of the warp's staging.
+__device__ __forceinline__ void staged_block_16(const CUtensorMap* map, int x, int y,
+                                                const float (&v)[32], bool fp16, Staging& st,
+                                                int lane) {
+  if (lane == 0) bulk_wait_group_read1();
+  __syncwarp();
+  uint4* stage = reinterpret_cast<uint4*>(st.buf + st.turn * 2048);
+  st.turn ^= 1;
+  uint32_t w[16];
+  if (fp16) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack_f16x2(v[2 * j], v[2 * j + 1]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    stage[lane * 4 + (q ^ ((lane >> 1) & 3))] =
+        make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(map, stage, x, y);
+    bulk_commit_group();
+  }
+}
+
 // One row (this lane's) of a warp's 32 x 32 block at (row0, col0). Warp-uniform
 // but for the values; rows and columns outside the output are clipped.
 __device__ __forceinline__ void put_block_16(const Out16& o, int rows, int cols, int row0, int col0,
-                                             const float (&v)[32], bool fp16, void* stage,
+                                             const float (&v)[32], bool fp16, Staging& st,
                                              int lane) {
   if (row0 >= rows || col0 >= cols) return;
   if (o.use_map) {
-    tma_block_16(&o.map, col0, row0, v, fp16, stage, lane);
+    staged_block_16(&o.map, col0, row0, v, fp16, st, lane);
   } else if (row0 + lane < rows) {
     uint16_t* p = o.ptr + static_cast<size_t>(row0 + lane) * o.ld + col0;
 #pragma unroll
@@ -142,29 +177,56 @@ __device__ __forceinline__ void put_block_16(const Out16& o, int rows, int cols,
   }
 }
 
-// v[j] += src[j] of one row's 32 columns (16-bit); vec: 16-byte loads allowed.
+// Two 16-bit values of a word.
+template <bool F16>
+__device__ __forceinline__ void unpack_2(uint32_t w, float& lo, float& hi) {
+  if constexpr (F16) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+    lo = f.x;
+    hi = f.y;
+  } else {
+    lo = __uint_as_float(w << 16);
+    hi = __uint_as_float(w & 0xFFFF0000u);
+  }
+}
+
+// v[j] += src[j] for 32 values at a 16-byte boundary.
+template <bool F16>
+__device__ __forceinline__ void add_32(const uint16_t* src, float (&v)[32]) {
+  uint4 u[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) u[q] = reinterpret_cast<const uint4*>(src)[q];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const uint32_t w[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int j = q * 8 + 2 * e;
+      float lo, hi;
+      unpack_2<F16>(w[e], lo, hi);
+      f32x2_split(fadd2(f32x2(v[j], v[j + 1]), f32x2(lo, hi)), v[j], v[j + 1]);
+    }
+  }
+}
+
+// The same for the first ncol of a row's 32 columns (16-bit); vec: at a 16-byte boundary.
 __device__ __forceinline__ void add_row_16(const uint16_t* src, int ncol, bool vec, bool fp16,
                                            float (&v)[32]) {
   if (vec && ncol >= 32) {
-    const uint4* p = reinterpret_cast<const uint4*>(src);
-    uint4 u[4];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) u[q] = p[q];
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint32_t w[4] = {u[q].x, u[q].y, u[q].z, u[q].w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        v[q * 8 + 2 * e] += unpack_16(w[e] & 0xFFFFu, fp16);
-        v[q * 8 + 2 * e + 1] += unpack_16(w[e] >> 16, fp16);
-      }
-    }
+    if (fp16)
+      add_32<true>(src, v);
+    else
+      add_32<false>(src, v);
   } else {
 #pragma unroll
     for (int j = 0; j < 32; ++j)
       if (j < ncol) v[j] += unpack_16(src[j], fp16);
   }
 }
+
+// The epilogues drain one warp's 32 rows from row0 (lane = row - row0) of its chunks
+// of a tile whose columns start at col_base. Chunks come in rising column order, so the
+// first one past the output is the last one looked at.
 
 // --------------------------------------------------------- linear: forward
 struct LinearArgs {
@@ -179,38 +241,33 @@ struct LinearArgs {
 
 struct LinearEpi {
   static constexpr bool kAMN = false, kBMN = false;
-  static constexpr int kWideWarps = 8, kStageNeed = 32 * 32 * 2;
+  static constexpr OperandPlan kPlan = kOneEach;
   using Args = LinearArgs;
-  __device__ static void tile(const Args& a, const GemmGeom&, int tm, int tn, int row_in_tile,
-                              int lane, int quad, uint32_t taddr, void* stage,
-                              const EpiSlice& sl) {
-    const int row = tm * kBM + row_in_tile, row0 = tm * kBM + quad * 32;
+  __device__ static void tile(const Args& a, const PairArgs&, int, int row0, int col_base, int lane,
+                              uint32_t taddr, Staging& st, const TileSlice& sl) {
+    const int row = row0 + lane;
     const bool f16 = a.fp16 != 0;
 #pragma unroll 1
     for (int c = sl.c_lo; c < sl.c_hi; ++c) {
-      const int col0 = tn * kBN + c * 32;
+      int acc_col, col0;
+      sl.at(c, acc_col, col0);
+      col0 += col_base;
       if (col0 >= a.N || row0 >= a.M) break;  // uniform over the warp
       float v[32];
-      tmem_ld_32cols(taddr + c * 32, v);
-      if (a.bias) {
-        float bv[32];
-        load_bias32<true>(a.bias, col0, a.N, bv, f16);
-#pragma unroll
-        for (int j = 0; j < 32; ++j) v[j] += bv[j];
-      }
-      if (a.keep) put_block_16(a.z, a.M, a.N, row0, col0, v, f16, stage, lane);
-      act_32(a.act, v);
+      tmem_ld_32cols(taddr + acc_col, v);
+      if (a.bias) add_row_16(a.bias + col0, a.N - col0, true, f16, v);
+      if (a.keep) put_block_16(a.z, a.M, a.N, row0, col0, v, f16, st, lane);
+      act_all(a.act, v);
       if (a.res && row < a.M)
         add_row_16(a.res + static_cast<size_t>(row) * a.ld_res + col0, a.N - col0, a.res_vec != 0,
                    f16, v);
-      put_block_16(a.y, a.M, a.N, row0, col0, v, f16, stage, lane);
+      put_block_16(a.y, a.M, a.N, row0, col0, v, f16, st, lane);
     }
   }
 };
 
 // ---------------------------------------------------------- gated: forward
 struct GatedArgs {
-  SecondOperand second;  // b2: Wu
   int act, fp16, keep;
   int M, F;
   Out16 h, g, u;
@@ -219,27 +276,27 @@ struct GatedArgs {
 struct GatedEpi {
   static constexpr bool kAMN = false, kBMN = false;
   static constexpr OperandPlan kPlan = kTwoB;
-  static constexpr int kWideWarps = 8, kStageNeed = 32 * 32 * 2;
   using Args = GatedArgs;
-  __device__ static void tile(const Args& a, const GemmGeom&, int tm, int tn, int, int lane,
-                              int quad, uint32_t taddr, void* stage, const EpiSlice& sl) {
-    const int row0 = tm * kBM + quad * 32;
+  __device__ static void tile(const Args& a, const PairArgs&, int, int row0, int col_base, int lane,
+                              uint32_t taddr, Staging& st, const TileSlice& sl) {
     const bool f16 = a.fp16 != 0;
 #pragma unroll 1
     for (int c = sl.c_lo; c < sl.c_hi; ++c) {
-      const int col0 = tn * sl.up_off + c * 32;
+      int acc_col, col0;
+      sl.at(c, acc_col, col0);
+      col0 += col_base;
       if (col0 >= a.F || row0 >= a.M) break;  // uniform over the warp
       float g[32], u[32];
-      tmem_ld_32cols(taddr + c * 32, g);
-      tmem_ld_32cols(taddr + sl.up_off + c * 32, u);
+      tmem_ld_32cols(taddr + acc_col, g);
+      tmem_ld_32cols(taddr + sl.up_off + acc_col, u);
       if (a.keep) {
-        put_block_16(a.g, a.M, a.F, row0, col0, g, f16, stage, lane);
-        put_block_16(a.u, a.M, a.F, row0, col0, u, f16, stage, lane);
+        put_block_16(a.g, a.M, a.F, row0, col0, g, f16, st, lane);
+        put_block_16(a.u, a.M, a.F, row0, col0, u, f16, st, lane);
       }
-      act_32(a.act, g);
+      act_all(a.act, g);
 #pragma unroll
       for (int j = 0; j < 32; ++j) g[j] *= u[j];
-      put_block_16(a.h, a.M, a.F, row0, col0, g, f16, stage, lane);
+      put_block_16(a.h, a.M, a.F, row0, col0, g, f16, st, lane);
     }
   }
 };
@@ -247,7 +304,6 @@ struct GatedEpi {
 // --------------------------------------------------- gradients of both
 // dx [M, K] in the operands' type: dz W, or dg Wg + du Wu in one sum.
 struct GradXArgs {
-  SecondOperand second;
   int fp16, M, K;
   Out16 dx;
 };
@@ -256,26 +312,25 @@ template <OperandPlan PLAN>
 struct GradXEpi {
   static constexpr bool kAMN = false, kBMN = true;
   static constexpr OperandPlan kPlan = PLAN;
-  static constexpr int kWideWarps = 8, kStageNeed = 32 * 32 * 2;
   using Args = GradXArgs;
-  __device__ static void tile(const Args& a, const GemmGeom&, int tm, int tn, int, int lane,
-                              int quad, uint32_t taddr, void* stage, const EpiSlice& sl) {
-    const int row0 = tm * kBM + quad * 32;
+  __device__ static void tile(const Args& a, const PairArgs&, int, int row0, int col_base, int lane,
+                              uint32_t taddr, Staging& st, const TileSlice& sl) {
 #pragma unroll 1
     for (int c = sl.c_lo; c < sl.c_hi; ++c) {
-      const int col0 = tn * kBN + c * 32;
+      int acc_col, col0;
+      sl.at(c, acc_col, col0);
+      col0 += col_base;
       if (col0 >= a.K || row0 >= a.M) break;  // uniform over the warp
       float v[32];
-      tmem_ld_32cols(taddr + c * 32, v);
-      put_block_16(a.dx, a.M, a.K, row0, col0, v, a.fp16 != 0, stage, lane);
+      tmem_ld_32cols(taddr + acc_col, v);
+      put_block_16(a.dx, a.M, a.K, row0, col0, v, a.fp16 != 0, st, lane);
     }
   }
 };
 
 // dW [N, K] = dz^T x, in fp32 or the operands' type; with two dz (gated), the
-// first m_split 256-row tiles are dWg and the others dWu.
+// first m_split row tiles are dWg and the others dWu.
 struct GradWArgs {
-  SecondOperand second;
   CUtensorMap out, out2;
   int out16, fp16;
   int N, K;  // rows of one dW, columns
@@ -285,28 +340,28 @@ template <OperandPlan PLAN>
 struct GradWEpi {
   static constexpr bool kAMN = true, kBMN = true;
   static constexpr OperandPlan kPlan = PLAN;
-  static constexpr int kWideWarps = 8, kStageNeed = 32 * 32 * 4;
   using Args = GradWArgs;
-  __device__ static void tile(const Args& a, const GemmGeom&, int tm, int tn, int, int lane,
-                              int quad, uint32_t taddr, void* stage, const EpiSlice& sl) {
+  __device__ static void tile(const Args& a, const PairArgs& g, int tm, int row0, int col_base,
+                              int lane, uint32_t taddr, Staging& st, const TileSlice& sl) {
     const CUtensorMap* out = &a.out;
-    int row0 = tm * kBM + quad * 32;
     if constexpr (PLAN == kTwoA) {
-      if (tm >= 2 * a.second.m_split) {
+      if (tm >= g.m_split) {
         out = &a.out2;
-        row0 -= 2 * a.second.m_split * kBM;
+        row0 -= g.m_split * 256;
       }
     }
 #pragma unroll 1
     for (int c = sl.c_lo; c < sl.c_hi; ++c) {
-      const int col0 = tn * kBN + c * 32;
+      int acc_col, col0;
+      sl.at(c, acc_col, col0);
+      col0 += col_base;
       if (col0 >= a.K || row0 >= a.N) break;  // uniform over the warp
       float v[32];
-      tmem_ld_32cols(taddr + c * 32, v);
+      tmem_ld_32cols(taddr + acc_col, v);
       if (a.out16)
-        tma_block_16(out, col0, row0, v, a.fp16 != 0, stage, lane);
+        staged_block_16(out, col0, row0, v, a.fp16 != 0, st, lane);
       else
-        tma_block_f32(out, col0, row0, v, stage, lane);
+        tma_block_f32(out, col0, row0, v, st.buf, lane);
     }
   }
 };

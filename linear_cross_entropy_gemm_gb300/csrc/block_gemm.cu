@@ -1,42 +1,76 @@
 // GEMM instantiations of the layer operators.
+#include <atomic>
+
 #include "block_epilogues.cuh"
 #include "block_internal.h"
-#include "gemm_launch.cuh"
 
 namespace flce {
 
+// Co-resident clusters of the kernel on the current device, asked once per device
+// and HALVES (whose instantiations share one footprint).
+template <int HALVES>
+static int max_clusters(const void* kernel) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> cache[kMaxDev];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDev) return 0;
+  int v = cache[dev].load(std::memory_order_relaxed);
+  if (v > 0) return v;
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(2, 1, 1);
+  cfg.blockDim = dim3(kLThreads, 1, 1);
+  cfg.dynamicSmemBytes = PairShape<HALVES>::kSmem;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaOccupancyMaxActiveClusters(&v, kernel, &cfg) != cudaSuccess || v <= 0) {
+    cudaGetLastError();
+    return 0;
+  }
+  cache[dev].store(v, std::memory_order_relaxed);
+  return v;
+}
+
+template <class Epi, int HALVES>
+static cudaError_t launch_halves(const PairArgs& g, const typename Epi::Args& ea, int sms,
+                                 cudaStream_t st) {
+  auto kernel = pair_gemm_kernel<Epi, HALVES>;
+  constexpr size_t smem = PairShape<HALVES>::kSmem;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  int clusters = max_clusters<HALVES>(reinterpret_cast<const void*>(kernel));
+  if (clusters <= 0) clusters = sms / 2;
+  const int tiles = g.tiles_m * g.tiles_n;
+  if (clusters > tiles) clusters = tiles;
+  kernel<<<2 * clusters, kLThreads, smem, st>>>(g, ea);
+  return cudaGetLastError();
+}
+
 template <class Epi>
-static cudaError_t launch_pairs(GemmKind kind, const CUtensorMap& a, const CUtensorMap& b,
-                                const GemmGeom& g, const typename Epi::Args& ea, int* dev_err,
-                                int sms, cudaStream_t st) {
-  return kind == kGemmWide ? launch_wide<Epi>(a, b, g, ea, dev_err, sms, st)
-                           : launch_pair<Epi>(a, b, g, ea, dev_err, sms, st);
-}
-
-cudaError_t launch_linear(GemmKind kind, const CUtensorMap& a, const CUtensorMap& b,
-                          const GemmGeom& g, const LinearArgs& ea, int* dev_err, int sms,
+static cudaError_t launch(const PairArgs& g, const typename Epi::Args& ea, int sms,
                           cudaStream_t st) {
-  return launch_pairs<LinearEpi>(kind, a, b, g, ea, dev_err, sms, st);
+  return g.halves == 2 ? launch_halves<Epi, 2>(g, ea, sms, st)
+                       : launch_halves<Epi, 1>(g, ea, sms, st);
 }
 
-cudaError_t launch_gated(GemmKind kind, const CUtensorMap& a, const CUtensorMap& b,
-                         const GemmGeom& g, const GatedArgs& ea, int* dev_err, int sms,
-                         cudaStream_t st) {
-  return launch_pairs<GatedEpi>(kind, a, b, g, ea, dev_err, sms, st);
+cudaError_t launch_linear(const PairArgs& g, const LinearArgs& ea, int sms, cudaStream_t st) {
+  return launch<LinearEpi>(g, ea, sms, st);
 }
-
-cudaError_t launch_grad_x(GemmKind kind, bool two, const CUtensorMap& a, const CUtensorMap& b,
-                          const GemmGeom& g, const GradXArgs& ea, int* dev_err, int sms,
+cudaError_t launch_gated(const PairArgs& g, const GatedArgs& ea, int sms, cudaStream_t st) {
+  return launch<GatedEpi>(g, ea, sms, st);
+}
+cudaError_t launch_grad_x(bool two, const PairArgs& g, const GradXArgs& ea, int sms,
                           cudaStream_t st) {
-  return two ? launch_pairs<GradXEpi<kTwoK>>(kind, a, b, g, ea, dev_err, sms, st)
-             : launch_pairs<GradXEpi<kOneEach>>(kind, a, b, g, ea, dev_err, sms, st);
+  return two ? launch<GradXEpi<kTwoK>>(g, ea, sms, st) : launch<GradXEpi<kOneEach>>(g, ea, sms, st);
 }
-
-cudaError_t launch_grad_w(GemmKind kind, bool two, const CUtensorMap& a, const CUtensorMap& b,
-                          const GemmGeom& g, const GradWArgs& ea, int* dev_err, int sms,
+cudaError_t launch_grad_w(bool two, const PairArgs& g, const GradWArgs& ea, int sms,
                           cudaStream_t st) {
-  return two ? launch_pairs<GradWEpi<kTwoA>>(kind, a, b, g, ea, dev_err, sms, st)
-             : launch_pairs<GradWEpi<kOneEach>>(kind, a, b, g, ea, dev_err, sms, st);
+  return two ? launch<GradWEpi<kTwoA>>(g, ea, sms, st) : launch<GradWEpi<kOneEach>>(g, ea, sms, st);
 }
 
 }  // namespace flce

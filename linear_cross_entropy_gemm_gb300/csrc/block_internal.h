@@ -9,6 +9,7 @@
 
 namespace flce {
 
+struct PairArgs;
 struct LinearArgs;
 struct GatedArgs;
 struct GradXArgs;
@@ -16,18 +17,33 @@ struct GradWArgs;
 
 // GEMMs of the layer operators (block_gemm.cu). `two`: the gated operator's
 // two-operand plan.
-cudaError_t launch_linear(GemmKind kind, const CUtensorMap& a, const CUtensorMap& b,
-                          const GemmGeom& g, const LinearArgs& ea, int* dev_err, int sms,
+cudaError_t launch_linear(const PairArgs& g, const LinearArgs& ea, int sms, cudaStream_t st);
+cudaError_t launch_gated(const PairArgs& g, const GatedArgs& ea, int sms, cudaStream_t st);
+cudaError_t launch_grad_x(bool two, const PairArgs& g, const GradXArgs& ea, int sms,
                           cudaStream_t st);
-cudaError_t launch_gated(GemmKind kind, const CUtensorMap& a, const CUtensorMap& b,
-                         const GemmGeom& g, const GatedArgs& ea, int* dev_err, int sms,
-                         cudaStream_t st);
-cudaError_t launch_grad_x(GemmKind kind, bool two, const CUtensorMap& a, const CUtensorMap& b,
-                          const GemmGeom& g, const GradXArgs& ea, int* dev_err, int sms,
+cudaError_t launch_grad_w(bool two, const PairArgs& g, const GradWArgs& ea, int sms,
                           cudaStream_t st);
-cudaError_t launch_grad_w(GemmKind kind, bool two, const CUtensorMap& a, const CUtensorMap& b,
-                          const GemmGeom& g, const GradWArgs& ea, int* dev_err, int sms,
-                          cudaStream_t st);
+
+// Few-token products (block_small.cu): y [M, N] = epilogue of x Wt^T, with the
+// weights on the MMA's rows. w: boxes of 128 features x 64 sum elements (64 x 64
+// with the features contiguous); x: 64 sum elements x small_tokens(M) tokens.
+struct SmallArgs {
+  CUtensorMap w, w2, x, x2;
+  const uint16_t* bias;
+  const uint16_t* res;
+  uint16_t* keep;  // z, or [2, M, N] (gated); null: not kept
+  uint16_t* y;
+  int64_t ld_res, ld_y;
+  int res_vec, y_vec;  // rows start on 16-byte boundaries
+  int act, fp16;
+  int M, N;
+  int k_blocks, k_split;  // blocks of 64 of the whole sum; those of the first segment
+  int slices;             // K slices = cluster size: 1, 2, 4 or 8
+  int* dev_err;
+};
+int small_tokens(int64_t M);  // tokens of a tile
+int small_slices(int64_t M, int64_t N, int k_blocks);
+cudaError_t launch_small(bool two, bool w_mn, const SmallArgs& a, cudaStream_t st);
 
 // Element-wise parts of the backward passes (block_rowwise.cu).
 struct DzArgs {

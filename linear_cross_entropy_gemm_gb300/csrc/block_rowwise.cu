@@ -65,12 +65,14 @@ __global__ void __launch_bounds__(32 * kDzRowGroups) dz_kernel(const DzArgs a, i
         float z[8];
         unpack8(__ldg(reinterpret_cast<const uint4*>(a.z + static_cast<size_t>(r) * a.N + vcol)),
                 f16, z);
+        with_act(a.act, [&](auto act) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float val, slope;
-          act_value_slope(a.act, z[j], val, slope);
-          v[j] *= slope;
-        }
+          for (int j = 0; j < 8; ++j) {
+            float val, slope;
+            act_value_slope<decltype(act)::value>(z[j], val, slope);
+            v[j] *= slope;
+          }
+        });
       }
       if (a.dz)
         *reinterpret_cast<uint4*>(a.dz + static_cast<size_t>(r) * a.ld_dz + vcol) = pack8(v, f16);
@@ -86,9 +88,12 @@ __global__ void __launch_bounds__(32 * kDzRowGroups) dz_kernel(const DzArgs a, i
         if (c >= a.N) continue;
         float v = unpack_16(a.dy[static_cast<size_t>(r) * a.ld_dy + c], f16);
         if (a.z) {
-          float val, slope;
-          act_value_slope(a.act, unpack_16(a.z[static_cast<size_t>(r) * a.N + c], f16), val, slope);
-          v *= slope;
+          const float z = unpack_16(a.z[static_cast<size_t>(r) * a.N + c], f16);
+          with_act(a.act, [&](auto act) {
+            float val, slope;
+            act_value_slope<decltype(act)::value>(z, val, slope);
+            v *= slope;
+          });
         }
         if (a.dz) a.dz[static_cast<size_t>(r) * a.ld_dz + c] = to16(v, f16);
         sum[j] += v;
@@ -130,13 +135,15 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradArgs a) 
           f16, d);
   unpack8(__ldg(reinterpret_cast<const uint4*>(a.g + at)), f16, g);
   unpack8(__ldg(reinterpret_cast<const uint4*>(a.u + at)), f16, u);
+  with_act(a.act, [&](auto act) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    float val, slope;
-    act_value_slope(a.act, g[j], val, slope);
-    g[j] = d[j] * u[j] * slope;
-    u[j] = d[j] * val;
-  }
+    for (int j = 0; j < 8; ++j) {
+      float val, slope;
+      act_value_slope<decltype(act)::value>(g[j], val, slope);
+      g[j] = d[j] * u[j] * slope;
+      u[j] = d[j] * val;
+    }
+  });
   *reinterpret_cast<uint4*>(a.dg + at) = pack8(g, f16);
   *reinterpret_cast<uint4*>(a.du + at) = pack8(u, f16);
 }

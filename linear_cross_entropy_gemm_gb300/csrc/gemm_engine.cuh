@@ -21,7 +21,6 @@
 // bits select the form, so dW = dL^T x and dx = dL W need no transposed copies.
 #pragma once
 #include <cstdint>
-#include <type_traits>
 #include <cuda.h>
 
 #include "sm103_primitives.cuh"
@@ -70,8 +69,6 @@ struct GemmGeom {
 // kernel's accumulator scheme lets it run.
 struct EpiSlice {
   int c_lo, c_hi;            // chunks [c_lo, c_hi) of the sub-tile's kBN / 32
-  int up_off;                // kTwoB: accumulator columns from B's product to B2's, which is
-                             // also the tile's output columns (else unused)
   int sub;                   // -1: the whole sub-tile; 0 / 1: first / second half
   uint64_t* xbar;            // sub >= 0: "published" barrier of the pair (32 arrivals)
   uint64_t* xfree;           // sub >= 0: "read" barrier of the pair (32 arrivals)
@@ -86,7 +83,6 @@ __device__ __forceinline__ EpiSlice whole_slice() {
   EpiSlice sl;
   sl.c_lo = 0;
   sl.c_hi = kBN / 32;
-  sl.up_off = 0;
   sl.sub = -1;
   sl.xbar = nullptr;
   sl.xfree = nullptr;
@@ -125,33 +121,6 @@ __device__ __forceinline__ void tile_coords(const GemmGeom& g, int t, int& tm, i
   }
 }
 
-// Where the operands of a GEMM come from. Most have one A and one B tensor. The
-// gated feed-forward products have two of one kind (gate and up), whose second
-// tensor map travels in the epilogue's arguments; an epilogue names its plan as
-// `kPlan` (absent: kOneEach). The CTA-pair forms only.
-//   kTwoB : the tile's B columns are half rows of B, half rows of B2 at the same
-//           offset, so both products of a token row and an output column land in
-//           the same CTA's TMEM lane (256 x 256 tile: columns [0, 128) from B
-//           and [128, 256) from B2; 256 x 512: [0, 256) and [256, 512)). A tile
-//           covers half as many output columns as it has accumulator columns.
-//   kTwoK : the sum runs over A B^T and then A2 B2^T (k_split K blocks of the
-//           first), each pair zero-filled to its own length.
-//   kTwoA : the first m_split 256-row tiles take A, the others A2.
-enum OperandPlan : int { kOneEach = 0, kTwoB = 1, kTwoK = 2, kTwoA = 3 };
-struct SecondOperand {
-  CUtensorMap a2, b2;
-  int k_split;  // kTwoK: K blocks of the first product
-  int m_split;  // kTwoA: 256-row tiles of the first A
-};
-template <class Epi, class = void>
-struct PlanOf {
-  static constexpr OperandPlan value = kOneEach;
-};
-template <class Epi>
-struct PlanOf<Epi, std::enable_if_t<(Epi::kPlan >= 0)>> {
-  static constexpr OperandPlan value = Epi::kPlan;
-};
-
 // Bounded wait that ignores the abort flag (used to drain in-flight work).
 __device__ __forceinline__ void mbar_drain(uint64_t* bar, uint32_t parity) {
   const long long t0 = clock64();
@@ -167,7 +136,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const __grid_constant__ typename Epi::Args ea, int* dev_err) {
   constexpr bool kAMN = Epi::kAMN;
   constexpr bool kBMN = Epi::kBMN;
-  static_assert(PlanOf<Epi>::value == kOneEach, "two operands of one kind: CTA-pair forms only");
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -358,7 +326,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                          const __grid_constant__ typename Epi::Args ea, int* dev_err) {
   constexpr bool kAMN = Epi::kAMN;
   constexpr bool kBMN = Epi::kBMN;
-  constexpr OperandPlan kPlan = PlanOf<Epi>::value;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -421,19 +388,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int t = cluster; t < num_tiles; t += nclusters) {
         int tm2, tn;
         tile_coords(pg, t, tm2, tn);
-        int m0 = tm2 * (2 * kBM) + static_cast<int>(rank) * kBM;
-        int n0 = tn * kBN + static_cast<int>(rank) * (kBN / 2);
-        const CUtensorMap *pa = &mapA, *pb = &mapB;
-        if constexpr (kPlan == kTwoB) {
-          n0 = tn * (kBN / 2);
-          if (!leader) pb = &ea.second.b2;
-        }
-        if constexpr (kPlan == kTwoA) {
-          if (tm2 >= ea.second.m_split) {
-            pa = &ea.second.a2;
-            m0 -= ea.second.m_split * (2 * kBM);
-          }
-        }
+        const int m0 = tm2 * (2 * kBM) + static_cast<int>(rank) * kBM;
+        const int n0 = tn * kBN + static_cast<int>(rank) * (kBN / 2);
         bool ok = true;
         for (int kb = 0; kb < g.k_blocks; ++kb) {
           if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, dev_err)) {
@@ -445,28 +401,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const uint32_t fb = full0 + static_cast<uint32_t>(s) * 8u;
           uint8_t* a = sA + s * kPairAStageBytes;
           uint8_t* b = sB + s * kPairBStageBytes;
-          int k0 = kb * kBK;
-          if constexpr (kPlan == kTwoK) {
-            if (kb >= ea.second.k_split) {
-              pa = &ea.second.a2;
-              pb = &ea.second.b2;
-              k0 -= ea.second.k_split * kBK;
-            }
-          }
+          const int k0 = kb * kBK;
           if constexpr (!kAMN) {
-            tma_load_2d_pair(a, pa, fb, k0 + g.a_k_off, m0 + g.a_mn_off, pol_a);
+            tma_load_2d_pair(a, &mapA, fb, k0 + g.a_k_off, m0 + g.a_mn_off, pol_a);
           } else {
 #pragma unroll
             for (int j = 0; j < kBM / 64; ++j)
-              tma_load_2d_pair(a + j * kMnBoxBytes, pa, fb, m0 + g.a_mn_off + j * 64,
+              tma_load_2d_pair(a + j * kMnBoxBytes, &mapA, fb, m0 + g.a_mn_off + j * 64,
                                k0 + g.a_k_off, pol_a);
           }
           if constexpr (!kBMN) {
-            tma_load_2d_pair(b, pb, fb, k0 + g.b_k_off, n0 + g.b_mn_off, pol_b);
+            tma_load_2d_pair(b, &mapB, fb, k0 + g.b_k_off, n0 + g.b_mn_off, pol_b);
           } else {
 #pragma unroll
             for (int j = 0; j < (kBN / 2) / 64; ++j)
-              tma_load_2d_pair(b + j * kMnBoxBytes, pb, fb, n0 + g.b_mn_off + j * 64,
+              tma_load_2d_pair(b + j * kMnBoxBytes, &mapB, fb, n0 + g.b_mn_off + j * 64,
                                k0 + g.b_k_off, pol_b);
           }
           ++issued;
@@ -533,11 +482,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ---------------------------------------------------- epilogue (both CTAs)
     const int quad = warp & 3;
     const int row_in_tile = quad * 32 + lane;
-    EpiSlice sl = whole_slice();
-    if constexpr (kPlan == kTwoB) {
-      sl.c_hi = kBN / 64;
-      sl.up_off = kBN / 2;
-    }
+    const EpiSlice sl = whole_slice();
     const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
     int acc = 0;
     uint32_t aph = 0;
@@ -602,7 +547,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wide_threads(kEW), 1
                          const __grid_constant__ typename Epi::Args ea, int* dev_err) {
   constexpr bool kAMN = Epi::kAMN;
   constexpr bool kBMN = Epi::kBMN;
-  constexpr OperandPlan kPlan = PlanOf<Epi>::value;
   static_assert(kEW == 8 || kEW == 16, "8 or 16 epilogue warps");
   constexpr int kWarpStage = kWideStageRegion / kEW;  // staging bytes per epilogue warp
   static_assert(Epi::kStageNeed <= kWarpStage, "epilogue staging does not fit");
@@ -676,16 +620,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wide_threads(kEW), 1
       for (int t = cluster; t < num_tiles; t += nclusters) {
         int tm2, tn2;
         tile_coords(pg, t, tm2, tn2);
-        int m0 = tm2 * (2 * kBM) + static_cast<int>(rank) * kBM;
-        const int n0 = tn2 * (kPlan == kTwoB ? kBN : 2 * kBN) +
-                       static_cast<int>(rank) * (kBN / 2);
-        const CUtensorMap *pa = &mapA, *pb = &mapB;
-        if constexpr (kPlan == kTwoA) {
-          if (tm2 >= ea.second.m_split) {
-            pa = &ea.second.a2;
-            m0 -= ea.second.m_split * (2 * kBM);
-          }
-        }
+        const int m0 = tm2 * (2 * kBM) + static_cast<int>(rank) * kBM;
+        const int n0 = tn2 * (2 * kBN) + static_cast<int>(rank) * (kBN / 2);
         bool ok = true;
         for (int kb = 0; kb < g.k_blocks; ++kb) {
           if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, dev_err)) {
@@ -697,33 +633,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wide_threads(kEW), 1
           const uint32_t fb = full0 + static_cast<uint32_t>(s) * 8u;
           uint8_t* a = sA + s * kPairAStageBytes;
           uint8_t* b = sB + s * kWideBStageBytes;
-          int k0 = kb * kBK;
-          if constexpr (kPlan == kTwoK) {
-            if (kb >= ea.second.k_split) {
-              pa = &ea.second.a2;
-              pb = &ea.second.b2;
-              k0 -= ea.second.k_split * kBK;
-            }
-          }
+          const int k0 = kb * kBK;
           if constexpr (!kAMN) {
-            tma_load_2d_pair(a, pa, fb, k0 + g.a_k_off, m0 + g.a_mn_off, pol);
+            tma_load_2d_pair(a, &mapA, fb, k0 + g.a_k_off, m0 + g.a_mn_off, pol);
           } else {
 #pragma unroll
             for (int j = 0; j < kBM / 64; ++j)
-              tma_load_2d_pair(a + j * kMnBoxBytes, pa, fb, m0 + g.a_mn_off + j * 64,
+              tma_load_2d_pair(a + j * kMnBoxBytes, &mapA, fb, m0 + g.a_mn_off + j * 64,
                                k0 + g.a_k_off, pol);
           }
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint8_t* bh = b + h * kWideBHalfBytes;
-            const int nh = n0 + (kPlan == kTwoB ? 0 : h * kBN) + g.b_mn_off;
-            if constexpr (kPlan == kTwoB) pb = h == 0 ? &mapB : &ea.second.b2;
+            const int nh = n0 + h * kBN + g.b_mn_off;
             if constexpr (!kBMN) {
-              tma_load_2d_pair(bh, pb, fb, k0 + g.b_k_off, nh, pol);
+              tma_load_2d_pair(bh, &mapB, fb, k0 + g.b_k_off, nh, pol);
             } else {
 #pragma unroll
               for (int j = 0; j < (kBN / 2) / 64; ++j)
-                tma_load_2d_pair(bh + j * kMnBoxBytes, pb, fb, nh + j * 64, k0 + g.b_k_off,
+                tma_load_2d_pair(bh + j * kMnBoxBytes, &mapB, fb, nh + j * 64, k0 + g.b_k_off,
                                  pol);
             }
           }
@@ -808,7 +736,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wide_threads(kEW), 1
     sl.sub = kPerHalf == 1 ? -1 : cs % kPerHalf;
     sl.c_lo = (sl.sub < 0 ? 0 : sl.sub) * kChunks;
     sl.c_hi = sl.c_lo + kChunks;
-    sl.up_off = 0;
     sl.xbar = &xbar[half * 4 + quad];
     sl.xfree = &xfree[half * 4 + quad];
     sl.xchg = reinterpret_cast<float4*>(sl.sub == 0 ? my_stage + 4 * kWarpStage : my_stage);
@@ -825,15 +752,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wide_threads(kEW), 1
       tc_fence_after();
       // The last wide tile's second half can lie wholly past N: no sub-tile.
       const int tn = tn2 * 2 + half;
-      if constexpr (kPlan == kTwoB) {
-        // One tile of 256 output columns; this warp takes its share of their
-        // chunks, with B's product at the chunk and B2's 256 columns above it.
-        sl.c_lo = cs * (kBN / 32) / (kEW / 4);
-        sl.c_hi = sl.c_lo + (kBN / 32) / (kEW / 4);
-        sl.up_off = kBN;
-        Epi::tile(ea, g, tm2 * 2 + static_cast<int>(rank), tn2, row_in_tile, lane, quad,
-                  tmem_base + (static_cast<uint32_t>(quad * 32) << 16), my_stage, sl);
-      } else if (tn < g.tiles_n) {
+      if (tn < g.tiles_n) {
         const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
                                static_cast<uint32_t>(half * kBN);
         Epi::tile(ea, g, tm2 * 2 + static_cast<int>(rank), tn, row_in_tile, lane, quad, taddr,
