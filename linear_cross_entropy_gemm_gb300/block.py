@@ -15,7 +15,9 @@ library's kernels, on the current CUDA stream, without a synchronisation.
 """
 from __future__ import annotations
 
+import array
 import ctypes
+import operator
 from typing import Iterable, Optional, Sequence
 
 import torch
@@ -26,23 +28,26 @@ from ._lib import ACTIVATIONS, FlceError, FlceGatedParams, FlceLinearParams
 _OPERANDS = (torch.bfloat16, torch.float16)
 _GRAD_TYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
-# Parameter structs with their addresses and workspace sizes, by their values
-# (sizes, pitches and options only). Bounded: emptied when it is full.
+# Parameter structs by their values (sizes, pitches and options only): (library,
+# address, forward and backward workspace bytes, the struct that keeps the address
+# alive). Bounded: emptied when it is full.
 _params = {}
 _PARAMS_MOST = 4096
 
 
-def _struct(kind, size_of, *values):
+def _struct(kind, *values):
     key = (kind, values)
     got = _params.get(key)
     if got is None:
-        p = kind(*values)
+        lib = _lib.load()
+        p = kind(*[int(v) for v in values])
         at = ctypes.addressof(p)
-        got = (p, at, int(size_of(at, 0)), int(size_of(at, 1)))
+        size = lib.flce_linear_workspace_size if kind is FlceLinearParams else \
+            lib.flce_gated_workspace_size
         if len(_params) >= _PARAMS_MOST:
             _params.clear()
-        _params[key] = got
-    return got
+        got = _params[key] = (lib, at, int(size(at, 0)), int(size(at, 1)), p)
+    return got[:4]
 
 
 def _activation(name) -> int:
@@ -54,18 +59,22 @@ def _activation(name) -> int:
 
 def _rows(t: torch.Tensor, rows: int, cols: int, dtype, name: str) -> int:
     """The row pitch (elements) of a [rows, cols] CUDA tensor whose rows are contiguous."""
-    if t.dtype != dtype or not t.is_cuda:
+    if t.dtype is not dtype or not t.is_cuda:
         raise TypeError(f"flce: {name} must be a CUDA tensor of type {dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"flce: {name} must have shape [{rows}, {cols}], got {tuple(t.shape)}")
+    if rows <= 1 or cols == 0:
+        if cols > 1 and t.stride(1) != 1:
+            raise ValueError(f"flce: the rows of {name} must be contiguous")
+        return cols
     ld, step = t.stride()
-    if (step != 1 and cols > 1) or (ld < cols and rows > 1):
+    if (step != 1 and cols > 1) or ld < cols:
         raise ValueError(f"flce: the rows of {name} must be contiguous and must not overlap")
-    return ld if rows > 1 else cols
+    return ld
 
 
 def _dense(t: torch.Tensor, shape, dtype, name: str):
-    if t.dtype != dtype or not t.is_cuda:
+    if t.dtype is not dtype or not t.is_cuda:
         raise TypeError(f"flce: {name} must be a CUDA tensor of type {dtype}")
     if t.shape != shape or not t.is_contiguous():
         raise ValueError(f"flce: {name} must be contiguous with shape {list(shape)}")
@@ -79,14 +88,13 @@ def _operand(x: torch.Tensor) -> None:
 
 
 class _On:
-    """The device and stream of a call. With a stream of its own, outputs and
-    scratch are allocated on that stream too, so that none of them can be
-    handed out again while its kernels still run."""
+    """The device and stream of a call that names a stream or runs on another
+    device than the current one. With a stream of its own, outputs and scratch are
+    allocated on that stream too, so that none of them can be handed out again
+    while its kernels still run."""
 
     def __init__(self, device, stream):
-        self.contexts = []
-        if device.index != torch.cuda.current_device():
-            self.contexts.append(torch.cuda.device(device))
+        self.contexts = [torch.cuda.device(device)]
         if stream is not None:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=device)
@@ -95,16 +103,28 @@ class _On:
     def __enter__(self):
         for c in self.contexts:
             c.__enter__()
-        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *exc):
         for c in reversed(self.contexts):
             c.__exit__(*exc)
 
 
-def _error_word(device) -> int:
-    from . import device_error_word
-    return device_error_word(device).data_ptr()
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_error_words = {}
+
+
+def _elsewhere(device, stream) -> bool:
+    return stream is not None or device.index != _current_device()
+
+
+def _error_word(index: int) -> int:
+    """Address of the device's error word (which lives as long as the process)."""
+    at = _error_words.get(index)
+    if at is None:
+        from . import device_error_word
+        at = _error_words[index] = device_error_word(torch.device("cuda", index)).data_ptr()
+    return at
 
 
 def _scratch(workspace, need: int, device):
@@ -129,22 +149,26 @@ def _done(status: int, what: str) -> None:
 
 
 # ------------------------------------------------------------------- linear
-def _linear_params(lib, x, W, b, res, y, activation, dW_fp32, db_fp32):
-    """Parameters of a linear call; y: the output, or the backward's dy."""
-    _operand(x)
+def _weight(W: torch.Tensor) -> None:
+    if W.dim() != 2:
+        raise ValueError(f"flce: weights must be two-dimensional, got shape {tuple(W.shape)}")
+
+
+def _linear_params(x, W, b, res, y, activation, dW_fp32, db_fp32):
+    """(library, address of the parameters, forward and backward workspace bytes) of a
+    linear call; y: the output, or the backward's dy."""
     M, K = x.shape
-    if W.dim() != 2 or W.shape[1] != K:
-        raise ValueError(f"flce: W must have shape [N, {K}], got {tuple(W.shape)}")
     N = W.shape[0]
-    _dense(W, (N, K), x.dtype, "W")
+    dtype = x.dtype
+    if W.shape[1] != K:
+        raise ValueError(f"flce: W must have shape [N, {K}], got {tuple(W.shape)}")
+    _dense(W, (N, K), dtype, "W")
     if b is not None:
-        _dense(b, (N,), x.dtype, "b")
-    ld_res = 0 if res is None else _rows(res, M, N, x.dtype, "residual")
-    ld_y = 0 if y is None else _rows(y, M, N, x.dtype, "the output or its gradient")
-    return _struct(FlceLinearParams, lib.flce_linear_workspace_size, M, K, N,
-                   _rows(x, M, K, x.dtype, "x"), ld_res, ld_y, _activation(activation),
-                   int(b is not None), int(res is not None), int(x.dtype == torch.float16),
-                   int(dW_fp32), int(db_fp32))
+        _dense(b, (N,), dtype, "b")
+    return _struct(FlceLinearParams, M, K, N, _rows(x, M, K, dtype, "x"),
+                   0 if res is None else _rows(res, M, N, dtype, "residual"),
+                   _rows(y, M, N, dtype, "the output or its gradient"), _activation(activation),
+                   b is not None, res is not None, dtype is torch.float16, dW_fp32, db_fp32)
 
 
 def flce_linear_forward(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tensor] = None,
@@ -158,18 +182,27 @@ def flce_linear_forward(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tens
     rows of any pitch, ``out`` may be the residual itself. ``pre`` (an [M, N]
     tensor of x's type) receives z = x W^T + b for flce_linear_backward; a layer
     without an activation needs none. ``workspace``: as in flce_forward."""
-    lib = _lib.load()
+    device = x.device
+    if device.type == "cuda" and _elsewhere(device, stream):
+        with _On(device, stream):
+            return flce_linear_forward(x, W, b, residual, activation=activation, pre=pre, out=out,
+                                       workspace=workspace)
     _operand(x)
-    with _On(x.device, stream) as s:
-        y = out if out is not None else torch.empty(x.shape[0], W.shape[0], dtype=x.dtype,
-                                                    device=x.device)
-        _, p, need, _ = _linear_params(lib, x, W, b, residual, y, activation, False, False)
-        if pre is not None:
-            _dense(pre, y.shape, x.dtype, "pre")
-        ws = _scratch(workspace, need, x.device)
-        _done(lib.flce_linear_forward(p, x.data_ptr(), W.data_ptr(), _ptr(b), _ptr(residual),
-                                      y.data_ptr(), _ptr(pre), _ptr(ws), need,
-                                      _error_word(x.device), s), "flce_linear_forward")
+    _weight(W)
+    y = torch.empty((x.shape[0], W.shape[0]), dtype=x.dtype, device=device) if out is None else out
+    lib, p, need, _ = _linear_params(x, W, b, residual, y, activation, False, False)
+    if pre is not None:
+        _dense(pre, y.shape, x.dtype, "pre")
+    ws = None if need == 0 else _scratch(workspace, need, device)
+    index = device.index
+    st = lib.flce_linear_forward(p, x.data_ptr(), W.data_ptr(),
+                                 None if b is None else b.data_ptr(),
+                                 None if residual is None else residual.data_ptr(), y.data_ptr(),
+                                 None if pre is None else pre.data_ptr(),
+                                 None if ws is None else ws.data_ptr(), need, _error_word(index),
+                                 _raw_stream(index))
+    if st:
+        raise FlceError(st, "flce_linear_forward")
     return y
 
 
@@ -185,43 +218,51 @@ def flce_linear_backward(dy: torch.Tensor, x: torch.Tensor, W: torch.Tensor,
     ``pre``: the forward's, with an activation. dz = dy a'(z) is rounded to x's
     type before the two products. ``needs``: which of (dx, dW, db) to compute;
     the others are None."""
-    lib = _lib.load()
+    device = x.device
+    if device.type == "cuda" and _elsewhere(device, stream):
+        with _On(device, stream):
+            return flce_linear_backward(dy, x, W, b, activation=activation, pre=pre,
+                                        dW_dtype=dW_dtype, db_dtype=db_dtype, needs=needs,
+                                        workspace=workspace)
     _operand(x)
-    for t in (dW_dtype, db_dtype):
-        if t not in (torch.float32, x.dtype):
-            raise TypeError("flce: dW_dtype and db_dtype must be fp32 or x's dtype")
-    _, p, _, need = _linear_params(lib, x, W, b, None, dy, activation,
-                                   dW_dtype == torch.float32, db_dtype == torch.float32)
+    _weight(W)
+    dtype, f32 = x.dtype, torch.float32
+    if (dW_dtype is not f32 and dW_dtype is not dtype) or \
+            (db_dtype is not f32 and db_dtype is not dtype):
+        raise TypeError("flce: dW_dtype and db_dtype must be fp32 or x's dtype")
+    lib, p, _, need = _linear_params(x, W, b, None, dy, activation, dW_dtype is f32,
+                                     db_dtype is f32)
+    z = None
     if activation != "none":
         if pre is None:
             raise ValueError("flce: the backward of a layer with an activation needs pre=")
-        _dense(pre, dy.shape, x.dtype, "pre")
-    (M, K), N, dev = x.shape, W.shape[0], x.device
-    with _On(dev, stream) as s:
-        dx = torch.empty(M, K, dtype=x.dtype, device=dev) if needs[0] else None
-        dW = torch.empty(N, K, dtype=dW_dtype, device=dev) if needs[1] else None
-        db = torch.empty(N, dtype=db_dtype, device=dev) if b is not None and needs[2] else None
-        ws = _scratch(workspace, need, dev)
-        _done(lib.flce_linear_backward(p, dy.data_ptr(), x.data_ptr(), W.data_ptr(),
-                                       _ptr(pre) if activation != "none" else None, _ptr(dx),
-                                       _ptr(dW), _ptr(db), _ptr(ws),
-                                       0 if ws is None else ws.numel(), _error_word(dev), s),
-              "flce_linear_backward")
+        _dense(pre, dy.shape, dtype, "pre")
+        z = pre.data_ptr()
+    (M, K), N, index = x.shape, W.shape[0], device.index
+    dx = torch.empty((M, K), dtype=dtype, device=device) if needs[0] else None
+    dW = torch.empty((N, K), dtype=dW_dtype, device=device) if needs[1] else None
+    db = torch.empty(N, dtype=db_dtype, device=device) if b is not None and needs[2] else None
+    ws = _scratch(workspace, need, device)
+    _done(lib.flce_linear_backward(p, dy.data_ptr(), x.data_ptr(), W.data_ptr(), z, _ptr(dx),
+                                   _ptr(dW), _ptr(db), _ptr(ws), 0 if ws is None else ws.numel(),
+                                   _error_word(index), _raw_stream(index)),
+          "flce_linear_backward")
     return dx, dW, db
 
 
 # -------------------------------------------------------------------- gated
-def _gated_params(lib, x, Wg, Wu, h, activation, dW_fp32):
-    _operand(x)
+def _gated_params(x, Wg, Wu, h, activation, dW_fp32):
+    """As _linear_params; h: the output, or the backward's dh."""
     M, K = x.shape
-    if Wg.dim() != 2 or Wg.shape[1] != K:
-        raise ValueError(f"flce: Wg must have shape [F, {K}], got {tuple(Wg.shape)}")
     F = Wg.shape[0]
-    _dense(Wg, (F, K), x.dtype, "Wg")
-    _dense(Wu, (F, K), x.dtype, "Wu")
-    return _struct(FlceGatedParams, lib.flce_gated_workspace_size, M, K, F,
-                   _rows(x, M, K, x.dtype, "x"), _rows(h, M, F, x.dtype, "h or its gradient"),
-                   _activation(activation), int(x.dtype == torch.float16), int(dW_fp32))
+    dtype = x.dtype
+    if Wg.shape[1] != K:
+        raise ValueError(f"flce: Wg must have shape [F, {K}], got {tuple(Wg.shape)}")
+    _dense(Wg, (F, K), dtype, "Wg")
+    _dense(Wu, (F, K), dtype, "Wu")
+    return _struct(FlceGatedParams, M, K, F, _rows(x, M, K, dtype, "x"),
+                   _rows(h, M, F, dtype, "h or its gradient"), _activation(activation),
+                   dtype is torch.float16, dW_fp32)
 
 
 def flce_gated_forward(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, *,
@@ -235,18 +276,25 @@ def flce_gated_forward(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, *,
     of x and ``out`` may be strided (a multiple of 8 elements). ``pre`` (a
     [2, M, F] tensor of x's type) receives both projections for
     flce_gated_backward. ``workspace``: as in flce_forward."""
-    lib = _lib.load()
+    device = x.device
+    if device.type == "cuda" and _elsewhere(device, stream):
+        with _On(device, stream):
+            return flce_gated_forward(x, Wg, Wu, activation=activation, pre=pre, out=out,
+                                      workspace=workspace)
     _operand(x)
-    with _On(x.device, stream) as s:
-        h = out if out is not None else torch.empty(x.shape[0], Wg.shape[0], dtype=x.dtype,
-                                                    device=x.device)
-        _, p, need, _ = _gated_params(lib, x, Wg, Wu, h, activation, False)
-        if pre is not None:
-            _dense(pre, (2,) + tuple(h.shape), x.dtype, "pre")
-        ws = _scratch(workspace, need, x.device)
-        _done(lib.flce_gated_forward(p, x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), h.data_ptr(),
-                                     _ptr(pre), _ptr(ws), need, _error_word(x.device), s),
-              "flce_gated_forward")
+    _weight(Wg)
+    h = torch.empty((x.shape[0], Wg.shape[0]), dtype=x.dtype, device=device) if out is None else out
+    lib, p, need, _ = _gated_params(x, Wg, Wu, h, activation, False)
+    if pre is not None:
+        _dense(pre, (2,) + tuple(h.shape), x.dtype, "pre")
+    ws = None if need == 0 else _scratch(workspace, need, device)
+    index = device.index
+    st = lib.flce_gated_forward(p, x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(), h.data_ptr(),
+                                None if pre is None else pre.data_ptr(),
+                                None if ws is None else ws.data_ptr(), need, _error_word(index),
+                                _raw_stream(index))
+    if st:
+        raise FlceError(st, "flce_gated_forward")
     return h
 
 
@@ -257,22 +305,26 @@ def flce_gated_backward(dh: torch.Tensor, x: torch.Tensor, Wg: torch.Tensor, Wu:
     """dx [M, K] in x's type, dWg and dWu [F, K] (fp32 or x's type) of
     flce_gated_forward, whose ``pre`` it takes. ``needs``: whether to compute dx,
     and the weight gradients; what is not computed is None."""
-    lib = _lib.load()
+    device = x.device
+    if device.type == "cuda" and _elsewhere(device, stream):
+        with _On(device, stream):
+            return flce_gated_backward(dh, x, Wg, Wu, pre, activation=activation,
+                                       dW_dtype=dW_dtype, needs=needs, workspace=workspace)
     _operand(x)
+    _weight(Wg)
     if dW_dtype not in (torch.float32, x.dtype):
         raise TypeError("flce: dW_dtype must be fp32 or x's dtype")
-    _, p, _, need = _gated_params(lib, x, Wg, Wu, dh, activation, dW_dtype == torch.float32)
+    lib, p, _, need = _gated_params(x, Wg, Wu, dh, activation, dW_dtype is torch.float32)
     _dense(pre, (2,) + tuple(dh.shape), x.dtype, "pre")
-    (M, K), F, dev = x.shape, Wg.shape[0], x.device
-    with _On(dev, stream) as s:
-        dx = torch.empty(M, K, dtype=x.dtype, device=dev) if needs[0] else None
-        dWg = torch.empty(F, K, dtype=dW_dtype, device=dev) if needs[1] else None
-        dWu = torch.empty(F, K, dtype=dW_dtype, device=dev) if needs[1] else None
-        ws = _scratch(workspace, need, dev)
-        _done(lib.flce_gated_backward(p, dh.data_ptr(), x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(),
-                                      pre.data_ptr(), _ptr(dx), _ptr(dWg), _ptr(dWu), _ptr(ws),
-                                      0 if ws is None else ws.numel(), _error_word(dev), s),
-              "flce_gated_backward")
+    (M, K), F, index = x.shape, Wg.shape[0], device.index
+    dx = torch.empty((M, K), dtype=x.dtype, device=device) if needs[0] else None
+    dWg = torch.empty((F, K), dtype=dW_dtype, device=device) if needs[1] else None
+    dWu = torch.empty((F, K), dtype=dW_dtype, device=device) if needs[1] else None
+    ws = _scratch(workspace, need, device)
+    _done(lib.flce_gated_backward(p, dh.data_ptr(), x.data_ptr(), Wg.data_ptr(), Wu.data_ptr(),
+                                  pre.data_ptr(), _ptr(dx), _ptr(dWg), _ptr(dWu), _ptr(ws),
+                                  0 if ws is None else ws.numel(), _error_word(index),
+                                  _raw_stream(index)), "flce_gated_backward")
     return dx, dWg, dWu
 
 
@@ -289,34 +341,42 @@ def _is_dense(t: torch.Tensor) -> bool:
     return True
 
 
+_data_ptr, _numel = torch.Tensor.data_ptr, torch.Tensor.numel
+_get_device, _is_contiguous = torch.Tensor.get_device, torch.Tensor.is_contiguous
+_dtype_of = operator.attrgetter("dtype")
+
+
 def _grad_arrays(grads: Sequence[torch.Tensor], out):
-    n = len(grads)
-    device = grads[0].device
-    numels, types, ptrs = [], [], []
-    for g in grads:
-        t = _GRAD_TYPES.get(g.dtype)
-        if t is None or not g.is_cuda:
-            raise TypeError("flce: gradients must be bf16, fp16 or fp32 CUDA tensors")
-        if g.device != device:
-            raise ValueError("flce: gradients must be on one device")
-        if not _is_dense(g):
-            raise ValueError("flce: gradients must be dense")
-        ptrs.append(g.data_ptr())
-        numels.append(g.numel())
-        types.append(t)
+    """(device index, HOST arrays of addresses, element counts, types, destinations)."""
+    try:
+        types = array.array("i", map(_GRAD_TYPES.__getitem__, map(_dtype_of, grads)))
+    except KeyError:
+        raise TypeError("flce: gradients must be bf16, fp16 or fp32 CUDA tensors") from None
+    index = grads[0].get_device()
+    if index < 0:
+        raise TypeError("flce: gradients must be CUDA tensors")
+    if set(map(_get_device, grads)) != {index}:
+        raise ValueError("flce: gradients must be on one device")
+    if not all(map(_is_contiguous, grads)) and not all(map(_is_dense, grads)):
+        raise ValueError("flce: gradients must be dense")
     outs = None
     if out is not None:
-        if len(out) != n:
-            raise ValueError(f"flce: out must hold {n} tensors, got {len(out)}")
+        if len(out) != len(grads):
+            raise ValueError(f"flce: out must hold {len(grads)} tensors, got {len(out)}")
+        if list(map(_dtype_of, out)) != list(map(_dtype_of, grads)) or \
+                set(map(_get_device, out)) != {index}:
+            raise TypeError("flce: out must match the gradients' types and device")
         for g, o in zip(grads, out):
-            if o.dtype != g.dtype or o.device != device:
-                raise TypeError("flce: out must match the gradients' types and device")
             if o.shape != g.shape or (o.stride() != g.stride() and
                                       not (o.is_contiguous() and g.is_contiguous())):
                 raise ValueError("flce: out must match the gradients' shapes and strides")
-        outs = (ctypes.c_void_p * n)(*[o.data_ptr() for o in out])
-    return (device, (ctypes.c_void_p * n)(*ptrs), (ctypes.c_int64 * n)(*numels),
-            (ctypes.c_int32 * n)(*types), outs)
+        outs = array.array("Q", map(_data_ptr, out))
+    return (index, array.array("Q", map(_data_ptr, grads)), array.array("q", map(_numel, grads)),
+            types, outs)
+
+
+def _at(a) -> int:
+    return a.buffer_info()[0]
 
 
 def _grad_list(grads) -> list:
@@ -330,14 +390,17 @@ def flce_grad_norm(grads: Iterable[torch.Tensor], *, workspace: Optional[torch.T
                    stream=None) -> torch.Tensor:
     """The global 2-norm of all elements of ``grads`` (dense bf16, fp16 and fp32
     CUDA tensors of any shapes) as a 0-dim fp32 tensor."""
-    lib = _lib.load()
     grads = _grad_list(grads)
-    device, ptrs, numels, types, _ = _grad_arrays(grads, None)
-    with _On(device, stream) as s:
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        ws = _scratch(workspace, int(lib.flce_grad_norm_workspace_size(len(grads))), device)
-        _done(lib.flce_grad_norm(len(grads), ptrs, numels, types, norm.data_ptr(), ws.data_ptr(),
-                                 ws.numel(), s), "flce_grad_norm")
+    device = grads[0].device
+    if device.type == "cuda" and _elsewhere(device, stream):
+        with _On(device, stream):
+            return flce_grad_norm(grads, workspace=workspace)
+    index, ptrs, numels, types, _ = _grad_arrays(grads, None)
+    lib, n = _lib.load(), len(grads)
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    ws = _scratch(workspace, lib.flce_grad_norm_workspace_size(n), device)
+    _done(lib.flce_grad_norm(n, _at(ptrs), _at(numels), _at(types), norm.data_ptr(), ws.data_ptr(),
+                             ws.numel(), _raw_stream(index)), "flce_grad_norm")
     return norm
 
 
@@ -349,16 +412,19 @@ def flce_clip_grads(grads: Iterable[torch.Tensor], max_norm: float, *,
     global norm before the scaling as a 0-dim fp32 tensor. Each tensor is given
     once. The scale is formed on the device: nothing is read back. A NaN norm
     makes every element NaN, an infinite one scales by 0."""
-    lib = _lib.load()
     grads = _grad_list(grads)
     out = None if out is None else list(out)
-    device, ptrs, numels, types, outs = _grad_arrays(grads, out)
-    with _On(device, stream) as s:
-        norm = torch.empty((), dtype=torch.float32, device=device)
-        ws = _scratch(workspace, int(lib.flce_grad_norm_workspace_size(len(grads))), device)
-        _done(lib.flce_clip_grads(len(grads), ptrs, outs, numels, types, float(max_norm),
-                                  float(eps), norm.data_ptr(), ws.data_ptr(), ws.numel(), s),
-              "flce_clip_grads")
+    device = grads[0].device
+    if device.type == "cuda" and _elsewhere(device, stream):
+        with _On(device, stream):
+            return flce_clip_grads(grads, max_norm, out=out, eps=eps, workspace=workspace)
+    index, ptrs, numels, types, outs = _grad_arrays(grads, out)
+    lib, n = _lib.load(), len(grads)
+    norm = torch.empty((), dtype=torch.float32, device=device)
+    ws = _scratch(workspace, lib.flce_grad_norm_workspace_size(n), device)
+    _done(lib.flce_clip_grads(n, _at(ptrs), None if outs is None else _at(outs), _at(numels),
+                              _at(types), float(max_norm), float(eps), norm.data_ptr(),
+                              ws.data_ptr(), ws.numel(), _raw_stream(index)), "flce_clip_grads")
     return norm
 
 

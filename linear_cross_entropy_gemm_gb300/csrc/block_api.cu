@@ -75,18 +75,33 @@ bool out16(Out16* o, void* ptr, int64_t rows, int64_t cols, int64_t ld) {
                                         false);
 }
 
+// 16-bit operand [outer, inner] with row pitch ld as one plane of a two-plane map
+// (pair_engine.cuh), 128-byte swizzled boxes; out-of-range elements read as 0.
+bool encode_plane(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld,
+                  int box_inner, int box_outer, bool f16) {
+  auto fn = encoder();
+  if (!fn) return false;
+  const uint64_t row = static_cast<uint64_t>(ld) * 2, span = row * static_cast<uint64_t>(outer);
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer), 2};
+  cuuint64_t strides[2] = {row, span < 131072 ? 131072 : span};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // K-major operand [rows, k]: boxes of 64 x 128 (or fewer rows). MN-major operand, the
 // transpose of a row-major [k, rows] array: boxes of 64 x 128, or 64 x 64 for the
 // few-token kernel.
 bool k_major(CUtensorMap* m, const void* p, int64_t rows, int64_t k, int64_t ld, bool f16,
              int box = kBM) {
-  return encode_2d(m, p, k, rows, static_cast<uint64_t>(ld) * 2, kBK, static_cast<uint32_t>(box),
-                   f16);
+  return encode_plane(m, p, k, rows, ld, kBK, box, f16);
 }
 bool mn_major(CUtensorMap* m, const void* p, int64_t rows, int64_t k, int64_t ld, bool f16,
               int box) {
-  return encode_2d(m, p, rows, k, static_cast<uint64_t>(ld) * 2, 64, static_cast<uint32_t>(box),
-                   f16);
+  return encode_plane(m, p, rows, k, ld, 64, box, f16);
 }
 
 // Products of at most this many tokens go to the few-token kernel.
@@ -109,8 +124,7 @@ bool small_args(SmallArgs* a, const void* x, int64_t ld_x, int64_t M, int64_t k,
   a->k_blocks = segments * a->k_split;
   a->slices = small_slices(M, N, a->k_blocks);
   a->dev_err = reinterpret_cast<int*>(dev_err);
-  return encode_2d(&a->x, x, k, M, static_cast<uint64_t>(ld_x) * 2, kBK,
-                   static_cast<uint32_t>(small_tokens(M)), f16);
+  return k_major(&a->x, x, M, k, ld_x, f16, small_tokens(M));
 }
 
 // ------------------------------------------------- tile width of a pair GEMM
@@ -463,8 +477,7 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
   if (dx && M <= small_most()) {
     SmallArgs sa;
     if (!small_args(&sa, w.dg, F, M, F, 2, K, dx, K, f16, dev_err) ||
-        !encode_2d(&sa.x2, w.du, F, M, static_cast<uint64_t>(F) * 2, kBK,
-                   static_cast<uint32_t>(small_tokens(M)), f16) ||
+        !k_major(&sa.x2, w.du, M, F, F, f16, small_tokens(M)) ||
         !mn_major(&sa.w, Wg, K, F, K, f16, kBK) || !mn_major(&sa.w2, Wu, K, F, K, f16, kBK) ||
         launch_small(false, true, sa, s) != cudaSuccess)
       return FLCE_ERR_CUDA;

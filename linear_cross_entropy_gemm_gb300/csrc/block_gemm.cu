@@ -47,8 +47,8 @@ static cudaError_t launch_halves(const PairArgs& g, const typename Epi::Args& ea
   if (clusters <= 0) clusters = sms / 2;
   const int tiles = g.tiles_m * g.tiles_n;
   if (clusters > tiles) clusters = tiles;
-  kernel<<<2 * clusters, kLThreads, smem, st>>>(g, ea);
-  return cudaGetLastError();
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(2 * clusters)), kLThreads, smem, 2, st,
+                          g, ea);
 }
 
 template <class Epi>

@@ -9,6 +9,40 @@
 
 namespace flce {
 
+// Every kernel of the layer operators may start while its predecessor on the stream
+// still runs (programmatic dependent launch): it sets up its barriers and TMEM and
+// then waits, in all threads and before its first access to global memory, until
+// the predecessor has completed and its writes are visible. It lets its own
+// successor start in the same way once all its blocks are running.
+#ifdef __CUDACC__
+__device__ __forceinline__ void griddep_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void griddep_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+template <class... P, class... A>
+static cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+                                    int cluster, cudaStream_t st, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+#endif
+
 struct PairArgs;
 struct LinearArgs;
 struct GatedArgs;

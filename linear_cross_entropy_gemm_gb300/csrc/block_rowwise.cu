@@ -49,6 +49,8 @@ int dz_parts(int64_t M, int64_t N) {
 
 __global__ void __launch_bounds__(32 * kDzRowGroups) dz_kernel(const DzArgs a, int rows_per_part) {
   __shared__ float s_sum[kDzRowGroups][kDzCols];
+  griddep_launch();
+  griddep_wait();
   const int cg = threadIdx.x & 31, rg = threadIdx.x >> 5;
   const bool f16 = a.fp16 != 0, vec = a.vec != 0;
   const int col0 = blockIdx.x * kDzCols;
@@ -115,14 +117,16 @@ __global__ void __launch_bounds__(32 * kDzRowGroups) dz_kernel(const DzArgs a, i
 
 cudaError_t launch_dz(const DzArgs& a, cudaStream_t st) {
   const dim3 grid((a.N + kDzCols - 1) / kDzCols, dz_parts(a.M, a.N));
-  dz_kernel<<<grid, 32 * kDzRowGroups, 0, st>>>(a, dz_rows_per_part(a.M, a.N));
-  return cudaGetLastError();
+  return launch_dependent(dz_kernel, grid, 32 * kDzRowGroups, 0, 1, st, a,
+                          dz_rows_per_part(a.M, a.N));
 }
 
 // One thread takes 8 columns of one row: three 16-byte loads, two 16-byte
 // stores. Index: the 32- or 64-bit type that holds M F / 8.
 template <class Index>
 __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradArgs a) {
+  griddep_launch();
+  griddep_wait();
   const Index f8 = static_cast<Index>(a.F / 8);
   const Index i = static_cast<Index>(blockIdx.x) * 256 + threadIdx.x;
   if (i >= f8 * static_cast<Index>(a.M)) return;
@@ -152,11 +156,10 @@ cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t st) {
   const uint64_t n = static_cast<uint64_t>(a.M) * (a.F / 8);
   const uint64_t blocks = (n + 255) / 256;
   if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-  if (n < (1ull << 32) - 256)
-    gated_grad_kernel<uint32_t><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a);
-  else
-    gated_grad_kernel<uint64_t><<<static_cast<unsigned>(blocks), 256, 0, st>>>(a);
-  return cudaGetLastError();
+  const dim3 grid(static_cast<unsigned>(blocks));
+  return n < (1ull << 32) - 256
+             ? launch_dependent(gated_grad_kernel<uint32_t>, grid, 256, 0, 1, st, a)
+             : launch_dependent(gated_grad_kernel<uint64_t>, grid, 256, 0, 1, st, a);
 }
 
 }  // namespace flce

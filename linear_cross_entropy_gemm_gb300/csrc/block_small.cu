@@ -8,10 +8,10 @@
 //
 // and a tile wastes at most 15 of the columns it computes. One CTA per tile and K
 // slice: the slices of a tile form a cluster (1, 2, 4 or 8 CTAs), so that even a
-// narrow layer keeps every SM streaming. The cluster joins its slices through
-// distributed shared memory, each CTA adding the fp32 partial sums of its share
-// of the features in rank order (the result does not depend on timing) and
-// applying the epilogue: no scratch memory, no second launch.
+// narrow layer keeps every SM streaming. The slices join through distributed shared
+// memory: each CTA sends the others the fp32 partial sums of their share of the
+// features, adds what it got in rank order (the result does not depend on timing) and
+// applies the epilogue: no scratch memory, no second launch.
 //
 // Warp 0 streams (W, x) slices by TMA through a ring, warp 1 issues the MMAs, and
 // four warps move the accumulator to shared memory.
@@ -32,12 +32,8 @@ struct SmallShape {
   static constexpr int kStage = (TWO ? 2 : 1) * kWTileBytes + NT * kBK * 2;
   static constexpr int kRing = NT <= 64 ? 108 * 1024 : 208 * 1024;
   static constexpr int kStages = kRing / kStage;
-  // An MMA waits about 137 cycles for the one before it on the same accumulator, far
-  // longer than its own products take here: the four K steps of a slice go to up to
-  // four accumulators, as many as TMEM holds for the CTAs of an SM.
-  static constexpr int kAcc = (TWO ? 2 : 1) * NT;
-  static constexpr int kWays = kAcc * 4 <= (NT <= 64 ? 256 : 512) ? 4 : 2;
-  static constexpr int kTmem = kWays * kAcc;  // columns: a power of two, at least 64
+  static constexpr int kAcc = (TWO ? 2 : 1) * NT;      // TMEM columns in use
+  static constexpr int kTmem = kAcc < 32 ? 32 : kAcc;  // allocated
   static constexpr int kPartial = (TWO ? 2 : 1) * NT * 128 * 4;  // joins reuse the ring
   static constexpr int kBody = kStages * kStage > kPartial ? kStages * kStage : kPartial;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kBody) + kBarrierBytes;
@@ -45,30 +41,28 @@ struct SmallShape {
   static_assert((2 * kStages + 1) * 8 + 8 <= kBarrierBytes, "barriers do not fit");
 };
 
-// 32 lanes x 16 consecutive fp32 columns.
-__device__ __forceinline__ void tmem_ld_16cols(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
+// 32 lanes x 16 consecutive fp32 columns: the load is complete after tmem_wait_16.
+__device__ __forceinline__ void tmem_issue_16(uint32_t taddr, uint32_t (&r)[16]) {
   __syncwarp();
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
         "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
         "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_wait_16(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
 }
 
-__device__ __forceinline__ float4 ld_cluster_f4(uint32_t addr) {
-  float4 v;
-  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
 
 // 8 consecutive 16-bit values of a row: one 16-byte access where `vec`, else as many
@@ -144,133 +138,143 @@ __global__ void __launch_bounds__(kSmThreads)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  griddep_launch();
+
+  griddep_wait();
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint64_t pol = l2_policy_evict_normal();
-      int s = 0, issued = 0;
-      uint32_t ph = 0;
-      for (int kb = kb_lo; kb < kb_hi; ++kb) {
-        if (!mbar_wait(&empty[s], ph ^ 1, abort_flag, a.dev_err)) break;
+    const uint64_t pol = l2_policy_evict_normal();
+    int s = 0, issued = 0;
+    uint32_t ph = 0;
+    for (int kb = kb_lo; kb < kb_hi; ++kb) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1, abort_flag, a.dev_err))) break;
+      uint8_t* w = smem + s * S::kStage;
+      const bool second = kb >= a.k_split;
+      const int k0 = (second ? kb - a.k_split : kb) * kBK;
+      const CUtensorMap* mw = second ? &a.w2 : &a.w;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&full[s], S::kStage);
-        uint8_t* w = smem + s * S::kStage;
-        const bool second = kb >= a.k_split;
-        const int k0 = (second ? kb - a.k_split : kb) * kBK;
-        const CUtensorMap* mw = second ? &a.w2 : &a.w;
         if constexpr (!W_MN) {
-          tma_load_2d(w, mw, &full[s], k0, f0, pol);
-          if constexpr (TWO) tma_load_2d(w + kWTileBytes, &a.w2, &full[s], k0, f0, pol);
+          tma_load_plane(w, mw, &full[s], k0, f0, pol);
+          if constexpr (TWO) tma_load_plane(w + kWTileBytes, &a.w2, &full[s], k0, f0, pol);
         } else {
-          tma_load_2d(w, mw, &full[s], f0, k0, pol);
-          tma_load_2d(w + kMnBoxBytes, mw, &full[s], f0 + 64, k0, pol);
+          tma_load_plane(w, mw, &full[s], f0, k0, pol);
+          tma_load_plane(w + kMnBoxBytes, mw, &full[s], f0 + 64, k0, pol);
         }
-        tma_load_2d(w + (TWO ? 2 : 1) * kWTileBytes, second ? &a.x2 : &a.x, &full[s], k0, m0, pol);
-        ++issued;
-        if (++s == S::kStages) {
-          s = 0;
-          ph ^= 1;
-        }
+        tma_load_plane(w + (TWO ? 2 : 1) * kWTileBytes, second ? &a.x2 : &a.x, &full[s], k0, m0, pol);
       }
-      // Drain: the last load issued into each stage must land before the ring is reused.
-      for (int i = issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i)
-        mbar_drain(&full[i % S::kStages], static_cast<uint32_t>((i / S::kStages) & 1));
+      __syncwarp();
+      ++issued;
+      if (++s == S::kStages) {
+        s = 0;
+        ph ^= 1;
+      }
     }
+    // Drain: the last load issued into each stage must land before the ring is reused.
+    for (int i = issued > S::kStages ? issued - S::kStages : 0; i < issued; ++i)
+      mbar_drain(&full[i % S::kStages], static_cast<uint32_t>((i / S::kStages) & 1));
   } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = idesc_f16kind_f32(128, NT, W_MN, false, a.fp16 != 0);
-      int s = 0;
-      uint32_t ph = 0;
-      for (int kb = kb_lo; kb < kb_hi; ++kb) {
-        if (!mbar_wait(&full[s], ph, abort_flag, a.dev_err)) break;
-        tc_fence_after();
-        const uint32_t w = smem_u32(smem + s * S::kStage);
-        const uint32_t x = w + (TWO ? 2 : 1) * kWTileBytes;
+    const uint32_t idesc = idesc_f16kind_f32(128, NT, W_MN, false, a.fp16 != 0);
+    const uint32_t s0 = smem_u32(smem);
+    const uint64_t w0 = smem_desc_sw128(s0, W_MN ? kMnBoxBytes : 16, 1024);
+    const uint64_t x0 = smem_desc_sw128(s0 + (TWO ? 2 : 1) * kWTileBytes, 16, 1024);
+    int s = 0;
+    uint32_t ph = 0;
+    for (int kb = kb_lo; kb < kb_hi; ++kb) {
+      if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag, a.dev_err))) break;
+      tc_fence_after();
+      const uint64_t off = static_cast<uint64_t>(s) * (S::kStage / 16);
+      if (elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kBK / kUmmaK; ++kk) {
-          const uint64_t xd = smem_desc_sw128(x + kk * (kUmmaK * 2), 16, 1024);
-          const uint32_t acc = kb != kb_lo || kk >= S::kWays ? 1u : 0u;
-          const uint32_t d = tmem_base + (kk % S::kWays) * S::kAcc;
-#pragma unroll
-          for (int h = 0; h < (TWO ? 2 : 1); ++h) {
-            const uint32_t wh = w + h * kWTileBytes;
-            const uint64_t wd = W_MN
-                                    ? smem_desc_sw128(wh + kk * (kUmmaK * 128), kMnBoxBytes, 1024)
-                                    : smem_desc_sw128(wh + kk * (kUmmaK * 2), 16, 1024);
-            umma_bf16(d + h * NT, wd, xd, idesc, acc);
-          }
+          const uint64_t wd = w0 + off + kk * (W_MN ? 128 : 2), xd = x0 + off + kk * 2;
+          const uint32_t acc = kb != kb_lo || kk != 0 ? 1u : 0u;
+          umma_bf16(tmem_base, wd, xd, idesc, acc);
+          if constexpr (TWO) umma_bf16(tmem_base + NT, wd + kWTileBytes / 16, xd, idesc, acc);
         }
         umma_commit(&empty[s]);
-        if (++s == S::kStages) {
-          s = 0;
-          ph ^= 1;
-        }
       }
-      umma_commit(done);
-      mbar_drain(done, 0);
+      __syncwarp();
+      if (++s == S::kStages) {
+        s = 0;
+        ph ^= 1;
+      }
     }
+    if (elect_one()) umma_commit(done);
+    __syncwarp();
+    mbar_drain(done, 0);
   }
   // The producer and the issuer leave their branches only when every load has
-  // landed and every MMA is done, so the ring may be overwritten.
+  // landed and every MMA is done, so the ring may be overwritten: by this CTA, and
+  // once the whole cluster is here, by the others.
   __syncwarp();
   tc_fence_before();
   __syncthreads();
+  if (slices > 1) cluster_sync();
   tc_fence_after();
 
   const int tokens = min(NT, a.M - m0);
-  float* part = reinterpret_cast<float*>(smem);  // [TWO ? 2 : 1][NT tokens][128 features]
+  // Received partial sums, fp32 [slices][TWO ? 2 : 1][NT tokens][own features].
+  const int own = 128 / slices;  // features whose outputs this CTA writes
+  const float* part = reinterpret_cast<const float*>(smem);
   if (warp >= 2) {
-    const int quad = warp & 3;
+    const int quad = warp & 3, f = quad * 32 + lane;
     const uint32_t base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
-#pragma unroll
-    for (int h = 0; h < (TWO ? 2 : 1); ++h) {
+    const int to = f / own;  // rank that writes feature f
+    const uint32_t mine = smem_u32(smem) +
+                          static_cast<uint32_t>(((rank * (TWO ? 2 : 1)) * NT * own + f - to * own) * 4);
+    const uint32_t dst = slices > 1 ? mapa_shared(mine, static_cast<uint32_t>(to)) : mine;
 #pragma unroll 1
-      for (int c = 0; c < tokens; c += 16) {
-        float v[16];
-        tmem_ld_16cols(base + h * NT + c, v);
+    for (int c = 0; c < tokens; c += 16) {
+      uint32_t r[16], q[16];
+      tmem_issue_16(base + c, r);
+      if constexpr (TWO) tmem_issue_16(base + NT + c, q);
+      tmem_wait_16(r);
+      if constexpr (TWO) tmem_wait_16(q);
 #pragma unroll
-        for (int w = 1; w < S::kWays; ++w) {
-          float q[16];
-          tmem_ld_16cols(base + w * S::kAcc + h * NT + c, q);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) v[j] += q[j];
-        }
-#pragma unroll
-        for (int j = 0; j < 16; ++j) part[(h * NT + c + j) * 128 + quad * 32 + lane] = v[j];
+      for (int j = 0; j < 16; ++j) {
+        if (c + j >= tokens) break;
+        const uint32_t at = dst + static_cast<uint32_t>((c + j) * own * 4);
+        st_cluster_f32(at, __uint_as_float(r[j]));
+        if constexpr (TWO)
+          st_cluster_f32(at + static_cast<uint32_t>(NT * own * 4), __uint_as_float(q[j]));
       }
     }
     tc_fence_before();
   }
   __syncthreads();
+  if (slices > 1) cluster_sync();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, S::kTmem);
-  if (slices > 1) cluster_sync();
 
-  // This CTA's features: [f_lo, f_lo + 128 / slices) of the tile, 8 at a time.
-  const int groups = 16 / slices;
-  const int g_lo = rank * groups;
+  // This CTA's features: [rank * own, rank * own + own) of the tile, 8 at a time.
+  const int groups = own / 8;
   const bool f16 = a.fp16 != 0;
-  const uint32_t part_addr = smem_u32(part);
   for (int i = threadIdx.x; i < tokens * groups; i += kSmThreads) {
-    const int t = i / groups, gi = g_lo + (i - t * groups);
-    const int col = f0 + gi * 8, n = a.N - col;
+    const int t = i / groups, gl = i - t * groups;
+    const int col = f0 + rank * own + gl * 8, n = a.N - col;
     if (n <= 0) continue;
     float v[TWO ? 2 : 1][8];
 #pragma unroll
     for (int h = 0; h < (TWO ? 2 : 1); ++h) {
-      const uint32_t off = part_addr + static_cast<uint32_t>(((h * NT + t) * 128 + gi * 8) * 4);
+      const float* p = part + (h * NT + t) * own + gl * 8;
+      const int step = (TWO ? 2 : 1) * NT * own;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[h][j] = 0.f;
-      for (int r = 0; r < slices; ++r) {
-        const uint32_t at = slices > 1 ? mapa_shared(off, r) : off;
-        const float4 p = ld_cluster_f4(at), q = ld_cluster_f4(at + 16);
-        v[h][0] += p.x;
-        v[h][1] += p.y;
-        v[h][2] += p.z;
-        v[h][3] += p.w;
-        v[h][4] += q.x;
-        v[h][5] += q.y;
-        v[h][6] += q.z;
-        v[h][7] += q.w;
+      for (int j = 0; j < 8; ++j) v[h][j] = p[j];
+#pragma unroll
+      for (int r = 1; r < 8; ++r) {
+        if (r < slices) {
+          const float4 q0 = *reinterpret_cast<const float4*>(p + r * step);
+          const float4 q1 = *reinterpret_cast<const float4*>(p + r * step + 4);
+          v[h][0] += q0.x;
+          v[h][1] += q0.y;
+          v[h][2] += q0.z;
+          v[h][3] += q0.w;
+          v[h][4] += q1.x;
+          v[h][5] += q1.y;
+          v[h][6] += q1.z;
+          v[h][7] += q1.w;
+        }
       }
     }
     const size_t row = static_cast<size_t>(m0 + t);
@@ -300,8 +304,6 @@ __global__ void __launch_bounds__(kSmThreads)
     }
     store8(a.y + row * a.ld_y + col, n, a.y_vec != 0, f16, v[0]);
   }
-  // No CTA leaves while another may still read its partial sums.
-  if (slices > 1) cluster_sync();
 }
 
 template <int NT, bool TWO, bool W_MN>
@@ -311,20 +313,9 @@ static cudaError_t launch_t(const SmallArgs& a, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(S::kSmem));
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(a.slices);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.gridDim = dim3(static_cast<unsigned>((a.N + 127) / 128 * a.slices),
-                     static_cast<unsigned>((a.M + NT - 1) / NT));
-  cfg.blockDim = dim3(kSmThreads);
-  cfg.dynamicSmemBytes = S::kSmem;
-  cfg.stream = st;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  const dim3 grid(static_cast<unsigned>((a.N + 127) / 128 * a.slices),
+                  static_cast<unsigned>((a.M + NT - 1) / NT));
+  return launch_dependent(kernel, grid, kSmThreads, S::kSmem, a.slices, st, a);
 }
 
 int small_tokens(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }

@@ -1,6 +1,7 @@
 // Host-side helpers shared by the C-ABI layers: TMA descriptor encoding, device
 // checks, workspace carving, GEMM geometry and NVTX ranges.
 #pragma once
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 #include <mutex>
@@ -70,16 +71,23 @@ inline int cdiv(int64_t a, int64_t b) { return static_cast<int>((a + b - 1) / b)
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// SM count and architecture of the current device.
+// SM count and architecture of the current device (asked once per device).
 inline flce_status_t device_info(int* sms) {
+  constexpr int kMaxDev = 64;
+  static std::atomic<int> known[kMaxDev];  // SM count of a supported device
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return FLCE_ERR_CUDA;
+  if (dev >= 0 && dev < kMaxDev) {
+    *sms = known[dev].load(std::memory_order_relaxed);
+    if (*sms > 0) return FLCE_OK;
+  }
   int major = 0, minor = 0;
   if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
       cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return FLCE_ERR_CUDA;
   if (major != 10 || minor != 3) return FLCE_ERR_UNSUPPORTED;
+  if (dev >= 0 && dev < kMaxDev) known[dev].store(*sms, std::memory_order_relaxed);
   return FLCE_OK;
 }
 
