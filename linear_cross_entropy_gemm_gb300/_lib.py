@@ -179,6 +179,34 @@ def load() -> ctypes.CDLL:
     return lib
 
 
+CALLS_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_flce_torch.so")
+_calls = None
+
+
+def calls(error_word):
+    """The module of the layer operators' calls (csrc/torch_calls.cpp). error_word:
+    device index -> the device's int32 error word."""
+    global _calls
+    if _calls is None:
+        load()
+        if not os.path.exists(CALLS_PATH):
+            raise ImportError(
+                f"{CALLS_PATH} is missing: build it with "
+                "`python -c 'import __graft_entry__ as g; g.build()'` or "
+                "`python linear_cross_entropy_gemm_gb300/build.py`")
+        import importlib.machinery
+        import importlib.util
+
+        import torch  # noqa: F401  (its libraries, before the module's)
+        loader = importlib.machinery.ExtensionFileLoader("_flce_torch", CALLS_PATH)
+        module = importlib.util.module_from_spec(
+            importlib.util.spec_from_loader("_flce_torch", loader))
+        loader.exec_module(module)
+        module.bind(FlceError, error_word)
+        _calls = module
+    return _calls
+
+
 def params(N, H, V, *, ignore_index=-100, label_smoothing=0.0, lse_square_scale=0.0,
            logit_scale=1.0, reduction="mean", has_bias=False, dW_fp32=True, db_fp32=True,
            bwd_vocab_block=0, vocab_start=0, vocab_total=0, input_fp16=False,

@@ -1,16 +1,19 @@
-"""Build the sm_103a shared library ``libflce_gb300.so`` in-tree with nvcc.
+"""Build the sm_103a shared library ``libflce_gb300.so`` in-tree with nvcc, and
+``_flce_torch.so``, the Python calls of the layer operators, with g++.
 
 Each translation unit under ``csrc/`` is compiled in parallel, then linked
 with the static CUDA runtime. Rebuilds only when a source or header is newer
-than the library. No CMake, no torch extension machinery.
+than the libraries. No CMake, no torch extension machinery.
 """
 from __future__ import annotations
 
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +21,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libflce_gb300.so")
+CALLS = os.path.join(PKG, "_flce_torch.so")
+CALLS_SRC = os.path.join(CSRC, "torch_calls.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
@@ -36,13 +41,29 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + \
-        glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [__file__]
+        glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [CALLS_SRC, __file__]
+
+
+def _calls_commands(obj: str):
+    """g++ commands that compile and link the Python calls against the installed torch."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if cxx is None:
+        raise RuntimeError("g++ not found: the FLCE library needs a C++ compiler to build")
+    compile_ = [cxx, "-O2", "-std=c++17", "-fPIC", "-D_GLIBCXX_USE_CXX11_ABI=1", "-I", INCLUDE,
+                "-I", os.path.join(torch, "include"), "-I", sysconfig.get_paths()["include"],
+                "-I", os.path.join(cuda, "include"), "-c", CALLS_SRC, "-o", obj]
+    link = [cxx, "-shared", "-o", CALLS + ".tmp", obj, "-L", os.path.join(torch, "lib"), "-L", PKG,
+            "-l:libflce_gb300.so", "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -61,6 +82,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    calls_obj = os.path.join(BUILD, "torch_calls.o")
+    calls_compile, calls_link = _calls_commands(calls_obj)
+    if verbose:
+        print(" ".join(calls_compile), flush=True)
+    procs.append((CALLS_SRC, subprocess.Popen(calls_compile, stdout=subprocess.PIPE,
+                                              stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -69,7 +96,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if p.returncode != 0:
             failed.append(src)
     if failed:
-        raise RuntimeError("nvcc failed on: " + ", ".join(os.path.basename(f) for f in failed))
+        raise RuntimeError("compilation failed on: " + ", ".join(os.path.basename(f) for f in failed))
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
@@ -77,6 +104,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         sys.stdout.write(r.stdout.decode(errors="replace"))
         raise RuntimeError("link of libflce_gb300.so failed")
     os.replace(tmp, LIB)
+    r = subprocess.run(calls_link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        sys.stdout.write(r.stdout.decode(errors="replace"))
+        raise RuntimeError("link of _flce_torch.so failed")
+    os.replace(CALLS + ".tmp", CALLS)
     return LIB
 
 
