@@ -104,10 +104,12 @@ bool mn_major(CUtensorMap* m, const void* p, int64_t rows, int64_t k, int64_t ld
   return encode_plane(m, p, rows, k, ld, 64, box, f16);
 }
 
-// Products of at most this many tokens go to the few-token kernel.
-constexpr int64_t kSmallTokens = 128;
+// Products of at most this many tokens go to the few-token kernel (measured: 128 tokens
+// through 4096 x 4096 12.4 us against 15.3 us, 256 17.7 against 15.3; gated 4096 x 14336,
+// 64 tokens 48 us against 51 us, 128 54 against 51).
+constexpr int64_t kSmallTokens = 128, kSmallGatedTokens = 64;
 
-int64_t small_most() { return kSmallTokens; }
+int64_t small_most(bool gated) { return gated ? kSmallGatedTokens : kSmallTokens; }
 
 // The parts of a few-token product's arguments that do not depend on the operator.
 // x: [M, k] with pitch ld_x; the sum runs over `segments` times k.
@@ -132,37 +134,58 @@ bool small_args(SmallArgs* a, const void* x, int64_t ld_x, int64_t M, int64_t k,
 // one wave of tiles at 1.92 GHz with a K-major and with an MN-major B, whose boxes
 // are 64 columns wide, so that only widths in multiples of 128 load nothing twice.
 struct TileShape {
-  int halves, bn;
+  int halves, bn, slices;
   float ns, ns_mn;  // 0: not used with that B
 };
 constexpr TileShape kTileShapes[] = {
-    {1, 256, 296.f, 296.f}, {1, 224, 243.f, 0.f},   {1, 192, 222.f, 255.f}, {1, 160, 196.f, 0.f},
-    {1, 128, 215.f, 202.f}, {1, 64, 170.f, 193.f},  {2, 256, 0.f, 530.f},   {2, 192, 0.f, 405.f},
+    {1, 256, 1, 296.f, 296.f}, {1, 240, 1, 250.f, 0.f},   {1, 224, 1, 243.f, 0.f},
+    {1, 208, 1, 232.f, 0.f},   {1, 192, 1, 222.f, 255.f}, {1, 160, 1, 196.f, 0.f},
+    {1, 128, 1, 215.f, 202.f}, {1, 64, 1, 170.f, 193.f},  {2, 256, 1, 0.f, 530.f},
+    {2, 192, 1, 0.f, 405.f},   {1, 256, 2, 296.f, 296.f}, {1, 128, 2, 215.f, 202.f},
+    {1, 192, 3, 222.f, 255.f},
 };
-constexpr int kPairClusters = 76;    // two CTAs of 152
+// Clusters of 2, 4 and 6 CTAs of 225 KiB that run at once on 152 SMs (76 and 36 as the
+// runtime says; 22 of 6 ran in one wave, 8 CTAs did not fill half of the SMs).
+constexpr int kClusters[] = {76, 36, 22};
 constexpr float kSustained[] = {1.66e6f, 1.75e6f};  // flop/ns under the power cap, by halves
+constexpr float kJoinNs = 2200.f;                   // set-up and exchange of a split tile
 
 // ns of a whole product: its waves of tiles, each as long as the sum or (where it
 // runs beside the next tile's sum) the epilogue; the last epilogue; and no less than
 // the padded flops take under the power cap. The two-half form, whose epilogue is not
 // overlapped, is kept to the weight and input gradients: at 8192 x 28672 x 4096 (gated)
 // it took 1213 us against 1133 us, for dW 4096 x 14336 x 8192 549 us against 579 us.
+// Split sums pay where the tiles are few: 512 x 4096 x 14336 46 us against 61 us.
 float tile_ns(const TileShape& t, bool mn, int64_t tiles_m, int64_t N, int64_t k64, bool two_b,
               float epi_ns) {
   const int cols = pair_cols(two_b ? kTwoB : kOneEach, t.halves, t.bn);
   const int64_t tiles = tiles_m * ((N + cols - 1) / cols);
-  const float waves = static_cast<float>((tiles + kPairClusters - 1) / kPairClusters);
-  const float sum = static_cast<float>(k64) * (mn ? t.ns_mn : t.ns), epi = epi_ns * cols;
-  const float busy = t.halves == 1 ? waves * std::max(sum, epi) + epi : waves * (sum + epi);
+  const int at_once = kClusters[t.slices - 1];
+  const float waves = static_cast<float>((tiles + at_once - 1) / at_once);
+  const float sum = static_cast<float>(k64) * (mn ? t.ns_mn : t.ns) / static_cast<float>(t.slices);
+  const float epi = epi_ns * static_cast<float>(cols) / static_cast<float>(t.slices);
+  const float busy = t.slices > 1    ? waves * (sum + kJoinNs + epi)
+                     : t.halves == 1 ? waves * std::max(sum, epi) + epi
+                                     : waves * (sum + epi);
   const float flops = 2.f * 256.f * 64.f * t.halves * t.bn * static_cast<float>(tiles) * k64;
   return std::max(busy, flops / kSustained[t.halves - 1]);
+}
+
+// Whether the shape can compute the product: every slice has a stage of the sum, every
+// pair of a split tile output columns, and (residuals are read in place) only the gated
+// tiles' chunks may overlap.
+bool tile_fits(const TileShape& t, bool mn, int64_t k64, bool two_b) {
+  if ((mn ? t.ns_mn : t.ns) == 0.f) return false;
+  if (!two_b && t.bn % 32 != 0) return false;
+  if (t.slices == 1) return true;
+  return (k64 + 1) / 2 >= t.slices && t.bn / 32 % (t.slices * (two_b ? 2 : 1)) == 0;
 }
 
 const TileShape& best_tile(bool mn, int64_t M, int64_t N, int64_t k64, bool two_b, float epi_ns) {
   const TileShape* best = nullptr;
   float least = 0.f;
   for (const TileShape& t : kTileShapes) {
-    if ((mn ? t.ns_mn : t.ns) == 0.f) continue;
+    if (!tile_fits(t, mn, k64, two_b)) continue;
     const float ns = tile_ns(t, mn, (M + 255) / 256, N, k64, two_b, epi_ns);
     if (!best || ns < least) {
       best = &t;
@@ -191,6 +214,7 @@ PairArgs pair_args(int M, int N, int K, int segments, bool mn, bool two_b, float
   const TileShape& t = best_tile(mn, M, N, static_cast<int64_t>(segments) * cdiv(K, 64), two_b,
                                  epi_ns);
   g.halves = t.halves;
+  g.slices = t.slices;
   g.bn = t.bn;
   g.band_m = 16;
   g.tiles_m = cdiv(M, 256);
@@ -264,7 +288,7 @@ flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, 
   if ((st = device_info(&sms)) != FLCE_OK) return st;
   const bool f16 = p->input_fp16 != 0;
   const int M = static_cast<int>(p->M), K = static_cast<int>(p->K), N = static_cast<int>(p->N);
-  if (M <= small_most()) {
+  if (M <= small_most(false)) {
     SmallArgs sa;
     if (!small_args(&sa, x, pitch(p->ld_x, K), M, K, 1, N, y, pitch(p->ld_y, N), f16, dev_err) ||
         !k_major(&sa.w, W, N, K, K, f16))
@@ -350,7 +374,7 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
   }
   const void* dz = copy ? static_cast<const void*>(w.dz) : dy;
   const int64_t ld_dz = copy ? w.ld_dz : ld_dy;
-  if (dx && M <= small_most()) {
+  if (dx && M <= small_most(false)) {
     SmallArgs sa;
     if (!small_args(&sa, dz, ld_dz, M, N, 1, K, dx, K, f16, dev_err) ||
         !mn_major(&sa.w, W, K, N, K, f16, kBK) || launch_small(false, true, sa, s) != cudaSuccess)
@@ -405,7 +429,7 @@ flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, co
   if ((st = device_info(&sms)) != FLCE_OK) return st;
   const bool f16 = p->input_fp16 != 0;
   const int M = static_cast<int>(p->M), K = static_cast<int>(p->K), F = static_cast<int>(p->F);
-  if (M <= small_most()) {
+  if (M <= small_most(true)) {
     SmallArgs sa;
     if (!small_args(&sa, x, pitch(p->ld_x, K), M, K, 1, F, h, pitch(p->ld_h, F), f16, dev_err) ||
         !k_major(&sa.w, Wg, F, K, K, f16) || !k_major(&sa.w2, Wu, F, K, K, f16))
@@ -474,7 +498,7 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
   ga.act = p->activation;
   ga.fp16 = f16 ? 1 : 0;
   if (launch_gated_grad(ga, s) != cudaSuccess) return FLCE_ERR_CUDA;
-  if (dx && M <= small_most()) {
+  if (dx && M <= small_most(false)) {
     SmallArgs sa;
     if (!small_args(&sa, w.dg, F, M, F, 2, K, dx, K, f16, dev_err) ||
         !k_major(&sa.x2, w.du, M, F, F, f16, small_tokens(M)) ||

@@ -243,8 +243,9 @@ struct LinearEpi {
   static constexpr bool kAMN = false, kBMN = false;
   static constexpr OperandPlan kPlan = kOneEach;
   using Args = LinearArgs;
+  template <class Acc>
   __device__ static void tile(const Args& a, const PairArgs&, int, int row0, int col_base, int lane,
-                              uint32_t taddr, Staging& st, const TileSlice& sl) {
+                              const Acc& acc, Staging& st, const TileSlice& sl) {
     const int row = row0 + lane;
     const bool f16 = a.fp16 != 0;
 #pragma unroll 1
@@ -254,7 +255,7 @@ struct LinearEpi {
       col0 += col_base;
       if (col0 >= a.N || row0 >= a.M) break;  // uniform over the warp
       float v[32];
-      tmem_ld_32cols(taddr + acc_col, v);
+      acc.load(acc_col, v);
       if (a.bias) add_row_16(a.bias + col0, a.N - col0, true, f16, v);
       if (a.keep) put_block_16(a.z, a.M, a.N, row0, col0, v, f16, st, lane);
       act_all(a.act, v);
@@ -277,8 +278,9 @@ struct GatedEpi {
   static constexpr bool kAMN = false, kBMN = false;
   static constexpr OperandPlan kPlan = kTwoB;
   using Args = GatedArgs;
+  template <class Acc>
   __device__ static void tile(const Args& a, const PairArgs&, int, int row0, int col_base, int lane,
-                              uint32_t taddr, Staging& st, const TileSlice& sl) {
+                              const Acc& acc, Staging& st, const TileSlice& sl) {
     const bool f16 = a.fp16 != 0;
 #pragma unroll 1
     for (int c = sl.c_lo; c < sl.c_hi; ++c) {
@@ -287,8 +289,8 @@ struct GatedEpi {
       col0 += col_base;
       if (col0 >= a.F || row0 >= a.M) break;  // uniform over the warp
       float g[32], u[32];
-      tmem_ld_32cols(taddr + acc_col, g);
-      tmem_ld_32cols(taddr + sl.up_off + acc_col, u);
+      acc.load(acc_col, g);
+      acc.load(sl.up_off + acc_col, u);
       if (a.keep) {
         put_block_16(a.g, a.M, a.F, row0, col0, g, f16, st, lane);
         put_block_16(a.u, a.M, a.F, row0, col0, u, f16, st, lane);
@@ -313,8 +315,9 @@ struct GradXEpi {
   static constexpr bool kAMN = false, kBMN = true;
   static constexpr OperandPlan kPlan = PLAN;
   using Args = GradXArgs;
+  template <class Acc>
   __device__ static void tile(const Args& a, const PairArgs&, int, int row0, int col_base, int lane,
-                              uint32_t taddr, Staging& st, const TileSlice& sl) {
+                              const Acc& acc, Staging& st, const TileSlice& sl) {
 #pragma unroll 1
     for (int c = sl.c_lo; c < sl.c_hi; ++c) {
       int acc_col, col0;
@@ -322,7 +325,7 @@ struct GradXEpi {
       col0 += col_base;
       if (col0 >= a.K || row0 >= a.M) break;  // uniform over the warp
       float v[32];
-      tmem_ld_32cols(taddr + acc_col, v);
+      acc.load(acc_col, v);
       put_block_16(a.dx, a.M, a.K, row0, col0, v, a.fp16 != 0, st, lane);
     }
   }
@@ -341,8 +344,9 @@ struct GradWEpi {
   static constexpr bool kAMN = true, kBMN = true;
   static constexpr OperandPlan kPlan = PLAN;
   using Args = GradWArgs;
+  template <class Acc>
   __device__ static void tile(const Args& a, const PairArgs& g, int tm, int row0, int col_base,
-                              int lane, uint32_t taddr, Staging& st, const TileSlice& sl) {
+                              int lane, const Acc& acc, Staging& st, const TileSlice& sl) {
     const CUtensorMap* out = &a.out;
     if constexpr (PLAN == kTwoA) {
       if (tm >= g.m_split) {
@@ -357,7 +361,7 @@ struct GradWEpi {
       col0 += col_base;
       if (col0 >= a.K || row0 >= a.N) break;  // uniform over the warp
       float v[32];
-      tmem_ld_32cols(taddr + acc_col, v);
+      acc.load(acc_col, v);
       if (a.out16)
         staged_block_16(out, col0, row0, v, a.fp16 != 0, st, lane);
       else

@@ -35,27 +35,31 @@ static int max_clusters(const void* kernel) {
   return v;
 }
 
-template <class Epi, int HALVES>
-static cudaError_t launch_halves(const PairArgs& g, const typename Epi::Args& ea, int sms,
-                                 cudaStream_t st) {
-  auto kernel = pair_gemm_kernel<Epi, HALVES>;
+template <class Epi, int HALVES, bool SPLIT>
+static cudaError_t launch_form(const PairArgs& g, const typename Epi::Args& ea, int sms,
+                               cudaStream_t st) {
+  auto kernel = pair_gemm_kernel<Epi, HALVES, SPLIT>;
   constexpr size_t smem = PairShape<HALVES>::kSmem;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  int clusters = max_clusters<HALVES>(reinterpret_cast<const void*>(kernel));
-  if (clusters <= 0) clusters = sms / 2;
-  const int tiles = g.tiles_m * g.tiles_n;
-  if (clusters > tiles) clusters = tiles;
-  return launch_dependent(kernel, dim3(static_cast<unsigned>(2 * clusters)), kLThreads, smem, 2, st,
-                          g, ea);
+  int clusters = g.tiles_m * g.tiles_n;
+  if constexpr (!SPLIT) {
+    int most = max_clusters<HALVES>(reinterpret_cast<const void*>(kernel));
+    if (most <= 0) most = sms / 2;
+    if (clusters > most) clusters = most;
+  }
+  const int ctas = SPLIT ? 2 * g.slices : 2;
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(ctas * clusters)), kLThreads, smem,
+                          ctas, st, g, ea);
 }
 
 template <class Epi>
 static cudaError_t launch(const PairArgs& g, const typename Epi::Args& ea, int sms,
                           cudaStream_t st) {
-  return g.halves == 2 ? launch_halves<Epi, 2>(g, ea, sms, st)
-                       : launch_halves<Epi, 1>(g, ea, sms, st);
+  if (g.slices > 1) return launch_form<Epi, 1, true>(g, ea, sms, st);
+  return g.halves == 2 ? launch_form<Epi, 2, false>(g, ea, sms, st)
+                       : launch_form<Epi, 1, false>(g, ea, sms, st);
 }
 
 cudaError_t launch_linear(const PairArgs& g, const LinearArgs& ea, int sms, cudaStream_t st) {

@@ -17,6 +17,10 @@
 //   - The issuing warps stay converged and elect their thread, and a stage of the
 //     HALVES = 1 ring holds 128 sum elements: with 64 and a diverged thread a stage took
 //     550 cycles at any width.
+//   - A long sum with few tiles is split: the 2, 4 pairs of a cluster take a part of one
+//     tile's sum each, send one another the fp32 partial sums of a share of its columns
+//     through distributed shared memory and add them in rank order (SPLIT; the result
+//     does not depend on timing).
 //   - 8 epilogue warps (two per SM sub-partition): the drain of a tile has to fit
 //     beside the next tile's short sum.
 // An operand is K-major (rows of the sum) or MN-major, as there, and a product may
@@ -51,6 +55,7 @@ struct PairArgs {
   int k_split;           // kTwoK: stages of the first product
   int m_split;           // kTwoA: 256-row tiles of the first A
   int halves, bn;        // accumulator columns of a tile: halves x bn
+  int slices;            // pairs that share a tile's sum: 1, 2 or 4
   int band_m, band_n;    // raster: bands of band_m row tiles or band_n column tiles
   int fp16;
   int* dev_err;
@@ -159,6 +164,46 @@ struct TileSlice {
   }
 };
 
+// Where an epilogue reads 32 accumulator columns of its row: TMEM; or, of a split tile,
+// TMEM plus what the other pairs sent, fp32 float4 [slices - 1][chunks][4 lane
+// quarters][8][32 rows].
+struct TmemAcc {
+  uint32_t taddr;
+  __device__ __forceinline__ void load(int col, float (&v)[32]) const {
+    tmem_ld_32cols(taddr + static_cast<uint32_t>(col), v);
+  }
+};
+struct SplitAcc {
+  uint32_t taddr;     // of the pair's first own chunk
+  int product_cols;   // TMEM columns from one product's own chunks to the other's
+  const float4* row;  // of this lane, in its quarter
+  int slices, own, chunks;  // own: chunks of one product; chunks: of all
+  __device__ __forceinline__ void load(int col, float (&v)[32]) const {
+    const int lc = col >> 5, h = lc / own;
+    tmem_ld_32cols(taddr + static_cast<uint32_t>(h * product_cols + (lc - h * own) * 32), v);
+    for (int r = 0; r < slices - 1; ++r) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const float4 t = row[static_cast<size_t>(r * chunks + lc) * 1024 + q * 32];
+        v[4 * q] += t.x;
+        v[4 * q + 1] += t.y;
+        v[4 * q + 2] += t.z;
+        v[4 * q + 3] += t.w;
+      }
+    }
+  }
+};
+// Copies `bytes` of this CTA's shared memory to another CTA of the cluster, completing
+// them on a barrier there. Addresses 16-byte aligned, bytes a multiple of 16.
+__device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst_cluster, uint32_t src, uint32_t bytes,
+                                                 uint32_t bar_cluster) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.shared::cta.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst_cluster),
+      "r"(src), "r"(bytes), "r"(bar_cluster)
+      : "memory");
+}
+
 __device__ __forceinline__ void pair_coords(const PairArgs& g, int t, int& tm, int& tn) {
   if (g.band_m > 0) {
     const int per = g.band_m * g.tiles_n, b = t / per, r = t - b * per;
@@ -173,7 +218,7 @@ __device__ __forceinline__ void pair_coords(const PairArgs& g, int t, int& tm, i
   }
 }
 
-template <class Epi, int HALVES>
+template <class Epi, int HALVES, bool SPLIT>
 __global__ void __launch_bounds__(kLThreads, 1)
     pair_gemm_kernel(const __grid_constant__ PairArgs g,
                      const __grid_constant__ typename Epi::Args ea) {
@@ -189,14 +234,24 @@ __global__ void __launch_bounds__(kLThreads, 1)
   uint64_t* tfull = empty + S::kStages;
   uint64_t* tempty = tfull + S::kAccs;
   uint64_t* done_bar = tempty + S::kAccs;
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done_bar + 1);
+  uint64_t* xbar = done_bar + 1;  // SPLIT: the other pairs' partial sums have arrived
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(xbar + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  const uint32_t rank = cluster_ctarank();
+  static_assert(!SPLIT || HALVES == 1, "only one-half tiles are split");
+  const int slices = SPLIT ? g.slices : 1;
+  const uint32_t cta = cluster_ctarank(), rank = cta & 1;  // in the cluster, in the pair
+  const uint32_t even = cta & ~1u;
+  const uint16_t both = static_cast<uint16_t>(3u << even);  // the pair's CTAs
   const bool leader = rank == 0;
-  const int cluster = blockIdx.x >> 1, nclusters = gridDim.x >> 1;
   const int num_tiles = g.tiles_m * g.tiles_n;
+  // Tiles go round the clusters of the grid; a split launch has one cluster per tile.
+  const int cluster = static_cast<int>(blockIdx.x) / (2 * slices);
+  const int nclusters = SPLIT ? num_tiles : static_cast<int>(gridDim.x) / 2;
+  const int slice = static_cast<int>(cta >> 1);
+  const int kb_lo = SPLIT ? g.k_stages * slice / slices : 0;
+  const int kb_hi = SPLIT ? g.k_stages * (slice + 1) / slices : g.k_stages;
   const int bn = g.bn;
   const int cols = pair_cols(kPlan, HALVES, bn);
 
@@ -210,8 +265,12 @@ __global__ void __launch_bounds__(kLThreads, 1)
       mbar_init(&tempty[a], 2 * 32 * kLEpiWarps);
     }
     mbar_init(done_bar, 1);
+    if constexpr (SPLIT) mbar_init(xbar, 1);
     *abort_flag = 0;
     fence_mbar_init();
+    // Chunks of 16 KiB from each other pair: its share of the tile's bn / 32 chunks.
+    if constexpr (SPLIT)
+      mbar_arrive_expect_tx(xbar, static_cast<uint32_t>((slices - 1) * (bn / 32 / slices) * 16384));
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&g.a);
@@ -229,7 +288,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
   if (warp == 0) {
     // -------------------------------------------------- TMA producer (both CTAs)
     const uint64_t pol = l2_policy_evict_normal();
-    const uint32_t full0 = mapa_shared(smem_u32(&full[0]), 0);
+    const uint32_t full0 = mapa_shared(smem_u32(&full[0]), even);
     const int b_boxes = (bn / 2 + 63) / 64;  // MN-major B: boxes of 64 columns
     const uint32_t b_bytes = kBMN ? static_cast<uint32_t>(b_boxes * 64 * S::kLK * 2)
                                   : static_cast<uint32_t>(bn / 2 * S::kLK * 2);
@@ -253,7 +312,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
           m0 -= g.m_split * 256;
         }
       }
-      for (int kb = 0; kb < g.k_stages; ++kb) {
+      for (int kb = kb_lo; kb < kb_hi; ++kb) {
         ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1, abort_flag, g.dev_err));
         if (!ok) break;
         int k0 = kb * S::kLK;
@@ -321,7 +380,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t d = tmem_base + static_cast<uint32_t>(acc * kBN);
-        for (int kb = 0; kb < g.k_stages; ++kb) {
+        for (int kb = kb_lo; kb < kb_hi; ++kb) {
           ok = __all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag, g.dev_err));
           if (!ok) break;
           tc_fence_after();
@@ -333,7 +392,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
               // Offsets of the K step in 16-byte units.
               const uint32_t km = (kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2, mn = kk * 128;
               const uint64_t ad = as + (kAMN ? mn : km), bd = bs + (kBMN ? mn : km);
-              const uint32_t accumulate = (kb | kk) != 0 ? 1u : 0u;
+              const uint32_t accumulate = kb != kb_lo || kk != 0 ? 1u : 0u;
               if constexpr (HALVES == 1) {
                 umma_bf16_pair(d, ad, bd, idesc, accumulate);
               } else {
@@ -341,7 +400,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
                 umma_pair_a_last(d + kBN, ad, bd + S::kBBytes / 16, idesc, accumulate);
               }
             }
-            umma_commit_pair(&empty[s], 0x3);
+            umma_commit_pair(&empty[s], both);
           }
           __syncwarp();
           if (++s == S::kStages) {
@@ -350,19 +409,19 @@ __global__ void __launch_bounds__(kLThreads, 1)
           }
         }
         if (!ok) break;
-        if (elect_one()) umma_commit_pair(&tfull[acc], 0x3);
+        if (elect_one()) umma_commit_pair(&tfull[acc], both);
         __syncwarp();
         if (++acc == S::kAccs) {
           acc = 0;
           aph ^= 1;
         }
       }
-      if (elect_one()) umma_commit_pair(done_bar, 0x3);
+      if (elect_one()) umma_commit_pair(done_bar, both);
       __syncwarp();
     }
     // Both CTAs: every pair MMA must finish before TMEM is released.
     mbar_drain(done_bar, 0);
-  } else {
+  } else if constexpr (!SPLIT) {
     // -------------------------------------------------------- epilogue (both CTAs)
     const int quad = warp & 3;
     TileSlice sl;
@@ -373,7 +432,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
     sl.c_lo = warp < 6 ? 0 : first;
     sl.c_hi = warp < 6 ? first : chunks;
     Staging st{stage + (warp - 2) * kStageBytes, 0};
-    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), 0);
+    const uint32_t tempty0 = mapa_shared(smem_u32(&tempty[0]), even);
     int acc = 0;
     uint32_t aph = 0;
     for (int t = cluster; t < num_tiles; t += nclusters) {
@@ -381,10 +440,10 @@ __global__ void __launch_bounds__(kLThreads, 1)
       pair_coords(g, t, tm, tn);
       if (!mbar_wait(&tfull[acc], aph, abort_flag, g.dev_err)) break;
       tc_fence_after();
-      const uint32_t taddr =
-          tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc * kBN);
+      const TmemAcc from{tmem_base + (static_cast<uint32_t>(quad * 32) << 16) +
+                         static_cast<uint32_t>(acc * kBN)};
       Epi::tile(ea, g, tm, tm * 256 + static_cast<int>(rank) * 128 + quad * 32, tn * cols, lane,
-                taddr, st, sl);
+                from, st, sl);
       tc_fence_before();
       tmem_release_arrive_cluster(tempty0 + static_cast<uint32_t>(acc) * 8u);
       if (++acc == S::kAccs) {
@@ -393,6 +452,68 @@ __global__ void __launch_bounds__(kLThreads, 1)
       }
     }
     if (lane == 0) bulk_wait_group0();  // this warp's epilogue stores have completed
+  }
+  if constexpr (SPLIT) {
+    // The ring is free once every CTA of the cluster is here: its loads have landed and
+    // its MMAs are done.
+    __syncwarp();
+    tc_fence_before();
+    cluster_sync();
+    tc_fence_after();
+    // Output chunk oc of the tile goes to the pair oc / own (with kTwoB both its products).
+    const int products = kPlan == kTwoB ? 2 : 1;
+    const int own = bn / 32 / products / slices;  // output chunks of a pair
+    const int quad = warp & 3, e = warp - 2;
+    if (warp >= 2) {
+      // Sent chunks are built above the received ones, 4 KiB a warp and chunk.
+      const uint32_t recv = smem_u32(smem);
+      const uint32_t send = recv + static_cast<uint32_t>((slices - 1) * products * own * 16384);
+      const uint32_t taddr = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
+#pragma unroll 1
+      for (int c = e >> 2; c < bn / 32; c += 2) {
+        const int h = c / (own * slices), oc = c - h * own * slices, to = oc / own;
+        if (to == slice) continue;
+        const int lc = h * own + oc - to * own;
+        const int slot = slice - (slice > to ? 1 : 0);  // the receiver has none of its own
+        const uint32_t src = send + static_cast<uint32_t>(
+                                        ((to - (to > slice ? 1 : 0)) * products * own + lc) * 16384 +
+                                        quad * 4096);
+        const uint32_t dst =
+            recv + static_cast<uint32_t>((slot * products * own + lc) * 16384 + quad * 4096);
+        float v[32];
+        tmem_ld_32cols(taddr + static_cast<uint32_t>(c * 32), v);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           src + static_cast<uint32_t>(q * 512 + lane * 16)),
+                       "f"(v[4 * q]), "f"(v[4 * q + 1]), "f"(v[4 * q + 2]), "f"(v[4 * q + 3])
+                       : "memory");
+        fence_proxy_async_smem();
+        __syncwarp();
+        const uint32_t there = static_cast<uint32_t>(2 * to) + rank;
+        if (lane == 0)
+          bulk_copy_to_cta(mapa_shared(dst, there), src, 4096, mapa_shared(smem_u32(xbar), there));
+        __syncwarp();
+      }
+      int tm, tn;
+      pair_coords(g, cluster, tm, tn);
+      Staging st{stage + e * kStageBytes, 0};
+      TileSlice sl;
+      sl.width = own * 32;
+      sl.per = own;
+      sl.up_off = own * 32;
+      const int first = (own + 1) / 2;
+      sl.c_lo = e < 4 ? 0 : first;
+      sl.c_hi = e < 4 ? first : own;
+      const SplitAcc from{taddr + static_cast<uint32_t>(slice * own * 32), own * slices * 32,
+                          reinterpret_cast<const float4*>(smem) + quad * 256 + lane, slices, own,
+                          products * own};
+      if (mbar_wait(xbar, 0, abort_flag, g.dev_err))
+        Epi::tile(ea, g, tm, tm * 256 + static_cast<int>(rank) * 128 + quad * 32,
+                tn * cols + slice * own * 32, lane, from, st, sl);
+      tc_fence_before();
+      if (lane == 0) bulk_wait_group0();
+    }
   }
   __syncwarp();
   tc_fence_before();
