@@ -114,7 +114,7 @@ int64_t small_most(bool gated) { return gated ? kSmallGatedTokens : kSmallTokens
 // The parts of a few-token product's arguments that do not depend on the operator.
 // x: [M, k] with pitch ld_x; the sum runs over `segments` times k.
 bool small_args(SmallArgs* a, const void* x, int64_t ld_x, int64_t M, int64_t k, int segments,
-                int64_t N, void* y, int64_t ld_y, bool f16, int32_t* dev_err) {
+                int64_t N, void* y, int64_t ld_y, bool two, bool f16, int32_t* dev_err) {
   std::memset(a, 0, sizeof(*a));
   a->y = static_cast<uint16_t*>(y);
   a->ld_y = ld_y;
@@ -124,7 +124,7 @@ bool small_args(SmallArgs* a, const void* x, int64_t ld_x, int64_t M, int64_t k,
   a->N = static_cast<int>(N);
   a->k_split = cdiv(k, kBK);
   a->k_blocks = segments * a->k_split;
-  a->slices = small_slices(M, N, a->k_blocks);
+  a->slices = small_slices(M, N, a->k_blocks, two);
   a->dev_err = reinterpret_cast<int*>(dev_err);
   return k_major(&a->x, x, M, k, ld_x, f16, small_tokens(M));
 }
@@ -148,7 +148,8 @@ constexpr TileShape kTileShapes[] = {
 // runtime says; 22 of 6 ran in one wave, 8 CTAs did not fill half of the SMs).
 constexpr int kClusters[] = {76, 36, 22};
 constexpr float kSustained[] = {1.66e6f, 1.75e6f};  // flop/ns under the power cap, by halves
-constexpr float kJoinNs = 2200.f;                   // set-up and exchange of a split tile
+constexpr float kJoinNs = 2200.f;   // exchange of a split tile
+constexpr float kSetUpNs = 5000.f;  // start and drain of each further wave of split tiles
 
 // ns of a whole product: its waves of tiles, each as long as the sum or (where it
 // runs beside the next tile's sum) the epilogue; the last epilogue; and no less than
@@ -164,7 +165,7 @@ float tile_ns(const TileShape& t, bool mn, int64_t tiles_m, int64_t N, int64_t k
   const float waves = static_cast<float>((tiles + at_once - 1) / at_once);
   const float sum = static_cast<float>(k64) * (mn ? t.ns_mn : t.ns) / static_cast<float>(t.slices);
   const float epi = epi_ns * static_cast<float>(cols) / static_cast<float>(t.slices);
-  const float busy = t.slices > 1    ? waves * (sum + kJoinNs + epi)
+  const float busy = t.slices > 1    ? waves * (sum + kJoinNs + epi) + (waves - 1.f) * kSetUpNs
                      : t.halves == 1 ? waves * std::max(sum, epi) + epi
                                      : waves * (sum + epi);
   const float flops = 2.f * 256.f * 64.f * t.halves * t.bn * static_cast<float>(tiles) * k64;
@@ -290,7 +291,7 @@ flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, 
   const int M = static_cast<int>(p->M), K = static_cast<int>(p->K), N = static_cast<int>(p->N);
   if (M <= small_most(false)) {
     SmallArgs sa;
-    if (!small_args(&sa, x, pitch(p->ld_x, K), M, K, 1, N, y, pitch(p->ld_y, N), f16, dev_err) ||
+    if (!small_args(&sa, x, pitch(p->ld_x, K), M, K, 1, N, y, pitch(p->ld_y, N), false, f16, dev_err) ||
         !k_major(&sa.w, W, N, K, K, f16))
       return FLCE_ERR_CUDA;
     sa.bias = static_cast<const uint16_t*>(p->has_bias ? b : nullptr);
@@ -368,15 +369,14 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
     za.fp16 = f16 ? 1 : 0;
     za.vec = dy_rows16 && (!act || N % 8 == 0) ? 1 : 0;
     if (launch_dz(za, s) != cudaSuccess) return FLCE_ERR_CUDA;
-    if (db && launch_db_finalize(w.part, dz_parts(M, N), N, 0, N, db, p->db_fp32 != 0, f16, s) !=
-                  cudaSuccess)
+    if (db && launch_db_sum(w.part, dz_parts(M, N), N, db, p->db_fp32 != 0, f16, s) != cudaSuccess)
       return FLCE_ERR_CUDA;
   }
   const void* dz = copy ? static_cast<const void*>(w.dz) : dy;
   const int64_t ld_dz = copy ? w.ld_dz : ld_dy;
   if (dx && M <= small_most(false)) {
     SmallArgs sa;
-    if (!small_args(&sa, dz, ld_dz, M, N, 1, K, dx, K, f16, dev_err) ||
+    if (!small_args(&sa, dz, ld_dz, M, N, 1, K, dx, K, false, f16, dev_err) ||
         !mn_major(&sa.w, W, K, N, K, f16, kBK) || launch_small(false, true, sa, s) != cudaSuccess)
       return FLCE_ERR_CUDA;
   } else if (dx) {
@@ -431,8 +431,8 @@ flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, co
   const int M = static_cast<int>(p->M), K = static_cast<int>(p->K), F = static_cast<int>(p->F);
   if (M <= small_most(true)) {
     SmallArgs sa;
-    if (!small_args(&sa, x, pitch(p->ld_x, K), M, K, 1, F, h, pitch(p->ld_h, F), f16, dev_err) ||
-        !k_major(&sa.w, Wg, F, K, K, f16) || !k_major(&sa.w2, Wu, F, K, K, f16))
+    if (!small_args(&sa, x, pitch(p->ld_x, K), M, K, 1, F, h, pitch(p->ld_h, F), true, f16, dev_err) ||
+        !k_major(&sa.w, Wg, F, K, K, f16, 64) || !k_major(&sa.w2, Wu, F, K, K, f16, 64))
       return FLCE_ERR_CUDA;
     sa.keep = static_cast<uint16_t*>(pre);
     sa.act = p->activation;
@@ -500,7 +500,7 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
   if (launch_gated_grad(ga, s) != cudaSuccess) return FLCE_ERR_CUDA;
   if (dx && M <= small_most(false)) {
     SmallArgs sa;
-    if (!small_args(&sa, w.dg, F, M, F, 2, K, dx, K, f16, dev_err) ||
+    if (!small_args(&sa, w.dg, F, M, F, 2, K, dx, K, false, f16, dev_err) ||
         !k_major(&sa.x2, w.du, M, F, F, f16, small_tokens(M)) ||
         !mn_major(&sa.w, Wg, K, F, K, f16, kBK) || !mn_major(&sa.w2, Wu, K, F, K, f16, kBK) ||
         launch_small(false, true, sa, s) != cudaSuccess)

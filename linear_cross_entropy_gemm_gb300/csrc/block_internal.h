@@ -60,7 +60,7 @@ cudaError_t launch_grad_w(bool two, const PairArgs& g, const GradWArgs& ea, int 
 
 // Few-token products (block_small.cu): y [M, N] = epilogue of x Wt^T, with the
 // weights on the MMA's rows. w: boxes of 128 features x 64 sum elements (64 x 64
-// with the features contiguous); x: 64 sum elements x small_tokens(M) tokens.
+// with the features contiguous, or for the gated projection); x: 64 sum elements x small_tokens(M) tokens.
 struct SmallArgs {
   CUtensorMap w, w2, x, x2;
   const uint16_t* bias;
@@ -76,7 +76,7 @@ struct SmallArgs {
   int* dev_err;
 };
 int small_tokens(int64_t M);  // tokens of a tile
-int small_slices(int64_t M, int64_t N, int k_blocks);
+int small_slices(int64_t M, int64_t N, int k_blocks, bool two);
 cudaError_t launch_small(bool two, bool w_mn, const SmallArgs& a, cudaStream_t st);
 
 // Element-wise parts of the backward passes (block_rowwise.cu).
@@ -92,6 +92,8 @@ struct DzArgs {
 };
 int dz_parts(int64_t M, int64_t N);
 cudaError_t launch_dz(const DzArgs& a, cudaStream_t st);
+cudaError_t launch_db_sum(const float* part, int parts, int N, void* db, bool fp32, bool fp16,
+                          cudaStream_t st);
 
 struct GatedGradArgs {
   const uint16_t* dh;  // [M, ld_dh]

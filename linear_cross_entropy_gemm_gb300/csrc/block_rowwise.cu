@@ -59,28 +59,44 @@ __global__ void __launch_bounds__(32 * kDzRowGroups) dz_kernel(const DzArgs a, i
   float sum[8] = {};
   const int vcol = col0 + cg * 8;
   if (vec && vcol + 8 <= a.N) {
-    for (int r = r_lo + rg; r < r_hi; r += kDzRowGroups) {
-      float v[8];
-      unpack8(*reinterpret_cast<const uint4*>(a.dy + static_cast<size_t>(r) * a.ld_dy + vcol), f16,
-              v);
-      if (a.z) {
-        float z[8];
-        unpack8(__ldg(reinterpret_cast<const uint4*>(a.z + static_cast<size_t>(r) * a.N + vcol)),
-                f16, z);
-        with_act(a.act, [&](auto act) {
+    // Four rows at a time: their loads are in flight together.
+    with_act(a.z ? a.act : static_cast<int>(kActNone), [&](auto act) {
+      constexpr int kAct = decltype(act)::value;
+      for (int r = r_lo + rg; r < r_hi; r += 4 * kDzRowGroups) {
+        uint4 d[4], q[4];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float val, slope;
-            act_value_slope<decltype(act)::value>(z[j], val, slope);
-            v[j] *= slope;
+        for (int i = 0; i < 4; ++i) {
+          const int row = r + i * kDzRowGroups;
+          if (row >= r_hi) break;
+          d[i] = *reinterpret_cast<const uint4*>(a.dy + static_cast<size_t>(row) * a.ld_dy + vcol);
+          if constexpr (kAct != kActNone)
+            q[i] = __ldg(
+                reinterpret_cast<const uint4*>(a.z + static_cast<size_t>(row) * a.N + vcol));
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = r + i * kDzRowGroups;
+          if (row >= r_hi) break;
+          float v[8];
+          unpack8(d[i], f16, v);
+          if constexpr (kAct != kActNone) {
+            float z[8];
+            unpack8(q[i], f16, z);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              float val, slope;
+              act_value_slope<kAct>(z[j], val, slope);
+              v[j] *= slope;
+            }
           }
-        });
-      }
-      if (a.dz)
-        *reinterpret_cast<uint4*>(a.dz + static_cast<size_t>(r) * a.ld_dz + vcol) = pack8(v, f16);
+          if (a.dz)
+            *reinterpret_cast<uint4*>(a.dz + static_cast<size_t>(row) * a.ld_dz + vcol) =
+                pack8(v, f16);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) sum[j] += v[j];
-    }
+          for (int j = 0; j < 8; ++j) sum[j] += v[j];
+        }
+      }
+    });
   } else {
     const int first = vec ? vcol : col0 + cg, step = vec ? 1 : 32;
     for (int r = r_lo + rg; r < r_hi; r += kDzRowGroups) {
@@ -119,6 +135,36 @@ cudaError_t launch_dz(const DzArgs& a, cudaStream_t st) {
   const dim3 grid((a.N + kDzCols - 1) / kDzCols, dz_parts(a.M, a.N));
   return launch_dependent(dz_kernel, grid, 32 * kDzRowGroups, 0, 1, st, a,
                           dz_rows_per_part(a.M, a.N));
+}
+
+// db = the ordered sum of the parts: a block takes 32 columns, its 8 warps every eighth
+// part each, and the warps' sums are added in warp order.
+__global__ void __launch_bounds__(256) db_sum_kernel(const float* part, int parts, int N, void* db,
+                                                     int fp32, int fp16) {
+  __shared__ float s_sum[8][32];
+  griddep_launch();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
+  float t = 0.f;
+  if (col < N) {
+#pragma unroll 4
+    for (int i = w; i < parts; i += 8) t += part[static_cast<size_t>(i) * N + col];
+  }
+  s_sum[w][lane] = t;
+  __syncthreads();
+  if (w != 0 || col >= N) return;
+#pragma unroll
+  for (int k = 1; k < 8; ++k) t += s_sum[k][lane];
+  if (fp32)
+    static_cast<float*>(db)[col] = t;
+  else
+    static_cast<uint16_t*>(db)[col] = to16(t, fp16 != 0);
+}
+
+cudaError_t launch_db_sum(const float* part, int parts, int N, void* db, bool fp32, bool fp16,
+                          cudaStream_t st) {
+  return launch_dependent(db_sum_kernel, dim3(static_cast<unsigned>((N + 31) / 32)), 256, 0, 1, st,
+                          part, parts, N, db, fp32 ? 1 : 0, fp16 ? 1 : 0);
 }
 
 // One thread takes 8 columns of one row: three 16-byte loads, two 16-byte

@@ -6,7 +6,8 @@
 //
 //   D[f, m] = sum_k Wt[f, k] x[m, k],   128 features x NT tokens, NT = 16 .. 128
 //
-// and a tile wastes at most 15 of the columns it computes. One CTA per tile and K
+// and a tile wastes at most 15 of the columns it computes. A tile of the gated
+// projection has 64 rows of each weight, so that its ring stage is no larger. One CTA per tile and K
 // slice: the slices of a tile form a cluster (1, 2, 4 or 8 CTAs), so that even a
 // narrow layer keeps every SM streaming. The slices join through distributed shared
 // memory: each CTA sends the others the fp32 partial sums of their share of the
@@ -27,14 +28,13 @@ constexpr int kWTileBytes = 128 * kBK * 2;  // one weight slice, 16 KiB
 
 // Ring stages: two CTAs per SM up to 64 tokens (their loads overlap each other's
 // epilogues), one above.
-template <int NT, bool TWO>
+template <int NT>
 struct SmallShape {
-  static constexpr int kStage = (TWO ? 2 : 1) * kWTileBytes + NT * kBK * 2;
+  static constexpr int kStage = kWTileBytes + NT * kBK * 2;
   static constexpr int kRing = NT <= 64 ? 108 * 1024 : 208 * 1024;
   static constexpr int kStages = kRing / kStage;
-  static constexpr int kAcc = (TWO ? 2 : 1) * NT;      // TMEM columns in use
-  static constexpr int kTmem = kAcc < 32 ? 32 : kAcc;  // allocated
-  static constexpr int kPartial = (TWO ? 2 : 1) * NT * 128 * 4;  // joins reuse the ring
+  static constexpr int kTmem = NT < 32 ? 32 : NT;  // TMEM columns
+  static constexpr int kPartial = NT * 128 * 4;    // joins reuse the ring
   static constexpr int kBody = kStages * kStage > kPartial ? kStages * kStage : kPartial;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kBody) + kBarrierBytes;
   static_assert(kSmem <= 232448, "dynamic shared memory above the 227 KiB a CTA may use");
@@ -98,11 +98,12 @@ __device__ __forceinline__ void store8(uint16_t* p, int n, bool vec, bool f16, c
 
 // W_MN: the weights' features are contiguous and its rows are the sum (dx: W and
 // dz), else its rows are the features. TWO: two weight tensors with one x (gated
-// forward). The two-segment sum of the gated dx is `k_split` < `k_blocks`.
+// forward); rows 0 .. 63 of a tile are the first's, 64 .. 127 the second's. The
+// two-segment sum of the gated dx is `k_split` < `k_blocks`.
 template <int NT, bool TWO, bool W_MN>
 __global__ void __launch_bounds__(kSmThreads)
     small_gemm_kernel(const __grid_constant__ SmallArgs a) {
-  using S = SmallShape<NT, TWO>;
+  using S = SmallShape<NT>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -115,7 +116,8 @@ __global__ void __launch_bounds__(kSmThreads)
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int slices = a.slices;
   const int rank = static_cast<int>(blockIdx.x) % slices;  // = the CTA's rank in its cluster
-  const int f0 = static_cast<int>(blockIdx.x) / slices * 128;
+  constexpr int kOut = TWO ? 64 : 128;  // output features of a tile
+  const int f0 = static_cast<int>(blockIdx.x) / slices * kOut;
   const int m0 = static_cast<int>(blockIdx.y) * NT;
   const int kb_lo = static_cast<int>(static_cast<int64_t>(a.k_blocks) * rank / slices);
   const int kb_hi = static_cast<int>(static_cast<int64_t>(a.k_blocks) * (rank + 1) / slices);
@@ -154,14 +156,16 @@ __global__ void __launch_bounds__(kSmThreads)
       const CUtensorMap* mw = second ? &a.w2 : &a.w;
       if (elect_one()) {
         mbar_arrive_expect_tx(&full[s], S::kStage);
-        if constexpr (!W_MN) {
+        if constexpr (TWO) {
+          tma_load_plane(w, &a.w, &full[s], k0, f0, pol);
+          tma_load_plane(w + kWTileBytes / 2, &a.w2, &full[s], k0, f0, pol);
+        } else if constexpr (!W_MN) {
           tma_load_plane(w, mw, &full[s], k0, f0, pol);
-          if constexpr (TWO) tma_load_plane(w + kWTileBytes, &a.w2, &full[s], k0, f0, pol);
         } else {
           tma_load_plane(w, mw, &full[s], f0, k0, pol);
           tma_load_plane(w + kMnBoxBytes, mw, &full[s], f0 + 64, k0, pol);
         }
-        tma_load_plane(w + (TWO ? 2 : 1) * kWTileBytes, second ? &a.x2 : &a.x, &full[s], k0, m0, pol);
+        tma_load_plane(w + kWTileBytes, second ? &a.x2 : &a.x, &full[s], k0, m0, pol);
       }
       __syncwarp();
       ++issued;
@@ -177,7 +181,7 @@ __global__ void __launch_bounds__(kSmThreads)
     const uint32_t idesc = idesc_f16kind_f32(128, NT, W_MN, false, a.fp16 != 0);
     const uint32_t s0 = smem_u32(smem);
     const uint64_t w0 = smem_desc_sw128(s0, W_MN ? kMnBoxBytes : 16, 1024);
-    const uint64_t x0 = smem_desc_sw128(s0 + (TWO ? 2 : 1) * kWTileBytes, 16, 1024);
+    const uint64_t x0 = smem_desc_sw128(s0 + kWTileBytes, 16, 1024);
     int s = 0;
     uint32_t ph = 0;
     for (int kb = kb_lo; kb < kb_hi; ++kb) {
@@ -190,7 +194,6 @@ __global__ void __launch_bounds__(kSmThreads)
           const uint64_t wd = w0 + off + kk * (W_MN ? 128 : 2), xd = x0 + off + kk * 2;
           const uint32_t acc = kb != kb_lo || kk != 0 ? 1u : 0u;
           umma_bf16(tmem_base, wd, xd, idesc, acc);
-          if constexpr (TWO) umma_bf16(tmem_base + NT, wd + kWTileBytes / 16, xd, idesc, acc);
         }
         umma_commit(&empty[s]);
       }
@@ -214,30 +217,28 @@ __global__ void __launch_bounds__(kSmThreads)
   tc_fence_after();
 
   const int tokens = min(NT, a.M - m0);
-  // Received partial sums, fp32 [slices][TWO ? 2 : 1][NT tokens][own features].
-  const int own = 128 / slices;  // features whose outputs this CTA writes
+  // Received partial sums, fp32 [slices][products][NT tokens][own features].
+  constexpr int kProducts = TWO ? 2 : 1;
+  const int own = kOut / slices;  // output features that this CTA writes
   const float* part = reinterpret_cast<const float*>(smem);
   if (warp >= 2) {
-    const int quad = warp & 3, f = quad * 32 + lane;
+    const int quad = warp & 3, lane_row = quad * 32 + lane;
+    const int h = lane_row / kOut, f = lane_row - h * kOut;
     const uint32_t base = tmem_base + (static_cast<uint32_t>(quad * 32) << 16);
     const int to = f / own;  // rank that writes feature f
-    const uint32_t mine = smem_u32(smem) +
-                          static_cast<uint32_t>(((rank * (TWO ? 2 : 1)) * NT * own + f - to * own) * 4);
+    const uint32_t mine =
+        smem_u32(smem) +
+        static_cast<uint32_t>(((rank * kProducts + h) * NT * own + f - to * own) * 4);
     const uint32_t dst = slices > 1 ? mapa_shared(mine, static_cast<uint32_t>(to)) : mine;
 #pragma unroll 1
     for (int c = 0; c < tokens; c += 16) {
-      uint32_t r[16], q[16];
+      uint32_t r[16];
       tmem_issue_16(base + c, r);
-      if constexpr (TWO) tmem_issue_16(base + NT + c, q);
       tmem_wait_16(r);
-      if constexpr (TWO) tmem_wait_16(q);
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         if (c + j >= tokens) break;
-        const uint32_t at = dst + static_cast<uint32_t>((c + j) * own * 4);
-        st_cluster_f32(at, __uint_as_float(r[j]));
-        if constexpr (TWO)
-          st_cluster_f32(at + static_cast<uint32_t>(NT * own * 4), __uint_as_float(q[j]));
+        st_cluster_f32(dst + static_cast<uint32_t>((c + j) * own * 4), __uint_as_float(r[j]));
       }
     }
     tc_fence_before();
@@ -254,11 +255,11 @@ __global__ void __launch_bounds__(kSmThreads)
     const int t = i / groups, gl = i - t * groups;
     const int col = f0 + rank * own + gl * 8, n = a.N - col;
     if (n <= 0) continue;
-    float v[TWO ? 2 : 1][8];
+    float v[kProducts][8];
 #pragma unroll
-    for (int h = 0; h < (TWO ? 2 : 1); ++h) {
+    for (int h = 0; h < kProducts; ++h) {
       const float* p = part + (h * NT + t) * own + gl * 8;
-      const int step = (TWO ? 2 : 1) * NT * own;
+      const int step = kProducts * NT * own;
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[h][j] = p[j];
 #pragma unroll
@@ -308,21 +309,22 @@ __global__ void __launch_bounds__(kSmThreads)
 
 template <int NT, bool TWO, bool W_MN>
 static cudaError_t launch_t(const SmallArgs& a, cudaStream_t st) {
-  using S = SmallShape<NT, TWO>;
+  using S = SmallShape<NT>;
   auto kernel = small_gemm_kernel<NT, TWO, W_MN>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(S::kSmem));
   if (e != cudaSuccess) return e;
-  const dim3 grid(static_cast<unsigned>((a.N + 127) / 128 * a.slices),
+  constexpr int kOut = TWO ? 64 : 128;
+  const dim3 grid(static_cast<unsigned>((a.N + kOut - 1) / kOut * a.slices),
                   static_cast<unsigned>((a.M + NT - 1) / NT));
   return launch_dependent(kernel, grid, kSmThreads, S::kSmem, a.slices, st, a);
 }
 
 int small_tokens(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
-int small_slices(int64_t M, int64_t N, int k_blocks) {
-  const int64_t nt = small_tokens(M);
-  const int64_t tiles = (N + 127) / 128 * ((M + nt - 1) / nt);
+int small_slices(int64_t M, int64_t N, int k_blocks, bool two) {
+  const int64_t nt = small_tokens(M), out = two ? 64 : 128;
+  const int64_t tiles = (N + out - 1) / out * ((M + nt - 1) / nt);
   int s = 1;
   const int64_t places = nt <= 64 ? 304 : 152;
   while (s < 8 && tiles * s * 2 <= places && 2 * s <= k_blocks) s *= 2;

@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/flce.h"
+#include "block_internal.h"
 #include "flce_host.h"
 
 namespace flce {
@@ -143,34 +144,73 @@ __device__ __forceinline__ double block_sum(double v) {
   return t;
 }
 
+// This thread's share of a chunk's squares.
+__device__ __forceinline__ float chunk_squares(const Chunk& k) {
+  const uint4* v = reinterpret_cast<const uint4*>(k.p + k.head);
+  float s = 0.f;
+  if (k.vecs == kVecs * kThreadsN) {
+    uint4 u[kVecs];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) u[i] = v[i * kThreadsN + threadIdx.x];
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) s += square_16b(u[i], k.type);
+  } else {
+    for (int i = threadIdx.x; i < k.vecs; i += kThreadsN) s += square_16b(v[i], k.type);
+    // Fewer than 16 bytes before the words and after them: at most 14 elements.
+    const int nh = k.head / k.esize, nt = (k.bytes - k.head - 16 * k.vecs) / k.esize;
+    const int e = threadIdx.x;
+    if (e < nh + nt) {
+      const int at = e < nh ? e * k.esize : k.head + 16 * k.vecs + (e - nh) * k.esize;
+      const float x = load_one(k.p + at, k.type);
+      s = fmaf(x, x, s);
+    }
+  }
+  return s;
+}
+
+// This thread's share of out = c chunk.
+__device__ __forceinline__ void scale_chunk(const Chunk& k, void* tensor_out, float c) {
+  uint8_t* out = static_cast<uint8_t*>(tensor_out) + k.off;
+  if (c == 1.f && out == k.p) return;
+  if (((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(k.p)) & 15) != 0) {
+    // Source and destination differ in alignment: element by element.
+    for (int e = threadIdx.x; e < k.bytes / k.esize; e += kThreadsN)
+      store_one(out + e * k.esize, load_one(k.p + e * k.esize, k.type) * c, k.type);
+    return;
+  }
+  const uint4* v = reinterpret_cast<const uint4*>(k.p + k.head);
+  uint4* o = reinterpret_cast<uint4*>(out + k.head);
+  if (k.vecs == kVecs * kThreadsN) {
+    uint4 u[kVecs];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) u[j] = v[j * kThreadsN + threadIdx.x];
+#pragma unroll
+    for (int j = 0; j < kVecs; ++j) __stcs(o + j * kThreadsN + threadIdx.x, scale_16b(u[j], c, k.type));
+  } else {
+    for (int j = threadIdx.x; j < k.vecs; j += kThreadsN) __stcs(o + j, scale_16b(v[j], c, k.type));
+    const int nh = k.head / k.esize, nt = (k.bytes - k.head - 16 * k.vecs) / k.esize;
+    const int e = threadIdx.x;
+    if (e < nh + nt) {
+      const int at = e < nh ? e * k.esize : k.head + 16 * k.vecs + (e - nh) * k.esize;
+      store_one(out + at, load_one(k.p + at, k.type) * c, k.type);
+    }
+  }
+}
+
+__device__ __forceinline__ float clip_scale(float norm, float max_norm, float eps) {
+  const float q = max_norm / (norm + eps);
+  return q > 1.f ? 1.f : q;  // a NaN stays one
+}
+
 template <int CAP>
 __global__ void __launch_bounds__(kThreadsN, kBlocksPerSm)
     square_sums_kernel(const __grid_constant__ Table<CAP> t, double* part) {
+  griddep_launch();
+  griddep_wait();
   double total = 0.0;
   const uint32_t chunks = t.begin[t.count];
-  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x) {
-    const Chunk k = chunk_of(t, c);
-    const uint4* v = reinterpret_cast<const uint4*>(k.p + k.head);
-    float s = 0.f;
-    if (k.vecs == kVecs * kThreadsN) {
-      uint4 u[kVecs];
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) u[i] = __ldg(v + i * kThreadsN + threadIdx.x);
-#pragma unroll
-      for (int i = 0; i < kVecs; ++i) s += square_16b(u[i], k.type);
-    } else {
-      for (int i = threadIdx.x; i < k.vecs; i += kThreadsN) s += square_16b(__ldg(v + i), k.type);
-      // Fewer than 16 bytes before the words and after them: at most 14 elements.
-      const int nh = k.head / k.esize, nt = (k.bytes - k.head - 16 * k.vecs) / k.esize;
-      const int e = threadIdx.x;
-      if (e < nh + nt) {
-        const int at = e < nh ? e * k.esize : k.head + 16 * k.vecs + (e - nh) * k.esize;
-        const float x = load_one(k.p + at, k.type);
-        s = fmaf(x, x, s);
-      }
-    }
-    total += static_cast<double>(s);
-  }
+  for (uint32_t c = blockIdx.x; c < chunks; c += gridDim.x)
+    total += static_cast<double>(chunk_squares(chunk_of(t, c)));
   total = block_sum(total);
   if (threadIdx.x == 0) part[blockIdx.x] = total;
 }
@@ -178,12 +218,14 @@ __global__ void __launch_bounds__(kThreadsN, kBlocksPerSm)
 // The norm from the blocks' sums, in every thread of a block.
 __device__ __forceinline__ float norm_of(const double* part, int parts) {
   double v = 0.0;
-  for (int i = threadIdx.x; i < parts; i += kThreadsN) v += __ldg(part + i);
+  for (int i = threadIdx.x; i < parts; i += kThreadsN) v += part[i];
   return static_cast<float>(sqrt(block_sum(v)));
 }
 
 __global__ void __launch_bounds__(kThreadsN) norm_kernel(const double* part, int parts,
                                                          float* norm) {
+  griddep_launch();
+  griddep_wait();
   const float n = norm_of(part, parts);
   if (threadIdx.x == 0) *norm = n;
 }
@@ -192,39 +234,15 @@ template <int CAP>
 __global__ void __launch_bounds__(kThreadsN, kBlocksPerSm)
     clip_kernel(const __grid_constant__ Table<CAP> t, const double* part, int parts, float max_norm,
                 float eps, float* norm) {
+  griddep_launch();
+  griddep_wait();
   const float n = norm_of(part, parts);
   if (blockIdx.x == 0 && threadIdx.x == 0) *norm = n;
-  const float q = max_norm / (n + eps);
-  const float c = q > 1.f ? 1.f : q;  // a NaN stays one
+  const float c = clip_scale(n, max_norm, eps);
   const uint32_t chunks = t.begin[t.count];
   for (uint32_t i = blockIdx.x; i < chunks; i += gridDim.x) {
     const Chunk k = chunk_of(t, chunks - 1 - i);
-    uint8_t* out = static_cast<uint8_t*>(t.out[k.tensor]) + k.off;
-    if (c == 1.f && out == k.p) continue;
-    if (((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(k.p)) & 15) != 0) {
-      // Source and destination differ in alignment: element by element.
-      for (int e = threadIdx.x; e < k.bytes / k.esize; e += kThreadsN)
-        store_one(out + e * k.esize, load_one(k.p + e * k.esize, k.type) * c, k.type);
-      continue;
-    }
-    const uint4* v = reinterpret_cast<const uint4*>(k.p + k.head);
-    uint4* o = reinterpret_cast<uint4*>(out + k.head);
-    if (k.vecs == kVecs * kThreadsN) {
-      uint4 u[kVecs];
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j) u[j] = v[j * kThreadsN + threadIdx.x];
-#pragma unroll
-      for (int j = 0; j < kVecs; ++j)
-        __stcs(o + j * kThreadsN + threadIdx.x, scale_16b(u[j], c, k.type));
-    } else {
-      for (int j = threadIdx.x; j < k.vecs; j += kThreadsN) __stcs(o + j, scale_16b(v[j], c, k.type));
-      const int nh = k.head / k.esize, nt = (k.bytes - k.head - 16 * k.vecs) / k.esize;
-      const int e = threadIdx.x;
-      if (e < nh + nt) {
-        const int at = e < nh ? e * k.esize : k.head + 16 * k.vecs + (e - nh) * k.esize;
-        store_one(out + at, load_one(k.p + at, k.type) * c, k.type);
-      }
-    }
+    scale_chunk(k, t.out[k.tensor], c);
   }
 }
 
@@ -251,9 +269,11 @@ flce_status_t check_grads(const Grads& g) {
     if (!g.ptrs[i] || !o) return FLCE_ERR_INVALID_ARG;
     if (((reinterpret_cast<uintptr_t>(g.ptrs[i]) | reinterpret_cast<uintptr_t>(o)) & mask) != 0)
       return FLCE_ERR_ALIGNMENT;
-    chunks += (static_cast<uint64_t>(g.numel[i]) * (mask + 1) + kChunkBytes - 1) / kChunkBytes;
+    const uint64_t n = static_cast<uint64_t>(g.numel[i]) * (mask + 1);
+    chunks += (n + kChunkBytes - 1) / kChunkBytes;
+    if (chunks >= (1ULL << 31)) return FLCE_ERR_UNSUPPORTED;
   }
-  return chunks < (1ULL << 31) ? FLCE_OK : FLCE_ERR_UNSUPPORTED;
+  return FLCE_OK;
 }
 
 template <int CAP>
@@ -288,22 +308,23 @@ template <int CAP>
 cudaError_t run_passes(const Grads& g, bool clip, float max_norm, float eps, float* norm,
                        double* part, int sms, cudaStream_t st) {
   Table<CAP> t;
+  int64_t next = 0;
   int parts = 0;
-  for (int64_t next = 0; next < g.count;) {
+  cudaError_t e = cudaSuccess;
+  for (next = 0; next < g.count && e == cudaSuccess;) {
     if (fill(&t, g, &next) == 0) break;
     const uint32_t grid = grid_of(t, sms);
-    square_sums_kernel<CAP><<<grid, kThreadsN, 0, st>>>(t, part + parts);
+    e = launch_dependent(square_sums_kernel<CAP>, dim3(grid), kThreadsN, 0, 1, st, t, part + parts);
     parts += static_cast<int>(grid);
   }
-  if (!clip || parts == 0) {
-    norm_kernel<<<1, kThreadsN, 0, st>>>(part, parts, norm);
-    return cudaGetLastError();
-  }
-  for (int64_t next = 0; next < g.count;) {
+  if (!clip && e == cudaSuccess)
+    return launch_dependent(norm_kernel, dim3(1), kThreadsN, 0, 1, st, part, parts, norm);
+  for (next = 0; next < g.count && e == cudaSuccess;) {
     if (fill(&t, g, &next) == 0) break;
-    clip_kernel<CAP><<<grid_of(t, sms), kThreadsN, 0, st>>>(t, part, parts, max_norm, eps, norm);
+    e = launch_dependent(clip_kernel<CAP>, dim3(grid_of(t, sms)), kThreadsN, 0, 1, st, t, part,
+                         parts, max_norm, eps, norm);
   }
-  return cudaGetLastError();
+  return e;
 }
 
 size_t workspace_of(int64_t count) {
