@@ -401,9 +401,9 @@ typedef struct {
 size_t flce_linear_workspace_size(const flce_linear_params_t* p, int which);
 
 /* Forward. W: [N, K] dense. y: [M, N]; it may be the residual's own buffer (with
- * the same pitch), which it then replaces. pre: NULL, or a dense [M, N] buffer
- * of the operands' type, 16-byte aligned, that receives z for the backward of
- * a call with an activation. */
+ * the same pitch), which it then replaces. pre: NULL, or a dense buffer of M N 16-bit
+ * words, 16-byte aligned, that receives what the backward of a call with an
+ * activation needs: the slopes a'(z) in steps of 2^-15. */
 flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, const void* W,
                                   const void* b, const void* residual, void* y, void* pre,
                                   void* workspace, size_t workspace_bytes, int32_t* dev_err,
@@ -412,8 +412,8 @@ flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, 
 /* Backward: with dz = dy a'(z), dx = dz W ([M, K] dense), dW = dz^T x ([N, K]),
  * db = column sums of dz ([N], with has_bias); the residual's gradient is dy
  * itself. dz is rounded to the operands' type before the two products (it is
- * exactly dy without an activation), not before the sums of db. pre: the
- * forward's kept z (not read without an activation). Each of dx, dW, db
+ * exactly dy without an activation), not before the sums of db. pre: what
+ * the forward kept (not read without an activation). Each of dx, dW, db
  * may be NULL: it is then not computed. Written outputs are overwritten;
  * with M == 0, dW and db are zeroed. dx and dW are 16-byte aligned. */
 flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy, const void* x,
@@ -435,14 +435,15 @@ typedef struct {
 
 size_t flce_gated_workspace_size(const flce_gated_params_t* p, int which);
 
-/* Forward. Wg, Wu: [F, K] dense. h: [M, F]. pre: NULL, or a dense [2, M, F] buffer of
- * the operands' type that receives the two projections for the backward. h, pre:
- * 16-byte aligned. */
+/* Forward. Wg, Wu: [F, K] dense. h: [M, F]. pre: NULL, or a dense buffer of 2 M F 16-bit
+ * words that receives what the backward needs: with g = x Wg^T and u = x Wu^T, the
+ * values a(g), then u a'(g), each with 15 bits and an exponent that 8 neighbours
+ * share. h, pre: 16-byte aligned. */
 flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, const void* Wg,
                                  const void* Wu, void* h, void* pre, void* workspace,
                                  size_t workspace_bytes, int32_t* dev_err, void* stream);
 
-/* Backward: with g, u the forward's kept projections, dg = dh u a'(g) and
+/* Backward: from what the forward kept, dg = dh u a'(g) and
  * du = dh a(g) (rounded to the operands' type), dx = dg Wg + du Wu ([M, K] dense,
  * one fp32 sum), dWg = dg^T x and dWu = du^T x ([F, K]). dx, or both of dWg and
  * dWu, may be NULL: not computed. Written outputs are overwritten; with

@@ -69,8 +69,8 @@ def flce_linear_forward(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tens
     x [M, K] and W [N, K] are bf16 or fp16, K a multiple of 8; x's rows may be
     strided (a multiple of 8 elements). b [N]; residual and ``out`` [M, N] with
     rows of any pitch, ``out`` may be the residual itself. ``pre`` (an [M, N]
-    tensor of x's type) receives z = x W^T + b for flce_linear_backward; a layer
-    without an activation needs none. ``workspace``: as in flce_forward."""
+    tensor of x's type, by its size alone) receives what flce_linear_backward
+    needs of a layer with an activation: the slopes a'(z), not numbers of x's type. ``workspace``: as in flce_forward."""
     if stream is not None:
         with _On(x.device, stream):
             return _calls.linear_forward(x, W, b, residual, activation, pre, out, workspace)
@@ -113,8 +113,8 @@ def flce_gated_forward(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, *,
 
     x [M, K], Wg and Wu [F, K] are bf16 or fp16, K and F multiples of 8; the rows
     of x and ``out`` may be strided (a multiple of 8 elements). ``pre`` (a
-    [2, M, F] tensor of x's type) receives both projections for
-    flce_gated_backward. ``workspace``: as in flce_forward."""
+    [2, M, F] tensor of x's type, by its size alone) receives what
+    flce_gated_backward needs, in a form of its own. ``workspace``: as in flce_forward."""
     if stream is not None:
         with _On(x.device, stream):
             return _calls.gated_forward(x, Wg, Wu, activation, pre, out, workspace)
@@ -193,7 +193,7 @@ def _usable(t: torch.Tensor) -> torch.Tensor:
 
 
 class FusedLinearFunction(torch.autograd.Function):
-    """Autograd form of the linear layer. It keeps x, and z where there is an activation."""
+    """Autograd form of the linear layer. It keeps x, and the slopes of an activation."""
 
     @staticmethod
     def forward(ctx, x, weight, bias, residual, activation):
@@ -219,7 +219,7 @@ class FusedLinearFunction(torch.autograd.Function):
 
 
 class GatedLinearFunction(torch.autograd.Function):
-    """Autograd form of the gated projection. It keeps x and both projections."""
+    """Autograd form of the gated projection. It keeps x and 32 bits for each output."""
 
     @staticmethod
     def forward(ctx, x, gate_weight, up_weight, activation):

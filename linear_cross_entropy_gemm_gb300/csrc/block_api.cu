@@ -2,7 +2,7 @@
 // workspace carving, TMA descriptors and the launch sequence.
 //
 // Linear  forward   one GEMM, x W^T with bias, activation and residual in its epilogue
-//         backward  dz = dy a'(z) with the bias gradient's column sums (no kernel
+//         backward  dz = dy a'(z) from the kept slopes, with the bias gradient's column sums (no kernel
 //                   without an activation and a bias: dz is dy), then the GEMMs
 //                   dx = dz W and dW = dz^T x
 // Gated   forward   one GEMM whose tiles hold both projections of the same outputs
@@ -75,33 +75,18 @@ bool out16(Out16* o, void* ptr, int64_t rows, int64_t cols, int64_t ld) {
                                         false);
 }
 
-// 16-bit operand [outer, inner] with row pitch ld as one plane of a two-plane map
-// (pair_engine.cuh), 128-byte swizzled boxes; out-of-range elements read as 0.
-bool encode_plane(CUtensorMap* m, const void* base, int64_t inner, int64_t outer, int64_t ld,
-                  int box_inner, int box_outer, bool f16) {
-  auto fn = encoder();
-  if (!fn) return false;
-  const uint64_t row = static_cast<uint64_t>(ld) * 2, span = row * static_cast<uint64_t>(outer);
-  cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(outer), 2};
-  cuuint64_t strides[2] = {row, span < 131072 ? 131072 : span};
-  cuuint32_t box[3] = {static_cast<cuuint32_t>(box_inner), static_cast<cuuint32_t>(box_outer), 1};
-  cuuint32_t estr[3] = {1, 1, 1};
-  return fn(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 // K-major operand [rows, k]: boxes of 64 x 128 (or fewer rows). MN-major operand, the
 // transpose of a row-major [k, rows] array: boxes of 64 x 128, or 64 x 64 for the
 // few-token kernel.
 bool k_major(CUtensorMap* m, const void* p, int64_t rows, int64_t k, int64_t ld, bool f16,
              int box = kBM) {
-  return encode_plane(m, p, k, rows, ld, kBK, box, f16);
+  return encode_2d(m, p, k, rows, static_cast<uint64_t>(ld) * 2, kBK, static_cast<uint32_t>(box),
+                   f16);
 }
 bool mn_major(CUtensorMap* m, const void* p, int64_t rows, int64_t k, int64_t ld, bool f16,
               int box) {
-  return encode_plane(m, p, rows, k, ld, 64, box, f16);
+  return encode_2d(m, p, rows, k, static_cast<uint64_t>(ld) * 2, 64, static_cast<uint32_t>(box),
+                   f16);
 }
 
 // Products of at most this many tokens go to the few-token kernel (measured: 128 tokens
@@ -229,30 +214,67 @@ PairArgs pair_args(int M, int N, int K, int segments, bool mn, bool two_b, float
 
 flce_status_t done(cudaError_t e) { return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA; }
 
-// Backward scratch of the linear layer: dz where it is not dy itself, and the
-// bias gradient's partial sums.
+// Loads through a TMA map whose tensor spans less than 128 KiB run up to several times
+// slower when many SMs share it (measured with the same boxes and bytes: 94 us with 15
+// rows of 8 KiB, 20 us with 16; a dW of 8 x 4096 over 2048 tokens 32 us, 17 us with both
+// operands spread). The backward's GEMMs therefore take such an operand from a copy
+// whose rows lie far enough apart: the row pitch, in elements, and the copy's bytes.
+constexpr int64_t kSpreadElems = 131072 / 2;  // from a tensor's first element to its last
+bool is_narrow(int64_t rows, int64_t cols, int64_t ld) {
+  return rows > 1 && (rows - 1) * ld + cols < kSpreadElems;
+}
+int64_t spread_ld(int64_t rows, int64_t cols) {
+  const int64_t ld = (kSpreadElems - cols + rows - 2) / (rows - 1);
+  return ((ld > cols ? ld : cols) + 7) / 8 * 8;
+}
+size_t spread_size(int64_t rows, int64_t cols) {
+  return is_narrow(rows, cols, cols) ? static_cast<size_t>(rows * spread_ld(rows, cols)) : 0;
+}
+
+// p [rows, cols] with pitch *ld, or its spread copy in `copy` where it is narrow.
+const void* spread(const void* p, int64_t rows, int64_t cols, int64_t* ld, uint16_t* copy,
+                   cudaStream_t s, cudaError_t* e) {
+  if (*e != cudaSuccess || !copy || !is_narrow(rows, cols, *ld)) return p;
+  const int64_t to = spread_ld(rows, cols);
+  *e = launch_spread(static_cast<const uint16_t*>(p), *ld, copy, to, static_cast<int>(rows),
+                     static_cast<int>(cols), s);
+  *ld = to;
+  return copy;
+}
+
+// Backward scratch of the linear layer: dz where it is not dy itself, the bias
+// gradient's partial sums, and the spread copies of narrow operands.
 struct LinearWs {
-  uint16_t* dz;
+  uint16_t *dz, *x, *W;
   float* part;
   int64_t ld_dz;
 };
 size_t carve(const flce_linear_params_t* p, void* base, LinearWs* w) {
   Carver c(base, 0);
-  w->ld_dz = (p->N + 7) / 8 * 8;
+  w->ld_dz = is_narrow(p->M, p->N, p->N) ? spread_ld(p->M, p->N) : (p->N + 7) / 8 * 8;
   // dy off the 16-byte boundaries also needs a copy: sized for it, since the
   // pointer is not known here.
   w->dz = c.take<uint16_t>(static_cast<size_t>(p->M) * w->ld_dz);
   w->part = p->has_bias ? c.take<float>(static_cast<size_t>(dz_parts(p->M, p->N)) * p->N) : nullptr;
+  const size_t nx = spread_size(p->M, p->K), nw = spread_size(p->N, p->K);
+  w->x = nx ? c.take<uint16_t>(nx) : nullptr;
+  w->W = nw ? c.take<uint16_t>(nw) : nullptr;
   return c.used() + kAlign;
 }
 
 struct GatedWs {
-  uint16_t *dg, *du;
+  uint16_t *dg, *du, *x, *Wg, *Wu;
+  int64_t ld;  // of dg and du
 };
 size_t carve(const flce_gated_params_t* p, void* base, GatedWs* w) {
   Carver c(base, 0);
-  w->dg = c.take<uint16_t>(static_cast<size_t>(p->M) * p->F);
-  w->du = c.take<uint16_t>(static_cast<size_t>(p->M) * p->F);
+  w->ld = is_narrow(p->M, p->F, p->F) ? spread_ld(p->M, p->F) : p->F;
+  w->dg = c.take<uint16_t>(static_cast<size_t>(p->M) * w->ld);
+  w->du = c.take<uint16_t>(static_cast<size_t>(p->M) * w->ld);
+  const size_t nx = spread_size(p->M, p->K), nw = spread_size(p->F, p->K);
+  w->x = nx ? c.take<uint16_t>(nx) : nullptr;
+  w->Wg = nw ? c.take<uint16_t>(nw) : nullptr;
+  w->Wu = nw ? c.take<uint16_t>(nw) : nullptr;
   return c.used() + kAlign;
 }
 
@@ -316,7 +338,7 @@ flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, 
   ea.N = N;
   PairArgs g = pair_args(M, N, K, 1, false, false,
                          epilogue_ns(p->activation, pre != nullptr, false), f16, dev_err);
-  if (!out16(&ea.y, y, M, N, pitch(p->ld_y, N)) || (pre && !out16(&ea.z, pre, M, N, N)) ||
+  if (!out16(&ea.y, y, M, N, pitch(p->ld_y, N)) || (pre && !out16(&ea.slope, pre, M, N, N)) ||
       !k_major(&g.a, x, M, K, pitch(p->ld_x, K), f16) || !k_major(&g.b, W, N, K, K, f16, g.bn / 2))
     return FLCE_ERR_CUDA;
   return done(launch_linear(g, ea, sms, static_cast<cudaStream_t>(stream)));
@@ -354,18 +376,19 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
 
   const int64_t ld_dy = pitch(p->ld_y, N);
   const bool dy_rows16 = aligned16(dy) && ld_dy % 8 == 0;
-  const bool copy = (act || !dy_rows16) && (dx || dW);
+  const bool small_dx = dx && M <= small_most(false), pair_dx = dx && !small_dx;
+  const bool copy =
+      (act || !dy_rows16 || ((pair_dx || dW) && is_narrow(M, N, ld_dy))) && (dx || dW);
   if (copy || db) {
     DzArgs za;
     za.dy = static_cast<const uint16_t*>(dy);
     za.ld_dy = ld_dy;
-    za.z = static_cast<const uint16_t*>(act ? pre : nullptr);
+    za.slope = static_cast<const uint16_t*>(act ? pre : nullptr);
     za.dz = copy ? w.dz : nullptr;
     za.ld_dz = w.ld_dz;
     za.part = db ? w.part : nullptr;
     za.M = M;
     za.N = N;
-    za.act = p->activation;
     za.fp16 = f16 ? 1 : 0;
     za.vec = dy_rows16 && (!act || N % 8 == 0) ? 1 : 0;
     if (launch_dz(za, s) != cudaSuccess) return FLCE_ERR_CUDA;
@@ -374,7 +397,8 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
   }
   const void* dz = copy ? static_cast<const void*>(w.dz) : dy;
   const int64_t ld_dz = copy ? w.ld_dz : ld_dy;
-  if (dx && M <= small_most(false)) {
+  cudaError_t e = cudaSuccess;
+  if (small_dx) {
     SmallArgs sa;
     if (!small_args(&sa, dz, ld_dz, M, N, 1, K, dx, K, false, f16, dev_err) ||
         !mn_major(&sa.w, W, K, N, K, f16, kBK) || launch_small(false, true, sa, s) != cudaSuccess)
@@ -386,8 +410,11 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
     ea.M = M;
     ea.K = K;
     PairArgs g = pair_args(M, K, N, 1, true, false, 6.f, f16, dev_err);
+    int64_t ld_w = K;
+    const void* Wn = spread(W, N, K, &ld_w, w.W, s, &e);
     if (!out16(&ea.dx, dx, M, K, K) || !k_major(&g.a, dz, M, N, ld_dz, f16) ||
-        !mn_major(&g.b, W, K, N, K, f16, pair_lk(g.halves)) || launch_grad_x(false, g, ea, sms, s) != cudaSuccess)
+        !mn_major(&g.b, Wn, K, N, ld_w, f16, pair_lk(g.halves)) || e != cudaSuccess ||
+        launch_grad_x(false, g, ea, sms, s) != cudaSuccess)
       return FLCE_ERR_CUDA;
   }
   if (dW) {
@@ -398,9 +425,12 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
     ea.N = N;
     ea.K = K;
     PairArgs g = pair_args(N, K, M, 1, true, false, 6.f, f16, dev_err);
+    int64_t ld_x = pitch(p->ld_x, K);
+    const void* xn = spread(x, M, K, &ld_x, w.x, s, &e);
     if (!encode_store_2d(&ea.out, dW, K, N, static_cast<uint64_t>(K) * (p->dW_fp32 ? 4 : 2),
                          p->dW_fp32 != 0) ||
-        !mn_major(&g.a, dz, N, M, ld_dz, f16, pair_lk(g.halves)) || !mn_major(&g.b, x, K, M, pitch(p->ld_x, K), f16, pair_lk(g.halves)) ||
+        !mn_major(&g.a, dz, N, M, ld_dz, f16, pair_lk(g.halves)) ||
+        !mn_major(&g.b, xn, K, M, ld_x, f16, pair_lk(g.halves)) || e != cudaSuccess ||
         launch_grad_w(false, g, ea, sms, s) != cudaSuccess)
       return FLCE_ERR_CUDA;
   }
@@ -450,8 +480,8 @@ flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, co
   PairArgs g = pair_args(M, F, K, 1, false, true, epilogue_ns(p->activation, pre != nullptr, true),
                          f16, dev_err);
   if (!out16(&ea.h, h, M, F, pitch(p->ld_h, F)) ||
-      (pre && (!out16(&ea.g, keep, M, F, F) ||
-               !out16(&ea.u, keep + static_cast<size_t>(M) * F, M, F, F))) ||
+      (pre && (!out16(&ea.val, keep, M, F, F) ||
+               !out16(&ea.cross, keep + static_cast<size_t>(M) * F, M, F, F))) ||
       !k_major(&g.a, x, M, K, pitch(p->ld_x, K), f16) || !k_major(&g.b, Wg, F, K, K, f16, g.bn / 2) ||
       !k_major(&g.b2, Wu, F, K, K, f16, g.bn / 2))
     return FLCE_ERR_CUDA;
@@ -489,19 +519,20 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
   GatedGradArgs ga;
   ga.dh = static_cast<const uint16_t*>(dh);
   ga.ld_dh = pitch(p->ld_h, F);
-  ga.g = static_cast<const uint16_t*>(pre);
-  ga.u = ga.g + static_cast<size_t>(M) * F;
+  ga.val = static_cast<const uint16_t*>(pre);
+  ga.cross = ga.val + static_cast<size_t>(M) * F;
+  ga.ld = w.ld;
   ga.dg = w.dg;
   ga.du = w.du;
   ga.M = M;
   ga.F = F;
-  ga.act = p->activation;
   ga.fp16 = f16 ? 1 : 0;
   if (launch_gated_grad(ga, s) != cudaSuccess) return FLCE_ERR_CUDA;
+  cudaError_t e = cudaSuccess;
   if (dx && M <= small_most(false)) {
     SmallArgs sa;
-    if (!small_args(&sa, w.dg, F, M, F, 2, K, dx, K, false, f16, dev_err) ||
-        !k_major(&sa.x2, w.du, M, F, F, f16, small_tokens(M)) ||
+    if (!small_args(&sa, w.dg, w.ld, M, F, 2, K, dx, K, false, f16, dev_err) ||
+        !k_major(&sa.x2, w.du, M, F, w.ld, f16, small_tokens(M)) ||
         !mn_major(&sa.w, Wg, K, F, K, f16, kBK) || !mn_major(&sa.w2, Wu, K, F, K, f16, kBK) ||
         launch_small(false, true, sa, s) != cudaSuccess)
       return FLCE_ERR_CUDA;
@@ -512,9 +543,14 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
     ea.M = M;
     ea.K = K;
     PairArgs g = pair_args(M, K, F, 2, true, false, 6.f, f16, dev_err);
-    if (!out16(&ea.dx, dx, M, K, K) || !k_major(&g.a, w.dg, M, F, F, f16) ||
-        !k_major(&g.a2, w.du, M, F, F, f16) || !mn_major(&g.b, Wg, K, F, K, f16, pair_lk(g.halves)) ||
-        !mn_major(&g.b2, Wu, K, F, K, f16, pair_lk(g.halves)) || launch_grad_x(true, g, ea, sms, s) != cudaSuccess)
+    int64_t ld_g = K, ld_u = K;
+    const void* Wgn = spread(Wg, F, K, &ld_g, w.Wg, s, &e);
+    const void* Wun = spread(Wu, F, K, &ld_u, w.Wu, s, &e);
+    const int lk = pair_lk(g.halves);
+    if (!out16(&ea.dx, dx, M, K, K) || !k_major(&g.a, w.dg, M, F, w.ld, f16) ||
+        !k_major(&g.a2, w.du, M, F, w.ld, f16) || !mn_major(&g.b, Wgn, K, F, ld_g, f16, lk) ||
+        !mn_major(&g.b2, Wun, K, F, ld_u, f16, lk) || e != cudaSuccess ||
+        launch_grad_x(true, g, ea, sms, s) != cudaSuccess)
       return FLCE_ERR_CUDA;
   }
   if (dWg) {
@@ -527,10 +563,13 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
     const uint64_t row = static_cast<uint64_t>(K) * (p->dW_fp32 ? 4 : 2);
     PairArgs g = pair_args(2 * cdiv(F, 256) * 256, K, M, 1, true, false, 6.f, f16, dev_err);
     g.m_split = g.tiles_m / 2;
+    int64_t ld_x = pitch(p->ld_x, K);
+    const void* xn = spread(x, M, K, &ld_x, w.x, s, &e);
+    const int lk = pair_lk(g.halves);
     if (!encode_store_2d(&ea.out, dWg, K, F, row, p->dW_fp32 != 0) ||
         !encode_store_2d(&ea.out2, dWu, K, F, row, p->dW_fp32 != 0) ||
-        !mn_major(&g.a, w.dg, F, M, F, f16, pair_lk(g.halves)) || !mn_major(&g.a2, w.du, F, M, F, f16, pair_lk(g.halves)) ||
-        !mn_major(&g.b, x, K, M, pitch(p->ld_x, K), f16, pair_lk(g.halves)) ||
+        !mn_major(&g.a, w.dg, F, M, w.ld, f16, lk) || !mn_major(&g.a2, w.du, F, M, w.ld, f16, lk) ||
+        !mn_major(&g.b, xn, K, M, ld_x, f16, lk) || e != cudaSuccess ||
         launch_grad_w(true, g, ea, sms, s) != cudaSuccess)
       return FLCE_ERR_CUDA;
   }

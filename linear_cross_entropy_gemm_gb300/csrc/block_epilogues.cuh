@@ -6,8 +6,7 @@
 //   gated    g = x Wg^T, u = x Wu^T,  h = a(g) u
 //
 // Everything between the fp32 accumulator and the one rounding of each output
-// stays in fp32; the kept z, g and u are rounded copies for the backward pass,
-// and the forward's own output is computed from the unrounded values.
+// stays in fp32.
 #pragma once
 #include <cstdint>
 #include <type_traits>
@@ -123,6 +122,63 @@ __device__ __forceinline__ void act_all(int act, float (&v)[N]) {
   });
 }
 
+// ------------------------------------------------------- kept for the backward
+// The backward's error should be that of its own roundings, so what the forward keeps
+// in 16 bits per value has more significant bits than the operands' types.
+//
+// Linear: the slope a'(z), which lies in (-0.2, 1.2) for every activation, as a fixed
+// point number of 2^-15 steps from -0.25 (0 and 1 are exact; 65535: NaN).
+//
+// Gated: a(g) and u a'(g), whose range has no bound, in groups of 8 columns that share
+// an exponent: value = q 2^(eb - 140) 16384 / 16383, q a 15-bit integer, eb the exponent
+// field of the group's largest magnitude, at least 14. A value's word is 2 q + bit j of
+// eb, j its place in the group, so that a 16-byte load holds all it needs. eb = 255 (an
+// infinity or NaN in the group) reads as NaN. Off by at most 2^-14 of the largest.
+constexpr float kRound = 12582912.f;  // 1.5 * 2^23: x + kRound holds round(x) in its low bits
+
+// Codes of two slopes in one word.
+__device__ __forceinline__ uint32_t encode_slopes(float a, float b) {
+  const uint32_t x = __float_as_uint(fmaf(a, 32768.f, kRound + 8192.f));
+  const uint32_t y = __float_as_uint(fmaf(b, 32768.f, kRound + 8192.f));
+  return __byte_perm(x, y, 0x5410);
+}
+__device__ __forceinline__ float decode_slope(uint32_t code) {
+  const float q = __uint_as_float(0x4B000000u + code) - 8388608.f;
+  return code == 65535u ? __uint_as_float(0x7FFFFFFFu) : fmaf(q, 1.f / 32768.f, -0.25f);
+}
+
+__device__ __forceinline__ uint4 encode_group(const float* v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) m = max(m, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+  const uint32_t eb = max(m >> 23, 14u);
+  const float scale = __uint_as_float((267u - eb) << 23) * (16383.f / 16384.f);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t x = __float_as_uint(fmaf(v[2 * i], scale, kRound));
+    const uint32_t y = __float_as_uint(fmaf(v[2 * i + 1], scale, kRound));
+    const uint32_t t = eb >> (2 * i);
+    w[i] = ((__byte_perm(x, y, 0x5410) << 1) & 0xFFFEFFFEu) | (t & 1u) | ((t & 2u) << 15);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ void decode_group(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t eb = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) eb |= ((w[i] & 1u) | ((w[i] >> 15) & 2u)) << (2 * i);
+  const float inv = eb == 255u ? __uint_as_float(0x7FFFFFFFu)
+                               : __uint_as_float((eb - 13u) << 23) * (16384.f / 16383.f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t lo = static_cast<uint32_t>(static_cast<int32_t>(w[i] << 16) >> 17);
+    const uint32_t hi = static_cast<uint32_t>(static_cast<int32_t>(w[i]) >> 17);
+    v[2 * i] = (__uint_as_float(0x4B400000u + lo) - kRound) * inv;
+    v[2 * i + 1] = (__uint_as_float(0x4B400000u + hi) - kRound) * inv;
+  }
+}
+
 // A 16-bit [rows, cols] output: through a TMA store map of 32 x 32 boxes where
 // its rows start on 16-byte boundaries, else by plain stores.
 struct Out16 {
@@ -132,16 +188,8 @@ struct Out16 {
   int use_map;
 };
 
-// As tma_block_16 (epilogues.cuh: the box and its swizzle), through the two buffers
-// of the warp's staging.
-__device__ __forceinline__ void staged_block_16(const CUtensorMap* map, int x, int y,
-                                                const float (&v)[32], bool fp16, Staging& st,
-                                                int lane) {
-  if (lane == 0) bulk_wait_group_read1();
-  __syncwarp();
-  uint4* stage = reinterpret_cast<uint4*>(st.buf + st.turn * 2048);
-  st.turn ^= 1;
-  uint32_t w[16];
+// A row's 32 values (this lane's) of a 32 x 32 16-bit block, two to a word.
+__device__ __forceinline__ void pack_32(const float (&v)[32], bool fp16, uint32_t (&w)[16]) {
   if (fp16) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) w[j] = pack_f16x2(v[2 * j], v[2 * j + 1]);
@@ -149,6 +197,16 @@ __device__ __forceinline__ void staged_block_16(const CUtensorMap* map, int x, i
 #pragma unroll
     for (int j = 0; j < 16; ++j) w[j] = pack_bf16x2(v[2 * j], v[2 * j + 1]);
   }
+}
+
+// As tma_block_16 (epilogues.cuh: the box and its swizzle), through the two buffers
+// of the warp's staging.
+__device__ __forceinline__ void staged_block_16(const CUtensorMap* map, int x, int y,
+                                                const uint32_t (&w)[16], Staging& st, int lane) {
+  if (lane == 0) bulk_wait_group_read1();
+  __syncwarp();
+  uint4* stage = reinterpret_cast<uint4*>(st.buf + st.turn * 2048);
+  st.turn ^= 1;
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     stage[lane * 4 + (q ^ ((lane >> 1) & 3))] =
@@ -163,18 +221,24 @@ __device__ __forceinline__ void staged_block_16(const CUtensorMap* map, int x, i
 
 // One row (this lane's) of a warp's 32 x 32 block at (row0, col0). Warp-uniform
 // but for the values; rows and columns outside the output are clipped.
-__device__ __forceinline__ void put_block_16(const Out16& o, int rows, int cols, int row0, int col0,
-                                             const float (&v)[32], bool fp16, Staging& st,
-                                             int lane) {
+__device__ __forceinline__ void put_words(const Out16& o, int rows, int cols, int row0, int col0,
+                                          const uint32_t (&w)[16], Staging& st, int lane) {
   if (row0 >= rows || col0 >= cols) return;
   if (o.use_map) {
-    staged_block_16(&o.map, col0, row0, v, fp16, st, lane);
+    staged_block_16(&o.map, col0, row0, w, st, lane);
   } else if (row0 + lane < rows) {
     uint16_t* p = o.ptr + static_cast<size_t>(row0 + lane) * o.ld + col0;
 #pragma unroll
     for (int j = 0; j < 32; ++j)
-      if (col0 + j < cols) p[j] = to16(v[j], fp16);
+      if (col0 + j < cols) p[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
   }
+}
+__device__ __forceinline__ void put_block_16(const Out16& o, int rows, int cols, int row0, int col0,
+                                             const float (&v)[32], bool fp16, Staging& st,
+                                             int lane) {
+  uint32_t w[16];
+  pack_32(v, fp16, w);
+  put_words(o, rows, cols, row0, col0, w, st, lane);
 }
 
 // Two 16-bit values of a word.
@@ -234,9 +298,9 @@ struct LinearArgs {
   const uint16_t* res;   // [M, ld_res] or null; may be the output itself
   int64_t ld_res;
   int res_vec;           // the residual's rows start on 16-byte boundaries
-  int act, fp16, keep;   // keep: also write z
+  int act, fp16, keep;   // keep: also write the slopes
   int M, N;
-  Out16 y, z;
+  Out16 y, slope;
 };
 
 struct LinearEpi {
@@ -257,8 +321,21 @@ struct LinearEpi {
       float v[32];
       acc.load(acc_col, v);
       if (a.bias) add_row_16(a.bias + col0, a.N - col0, true, f16, v);
-      if (a.keep) put_block_16(a.z, a.M, a.N, row0, col0, v, f16, st, lane);
-      act_all(a.act, v);
+      if (a.keep) {
+        uint32_t w[16];
+        with_act(a.act, [&](auto act) {
+#pragma unroll
+          for (int j = 0; j < 32; j += 2) {
+            float s0, s1;
+            act_value_slope<decltype(act)::value>(v[j], v[j], s0);
+            act_value_slope<decltype(act)::value>(v[j + 1], v[j + 1], s1);
+            w[j >> 1] = encode_slopes(s0, s1);
+          }
+        });
+        put_words(a.slope, a.M, a.N, row0, col0, w, st, lane);
+      } else {
+        act_all(a.act, v);
+      }
       if (a.res && row < a.M)
         add_row_16(a.res + static_cast<size_t>(row) * a.ld_res + col0, a.N - col0, a.res_vec != 0,
                    f16, v);
@@ -269,9 +346,9 @@ struct LinearEpi {
 
 // ---------------------------------------------------------- gated: forward
 struct GatedArgs {
-  int act, fp16, keep;
+  int act, fp16, keep;  // keep: also write a(g) and u a'(g)
   int M, F;
-  Out16 h, g, u;
+  Out16 h, val, cross;
 };
 
 struct GatedEpi {
@@ -292,10 +369,37 @@ struct GatedEpi {
       acc.load(acc_col, g);
       acc.load(sl.up_off + acc_col, u);
       if (a.keep) {
-        put_block_16(a.g, a.M, a.F, row0, col0, g, f16, st, lane);
-        put_block_16(a.u, a.M, a.F, row0, col0, u, f16, st, lane);
+        float x[32];  // u a'(g)
+        with_act(a.act, [&](auto act) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) {
+            float slope;
+            act_value_slope<decltype(act)::value>(g[j], g[j], slope);
+            x[j] = u[j] * slope;
+          }
+        });
+        uint32_t w[16];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 c = encode_group(&g[8 * q]);
+          w[4 * q] = c.x;
+          w[4 * q + 1] = c.y;
+          w[4 * q + 2] = c.z;
+          w[4 * q + 3] = c.w;
+        }
+        put_words(a.val, a.M, a.F, row0, col0, w, st, lane);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint4 c = encode_group(&x[8 * q]);
+          w[4 * q] = c.x;
+          w[4 * q + 1] = c.y;
+          w[4 * q + 2] = c.z;
+          w[4 * q + 3] = c.w;
+        }
+        put_words(a.cross, a.M, a.F, row0, col0, w, st, lane);
+      } else {
+        act_all(a.act, g);
       }
-      act_all(a.act, g);
 #pragma unroll
       for (int j = 0; j < 32; ++j) g[j] *= u[j];
       put_block_16(a.h, a.M, a.F, row0, col0, g, f16, st, lane);
@@ -362,10 +466,13 @@ struct GradWEpi {
       if (col0 >= a.K || row0 >= a.N) break;  // uniform over the warp
       float v[32];
       acc.load(acc_col, v);
-      if (a.out16)
-        staged_block_16(out, col0, row0, v, a.fp16 != 0, st, lane);
-      else
+      if (a.out16) {
+        uint32_t w[16];
+        pack_32(v, a.fp16 != 0, w);
+        staged_block_16(out, col0, row0, w, st, lane);
+      } else {
         tma_block_f32(out, col0, row0, v, st.buf, lane);
+      }
     }
   }
 };

@@ -65,7 +65,7 @@ struct SmallArgs {
   CUtensorMap w, w2, x, x2;
   const uint16_t* bias;
   const uint16_t* res;
-  uint16_t* keep;  // z, or [2, M, N] (gated); null: not kept
+  uint16_t* keep;  // for the backward (block_epilogues.cuh): [M, N], or [2, M, N] (gated); or null
   uint16_t* y;
   int64_t ld_res, ld_y;
   int res_vec, y_vec;  // rows start on 16-byte boundaries
@@ -83,12 +83,12 @@ cudaError_t launch_small(bool two, bool w_mn, const SmallArgs& a, cudaStream_t s
 struct DzArgs {
   const uint16_t* dy;  // [M, ld_dy]
   int64_t ld_dy;
-  const uint16_t* z;   // [M, N] pre-activations, or null (activation "none")
+  const uint16_t* slope;  // [M, N] kept slopes, or null (activation "none")
   uint16_t* dz;        // [M, ld_dz], or null: column sums only
   int64_t ld_dz;
   float* part;         // [dz_parts(M, N), N] column sums of dz, or null
-  int M, N, act, fp16;
-  int vec;             // dy, z and dz rows start on 16-byte boundaries
+  int M, N, fp16;
+  int vec;             // dy, slope and dz rows start on 16-byte boundaries
 };
 int dz_parts(int64_t M, int64_t N);
 cudaError_t launch_dz(const DzArgs& a, cudaStream_t st);
@@ -98,12 +98,16 @@ cudaError_t launch_db_sum(const float* part, int parts, int N, void* db, bool fp
 struct GatedGradArgs {
   const uint16_t* dh;  // [M, ld_dh]
   int64_t ld_dh;
-  const uint16_t* g;   // [M, F]
-  const uint16_t* u;   // [M, F]
-  uint16_t* dg;        // [M, F]
-  uint16_t* du;        // [M, F]
-  int M, F, act, fp16;
+  const uint16_t* val;    // [M, F] kept a(g)
+  const uint16_t* cross;  // [M, F] kept u a'(g)
+  uint16_t* dg;           // [M, ld]
+  uint16_t* du;           // [M, ld]
+  int64_t ld;
+  int M, F, fp16;
 };
+// A copy of 16-bit rows to another pitch, all on 16-byte boundaries.
+cudaError_t launch_spread(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst,
+                          int rows, int cols, cudaStream_t st);
 cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t st);
 
 }  // namespace flce

@@ -2,6 +2,8 @@
 //   dz     : dz = dy a'(z) in the operands' type, with its fp32 column sums
 //            (the bias gradient's partials)
 //   gated  : dg = dh u a'(g), du = dh a(g)
+// a'(z), a(g) and u a'(g) are what the forward kept (block_epilogues.cuh): reading them
+// takes a few operations a value where recomputing an activation took thirty.
 #include <cuda_runtime.h>
 
 #include "block_epilogues.cuh"
@@ -60,43 +62,39 @@ __global__ void __launch_bounds__(32 * kDzRowGroups) dz_kernel(const DzArgs a, i
   const int vcol = col0 + cg * 8;
   if (vec && vcol + 8 <= a.N) {
     // Four rows at a time: their loads are in flight together.
-    with_act(a.z ? a.act : static_cast<int>(kActNone), [&](auto act) {
-      constexpr int kAct = decltype(act)::value;
-      for (int r = r_lo + rg; r < r_hi; r += 4 * kDzRowGroups) {
-        uint4 d[4], q[4];
+    const bool scaled = a.slope != nullptr;
+    for (int r = r_lo + rg; r < r_hi; r += 4 * kDzRowGroups) {
+      uint4 d[4], q[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = r + i * kDzRowGroups;
-          if (row >= r_hi) break;
-          d[i] = *reinterpret_cast<const uint4*>(a.dy + static_cast<size_t>(row) * a.ld_dy + vcol);
-          if constexpr (kAct != kActNone)
-            q[i] = __ldg(
-                reinterpret_cast<const uint4*>(a.z + static_cast<size_t>(row) * a.N + vcol));
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = r + i * kDzRowGroups;
-          if (row >= r_hi) break;
-          float v[8];
-          unpack8(d[i], f16, v);
-          if constexpr (kAct != kActNone) {
-            float z[8];
-            unpack8(q[i], f16, z);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              float val, slope;
-              act_value_slope<kAct>(z[j], val, slope);
-              v[j] *= slope;
-            }
-          }
-          if (a.dz)
-            *reinterpret_cast<uint4*>(a.dz + static_cast<size_t>(row) * a.ld_dz + vcol) =
-                pack8(v, f16);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sum[j] += v[j];
-        }
+      for (int i = 0; i < 4; ++i) {
+        const int row = r + i * kDzRowGroups;
+        if (row >= r_hi) break;
+        d[i] = *reinterpret_cast<const uint4*>(a.dy + static_cast<size_t>(row) * a.ld_dy + vcol);
+        if (scaled)
+          q[i] =
+              *reinterpret_cast<const uint4*>(a.slope + static_cast<size_t>(row) * a.N + vcol);
       }
-    });
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = r + i * kDzRowGroups;
+        if (row >= r_hi) break;
+        float v[8];
+        unpack8(d[i], f16, v);
+        if (scaled) {
+          const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[2 * j] *= decode_slope(w[j] & 0xFFFFu);
+            v[2 * j + 1] *= decode_slope(w[j] >> 16);
+          }
+        }
+        if (a.dz)
+          *reinterpret_cast<uint4*>(a.dz + static_cast<size_t>(row) * a.ld_dz + vcol) =
+              pack8(v, f16);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum[j] += v[j];
+      }
+    }
   } else {
     const int first = vec ? vcol : col0 + cg, step = vec ? 1 : 32;
     for (int r = r_lo + rg; r < r_hi; r += kDzRowGroups) {
@@ -105,14 +103,7 @@ __global__ void __launch_bounds__(32 * kDzRowGroups) dz_kernel(const DzArgs a, i
         const int c = first + j * step;
         if (c >= a.N) continue;
         float v = unpack_16(a.dy[static_cast<size_t>(r) * a.ld_dy + c], f16);
-        if (a.z) {
-          const float z = unpack_16(a.z[static_cast<size_t>(r) * a.N + c], f16);
-          with_act(a.act, [&](auto act) {
-            float val, slope;
-            act_value_slope<decltype(act)::value>(z, val, slope);
-            v *= slope;
-          });
-        }
+        if (a.slope) v *= decode_slope(a.slope[static_cast<size_t>(r) * a.N + c]);
         if (a.dz) a.dz[static_cast<size_t>(r) * a.ld_dz + c] = to16(v, f16);
         sum[j] += v;
       }
@@ -167,6 +158,27 @@ cudaError_t launch_db_sum(const float* part, int parts, int N, void* db, bool fp
                           part, parts, N, db, fp32 ? 1 : 0, fp16 ? 1 : 0);
 }
 
+// One thread takes 8 columns (rows * cols is below 65,536 here). A row's last columns are
+// never fewer: cols is a multiple of 8.
+__global__ void __launch_bounds__(256) spread_kernel(const uint16_t* src, int64_t ld_src,
+                                                     uint16_t* dst, int64_t ld_dst, int rows,
+                                                     int cols) {
+  griddep_launch();
+  griddep_wait();
+  const int c8 = cols / 8, i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= rows * c8) return;
+  const int row = i / c8, col = (i - row * c8) * 8;
+  *reinterpret_cast<uint4*>(dst + static_cast<size_t>(row) * ld_dst + col) =
+      *reinterpret_cast<const uint4*>(src + static_cast<size_t>(row) * ld_src + col);
+}
+
+cudaError_t launch_spread(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst,
+                          int rows, int cols, cudaStream_t st) {
+  const int n = rows * (cols / 8);
+  return launch_dependent(spread_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, 1,
+                          st, src, ld_src, dst, ld_dst, rows, cols);
+}
+
 // One thread takes 8 columns of one row: three 16-byte loads, two 16-byte
 // stores. Index: the 32- or 64-bit type that holds M F / 8.
 template <class Index>
@@ -183,19 +195,16 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradArgs a) 
   float d[8], g[8], u[8];
   unpack8(__ldg(reinterpret_cast<const uint4*>(a.dh + static_cast<size_t>(row) * a.ld_dh + col)),
           f16, d);
-  unpack8(__ldg(reinterpret_cast<const uint4*>(a.g + at)), f16, g);
-  unpack8(__ldg(reinterpret_cast<const uint4*>(a.u + at)), f16, u);
-  with_act(a.act, [&](auto act) {
+  decode_group(__ldg(reinterpret_cast<const uint4*>(a.cross + at)), g);
+  decode_group(__ldg(reinterpret_cast<const uint4*>(a.val + at)), u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      float val, slope;
-      act_value_slope<decltype(act)::value>(g[j], val, slope);
-      g[j] = d[j] * u[j] * slope;
-      u[j] = d[j] * val;
-    }
-  });
-  *reinterpret_cast<uint4*>(a.dg + at) = pack8(g, f16);
-  *reinterpret_cast<uint4*>(a.du + at) = pack8(u, f16);
+  for (int j = 0; j < 8; ++j) {
+    g[j] *= d[j];
+    u[j] *= d[j];
+  }
+  const size_t to = static_cast<size_t>(row) * a.ld + col;
+  *reinterpret_cast<uint4*>(a.dg + to) = pack8(g, f16);
+  *reinterpret_cast<uint4*>(a.du + to) = pack8(u, f16);
 }
 
 cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t st) {

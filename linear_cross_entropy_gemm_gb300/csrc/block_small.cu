@@ -157,15 +157,15 @@ __global__ void __launch_bounds__(kSmThreads)
       if (elect_one()) {
         mbar_arrive_expect_tx(&full[s], S::kStage);
         if constexpr (TWO) {
-          tma_load_plane(w, &a.w, &full[s], k0, f0, pol);
-          tma_load_plane(w + kWTileBytes / 2, &a.w2, &full[s], k0, f0, pol);
+          tma_load_2d(w, &a.w, &full[s], k0, f0, pol);
+          tma_load_2d(w + kWTileBytes / 2, &a.w2, &full[s], k0, f0, pol);
         } else if constexpr (!W_MN) {
-          tma_load_plane(w, mw, &full[s], k0, f0, pol);
+          tma_load_2d(w, mw, &full[s], k0, f0, pol);
         } else {
-          tma_load_plane(w, mw, &full[s], f0, k0, pol);
-          tma_load_plane(w + kMnBoxBytes, mw, &full[s], f0 + 64, k0, pol);
+          tma_load_2d(w, mw, &full[s], f0, k0, pol);
+          tma_load_2d(w + kMnBoxBytes, mw, &full[s], f0 + 64, k0, pol);
         }
-        tma_load_plane(w + kWTileBytes, second ? &a.x2 : &a.x, &full[s], k0, m0, pol);
+        tma_load_2d(w + kWTileBytes, second ? &a.x2 : &a.x, &full[s], k0, m0, pol);
       }
       __syncwarp();
       ++issued;
@@ -280,13 +280,25 @@ __global__ void __launch_bounds__(kSmThreads)
     }
     const size_t row = static_cast<size_t>(m0 + t);
     if constexpr (TWO) {
+      float (&u)[8] = v[kProducts - 1];
       if (a.keep) {
-        store8(a.keep + row * a.N + col, n, true, f16, v[0]);
-        store8(a.keep + (static_cast<size_t>(a.M) + row) * a.N + col, n, true, f16, v[1]);
-      }
-      act_all(a.act, v[0]);
+        float x[8];
+        with_act(a.act, [&](auto act) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[0][j] *= v[TWO ? 1 : 0][j];
+          for (int j = 0; j < 8; ++j) {
+            float slope;
+            act_value_slope<decltype(act)::value>(v[0][j], v[0][j], slope);
+            x[j] = u[j] * slope;
+          }
+        });
+        uint16_t* k = a.keep + row * a.N + col;
+        *reinterpret_cast<uint4*>(k) = encode_group(v[0]);
+        *reinterpret_cast<uint4*>(k + static_cast<size_t>(a.M) * a.N) = encode_group(x);
+      } else {
+        act_all(a.act, v[0]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[0][j] *= u[j];
     } else {
       if (a.bias) {
         float b[8];
@@ -294,8 +306,28 @@ __global__ void __launch_bounds__(kSmThreads)
 #pragma unroll
         for (int j = 0; j < 8; ++j) v[0][j] += b[j];
       }
-      if (a.keep) store8(a.keep + row * a.N + col, n, a.N % 8 == 0, f16, v[0]);
-      act_all(a.act, v[0]);
+      if (a.keep) {
+        uint32_t w[4];
+        with_act(a.act, [&](auto act) {
+#pragma unroll
+          for (int j = 0; j < 8; j += 2) {
+            float s0, s1;
+            act_value_slope<decltype(act)::value>(v[0][j], v[0][j], s0);
+            act_value_slope<decltype(act)::value>(v[0][j + 1], v[0][j + 1], s1);
+            w[j >> 1] = encode_slopes(s0, s1);
+          }
+        });
+        uint16_t* k = a.keep + row * a.N + col;
+        if (a.N % 8 == 0) {
+          *reinterpret_cast<uint4*>(k) = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            if (j < n) k[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+        }
+      } else {
+        act_all(a.act, v[0]);
+      }
       if (a.res) {
         float r[8];
         load8(a.res + row * a.ld_res + col, n, a.res_vec != 0, f16, r);

@@ -87,28 +87,6 @@ __device__ __forceinline__ void bulk_wait_group_read1() {
   asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
 }
 
-// The layer operators' load maps have a third dimension of two planes, the second never
-// read, that lies at least 128 KiB past the first: loads through a map whose tensor
-// spans less than that ran up to ten times slower when many SMs shared it
-// (measured with the same boxes and bytes: 94 us at 15 rows of 8 KiB, 20 us at 16).
-__device__ __forceinline__ void tma_load_plane(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
-                                               int32_t x, int32_t y, uint64_t l2_hint) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
-      " [%0], [%1, {%3, %4, %6}], [%2], %5;" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "l"(l2_hint), "r"(0)
-      : "memory");
-}
-__device__ __forceinline__ void tma_load_plane_pair(void* smem_dst, const CUtensorMap* map,
-                                                    uint32_t bar_cluster_addr, int32_t x, int32_t y,
-                                                    uint64_t l2_hint) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
-      ".L2::cache_hint [%0], [%1, {%3, %4, %6}], [%2], %5;" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster_addr), "r"(x), "r"(y), "l"(l2_hint), "r"(0)
-      : "memory");
-}
-
 // One lane of a converged warp, known to the compiler as such.
 __device__ __forceinline__ bool elect_one() {
   uint32_t ok;
@@ -330,11 +308,11 @@ __global__ void __launch_bounds__(kLThreads, 1)
           if constexpr (!kAMN) {
 #pragma unroll
             for (int j = 0; j < S::kLK / 64; ++j)
-              tma_load_plane_pair(a + j * 128 * 128, pa, fb, k0 + j * 64, m0, pol);
+              tma_load_2d_pair(a + j * 128 * 128, pa, fb, k0 + j * 64, m0, pol);
           } else {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
-              tma_load_plane_pair(a + j * 128 * S::kLK, pa, fb, m0 + j * 64, k0, pol);
+              tma_load_2d_pair(a + j * 128 * S::kLK, pa, fb, m0 + j * 64, k0, pol);
           }
 #pragma unroll
           for (int h = 0; h < HALVES; ++h) {
@@ -344,12 +322,12 @@ __global__ void __launch_bounds__(kLThreads, 1)
             if constexpr (!kBMN) {
 #pragma unroll
               for (int j = 0; j < S::kLK / 64; ++j)
-                tma_load_plane_pair(b + j * 128 * 128, pb, fb, k0 + j * 64, nh, pol);
+                tma_load_2d_pair(b + j * 128 * 128, pb, fb, k0 + j * 64, nh, pol);
             } else {
 #pragma unroll
               for (int j = 0; j < 2; ++j)
                 if (j < b_boxes)
-                  tma_load_plane_pair(b + j * 128 * S::kLK, pb, fb, nh + j * 64, k0, pol);
+                  tma_load_2d_pair(b + j * 128 * S::kLK, pb, fb, nh + j * 64, k0, pol);
             }
           }
         }
@@ -409,8 +387,10 @@ __global__ void __launch_bounds__(kLThreads, 1)
           }
         }
         if (!ok) break;
-        if (elect_one()) umma_commit_pair(&tfull[acc], both);
-        __syncwarp();
+        if constexpr (!SPLIT) {
+          if (elect_one()) umma_commit_pair(&tfull[acc], both);
+          __syncwarp();
+        }
         if (++acc == S::kAccs) {
           acc = 0;
           aph ^= 1;

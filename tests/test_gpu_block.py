@@ -57,13 +57,14 @@ def check_linear(M, K, N, act, dtype=BF16, bias=True, res=True, dW_dtype=FP32, d
     pre = torch.full((M, N), float("nan"), dtype=dtype, device="cuda")
     y = F.flce_linear_forward(x, W, b, r, activation=act, pre=pre)
     lean = F.flce_linear_forward(x, W, b, r, activation=act)
-    z_ref, y_ref = R.linear(x, W, b, r, act)
+    s_ref, y_ref = R.linear(x, W, b, r, act)
+    slope = R.kept_slopes(pre)
     R.assert_within(y, y_ref, "y")
-    R.assert_within(pre, z_ref, "z")
+    R.assert_within(slope, s_ref, "kept slopes")
     assert torch.equal(y, lean)
     dx, dW, db = F.flce_linear_backward(dy, x, W, b, activation=act, pre=pre, dW_dtype=dW_dtype,
                                         db_dtype=db_dtype)
-    want = R.linear_grad(dy, x, W, pre, act, dW_dtype, db_dtype)
+    want = R.linear_grad(dy, x, W, slope if act != "none" else None, dW_dtype, db_dtype)
     R.assert_within(dx, want[0], "dx")
     R.assert_within(dW, want[1], "dW")
     if bias:
@@ -190,6 +191,35 @@ def test_a_bad_token_stays_in_its_row(M):
     bad[1, 3] = float("nan")
     y = F.flce_linear_backward(bad, x, W, b)[0]
     assert torch.equal(y[keep], dx[keep]) and bool(y[1].isnan().all())
+    pre, bad_pre = (torch.empty(2, M, 136, dtype=BF16, device="cuda") for _ in range(2))
+    bad = x.clone()
+    bad[1, 5] = float("inf")
+    F.flce_gated_forward(x, W, W, pre=pre)
+    F.flce_gated_forward(bad, W, W, pre=bad_pre)
+    dx = F.flce_gated_backward(dy, x, W, W, pre)[0]
+    y, dWg, dWu = F.flce_gated_backward(dy, bad, W, W, bad_pre)
+    assert torch.equal(y[keep], dx[keep]) and not bool(y[1].isfinite().any())
+    assert not bool(dWg.isfinite().any()) and not bool(dWu.isfinite().any())
+    F.flce_linear_forward(bad, W, b, activation="silu", pre=pre[0])
+    dW = F.flce_linear_backward(dy, bad, W, b, activation="silu", pre=pre[0])[1]
+    assert not bool(dW.isfinite().all())
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -60, 2.0 ** -20, 2.0 ** 20, 2.0 ** 60])
+@pytest.mark.parametrize("M", [5, 200])
+def test_kept_groups_keep_their_precision_at_any_size(M, scale):
+    """u from tiny to huge: the kept u a'(g) stays within 2^-14 of its group's largest."""
+    x, Wg, Wu, dh = gated_problem(M, 64, 72, BF16)
+    Wu = (Wu.double() * scale).to(BF16)
+    pre = torch.empty(2, M, 72, dtype=BF16, device="cuda")
+    h = F.flce_gated_forward(x, Wg, Wu, pre=pre)
+    v_ref, c_ref, h_ref = R.gated(x, Wg, Wu, "silu")
+    R.assert_within(h, h_ref, "h")
+    R.assert_within(R.kept_groups(pre[1]), c_ref, "kept u a'(g)")
+    got = F.flce_gated_backward(dh, x, Wg, Wu, pre)
+    for a, want in zip(got, R.gated_grad(dh, x, Wg, Wu, R.kept_groups(pre[0]),
+                                         R.kept_groups(pre[1]), FP32)):
+        R.assert_within(a, want, "gradient")
 
 
 @pytest.mark.parametrize("act", ACTS)
@@ -202,13 +232,14 @@ def test_activation_range(act):
     W = torch.eye(8, dtype=BF16, device="cuda")
     pre = torch.empty_like(x)
     y = F.flce_linear_forward(x, W, activation=act, pre=pre)
-    assert torch.equal(pre, x)
     want, slope = R.act(x.double(), act)
+    R.assert_within(R.kept_slopes(pre), (slope, torch.full_like(slope, 2.0 ** -15 + 4 * R.ACT)),
+                    "kept slopes")
     bound = R.rounded(want, R.ACT * (x.double().abs() + 1), BF16)
     R.assert_within(y, (want, bound), "y")
     dy = torch.ones_like(x)
     dx = F.flce_linear_backward(dy, x, W, activation=act, pre=pre, needs=(True, False, False))[0]
-    R.assert_within(dx, (slope, R.rounded(slope, torch.full_like(slope, 8 * R.ACT), BF16)), "a'")
+    R.assert_within(dx, (slope, R.rounded(slope, torch.full_like(slope, 2.0 ** -15 + 4 * R.ACT), BF16)), "a'")
 
 
 # -------------------------------------------------------------------- gated
@@ -224,12 +255,13 @@ def check_gated(M, K, N, act, dtype=BF16, dW_dtype=FP32):
     pre = torch.full((2, M, N), float("nan"), dtype=dtype, device="cuda")
     h = F.flce_gated_forward(x, Wg, Wu, activation=act, pre=pre)
     assert torch.equal(h, F.flce_gated_forward(x, Wg, Wu, activation=act))
-    g_ref, u_ref, h_ref = R.gated(x, Wg, Wu, act)
-    R.assert_within(pre[0], g_ref, "g")
-    R.assert_within(pre[1], u_ref, "u")
+    v_ref, c_ref, h_ref = R.gated(x, Wg, Wu, act)
+    val, cross = R.kept_groups(pre[0]), R.kept_groups(pre[1])
+    R.assert_within(val, v_ref, "kept a(g)")
+    R.assert_within(cross, c_ref, "kept u a'(g)")
     R.assert_within(h, h_ref, "h")
     got = F.flce_gated_backward(dh, x, Wg, Wu, pre, activation=act, dW_dtype=dW_dtype)
-    for a, want, what in zip(got, R.gated_grad(dh, x, Wg, Wu, pre, act, dW_dtype),
+    for a, want, what in zip(got, R.gated_grad(dh, x, Wg, Wu, val, cross, dW_dtype),
                              ("dx", "dWg", "dWu")):
         R.assert_within(a, want, what)
     no_device_error()
@@ -278,8 +310,9 @@ def directional(f, t, d, h=1e-4):
 @pytest.mark.parametrize("act", ["gelu", "gelu_tanh", "silu", "sigmoid"])
 def test_gradients_against_differences(M, act):
     """<gradient, direction> against a central difference of the 64-bit definition.
-    The kept z, g and u are rounded (u of their size, times |a''| <= 1), the
-    gradients too; h^2 times the third derivative is far below that."""
+    The kept slopes are off by 2^-15, the kept groups by 2^-14 of their largest; dz, dg, du
+    and the gradients are rounded to u of their size. h^2 times the third derivative is
+    far below that."""
     g = gen(M)
     x, W, b, r, dy = linear_problem(M, 72, 88, BF16, True, True)
 
@@ -290,9 +323,8 @@ def test_gradients_against_differences(M, act):
     pre = torch.empty(M, 88, dtype=BF16, device="cuda")
     F.flce_linear_forward(x, W, b, r, activation=act, pre=pre)
     grads = F.flce_linear_backward(dy, x, W, b, activation=act, pre=pre)
-    z = x64 @ W64.t() + b64
     u = R.UNIT[BF16]
-    dz_off = (u * z.abs() + 2 * u) * dy.double().abs() * 1.2
+    dz_off = (1.2 * u + 2.0 ** -14) * dy.double().abs()
     offs = (dz_off @ W64.abs(), dz_off.t() @ x64.abs(), dz_off.sum(0))
     for i, (t, off) in enumerate(zip((x64, W64, b64), offs)):
         d = torch.randn(t.shape, generator=g, device="cuda", dtype=torch.float64)
@@ -313,9 +345,10 @@ def test_gradients_against_differences(M, act):
     pre = torch.empty(2, M, 88, dtype=BF16, device="cuda")
     F.flce_gated_forward(x, W, Wu, activation=act, pre=pre)
     grads = F.flce_gated_backward(dy, x, W, Wu, pre, activation=act)
-    gate, up = x64 @ W64.t(), x64 @ Wu64.t()
-    dg_off = (u * gate.abs() + 3 * u) * (dy.double() * up).abs() * 1.2
-    du_off = (u * gate.abs() * 1.2 + 2 * u * (gate.abs() + 1)) * dy.double().abs()
+    val, cross = R.kept_groups(pre[0]), R.kept_groups(pre[1])
+    d, none = dy.double().abs(), torch.zeros_like(val)
+    dg_off = d * (u * cross.abs() + 2 * R.group_off(cross, none))
+    du_off = d * (u * val.abs() + 2 * R.group_off(val, none))
     offs = (dg_off @ W64.abs() + du_off @ Wu64.abs(), dg_off.t() @ x64.abs(),
             du_off.t() @ x64.abs())
     for i, (t, off) in enumerate(zip((x64, W64, Wu64), offs)):
