@@ -397,7 +397,8 @@ typedef struct {
 } flce_linear_params_t;
 
 /* Workspace bytes: which = 0 forward, 1 backward. 0 for invalid parameters, for
- * M == 0, and for calls that need none (workspace may then be NULL). */
+ * M == 0, and for calls that need none (workspace may then be NULL). A forward needs
+ * some where an operand's pitch makes a repacked copy pay. */
 size_t flce_linear_workspace_size(const flce_linear_params_t* p, int which);
 
 /* Forward. W: [N, K] dense. y: [M, N]; it may be the residual's own buffer (with

@@ -89,13 +89,6 @@ bool mn_major(CUtensorMap* m, const void* p, int64_t rows, int64_t k, int64_t ld
                    f16);
 }
 
-// Products of at most this many tokens go to the few-token kernel (measured: 128 tokens
-// through 4096 x 4096 12.4 us against 15.3 us, 256 17.7 against 15.3; gated 4096 x 14336,
-// 64 tokens 48 us against 51 us, 128 54 against 51).
-constexpr int64_t kSmallTokens = 128, kSmallGatedTokens = 64;
-
-int64_t small_most(bool gated) { return gated ? kSmallGatedTokens : kSmallTokens; }
-
 // The parts of a few-token product's arguments that do not depend on the operator.
 // x: [M, k] with pitch ld_x; the sum runs over `segments` times k.
 bool small_args(SmallArgs* a, const void* x, int64_t ld_x, int64_t M, int64_t k, int segments,
@@ -111,7 +104,10 @@ bool small_args(SmallArgs* a, const void* x, int64_t ld_x, int64_t M, int64_t k,
   a->k_blocks = segments * a->k_split;
   a->slices = small_slices(M, N, a->k_blocks, two);
   a->dev_err = reinterpret_cast<int*>(dev_err);
-  return k_major(&a->x, x, M, k, ld_x, f16, small_tokens(M));
+  a->xp = static_cast<const uint16_t*>(x);
+  a->ld_x = ld_x;
+  a->k_len = static_cast<int>(k);
+  return small_tokens(M) <= 32 || k_major(&a->x, x, M, k, ld_x, f16, small_tokens(M));
 }
 
 // ------------------------------------------------- tile width of a pair GEMM
@@ -181,6 +177,28 @@ const TileShape& best_tile(bool mn, int64_t M, int64_t N, int64_t k64, bool two_
   return *best;
 }
 
+// Products of at most this many tokens go to the few-token kernel (measured: 128 tokens
+// through 4096 x 4096 12.4 us against 15.3 us, 256 17.7 against 15.3; gated 4096 x 14336,
+// 64 tokens 48 us against 51 us, 128 54 against 51).
+constexpr int64_t kSmallTokens = 128, kSmallGatedTokens = 64;
+
+int64_t small_most(bool gated) { return gated ? kSmallGatedTokens : kSmallTokens; }
+
+// And larger ones with few tiles of a long sum, which that kernel cuts into eight slices:
+// 267 x 376 x 12800 25 us by CTA pairs (four tiles, three slices), 13 us. Its ns: 270 for
+// 64 sum elements of a 128-token tile, measured at 256 x 4096 x 14336, and the join.
+constexpr float kSmallNs = 270.f, kSmallJoinNs = 1500.f;
+bool few_tokens(bool mn, int64_t M, int64_t N, int64_t k64, bool two_b) {
+  if (M <= small_most(two_b)) return true;
+  const int64_t nt = small_tokens(M), out = two_b ? 64 : 128;
+  const int slices = small_slices(M, N, static_cast<int>(k64), two_b);
+  const int64_t ctas = (N + out - 1) / out * ((M + nt - 1) / nt) * slices;
+  if (ctas > 152) return false;
+  const float ns = static_cast<float>((k64 + slices - 1) / slices) * kSmallNs + kSmallJoinNs;
+  const TileShape& t = best_tile(mn, M, N, k64, two_b, 6.f);
+  return ns < tile_ns(t, mn, (M + 255) / 256, N, k64, two_b, 6.f);
+}
+
 // ns that an epilogue takes per output column of a 256-row tile (measured: 1.5 us for
 // 256 stored columns, 6.5 us with gelu and a kept z).
 float epilogue_ns(int act, bool keep, bool two_b) {
@@ -214,68 +232,150 @@ PairArgs pair_args(int M, int N, int K, int segments, bool mn, bool two_b, float
 
 flce_status_t done(cudaError_t e) { return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA; }
 
-// Loads through a TMA map whose tensor spans less than 128 KiB run up to several times
-// slower when many SMs share it (measured with the same boxes and bytes: 94 us with 15
-// rows of 8 KiB, 20 us with 16; a dW of 8 x 4096 over 2048 tokens 32 us, 17 us with both
-// operands spread). The backward's GEMMs therefore take such an operand from a copy
-// whose rows lie far enough apart: the row pitch, in elements, and the copy's bytes.
+// ----------------------------------------------- operands in scratch memory
+// The pair GEMM takes an operand from a repacked copy where its own pitch costs more
+// than the copy:
+//   - Loads through a TMA map whose tensor spans less than 128 KiB run up to several times
+//     slower when many SMs share it (measured with the same boxes and bytes: 94 us with
+//     15 rows of 8 KiB, 20 us with 16; a dW of 8 x 4096 over 2048 tokens 32 us, 13 us with
+//     both operands spread): the copy's rows lie far enough apart.
+//   - Rows that start between 32-byte sectors (a pitch of 8 elements modulo 16) cost an
+//     operand about a third of the product's time: 2048 x 4096 x 4104 70 us, 54 us with
+//     x repacked, against 42 us at 4096. (A pitch of 16 modulo 32 costs a tenth: left.)
 constexpr int64_t kSpreadElems = 131072 / 2;  // from a tensor's first element to its last
+constexpr int64_t kManyTiles = 32;            // SMs enough to slow a narrow tensor's loads
+constexpr float kOddRowsShare = 0.3f;
+constexpr float kCopyNs = 2500.f, kCopyBytesNs = 5500.f;  // a launch; bytes read and written a ns
+
 bool is_narrow(int64_t rows, int64_t cols, int64_t ld) {
   return rows > 1 && (rows - 1) * ld + cols < kSpreadElems;
 }
-int64_t spread_ld(int64_t rows, int64_t cols) {
-  const int64_t ld = (kSpreadElems - cols + rows - 2) / (rows - 1);
-  return ((ld > cols ? ld : cols) + 7) / 8 * 8;
+// A pitch for rows in scratch memory: whole 128-byte lines, and not narrow.
+int64_t scratch_ld(int64_t rows, int64_t cols) {
+  int64_t ld = (cols + 63) / 64 * 64;
+  if (is_narrow(rows, cols, ld)) {
+    const int64_t apart = (kSpreadElems - cols + rows - 2) / (rows - 1);
+    ld = (apart + 63) / 64 * 64;
+  }
+  return ld;
 }
-size_t spread_size(int64_t rows, int64_t cols) {
-  return is_narrow(rows, cols, cols) ? static_cast<size_t>(rows * spread_ld(rows, cols)) : 0;
+// A product that reads an operand: what it takes, and its tiles.
+struct Product {
+  float ns;
+  int64_t tiles;
+};
+// The pitch of a repacked copy of [rows, cols] with pitch ld; 0: read it as it is.
+int64_t repack_ld(int64_t rows, int64_t cols, int64_t ld, const Product& by) {
+  const bool narrow = by.tiles >= kManyTiles && is_narrow(rows, cols, ld);
+  const float copy = kCopyNs + 4.f * static_cast<float>(rows) * static_cast<float>(cols) / kCopyBytesNs;
+  const bool odd = rows > 1 && ld % 16 != 0 && kOddRowsShare * by.ns > copy;
+  return narrow || odd ? scratch_ld(rows, cols) : 0;
+}
+Product product_of(bool mn, int64_t M, int64_t N, int64_t k64, bool two_b) {
+  const TileShape& t = best_tile(mn, M, N, k64, two_b, 6.f);
+  const int cols = pair_cols(two_b ? kTwoB : kOneEach, t.halves, t.bn);
+  return {tile_ns(t, mn, (M + 255) / 256, N, k64, two_b, 6.f),
+          (M + 255) / 256 * ((N + cols - 1) / cols) * t.slices};
 }
 
-// p [rows, cols] with pitch *ld, or its spread copy in `copy` where it is narrow.
-const void* spread(const void* p, int64_t rows, int64_t cols, int64_t* ld, uint16_t* copy,
-                   cudaStream_t s, cudaError_t* e) {
-  if (*e != cudaSuccess || !copy || !is_narrow(rows, cols, *ld)) return p;
-  const int64_t to = spread_ld(rows, cols);
-  *e = launch_spread(static_cast<const uint16_t*>(p), *ld, copy, to, static_cast<int>(rows),
+// p [rows, cols] with pitch *ld, or its copy in `buf` with the pitch `to` (0: none).
+const void* repacked(const void* p, int64_t rows, int64_t cols, int64_t* ld, int64_t to,
+                     uint16_t* buf, cudaStream_t s, cudaError_t* e) {
+  if (*e != cudaSuccess || to == 0) return p;
+  *e = launch_repack(static_cast<const uint16_t*>(p), *ld, buf, to, static_cast<int>(rows),
                      static_cast<int>(cols), s);
   *ld = to;
-  return copy;
+  return buf;
 }
 
-// Backward scratch of the linear layer: dz where it is not dy itself, the bias
-// gradient's partial sums, and the spread copies of narrow operands.
+// The bytes of a workspace that `c` has carved, at whatever address it lies.
+size_t bytes_of(const Carver& c) { return c.cur - (c.base + kAlign - 1) / kAlign * kAlign + kAlign; }
+
+uint16_t* take_rows(Carver* c, int64_t rows, int64_t ld) {
+  return ld > 0 ? c->take<uint16_t>(static_cast<size_t>(rows) * static_cast<size_t>(ld)) : nullptr;
+}
+
+// Scratch of the linear layer. Forward: repacked x and W. Backward: dz where it is not dy
+// itself, the bias gradient's partial sums, and x and W repacked. The pitches (0: no
+// copy) depend on the parameters alone.
 struct LinearWs {
   uint16_t *dz, *x, *W;
   float* part;
-  int64_t ld_dz;
+  int64_t ld_dz, ld_x, ld_w;
+  bool repack_dy;  // dy is better copied, even where dz is dy
+  bool few;        // forward, dx: by the few-token kernel
 };
-size_t carve(const flce_linear_params_t* p, void* base, LinearWs* w) {
+size_t carve_forward(const flce_linear_params_t* p, void* base, LinearWs* w) {
+  std::memset(w, 0, sizeof(*w));
+  const int64_t k64 = (p->K + 63) / 64;
+  if ((w->few = few_tokens(false, p->M, p->N, k64, false))) return 0;
+  const Product by = product_of(false, p->M, p->N, k64, false);
+  w->ld_x = repack_ld(p->M, p->K, pitch(p->ld_x, p->K), by);
+  w->ld_w = repack_ld(p->N, p->K, p->K, by);
+  if (w->ld_x == 0 && w->ld_w == 0) return 0;
   Carver c(base, 0);
-  w->ld_dz = is_narrow(p->M, p->N, p->N) ? spread_ld(p->M, p->N) : (p->N + 7) / 8 * 8;
+  w->x = take_rows(&c, p->M, w->ld_x);
+  w->W = take_rows(&c, p->N, w->ld_w);
+  return bytes_of(c);
+}
+size_t carve(const flce_linear_params_t* p, void* base, LinearWs* w) {
+  std::memset(w, 0, sizeof(*w));
+  const int64_t n64 = (p->N + 63) / 64;
+  w->few = few_tokens(true, p->M, p->K, n64, false);
+  const Product dx = w->few ? Product{0.f, 0} : product_of(true, p->M, p->K, n64, false);
+  const Product dw = product_of(true, p->N, p->K, (p->M + 63) / 64, false);
+  w->ld_w = repack_ld(p->N, p->K, p->K, dx);
+  w->ld_x = repack_ld(p->M, p->K, pitch(p->ld_x, p->K), dw);
+  w->ld_dz = scratch_ld(p->M, p->N);
+  w->repack_dy = repack_ld(p->M, p->N, pitch(p->ld_y, p->N),
+                           {dx.ns + dw.ns, std::max(dx.tiles, dw.tiles)}) != 0;
+  Carver c(base, 0);
   // dy off the 16-byte boundaries also needs a copy: sized for it, since the
   // pointer is not known here.
-  w->dz = c.take<uint16_t>(static_cast<size_t>(p->M) * w->ld_dz);
+  w->dz = take_rows(&c, p->M, w->ld_dz);
   w->part = p->has_bias ? c.take<float>(static_cast<size_t>(dz_parts(p->M, p->N)) * p->N) : nullptr;
-  const size_t nx = spread_size(p->M, p->K), nw = spread_size(p->N, p->K);
-  w->x = nx ? c.take<uint16_t>(nx) : nullptr;
-  w->W = nw ? c.take<uint16_t>(nw) : nullptr;
-  return c.used() + kAlign;
+  w->x = take_rows(&c, p->M, w->ld_x);
+  w->W = take_rows(&c, p->N, w->ld_w);
+  return bytes_of(c);
 }
 
+// Scratch of the gated projection. Forward: repacked x, Wg and Wu. Backward: dg and du,
+// and the operands repacked.
 struct GatedWs {
   uint16_t *dg, *du, *x, *Wg, *Wu;
-  int64_t ld;  // of dg and du
+  int64_t ld, ld_x, ld_w;  // ld: of dg and du
+  bool few;                // forward, dx: by the few-token kernel
 };
-size_t carve(const flce_gated_params_t* p, void* base, GatedWs* w) {
+size_t carve_forward(const flce_gated_params_t* p, void* base, GatedWs* w) {
+  std::memset(w, 0, sizeof(*w));
+  const int64_t k64 = (p->K + 63) / 64;
+  if ((w->few = few_tokens(false, p->M, p->F, k64, true))) return 0;
+  const Product by = product_of(false, p->M, p->F, k64, true);
+  w->ld_x = repack_ld(p->M, p->K, pitch(p->ld_x, p->K), by);
+  w->ld_w = repack_ld(2 * p->F, p->K, p->K, by) != 0 ? scratch_ld(p->F, p->K) : 0;
+  if (w->ld_x == 0 && w->ld_w == 0) return 0;
   Carver c(base, 0);
-  w->ld = is_narrow(p->M, p->F, p->F) ? spread_ld(p->M, p->F) : p->F;
-  w->dg = c.take<uint16_t>(static_cast<size_t>(p->M) * w->ld);
-  w->du = c.take<uint16_t>(static_cast<size_t>(p->M) * w->ld);
-  const size_t nx = spread_size(p->M, p->K), nw = spread_size(p->F, p->K);
-  w->x = nx ? c.take<uint16_t>(nx) : nullptr;
-  w->Wg = nw ? c.take<uint16_t>(nw) : nullptr;
-  w->Wu = nw ? c.take<uint16_t>(nw) : nullptr;
-  return c.used() + kAlign;
+  w->x = take_rows(&c, p->M, w->ld_x);
+  w->Wg = take_rows(&c, p->F, w->ld_w);
+  w->Wu = take_rows(&c, p->F, w->ld_w);
+  return bytes_of(c);
+}
+size_t carve(const flce_gated_params_t* p, void* base, GatedWs* w) {
+  std::memset(w, 0, sizeof(*w));
+  const int64_t f64 = 2 * ((p->F + 63) / 64);
+  w->few = few_tokens(true, p->M, p->K, f64, false);
+  const Product dx = w->few ? Product{0.f, 0} : product_of(true, p->M, p->K, f64, false);
+  const Product dw = product_of(true, 2 * p->F, p->K, (p->M + 63) / 64, false);
+  w->ld = scratch_ld(p->M, p->F);
+  w->ld_w = repack_ld(2 * p->F, p->K, p->K, dx) != 0 ? scratch_ld(p->F, p->K) : 0;
+  w->ld_x = repack_ld(p->M, p->K, pitch(p->ld_x, p->K), dw);
+  Carver c(base, 0);
+  w->dg = take_rows(&c, p->M, w->ld);
+  w->du = take_rows(&c, p->M, w->ld);
+  w->x = take_rows(&c, p->M, w->ld_x);
+  w->Wg = take_rows(&c, p->F, w->ld_w);
+  w->Wu = take_rows(&c, p->F, w->ld_w);
+  return bytes_of(c);
 }
 
 bool zero(void* p, size_t bytes, cudaStream_t s) {
@@ -287,9 +387,9 @@ bool zero(void* p, size_t bytes, cudaStream_t s) {
 extern "C" {
 
 size_t flce_linear_workspace_size(const flce_linear_params_t* p, int which) {
-  if (check(p) != FLCE_OK || p->M == 0 || which != 1) return 0;
+  if (check(p) != FLCE_OK || p->M == 0 || which < 0 || which > 1) return 0;
   LinearWs w;
-  return carve(p, nullptr, &w);
+  return which == 0 ? carve_forward(p, nullptr, &w) : carve(p, nullptr, &w);
 }
 
 flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, const void* W,
@@ -297,8 +397,6 @@ flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, 
                                   void* workspace, size_t workspace_bytes, int32_t* dev_err,
                                   void* stream) {
   NvtxRange nvtx_range("flce_linear_forward");
-  (void)workspace;
-  (void)workspace_bytes;
   flce_status_t st = check(p);
   if (st != FLCE_OK) return st;
   if (p->M == 0) return FLCE_OK;
@@ -307,11 +405,15 @@ flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, 
   if (!aligned16(x) || !aligned16(W) || (p->has_bias && !aligned16(b)) || !aligned16(pre) ||
       !aligned2(y) || (p->has_residual && !aligned2(residual)))
     return FLCE_ERR_ALIGNMENT;
+  LinearWs w;
+  const size_t need = carve_forward(p, workspace, &w);
+  if (need > 0 && !workspace) return FLCE_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0;
   if ((st = device_info(&sms)) != FLCE_OK) return st;
   const bool f16 = p->input_fp16 != 0;
   const int M = static_cast<int>(p->M), K = static_cast<int>(p->K), N = static_cast<int>(p->N);
-  if (M <= small_most(false)) {
+  if (w.few) {
     SmallArgs sa;
     if (!small_args(&sa, x, pitch(p->ld_x, K), M, K, 1, N, y, pitch(p->ld_y, N), false, f16, dev_err) ||
         !k_major(&sa.w, W, N, K, K, f16))
@@ -338,10 +440,16 @@ flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, 
   ea.N = N;
   PairArgs g = pair_args(M, N, K, 1, false, false,
                          epilogue_ns(p->activation, pre != nullptr, false), f16, dev_err);
-  if (!out16(&ea.y, y, M, N, pitch(p->ld_y, N)) || (pre && !out16(&ea.slope, pre, M, N, N)) ||
-      !k_major(&g.a, x, M, K, pitch(p->ld_x, K), f16) || !k_major(&g.b, W, N, K, K, f16, g.bn / 2))
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  int64_t ld_x = pitch(p->ld_x, K), ld_w = K;
+  const void* xn = repacked(x, M, K, &ld_x, w.ld_x, w.x, s, &e);
+  const void* Wn = repacked(W, N, K, &ld_w, w.ld_w, w.W, s, &e);
+  if (e != cudaSuccess || !out16(&ea.y, y, M, N, pitch(p->ld_y, N)) ||
+      (pre && !out16(&ea.slope, pre, M, N, N)) || !k_major(&g.a, xn, M, K, ld_x, f16) ||
+      !k_major(&g.b, Wn, N, K, ld_w, f16, g.bn / 2))
     return FLCE_ERR_CUDA;
-  return done(launch_linear(g, ea, sms, static_cast<cudaStream_t>(stream)));
+  return done(launch_linear(g, ea, sms, s));
 }
 
 flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy, const void* x,
@@ -367,8 +475,7 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
     return FLCE_ERR_ALIGNMENT;
   LinearWs w;
   if (!workspace) return FLCE_ERR_INVALID_ARG;
-  if (workspace_bytes < carve(p, nullptr, &w)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
-  carve(p, workspace, &w);
+  if (workspace_bytes < carve(p, workspace, &w)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0;
   if ((st = device_info(&sms)) != FLCE_OK) return st;
   const bool f16 = p->input_fp16 != 0;
@@ -376,9 +483,7 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
 
   const int64_t ld_dy = pitch(p->ld_y, N);
   const bool dy_rows16 = aligned16(dy) && ld_dy % 8 == 0;
-  const bool small_dx = dx && M <= small_most(false), pair_dx = dx && !small_dx;
-  const bool copy =
-      (act || !dy_rows16 || ((pair_dx || dW) && is_narrow(M, N, ld_dy))) && (dx || dW);
+  const bool copy = (act || !dy_rows16 || w.repack_dy) && (dx || dW);
   if (copy || db) {
     DzArgs za;
     za.dy = static_cast<const uint16_t*>(dy);
@@ -398,7 +503,7 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
   const void* dz = copy ? static_cast<const void*>(w.dz) : dy;
   const int64_t ld_dz = copy ? w.ld_dz : ld_dy;
   cudaError_t e = cudaSuccess;
-  if (small_dx) {
+  if (dx && w.few) {
     SmallArgs sa;
     if (!small_args(&sa, dz, ld_dz, M, N, 1, K, dx, K, false, f16, dev_err) ||
         !mn_major(&sa.w, W, K, N, K, f16, kBK) || launch_small(false, true, sa, s) != cudaSuccess)
@@ -411,7 +516,7 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
     ea.K = K;
     PairArgs g = pair_args(M, K, N, 1, true, false, 6.f, f16, dev_err);
     int64_t ld_w = K;
-    const void* Wn = spread(W, N, K, &ld_w, w.W, s, &e);
+    const void* Wn = repacked(W, N, K, &ld_w, w.ld_w, w.W, s, &e);
     if (!out16(&ea.dx, dx, M, K, K) || !k_major(&g.a, dz, M, N, ld_dz, f16) ||
         !mn_major(&g.b, Wn, K, N, ld_w, f16, pair_lk(g.halves)) || e != cudaSuccess ||
         launch_grad_x(false, g, ea, sms, s) != cudaSuccess)
@@ -426,7 +531,7 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
     ea.K = K;
     PairArgs g = pair_args(N, K, M, 1, true, false, 6.f, f16, dev_err);
     int64_t ld_x = pitch(p->ld_x, K);
-    const void* xn = spread(x, M, K, &ld_x, w.x, s, &e);
+    const void* xn = repacked(x, M, K, &ld_x, w.ld_x, w.x, s, &e);
     if (!encode_store_2d(&ea.out, dW, K, N, static_cast<uint64_t>(K) * (p->dW_fp32 ? 4 : 2),
                          p->dW_fp32 != 0) ||
         !mn_major(&g.a, dz, N, M, ld_dz, f16, pair_lk(g.halves)) ||
@@ -438,28 +543,30 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
 }
 
 size_t flce_gated_workspace_size(const flce_gated_params_t* p, int which) {
-  if (check(p) != FLCE_OK || p->M == 0 || which != 1) return 0;
+  if (check(p) != FLCE_OK || p->M == 0 || which < 0 || which > 1) return 0;
   GatedWs w;
-  return carve(p, nullptr, &w);
+  return which == 0 ? carve_forward(p, nullptr, &w) : carve(p, nullptr, &w);
 }
 
 flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, const void* Wg,
                                  const void* Wu, void* h, void* pre, void* workspace,
                                  size_t workspace_bytes, int32_t* dev_err, void* stream) {
   NvtxRange nvtx_range("flce_gated_forward");
-  (void)workspace;
-  (void)workspace_bytes;
   flce_status_t st = check(p);
   if (st != FLCE_OK) return st;
   if (p->M == 0) return FLCE_OK;
   if (!x || !Wg || !Wu || !h) return FLCE_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(Wg) || !aligned16(Wu) || !aligned16(h) || !aligned16(pre))
     return FLCE_ERR_ALIGNMENT;
+  GatedWs w;
+  const size_t need = carve_forward(p, workspace, &w);
+  if (need > 0 && !workspace) return FLCE_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0;
   if ((st = device_info(&sms)) != FLCE_OK) return st;
   const bool f16 = p->input_fp16 != 0;
   const int M = static_cast<int>(p->M), K = static_cast<int>(p->K), F = static_cast<int>(p->F);
-  if (M <= small_most(true)) {
+  if (w.few) {
     SmallArgs sa;
     if (!small_args(&sa, x, pitch(p->ld_x, K), M, K, 1, F, h, pitch(p->ld_h, F), true, f16, dev_err) ||
         !k_major(&sa.w, Wg, F, K, K, f16, 64) || !k_major(&sa.w2, Wu, F, K, K, f16, 64))
@@ -479,13 +586,19 @@ flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, co
   uint16_t* keep = static_cast<uint16_t*>(pre);
   PairArgs g = pair_args(M, F, K, 1, false, true, epilogue_ns(p->activation, pre != nullptr, true),
                          f16, dev_err);
-  if (!out16(&ea.h, h, M, F, pitch(p->ld_h, F)) ||
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaSuccess;
+  int64_t ld_x = pitch(p->ld_x, K), ld_g = K, ld_u = K;
+  const void* xn = repacked(x, M, K, &ld_x, w.ld_x, w.x, s, &e);
+  const void* Wgn = repacked(Wg, F, K, &ld_g, w.ld_w, w.Wg, s, &e);
+  const void* Wun = repacked(Wu, F, K, &ld_u, w.ld_w, w.Wu, s, &e);
+  if (e != cudaSuccess || !out16(&ea.h, h, M, F, pitch(p->ld_h, F)) ||
       (pre && (!out16(&ea.val, keep, M, F, F) ||
                !out16(&ea.cross, keep + static_cast<size_t>(M) * F, M, F, F))) ||
-      !k_major(&g.a, x, M, K, pitch(p->ld_x, K), f16) || !k_major(&g.b, Wg, F, K, K, f16, g.bn / 2) ||
-      !k_major(&g.b2, Wu, F, K, K, f16, g.bn / 2))
+      !k_major(&g.a, xn, M, K, ld_x, f16) || !k_major(&g.b, Wgn, F, K, ld_g, f16, g.bn / 2) ||
+      !k_major(&g.b2, Wun, F, K, ld_u, f16, g.bn / 2))
     return FLCE_ERR_CUDA;
-  return done(launch_gated(g, ea, sms, static_cast<cudaStream_t>(stream)));
+  return done(launch_gated(g, ea, sms, s));
 }
 
 flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, const void* x,
@@ -509,8 +622,7 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
       !aligned16(dWu))
     return FLCE_ERR_ALIGNMENT;
   GatedWs w;
-  if (workspace_bytes < carve(p, nullptr, &w)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
-  carve(p, workspace, &w);
+  if (workspace_bytes < carve(p, workspace, &w)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0;
   if ((st = device_info(&sms)) != FLCE_OK) return st;
   const bool f16 = p->input_fp16 != 0;
@@ -529,10 +641,11 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
   ga.fp16 = f16 ? 1 : 0;
   if (launch_gated_grad(ga, s) != cudaSuccess) return FLCE_ERR_CUDA;
   cudaError_t e = cudaSuccess;
-  if (dx && M <= small_most(false)) {
+  if (dx && w.few) {
     SmallArgs sa;
-    if (!small_args(&sa, w.dg, w.ld, M, F, 2, K, dx, K, false, f16, dev_err) ||
-        !k_major(&sa.x2, w.du, M, F, w.ld, f16, small_tokens(M)) ||
+    const bool ok = small_args(&sa, w.dg, w.ld, M, F, 2, K, dx, K, false, f16, dev_err);
+    sa.xp2 = w.du;
+    if (!ok || (small_tokens(M) > 32 && !k_major(&sa.x2, w.du, M, F, w.ld, f16, small_tokens(M))) ||
         !mn_major(&sa.w, Wg, K, F, K, f16, kBK) || !mn_major(&sa.w2, Wu, K, F, K, f16, kBK) ||
         launch_small(false, true, sa, s) != cudaSuccess)
       return FLCE_ERR_CUDA;
@@ -544,8 +657,8 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
     ea.K = K;
     PairArgs g = pair_args(M, K, F, 2, true, false, 6.f, f16, dev_err);
     int64_t ld_g = K, ld_u = K;
-    const void* Wgn = spread(Wg, F, K, &ld_g, w.Wg, s, &e);
-    const void* Wun = spread(Wu, F, K, &ld_u, w.Wu, s, &e);
+    const void* Wgn = repacked(Wg, F, K, &ld_g, w.ld_w, w.Wg, s, &e);
+    const void* Wun = repacked(Wu, F, K, &ld_u, w.ld_w, w.Wu, s, &e);
     const int lk = pair_lk(g.halves);
     if (!out16(&ea.dx, dx, M, K, K) || !k_major(&g.a, w.dg, M, F, w.ld, f16) ||
         !k_major(&g.a2, w.du, M, F, w.ld, f16) || !mn_major(&g.b, Wgn, K, F, ld_g, f16, lk) ||
@@ -564,7 +677,7 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
     PairArgs g = pair_args(2 * cdiv(F, 256) * 256, K, M, 1, true, false, 6.f, f16, dev_err);
     g.m_split = g.tiles_m / 2;
     int64_t ld_x = pitch(p->ld_x, K);
-    const void* xn = spread(x, M, K, &ld_x, w.x, s, &e);
+    const void* xn = repacked(x, M, K, &ld_x, w.ld_x, w.x, s, &e);
     const int lk = pair_lk(g.halves);
     if (!encode_store_2d(&ea.out, dWg, K, F, row, p->dW_fp32 != 0) ||
         !encode_store_2d(&ea.out2, dWu, K, F, row, p->dW_fp32 != 0) ||

@@ -62,7 +62,10 @@ cudaError_t launch_grad_w(bool two, const PairArgs& g, const GradWArgs& ea, int 
 // weights on the MMA's rows. w: boxes of 128 features x 64 sum elements (64 x 64
 // with the features contiguous, or for the gated projection); x: 64 sum elements x small_tokens(M) tokens.
 struct SmallArgs {
-  CUtensorMap w, w2, x, x2;
+  CUtensorMap w, w2, x, x2;  // x, x2: above 32 tokens only
+  const uint16_t *xp, *xp2;  // x and the second segment's, [M, ld_x]
+  int64_t ld_x;
+  int k_len;                 // sum elements of a segment
   const uint16_t* bias;
   const uint16_t* res;
   uint16_t* keep;  // for the backward (block_epilogues.cuh): [M, N], or [2, M, N] (gated); or null
@@ -105,8 +108,8 @@ struct GatedGradArgs {
   int64_t ld;
   int M, F, fp16;
 };
-// A copy of 16-bit rows to another pitch, all on 16-byte boundaries.
-cudaError_t launch_spread(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst,
+// A copy of 16-bit rows to another pitch; both on 16-byte boundaries, cols a multiple of 8.
+cudaError_t launch_repack(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst,
                           int rows, int cols, cudaStream_t st);
 cudaError_t launch_gated_grad(const GatedGradArgs& a, cudaStream_t st);
 

@@ -128,24 +128,25 @@ cudaError_t launch_dz(const DzArgs& a, cudaStream_t st) {
                           dz_rows_per_part(a.M, a.N));
 }
 
-// db = the ordered sum of the parts: a block takes 32 columns, its 8 warps every eighth
+// db = the ordered sum of the parts: a block takes 32 columns, its 32 warps every 32nd
 // part each, and the warps' sums are added in warp order.
-__global__ void __launch_bounds__(256) db_sum_kernel(const float* part, int parts, int N, void* db,
-                                                     int fp32, int fp16) {
-  __shared__ float s_sum[8][32];
+constexpr int kDbSumWarps = 32;
+__global__ void __launch_bounds__(32 * kDbSumWarps)
+    db_sum_kernel(const float* part, int parts, int N, void* db, int fp32, int fp16) {
+  __shared__ float s_sum[kDbSumWarps][33];
   griddep_launch();
   griddep_wait();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, col = blockIdx.x * 32 + lane;
   float t = 0.f;
   if (col < N) {
-#pragma unroll 4
-    for (int i = w; i < parts; i += 8) t += part[static_cast<size_t>(i) * N + col];
+#pragma unroll 8
+    for (int i = w; i < parts; i += kDbSumWarps) t += part[static_cast<size_t>(i) * N + col];
   }
   s_sum[w][lane] = t;
   __syncthreads();
   if (w != 0 || col >= N) return;
 #pragma unroll
-  for (int k = 1; k < 8; ++k) t += s_sum[k][lane];
+  for (int k = 1; k < kDbSumWarps; ++k) t += s_sum[k][lane];
   if (fp32)
     static_cast<float*>(db)[col] = t;
   else
@@ -154,29 +155,48 @@ __global__ void __launch_bounds__(256) db_sum_kernel(const float* part, int part
 
 cudaError_t launch_db_sum(const float* part, int parts, int N, void* db, bool fp32, bool fp16,
                           cudaStream_t st) {
-  return launch_dependent(db_sum_kernel, dim3(static_cast<unsigned>((N + 31) / 32)), 256, 0, 1, st,
-                          part, parts, N, db, fp32 ? 1 : 0, fp16 ? 1 : 0);
+  return launch_dependent(db_sum_kernel, dim3(static_cast<unsigned>((N + 31) / 32)),
+                          32 * kDbSumWarps, 0, 1, st, part, parts, N, db, fp32 ? 1 : 0,
+                          fp16 ? 1 : 0);
 }
 
-// One thread takes 8 columns (rows * cols is below 65,536 here). A row's last columns are
-// never fewer: cols is a multiple of 8.
-__global__ void __launch_bounds__(256) spread_kernel(const uint16_t* src, int64_t ld_src,
+// A block copies 1024 groups of 8 columns, a thread four of them 256 apart. Index: the 32-
+// or 64-bit type that holds rows * cols / 8.
+template <class Index>
+__global__ void __launch_bounds__(256) repack_kernel(const uint16_t* src, int64_t ld_src,
                                                      uint16_t* dst, int64_t ld_dst, int rows,
                                                      int cols) {
   griddep_launch();
   griddep_wait();
-  const int c8 = cols / 8, i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= rows * c8) return;
-  const int row = i / c8, col = (i - row * c8) * 8;
-  *reinterpret_cast<uint4*>(dst + static_cast<size_t>(row) * ld_dst + col) =
-      *reinterpret_cast<const uint4*>(src + static_cast<size_t>(row) * ld_src + col);
+  const Index c8 = static_cast<Index>(cols / 8), n = c8 * static_cast<Index>(rows);
+  const Index first = static_cast<Index>(blockIdx.x) * 1024 + threadIdx.x;
+  uint4 v[4];
+  size_t to[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const Index i = first + 256 * k;
+    if (i >= n) break;
+    const Index row = i / c8;
+    const size_t col = static_cast<size_t>(i - row * c8) * 8;
+    v[k] = __ldcs(
+        reinterpret_cast<const uint4*>(src + static_cast<size_t>(row) * ld_src + col));
+    to[k] = static_cast<size_t>(row) * ld_dst + col;
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    if (first + 256 * k < n) *reinterpret_cast<uint4*>(dst + to[k]) = v[k];
 }
 
-cudaError_t launch_spread(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst,
+cudaError_t launch_repack(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst,
                           int rows, int cols, cudaStream_t st) {
-  const int n = rows * (cols / 8);
-  return launch_dependent(spread_kernel, dim3(static_cast<unsigned>((n + 255) / 256)), 256, 0, 1,
-                          st, src, ld_src, dst, ld_dst, rows, cols);
+  const uint64_t n = static_cast<uint64_t>(rows) * (cols / 8), blocks = (n + 1023) / 1024;
+  if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>(blocks));
+  return n < (1ull << 32) - 1024
+             ? launch_dependent(repack_kernel<uint32_t>, grid, 256, 0, 1, st, src, ld_src, dst,
+                                ld_dst, rows, cols)
+             : launch_dependent(repack_kernel<uint64_t>, grid, 256, 0, 1, st, src, ld_src, dst,
+                                ld_dst, rows, cols);
 }
 
 // One thread takes 8 columns of one row: three 16-byte loads, two 16-byte

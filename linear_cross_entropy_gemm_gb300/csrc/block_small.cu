@@ -15,7 +15,10 @@
 // applies the epilogue: no scratch memory, no second launch.
 //
 // Warp 0 streams (W, x) slices by TMA through a ring, warp 1 issues the MMAs, and
-// four warps move the accumulator to shared memory.
+// four warps move the accumulator to shared memory. Up to 32 tokens those four also
+// bring x into the ring, by plain loads a ring's length ahead: so small a tensor is
+// slow to load by TMA when every SM shares it (gated 1 token x 4096 x 14336 45 us, 38 us
+// with plain loads).
 #include <cuda_runtime.h>
 
 #include "block_epilogues.cuh"
@@ -34,6 +37,8 @@ struct SmallShape {
   static constexpr int kRing = NT <= 64 ? 108 * 1024 : 208 * 1024;
   static constexpr int kStages = kRing / kStage;
   static constexpr int kTmem = NT < 32 ? 32 : NT;  // TMEM columns
+  static constexpr bool kPlainX = NT <= 32;        // x by plain loads
+  static constexpr int kXChunks = NT * 8 / 128;    // 16-byte words of a slice for each of 128 threads
   static constexpr int kPartial = NT * 128 * 4;    // joins reuse the ring
   static constexpr int kBody = kStages * kStage > kPartial ? kStages * kStage : kPartial;
   static constexpr size_t kSmem = 1024 + static_cast<size_t>(kBody) + kBarrierBytes;
@@ -96,6 +101,31 @@ __device__ __forceinline__ void store8(uint16_t* p, int n, bool vec, bool f16, c
   }
 }
 
+// Thread t's 16-byte words of x in slice kb: eight threads to a token's 64 sum elements;
+// zeros past the sum's end and past the last token.
+template <int CHUNKS>
+__device__ __forceinline__ void fetch_x(const SmallArgs& a, int kb, int m0, int t,
+                                        uint4 (&v)[CHUNKS]) {
+  const bool second = kb >= a.k_split;
+  const int col = (second ? kb - a.k_split : kb) * kBK + (t & 7) * 8, n = a.k_len - col;
+#pragma unroll
+  for (int c = 0; c < CHUNKS; ++c) {
+    const int m = m0 + (t >> 3) + c * 16;
+    v[c] = make_uint4(0u, 0u, 0u, 0u);
+    if (m >= a.M || n <= 0) continue;
+    const uint16_t* p = (second ? a.xp2 : a.xp) + static_cast<size_t>(m) * a.ld_x + col;
+    if (n >= 8) {
+      v[c] = *reinterpret_cast<const uint4*>(p);
+    } else {
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int j = 0; j < 7; ++j)
+        if (j < n) w[j >> 1] |= static_cast<uint32_t>(p[j]) << (16 * (j & 1));
+      v[c] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+  }
+}
+
 // W_MN: the weights' features are contiguous and its rows are the sum (dx: W and
 // dz), else its rows are the features. TWO: two weight tensors with one x (gated
 // forward); rows 0 .. 63 of a tile are the first's, 64 .. 127 the second's. The
@@ -124,7 +154,7 @@ __global__ void __launch_bounds__(kSmThreads)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], S::kPlainX ? 5 : 1);  // the producer, and the warps that bring x
       mbar_init(&empty[s], 1);
     }
     mbar_init(done, 1);
@@ -133,7 +163,7 @@ __global__ void __launch_bounds__(kSmThreads)
   }
   if (warp == 0 && lane == 0) {
     tma_prefetch_desc(&a.w);
-    tma_prefetch_desc(&a.x);
+    if constexpr (!S::kPlainX) tma_prefetch_desc(&a.x);
   }
   if (warp == 1) tmem_alloc(tmem_slot, S::kTmem);
   tc_fence_before();
@@ -155,7 +185,7 @@ __global__ void __launch_bounds__(kSmThreads)
       const int k0 = (second ? kb - a.k_split : kb) * kBK;
       const CUtensorMap* mw = second ? &a.w2 : &a.w;
       if (elect_one()) {
-        mbar_arrive_expect_tx(&full[s], S::kStage);
+        mbar_arrive_expect_tx(&full[s], S::kPlainX ? kWTileBytes : S::kStage);
         if constexpr (TWO) {
           tma_load_2d(w, &a.w, &full[s], k0, f0, pol);
           tma_load_2d(w + kWTileBytes / 2, &a.w2, &full[s], k0, f0, pol);
@@ -165,7 +195,8 @@ __global__ void __launch_bounds__(kSmThreads)
           tma_load_2d(w, mw, &full[s], f0, k0, pol);
           tma_load_2d(w + kMnBoxBytes, mw, &full[s], f0 + 64, k0, pol);
         }
-        tma_load_2d(w + kWTileBytes, second ? &a.x2 : &a.x, &full[s], k0, m0, pol);
+        if constexpr (!S::kPlainX)
+          tma_load_2d(w + kWTileBytes, second ? &a.x2 : &a.x, &full[s], k0, m0, pol);
       }
       __syncwarp();
       ++issued;
@@ -206,6 +237,34 @@ __global__ void __launch_bounds__(kSmThreads)
     if (elect_one()) umma_commit(done);
     __syncwarp();
     mbar_drain(done, 0);
+  } else if constexpr (S::kPlainX) {
+    const int t = static_cast<int>(threadIdx.x) - 64;
+    uint4 ahead[S::kStages][S::kXChunks];
+#pragma unroll
+    for (int i = 0; i < S::kStages; ++i)
+      if (kb_lo + i < kb_hi) fetch_x<S::kXChunks>(a, kb_lo + i, m0, t, ahead[i]);
+    uint32_t ph = 0;
+    bool ok = true;
+    for (int kb = kb_lo; kb < kb_hi && ok; kb += S::kStages) {
+#pragma unroll
+      for (int i = 0; i < S::kStages; ++i) {
+        if (kb + i >= kb_hi || !ok) break;
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[i], ph ^ 1, abort_flag, a.dev_err));
+        if (!ok) break;
+        uint8_t* x = smem + i * S::kStage + kWTileBytes;
+#pragma unroll
+        for (int c = 0; c < S::kXChunks; ++c) {
+          const int row = (t >> 3) + c * 16, word = (t & 7) ^ (row & 7);  // the 128-byte swizzle
+          *reinterpret_cast<uint4*>(x + row * 128 + word * 16) = ahead[i][c];
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[i]);
+        if (kb + i + S::kStages < kb_hi)
+          fetch_x<S::kXChunks>(a, kb + i + S::kStages, m0, t, ahead[i]);
+      }
+      ph ^= 1;
+    }
   }
   // The producer and the issuer leave their branches only when every load has
   // landed and every MMA is done, so the ring may be overwritten: by this CTA, and
