@@ -31,72 +31,85 @@ constexpr float kGeluC3 = 0.044715f;
 constexpr float kInvSqrt2 = 0.7071067811865476f;
 constexpr float kInvSqrt2Pi = 0.3989422804014327f;
 
-// 1 / (1 + e^-z) from ex2 and the approximate division: relative error a few
-// 2^-22, far below the 16-bit rounding of anything made from it. e^-z
-// overflows to +inf for z < -88, and the quotient is then 0, its limit.
-__device__ __forceinline__ float sigmoid_f(float z) {
-  return __fdividef(1.f, 1.f + fast_exp2(-kLog2e * z));
+// Activations work on packed fp32 pairs: an epilogue beside a short sum is bound by its
+// instructions, and a packed one does the work of two.
+__device__ __forceinline__ uint64_t splat(float c) { return f32x2(c, c); }
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
 }
-// gelu_tanh: (1 + tanh w) / 2 = 1 / (1 + e^-2w), w = c (z + 0.044715 z^3).
-__device__ __forceinline__ float gelu_tanh_gate(float z) {
-  return sigmoid_f(2.f * kGeluC * z * fmaf(kGeluC3 * z, z, 1.f));
+__device__ __forceinline__ uint64_t rcp2(uint64_t x) {
+  float a, b;
+  f32x2_split(x, a, b);
+  return f32x2(rcp_approx(a), rcp_approx(b));
 }
-// gelu: Phi(z) = 1 - Q(z) with, for x = |z| / sqrt(2), Q = erfc(x) / 2 and
+__device__ __forceinline__ uint64_t exp2_2(uint64_t x) {
+  float a, b;
+  f32x2_split(x, a, b);
+  return f32x2(fast_exp2(a), fast_exp2(b));
+}
+// 1 / (1 + e^-z) from ex2 and the approximate reciprocal: relative error a few 2^-22,
+// far below the 16-bit rounding of anything made from it. e^-z overflows to +inf for
+// z < -88, and the reciprocal is then 0, its limit.
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t z) {
+  return rcp2(fadd2(exp2_2(fmul2(z, splat(-kLog2e))), splat(1.f)));
+}
+// Phi(z) = 1/2 + sign(z) (1/2 - Q(|z|)) with, for x = |z| / sqrt(2), Q = erfc(x) / 2 and
 // erfc(x) = (a1 t + ... + a5 t^5) e^(-x^2) + e, t = 1 / (1 + p x), |e| <= 1.5e-7
 // (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26, after
 // Hastings). A third of erff's instructions, no branch, and e^(-z^2 / 2) is the
 // density that the derivative needs. gauss: e^(-z^2 / 2).
-__device__ __forceinline__ float gelu_cdf(float z, float& gauss) {
-  const float t = __fdividef(1.f, fmaf(0.3275911f * kInvSqrt2, fabsf(z), 1.f));
-  gauss = fast_exp2(-0.5f * kLog2e * z * z);
-  float q = fmaf(t, 0.5f * 1.061405429f, 0.5f * -1.453152027f);
-  q = fmaf(t, q, 0.5f * 1.421413741f);
-  q = fmaf(t, q, 0.5f * -0.284496736f);
-  q = fmaf(t, q, 0.5f * 0.254829592f);
-  q *= t * gauss;
-  return z < 0.f ? q : 1.f - q;
+__device__ __forceinline__ uint64_t gelu_cdf2(uint64_t z, uint64_t& gauss) {
+  constexpr uint64_t kSign = 0x8000000080000000ull;
+  const uint64_t t = rcp2(ffma2(z & ~kSign, splat(0.3275911f * kInvSqrt2), splat(1.f)));
+  gauss = exp2_2(fmul2(fmul2(z, z), splat(-0.5f * kLog2e)));
+  uint64_t q = ffma2(t, splat(0.5f * 1.061405429f), splat(0.5f * -1.453152027f));
+  q = ffma2(t, q, splat(0.5f * 1.421413741f));
+  q = ffma2(t, q, splat(0.5f * -0.284496736f));
+  q = ffma2(t, q, splat(0.5f * 0.254829592f));
+  q = fmul2(fmul2(q, t), gauss);
+  return fadd2(ffma2(q, splat(-1.f), splat(0.5f)) ^ (z & kSign), splat(0.5f));
+}
+// gelu_tanh: (1 + tanh w) / 2 = 1 / (1 + e^-2w), w = c (z + 0.044715 z^3).
+__device__ __forceinline__ uint64_t gelu_tanh_gate2(uint64_t z) {
+  return sigmoid2(
+      fmul2(fmul2(z, splat(2.f * kGeluC)), ffma2(fmul2(z, z), splat(kGeluC3), splat(1.f))));
 }
 
+// a(z) and a'(z) of two values.
 template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-  if constexpr (ACT == kActRelu) return z < 0.f ? 0.f : z;  // a NaN stays one
-  if constexpr (ACT == kActGelu) {
-    float gauss;
-    return z * gelu_cdf(z, gauss);
-  }
-  if constexpr (ACT == kActGeluTanh) return z * gelu_tanh_gate(z);
-  if constexpr (ACT == kActSilu) return z * sigmoid_f(z);
-  if constexpr (ACT == kActSigmoid) return sigmoid_f(z);
-  return z;
-}
-
-// a(z) and a'(z).
-template <int ACT>
-__device__ __forceinline__ void act_value_slope(float z, float& val, float& slope) {
+__device__ __forceinline__ void act2(uint64_t z, uint64_t& val, uint64_t& slope) {
   if constexpr (ACT == kActRelu) {
-    val = z < 0.f ? 0.f : z;
-    slope = z > 0.f ? 1.f : 0.f;
+    float a, b;
+    f32x2_split(z, a, b);
+    val = f32x2(a < 0.f ? 0.f : a, b < 0.f ? 0.f : b);  // a NaN stays one
+    slope = f32x2(a > 0.f ? 1.f : 0.f, b > 0.f ? 1.f : 0.f);
   } else if constexpr (ACT == kActGelu) {
-    float gauss;
-    const float c = gelu_cdf(z, gauss);
-    val = z * c;
-    slope = fmaf(z * kInvSqrt2Pi, gauss, c);
+    uint64_t gauss;
+    const uint64_t c = gelu_cdf2(z, gauss);
+    val = fmul2(z, c);
+    slope = ffma2(fmul2(z, splat(kInvSqrt2Pi)), gauss, c);
   } else if constexpr (ACT == kActGeluTanh) {
-    const float p = gelu_tanh_gate(z);
-    val = z * p;
+    const uint64_t p = gelu_tanh_gate2(z);
+    val = fmul2(z, p);
     // Beyond |z| = 64 p is 0 or 1 and the second term is 0; its polynomial must not overflow.
-    const float zc = fminf(fmaxf(z, -64.f), 64.f);
-    slope = fmaf(zc * p * (1.f - p), 2.f * kGeluC * fmaf(3.f * kGeluC3 * zc, zc, 1.f), p);
+    float a, b;
+    f32x2_split(z, a, b);
+    const uint64_t zc = f32x2(fminf(fmaxf(a, -64.f), 64.f), fminf(fmaxf(b, -64.f), 64.f));
+    const uint64_t poly =
+        ffma2(fmul2(zc, zc), splat(6.f * kGeluC * kGeluC3), splat(2.f * kGeluC));
+    slope = ffma2(fmul2(fmul2(zc, p), ffma2(p, splat(-1.f), splat(1.f))), poly, p);
   } else if constexpr (ACT == kActSilu) {
-    const float p = sigmoid_f(z);
-    val = z * p;
-    slope = fmaf(val, 1.f - p, p);
+    const uint64_t p = sigmoid2(z);
+    val = fmul2(z, p);
+    slope = ffma2(val, ffma2(p, splat(-1.f), splat(1.f)), p);
   } else if constexpr (ACT == kActSigmoid) {
-    val = sigmoid_f(z);
-    slope = val * (1.f - val);
+    val = sigmoid2(z);
+    slope = fmul2(val, ffma2(val, splat(-1.f), splat(1.f)));
   } else {
     val = z;
-    slope = 1.f;
+    slope = splat(1.f);
   }
 }
 
@@ -114,11 +127,17 @@ __device__ __forceinline__ void with_act(int act, Fn f) {
   }
 }
 
+// v = a(v).
 template <int N>
 __device__ __forceinline__ void act_all(int act, float (&v)[N]) {
+  if (act == kActNone) return;
   with_act(act, [&](auto a) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) v[j] = act_value<decltype(a)::value>(v[j]);
+    for (int j = 0; j < N; j += 2) {
+      uint64_t val, slope;
+      act2<decltype(a)::value>(f32x2(v[j], v[j + 1]), val, slope);
+      f32x2_split(val, v[j], v[j + 1]);
+    }
   });
 }
 
@@ -137,10 +156,37 @@ __device__ __forceinline__ void act_all(int act, float (&v)[N]) {
 constexpr float kRound = 12582912.f;  // 1.5 * 2^23: x + kRound holds round(x) in its low bits
 
 // Codes of two slopes in one word.
-__device__ __forceinline__ uint32_t encode_slopes(float a, float b) {
-  const uint32_t x = __float_as_uint(fmaf(a, 32768.f, kRound + 8192.f));
-  const uint32_t y = __float_as_uint(fmaf(b, 32768.f, kRound + 8192.f));
-  return __byte_perm(x, y, 0x5410);
+__device__ __forceinline__ uint32_t encode_slopes(uint64_t s) {
+  float a, b;
+  f32x2_split(ffma2(s, splat(32768.f), splat(kRound + 8192.f)), a, b);
+  return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
+}
+
+// v = a(v), and the codes of the slopes.
+template <int N>
+__device__ __forceinline__ void act_keep_slopes(int act, float (&v)[N], uint32_t (&w)[N / 2]) {
+  with_act(act, [&](auto a) {
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+      uint64_t val, slope;
+      act2<decltype(a)::value>(f32x2(v[j], v[j + 1]), val, slope);
+      w[j / 2] = encode_slopes(slope);
+      f32x2_split(val, v[j], v[j + 1]);
+    }
+  });
+}
+// v = a(v), and x = u a'(v).
+template <int N>
+__device__ __forceinline__ void act_cross(int act, float (&v)[N], const float (&u)[N], float (&x)[N]) {
+  with_act(act, [&](auto a) {
+#pragma unroll
+    for (int j = 0; j < N; j += 2) {
+      uint64_t val, slope;
+      act2<decltype(a)::value>(f32x2(v[j], v[j + 1]), val, slope);
+      f32x2_split(val, v[j], v[j + 1]);
+      f32x2_split(fmul2(f32x2(u[j], u[j + 1]), slope), x[j], x[j + 1]);
+    }
+  });
 }
 __device__ __forceinline__ float decode_slope(uint32_t code) {
   const float q = __uint_as_float(0x4B000000u + code) - 8388608.f;
@@ -156,10 +202,10 @@ __device__ __forceinline__ uint4 encode_group(const float* v) {
   uint32_t w[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const uint32_t x = __float_as_uint(fmaf(v[2 * i], scale, kRound));
-    const uint32_t y = __float_as_uint(fmaf(v[2 * i + 1], scale, kRound));
+    float x, y;
+    f32x2_split(ffma2(f32x2(v[2 * i], v[2 * i + 1]), splat(scale), splat(kRound)), x, y);
     const uint32_t t = eb >> (2 * i);
-    w[i] = ((__byte_perm(x, y, 0x5410) << 1) & 0xFFFEFFFEu) | (t & 1u) | ((t & 2u) << 15);
+    w[i] = ((__byte_perm(__float_as_uint(x), __float_as_uint(y), 0x5410) << 1) & 0xFFFEFFFEu) | (t & 1u) | ((t & 2u) << 15);
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
@@ -272,8 +318,7 @@ __device__ __forceinline__ void add_32(const uint16_t* src, float (&v)[32]) {
     }
   }
 }
-
-// The same for the first ncol of a row's 32 columns (16-bit); vec: at a 16-byte boundary.
+// The same for the first ncol of a row's 32 columns; vec: at a 16-byte boundary.
 __device__ __forceinline__ void add_row_16(const uint16_t* src, int ncol, bool vec, bool fp16,
                                            float (&v)[32]) {
   if (vec && ncol >= 32) {
@@ -323,15 +368,7 @@ struct LinearEpi {
       if (a.bias) add_row_16(a.bias + col0, a.N - col0, true, f16, v);
       if (a.keep) {
         uint32_t w[16];
-        with_act(a.act, [&](auto act) {
-#pragma unroll
-          for (int j = 0; j < 32; j += 2) {
-            float s0, s1;
-            act_value_slope<decltype(act)::value>(v[j], v[j], s0);
-            act_value_slope<decltype(act)::value>(v[j + 1], v[j + 1], s1);
-            w[j >> 1] = encode_slopes(s0, s1);
-          }
-        });
+        act_keep_slopes(a.act, v, w);
         put_words(a.slope, a.M, a.N, row0, col0, w, st, lane);
       } else {
         act_all(a.act, v);
@@ -370,14 +407,7 @@ struct GatedEpi {
       acc.load(sl.up_off + acc_col, u);
       if (a.keep) {
         float x[32];  // u a'(g)
-        with_act(a.act, [&](auto act) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            float slope;
-            act_value_slope<decltype(act)::value>(g[j], g[j], slope);
-            x[j] = u[j] * slope;
-          }
-        });
+        act_cross(a.act, g, u, x);
         uint32_t w[16];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
@@ -401,7 +431,8 @@ struct GatedEpi {
         act_all(a.act, g);
       }
 #pragma unroll
-      for (int j = 0; j < 32; ++j) g[j] *= u[j];
+      for (int j = 0; j < 32; j += 2)
+        f32x2_split(fmul2(f32x2(g[j], g[j + 1]), f32x2(u[j], u[j + 1])), g[j], g[j + 1]);
       put_block_16(a.h, a.M, a.F, row0, col0, g, f16, st, lane);
     }
   }

@@ -342,14 +342,7 @@ __global__ void __launch_bounds__(kSmThreads)
       float (&u)[8] = v[kProducts - 1];
       if (a.keep) {
         float x[8];
-        with_act(a.act, [&](auto act) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float slope;
-            act_value_slope<decltype(act)::value>(v[0][j], v[0][j], slope);
-            x[j] = u[j] * slope;
-          }
-        });
+        act_cross(a.act, v[0], u, x);
         uint16_t* k = a.keep + row * a.N + col;
         *reinterpret_cast<uint4*>(k) = encode_group(v[0]);
         *reinterpret_cast<uint4*>(k + static_cast<size_t>(a.M) * a.N) = encode_group(x);
@@ -367,15 +360,7 @@ __global__ void __launch_bounds__(kSmThreads)
       }
       if (a.keep) {
         uint32_t w[4];
-        with_act(a.act, [&](auto act) {
-#pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            float s0, s1;
-            act_value_slope<decltype(act)::value>(v[0][j], v[0][j], s0);
-            act_value_slope<decltype(act)::value>(v[0][j + 1], v[0][j + 1], s1);
-            w[j >> 1] = encode_slopes(s0, s1);
-          }
-        });
+        act_keep_slopes(a.act, v[0], w);
         uint16_t* k = a.keep + row * a.N + col;
         if (a.N % 8 == 0) {
           *reinterpret_cast<uint4*>(k) = make_uint4(w[0], w[1], w[2], w[3]);
