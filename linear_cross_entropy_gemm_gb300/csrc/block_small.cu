@@ -150,7 +150,11 @@ __global__ void __launch_bounds__(kSmThreads)
   const int f0 = static_cast<int>(blockIdx.x) / slices * kOut;
   const int m0 = static_cast<int>(blockIdx.y) * NT;
   const int kb_lo = static_cast<int>(static_cast<int64_t>(a.k_blocks) * rank / slices);
-  const int kb_hi = static_cast<int>(static_cast<int64_t>(a.k_blocks) * (rank + 1) / slices);
+  const int kb_n = static_cast<int>(static_cast<int64_t>(a.k_blocks) * (rank + 1) / slices) - kb_lo;
+  // Tiles start at different places of their slice and go round it, so that the CTAs of
+  // an x do not all read the same few lines of it at the same time.
+  const int turn = static_cast<int>(blockIdx.x) / slices * 5 % kb_n;
+  const auto block = [&](int j) { return kb_lo + (j + turn < kb_n ? j + turn : j + turn - kb_n); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < S::kStages; ++s) {
@@ -178,8 +182,9 @@ __global__ void __launch_bounds__(kSmThreads)
     const uint64_t pol = l2_policy_evict_normal();
     int s = 0, issued = 0;
     uint32_t ph = 0;
-    for (int kb = kb_lo; kb < kb_hi; ++kb) {
+    for (int j = 0; j < kb_n; ++j) {
       if (!__all_sync(0xffffffffu, mbar_wait(&empty[s], ph ^ 1, abort_flag, a.dev_err))) break;
+      const int kb = block(j);
       uint8_t* w = smem + s * S::kStage;
       const bool second = kb >= a.k_split;
       const int k0 = (second ? kb - a.k_split : kb) * kBK;
@@ -215,7 +220,7 @@ __global__ void __launch_bounds__(kSmThreads)
     const uint64_t x0 = smem_desc_sw128(s0 + kWTileBytes, 16, 1024);
     int s = 0;
     uint32_t ph = 0;
-    for (int kb = kb_lo; kb < kb_hi; ++kb) {
+    for (int j = 0; j < kb_n; ++j) {
       if (!__all_sync(0xffffffffu, mbar_wait(&full[s], ph, abort_flag, a.dev_err))) break;
       tc_fence_after();
       const uint64_t off = static_cast<uint64_t>(s) * (S::kStage / 16);
@@ -223,7 +228,7 @@ __global__ void __launch_bounds__(kSmThreads)
 #pragma unroll
         for (int kk = 0; kk < kBK / kUmmaK; ++kk) {
           const uint64_t wd = w0 + off + kk * (W_MN ? 128 : 2), xd = x0 + off + kk * 2;
-          const uint32_t acc = kb != kb_lo || kk != 0 ? 1u : 0u;
+          const uint32_t acc = j != 0 || kk != 0 ? 1u : 0u;
           umma_bf16(tmem_base, wd, xd, idesc, acc);
         }
         umma_commit(&empty[s]);
@@ -242,13 +247,13 @@ __global__ void __launch_bounds__(kSmThreads)
     uint4 ahead[S::kStages][S::kXChunks];
 #pragma unroll
     for (int i = 0; i < S::kStages; ++i)
-      if (kb_lo + i < kb_hi) fetch_x<S::kXChunks>(a, kb_lo + i, m0, t, ahead[i]);
+      if (i < kb_n) fetch_x<S::kXChunks>(a, block(i), m0, t, ahead[i]);
     uint32_t ph = 0;
     bool ok = true;
-    for (int kb = kb_lo; kb < kb_hi && ok; kb += S::kStages) {
+    for (int j = 0; j < kb_n && ok; j += S::kStages) {
 #pragma unroll
       for (int i = 0; i < S::kStages; ++i) {
-        if (kb + i >= kb_hi || !ok) break;
+        if (j + i >= kb_n || !ok) break;
         ok = __all_sync(0xffffffffu, mbar_wait(&empty[i], ph ^ 1, abort_flag, a.dev_err));
         if (!ok) break;
         uint8_t* x = smem + i * S::kStage + kWTileBytes;
@@ -260,8 +265,8 @@ __global__ void __launch_bounds__(kSmThreads)
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[i]);
-        if (kb + i + S::kStages < kb_hi)
-          fetch_x<S::kXChunks>(a, kb + i + S::kStages, m0, t, ahead[i]);
+        if (j + i + S::kStages < kb_n)
+          fetch_x<S::kXChunks>(a, block(j + i + S::kStages), m0, t, ahead[i]);
       }
       ph ^= 1;
     }
