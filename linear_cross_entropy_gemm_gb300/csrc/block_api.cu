@@ -111,26 +111,36 @@ bool small_args(SmallArgs* a, const void* x, int64_t ld_x, int64_t M, int64_t k,
 }
 
 // ------------------------------------------------- tile width of a pair GEMM
-// A tile shape (pair_engine.cuh) and the ns it takes for 64 sum elements, measured on
-// one wave of tiles at 1.92 GHz with a K-major and with an MN-major B, whose boxes
-// are 64 columns wide, so that only widths in multiples of 128 load nothing twice.
+// A tile shape (pair_engine.cuh) and the ns it takes for 64 sum elements with a K-major
+// and with an MN-major B, whose boxes are 64 columns wide, so that only widths in
+// multiples of 128 load nothing twice.
+//
+// The numbers below are fitted to the choice they are for: about 1300 products of 140 to
+// 4096 rows, 64 to 5000 sum elements and 256 to 12800 columns, of all kinds, each timed in
+// every shape. Of 500 others the choice (with the one below) is 2.0 % slower than the
+// fastest shape on average, none above 21 %; with rates of single waves and an epilogue
+// priced by its activation it was 6 % (gated 9 %, up to 81 %). Widths of 160, 208 and 240
+// gained less than 0.2 %.
 struct TileShape {
   int halves, bn, slices;
   float ns, ns_mn;  // 0: not used with that B
 };
 constexpr TileShape kTileShapes[] = {
-    {1, 256, 1, 296.f, 296.f}, {1, 240, 1, 250.f, 0.f},   {1, 224, 1, 243.f, 0.f},
-    {1, 208, 1, 232.f, 0.f},   {1, 192, 1, 222.f, 255.f}, {1, 160, 1, 196.f, 0.f},
-    {1, 128, 1, 215.f, 202.f}, {1, 64, 1, 170.f, 193.f},  {2, 256, 1, 0.f, 530.f},
-    {2, 192, 1, 0.f, 405.f},   {1, 256, 2, 296.f, 296.f}, {1, 128, 2, 215.f, 202.f},
-    {1, 192, 3, 222.f, 255.f},
+    {1, 256, 1, 296.f, 296.f}, {1, 224, 1, 290.f, 0.f},   {1, 192, 1, 285.f, 0.f},
+    {1, 128, 1, 192.f, 200.f}, {1, 64, 1, 186.f, 280.f},  {2, 256, 1, 0.f, 555.f},
+    {2, 192, 1, 0.f, 505.f},   {1, 256, 2, 296.f, 296.f}, {1, 128, 2, 192.f, 200.f},
+    {1, 192, 3, 285.f, 0.f},
 };
-// Clusters of 2, 4 and 6 CTAs of 225 KiB that run at once on 152 SMs (76 and 36 as the
-// runtime says; 22 of 6 ran in one wave, 8 CTAs did not fill half of the SMs).
-constexpr int kClusters[] = {76, 36, 22};
+// Clusters of 2, 4 and 6 CTAs of 225 KiB that run at once on 152 SMs, as the runtime
+// says (of 8 CTAs it is 15).
+constexpr int kClusters[] = {76, 36, 23};
 constexpr float kSustained[] = {1.66e6f, 1.75e6f};  // flop/ns under the power cap, by halves
-constexpr float kJoinNs = 2200.f;   // exchange of a split tile
-constexpr float kSetUpNs = 5000.f;  // start and drain of each further wave of split tiles
+constexpr float kWaveNs = 1400.f;   // of a wave of tiles, beside their sums
+constexpr float kWideNs = 600.f;    // the same of two-half tiles
+constexpr float kJoinNs = 3900.f;   // exchange of a split tile
+constexpr float kSetUpNs = 3600.f;  // start and drain of each further wave of split tiles
+// Epilogue ns of an output column; of the gated forward's, which are two sums.
+constexpr float kColumnNs = 9.5f, kGatedColumnNs = 16.5f;
 
 // ns of a whole product: its waves of tiles, each as long as the sum or (where it
 // runs beside the next tile's sum) the epilogue; the last epilogue; and no less than
@@ -138,37 +148,35 @@ constexpr float kSetUpNs = 5000.f;  // start and drain of each further wave of s
 // overlapped, is kept to the weight and input gradients: at 8192 x 28672 x 4096 (gated)
 // it took 1213 us against 1133 us, for dW 4096 x 14336 x 8192 549 us against 579 us.
 // Split sums pay where the tiles are few: 512 x 4096 x 14336 46 us against 61 us.
-float tile_ns(const TileShape& t, bool mn, int64_t tiles_m, int64_t N, int64_t k64, bool two_b,
-              float epi_ns) {
+float tile_ns(const TileShape& t, bool mn, int64_t tiles_m, int64_t N, int64_t k64, bool two_b) {
   const int cols = pair_cols(two_b ? kTwoB : kOneEach, t.halves, t.bn);
   const int64_t tiles = tiles_m * ((N + cols - 1) / cols);
   const int at_once = kClusters[t.slices - 1];
   const float waves = static_cast<float>((tiles + at_once - 1) / at_once);
   const float sum = static_cast<float>(k64) * (mn ? t.ns_mn : t.ns) / static_cast<float>(t.slices);
-  const float epi = epi_ns * static_cast<float>(cols) / static_cast<float>(t.slices);
+  const float epi = (two_b ? kGatedColumnNs : kColumnNs) *
+                    static_cast<float>(std::min<int64_t>(cols, N)) / static_cast<float>(t.slices);
   const float busy = t.slices > 1    ? waves * (sum + kJoinNs + epi) + (waves - 1.f) * kSetUpNs
-                     : t.halves == 1 ? waves * std::max(sum, epi) + epi
-                                     : waves * (sum + epi);
+                     : t.halves == 1 ? waves * std::max(sum + kWaveNs, epi) + epi
+                                     : waves * (sum + epi + kWideNs);
   const float flops = 2.f * 256.f * 64.f * t.halves * t.bn * static_cast<float>(tiles) * k64;
   return std::max(busy, flops / kSustained[t.halves - 1]);
 }
 
-// Whether the shape can compute the product: every slice has a stage of the sum, every
-// pair of a split tile output columns, and (residuals are read in place) only the gated
-// tiles' chunks may overlap.
+// Whether the shape can compute the product: every slice has a stage of the sum, and every
+// pair of a split tile output columns.
 bool tile_fits(const TileShape& t, bool mn, int64_t k64, bool two_b) {
   if ((mn ? t.ns_mn : t.ns) == 0.f) return false;
-  if (!two_b && t.bn % 32 != 0) return false;
   if (t.slices == 1) return true;
   return (k64 + 1) / 2 >= t.slices && t.bn / 32 % (t.slices * (two_b ? 2 : 1)) == 0;
 }
 
-const TileShape& best_tile(bool mn, int64_t M, int64_t N, int64_t k64, bool two_b, float epi_ns) {
+const TileShape& best_tile(bool mn, int64_t M, int64_t N, int64_t k64, bool two_b) {
   const TileShape* best = nullptr;
   float least = 0.f;
   for (const TileShape& t : kTileShapes) {
     if (!tile_fits(t, mn, k64, two_b)) continue;
-    const float ns = tile_ns(t, mn, (M + 255) / 256, N, k64, two_b, epi_ns);
+    const float ns = tile_ns(t, mn, (M + 255) / 256, N, k64, two_b);
     if (!best || ns < least) {
       best = &t;
       least = ns;
@@ -185,38 +193,29 @@ constexpr int64_t kSmallTokens = 128, kSmallGatedTokens = 64;
 int64_t small_most(bool gated) { return gated ? kSmallGatedTokens : kSmallTokens; }
 
 // And larger ones with few tiles of a long sum, which that kernel cuts into eight slices:
-// 267 x 376 x 12800 25 us by CTA pairs (four tiles, three slices), 13 us. Its ns: 270 for
-// 64 sum elements of a 128-token tile, measured at 256 x 4096 x 14336, and the join.
-constexpr float kSmallNs = 270.f, kSmallJoinNs = 1500.f;
+// 267 x 376 x 12800 25 us by CTA pairs (four tiles, three slices), 13 us. Its ns for 64 sum
+// elements and the rest of it are fitted like the shapes' above: of 300 products of 70 to
+// 1024 rows, sums of 720 to 16384 and 128 to 2900 columns the choice is 0.5 % slower than the
+// faster kernel on average, CTA pairs for all of them 13 %. In one wave of clusters only: of
+// eight CTAs 15 run at once, and a second wave of them doubled 251 x 1032 x 1312's time.
+constexpr float kSmallNs = 300.f, kSmallRestNs = 4500.f;
 bool few_tokens(bool mn, int64_t M, int64_t N, int64_t k64, bool two_b) {
   if (M <= small_most(two_b)) return true;
-  const int64_t nt = small_tokens(M), out = two_b ? 64 : 128;
   const int slices = small_slices(M, N, static_cast<int>(k64), two_b);
-  const int64_t ctas = (N + out - 1) / out * ((M + nt - 1) / nt) * slices;
-  if (ctas > 152) return false;
-  const float ns = static_cast<float>((k64 + slices - 1) / slices) * kSmallNs + kSmallJoinNs;
-  const TileShape& t = best_tile(mn, M, N, k64, two_b, 6.f);
-  return ns < tile_ns(t, mn, (M + 255) / 256, N, k64, two_b, 6.f);
-}
-
-// ns that an epilogue takes per output column of a 256-row tile (measured: 1.5 us for
-// 256 stored columns, 6.5 us with gelu and a kept z).
-float epilogue_ns(int act, bool keep, bool two_b) {
-  const float a = act == FLCE_ACT_NONE || act == FLCE_ACT_RELU ? 0.f
-                  : act == FLCE_ACT_GELU                       ? 14.f
-                                                               : 8.f;
-  return 6.f + a + (keep ? (two_b ? 12.f : 6.f) : 0.f) + (two_b ? 2.f : 0.f);
+  if (small_tiles(M, N, two_b) > small_clusters(M, slices)) return false;
+  const float ns = static_cast<float>((k64 + slices - 1) / slices) * kSmallNs + kSmallRestNs;
+  const TileShape& t = best_tile(mn, M, N, k64, two_b);
+  return ns < tile_ns(t, mn, (M + 255) / 256, N, k64, two_b);
 }
 
 // The geometry of a pair GEMM D[M, N] with a sum of K (`segments` of them): tile shape and
 // raster. Bands of 16 row tiles keep 4096 rows of A in L2 while B streams: at 8192 x
 // 4096 x 14336, 573 us against 596 us with bands of 8 column tiles.
-PairArgs pair_args(int M, int N, int K, int segments, bool mn, bool two_b, float epi_ns, bool f16,
+PairArgs pair_args(int M, int N, int K, int segments, bool mn, bool two_b, bool f16,
                    int32_t* dev_err) {
   PairArgs g;
   std::memset(&g, 0, sizeof(g));
-  const TileShape& t = best_tile(mn, M, N, static_cast<int64_t>(segments) * cdiv(K, 64), two_b,
-                                 epi_ns);
+  const TileShape& t = best_tile(mn, M, N, static_cast<int64_t>(segments) * cdiv(K, 64), two_b);
   g.halves = t.halves;
   g.slices = t.slices;
   g.bn = t.bn;
@@ -272,9 +271,9 @@ int64_t repack_ld(int64_t rows, int64_t cols, int64_t ld, const Product& by) {
   return narrow || odd ? scratch_ld(rows, cols) : 0;
 }
 Product product_of(bool mn, int64_t M, int64_t N, int64_t k64, bool two_b) {
-  const TileShape& t = best_tile(mn, M, N, k64, two_b, 6.f);
+  const TileShape& t = best_tile(mn, M, N, k64, two_b);
   const int cols = pair_cols(two_b ? kTwoB : kOneEach, t.halves, t.bn);
-  return {tile_ns(t, mn, (M + 255) / 256, N, k64, two_b, 6.f),
+  return {tile_ns(t, mn, (M + 255) / 256, N, k64, two_b),
           (M + 255) / 256 * ((N + cols - 1) / cols) * t.slices};
 }
 
@@ -438,8 +437,7 @@ flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, 
   ea.keep = pre ? 1 : 0;
   ea.M = M;
   ea.N = N;
-  PairArgs g = pair_args(M, N, K, 1, false, false,
-                         epilogue_ns(p->activation, pre != nullptr, false), f16, dev_err);
+  PairArgs g = pair_args(M, N, K, 1, false, false, f16, dev_err);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   int64_t ld_x = pitch(p->ld_x, K), ld_w = K;
@@ -514,7 +512,7 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
     ea.fp16 = f16 ? 1 : 0;
     ea.M = M;
     ea.K = K;
-    PairArgs g = pair_args(M, K, N, 1, true, false, 6.f, f16, dev_err);
+    PairArgs g = pair_args(M, K, N, 1, true, false, f16, dev_err);
     int64_t ld_w = K;
     const void* Wn = repacked(W, N, K, &ld_w, w.ld_w, w.W, s, &e);
     if (!out16(&ea.dx, dx, M, K, K) || !k_major(&g.a, dz, M, N, ld_dz, f16) ||
@@ -529,7 +527,7 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
     ea.fp16 = f16 ? 1 : 0;
     ea.N = N;
     ea.K = K;
-    PairArgs g = pair_args(N, K, M, 1, true, false, 6.f, f16, dev_err);
+    PairArgs g = pair_args(N, K, M, 1, true, false, f16, dev_err);
     int64_t ld_x = pitch(p->ld_x, K);
     const void* xn = repacked(x, M, K, &ld_x, w.ld_x, w.x, s, &e);
     if (!encode_store_2d(&ea.out, dW, K, N, static_cast<uint64_t>(K) * (p->dW_fp32 ? 4 : 2),
@@ -584,8 +582,7 @@ flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, co
   ea.M = M;
   ea.F = F;
   uint16_t* keep = static_cast<uint16_t*>(pre);
-  PairArgs g = pair_args(M, F, K, 1, false, true, epilogue_ns(p->activation, pre != nullptr, true),
-                         f16, dev_err);
+  PairArgs g = pair_args(M, F, K, 1, false, true, f16, dev_err);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
   int64_t ld_x = pitch(p->ld_x, K), ld_g = K, ld_u = K;
@@ -655,7 +652,7 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
     ea.fp16 = f16 ? 1 : 0;
     ea.M = M;
     ea.K = K;
-    PairArgs g = pair_args(M, K, F, 2, true, false, 6.f, f16, dev_err);
+    PairArgs g = pair_args(M, K, F, 2, true, false, f16, dev_err);
     int64_t ld_g = K, ld_u = K;
     const void* Wgn = repacked(Wg, F, K, &ld_g, w.ld_w, w.Wg, s, &e);
     const void* Wun = repacked(Wu, F, K, &ld_u, w.ld_w, w.Wu, s, &e);
@@ -674,7 +671,7 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
     ea.N = F;
     ea.K = K;
     const uint64_t row = static_cast<uint64_t>(K) * (p->dW_fp32 ? 4 : 2);
-    PairArgs g = pair_args(2 * cdiv(F, 256) * 256, K, M, 1, true, false, 6.f, f16, dev_err);
+    PairArgs g = pair_args(2 * cdiv(F, 256) * 256, K, M, 1, true, false, f16, dev_err);
     g.m_split = g.tiles_m / 2;
     int64_t ld_x = pitch(p->ld_x, K);
     const void* xn = repacked(x, M, K, &ld_x, w.ld_x, w.x, s, &e);

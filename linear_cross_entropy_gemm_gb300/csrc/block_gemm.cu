@@ -58,8 +58,10 @@ template <class Epi>
 static cudaError_t launch(const PairArgs& g, const typename Epi::Args& ea, int sms,
                           cudaStream_t st) {
   if (g.slices > 1) return launch_form<Epi, 1, true>(g, ea, sms, st);
-  return g.halves == 2 ? launch_form<Epi, 2, false>(g, ea, sms, st)
-                       : launch_form<Epi, 1, false>(g, ea, sms, st);
+  if constexpr (Epi::kBMN) {  // the gradients
+    if (g.halves == 2) return launch_form<Epi, 2, false>(g, ea, sms, st);
+  }
+  return launch_form<Epi, 1, false>(g, ea, sms, st);
 }
 
 cudaError_t launch_linear(const PairArgs& g, const LinearArgs& ea, int sms, cudaStream_t st) {

@@ -79,6 +79,8 @@ struct SmallArgs {
   int* dev_err;
 };
 int small_tokens(int64_t M);  // tokens of a tile
+int64_t small_tiles(int64_t M, int64_t N, bool two);
+int64_t small_clusters(int64_t M, int slices);
 int small_slices(int64_t M, int64_t N, int k_blocks, bool two);
 cudaError_t launch_small(bool two, bool w_mn, const SmallArgs& a, cudaStream_t st);
 

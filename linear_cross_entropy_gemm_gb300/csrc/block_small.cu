@@ -403,12 +403,21 @@ static cudaError_t launch_t(const SmallArgs& a, cudaStream_t st) {
 
 int small_tokens(int64_t M) { return M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128; }
 
-int small_slices(int64_t M, int64_t N, int k_blocks, bool two) {
+// Tiles of a product, and the clusters of 1, 2, 4 and 8 CTAs that run at once (as the
+// runtime says) with one CTA to an SM (128 tokens) and with two.
+int64_t small_tiles(int64_t M, int64_t N, bool two) {
   const int64_t nt = small_tokens(M), out = two ? 64 : 128;
-  const int64_t tiles = (N + out - 1) / out * ((M + nt - 1) / nt);
+  return (N + out - 1) / out * ((M + nt - 1) / nt);
+}
+int64_t small_clusters(int64_t M, int slices) {
+  constexpr int kOne[] = {152, 76, 36, 15}, kTwo[] = {304, 152, 74, 36};
+  const int i = slices == 8 ? 3 : slices / 2;
+  return small_tokens(M) <= 64 ? kTwo[i] : kOne[i];
+}
+int small_slices(int64_t M, int64_t N, int k_blocks, bool two) {
+  const int64_t tiles = small_tiles(M, N, two);
   int s = 1;
-  const int64_t places = nt <= 64 ? 304 : 152;
-  while (s < 8 && tiles * s * 2 <= places && 2 * s <= k_blocks) s *= 2;
+  while (s < 8 && tiles <= small_clusters(M, 2 * s) && 2 * s <= k_blocks) s *= 2;
   return s;
 }
 

@@ -5,7 +5,7 @@
 // TMA, warp 1 MMA, the others the epilogue) and computes tiles of 256 rows with
 // cta_group::2. It differs in what bounds layers, whose sums are short and whose
 // tiles are few:
-//   - A tile is HALVES x bn columns wide, bn <= 256 any multiple of 16, so that the
+//   - A tile is HALVES x bn columns wide, bn <= 256 a multiple of 32, so that the
 //     tiles can be cut to fill the GPU's last wave. HALVES = 1 double-buffers the
 //     accumulator: a tile's epilogue runs beside the next tile's MMAs. HALVES = 2
 //     issues two MMAs per K step that share A and fill TMEM with one tile.
@@ -43,7 +43,7 @@ namespace flce {
 // feed-forward products have two of one kind (gate and up).
 //   kTwoB : a tile's columns are the same rows of B and of B2, so both products of a
 //           token and an output column land in one TMEM lane: bn / 2 rows of each, one
-//           from each CTA (HALVES = 1), or bn rows of each, one for each half.
+//           from each CTA. Such tiles have one half.
 //   kTwoK : the sum runs over A B^T and then A2 B2^T, each zero-filled to whole stages.
 //   kTwoA : the first m_split 256-row tiles take A, the others A2.
 enum OperandPlan : int { kOneEach = 0, kTwoB = 1, kTwoK = 2, kTwoA = 3 };
@@ -56,7 +56,7 @@ struct PairArgs {
   int m_split;           // kTwoA: 256-row tiles of the first A
   int halves, bn;        // accumulator columns of a tile: halves x bn
   int slices;            // pairs that share a tile's sum: 1, 2 or 4
-  int band_m, band_n;    // raster: bands of band_m row tiles or band_n column tiles
+  int band_m;            // raster: bands of this many row tiles
   int fp16;
   int* dev_err;
 };
@@ -64,7 +64,7 @@ struct PairArgs {
 __host__ __device__ constexpr int pair_lk(int halves) { return 128 / halves; }  // sum elements of a stage
 // Output columns of a tile.
 __host__ __device__ constexpr int pair_cols(OperandPlan plan, int halves, int bn) {
-  return plan == kTwoB ? halves * bn / 2 : halves * bn;
+  return plan == kTwoB ? bn / 2 : halves * bn;
 }
 
 template <int HALVES>
@@ -183,17 +183,10 @@ __device__ __forceinline__ void bulk_copy_to_cta(uint32_t dst_cluster, uint32_t 
 }
 
 __device__ __forceinline__ void pair_coords(const PairArgs& g, int t, int& tm, int& tn) {
-  if (g.band_m > 0) {
-    const int per = g.band_m * g.tiles_n, b = t / per, r = t - b * per;
-    const int height = min(g.band_m, g.tiles_m - b * g.band_m);
-    tn = r / height;
-    tm = b * g.band_m + (r - tn * height);
-  } else {
-    const int per = g.band_n * g.tiles_m, b = t / per, r = t - b * per;
-    const int width = min(g.band_n, g.tiles_n - b * g.band_n);
-    tm = r / width;
-    tn = b * g.band_n + (r - tm * width);
-  }
+  const int per = g.band_m * g.tiles_n, b = t / per, r = t - b * per;
+  const int height = min(g.band_m, g.tiles_m - b * g.band_m);
+  tn = r / height;
+  tm = b * g.band_m + (r - tn * height);
 }
 
 template <class Epi, int HALVES, bool SPLIT>
@@ -217,7 +210,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  static_assert(!SPLIT || HALVES == 1, "only one-half tiles are split");
+  static_assert(HALVES == 1 || (!SPLIT && kPlan != kTwoB), "forms of one half");
   const int slices = SPLIT ? g.slices : 1;
   const uint32_t cta = cluster_ctarank(), rank = cta & 1;  // in the cluster, in the pair
   const uint32_t even = cta & ~1u;
@@ -280,7 +273,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
       int m0 = tm * 256 + static_cast<int>(rank) * 128;
       const CUtensorMap *pa = &g.a, *pb = &g.b;
       int n0 = tn * cols + static_cast<int>(rank) * (bn / 2);
-      if constexpr (kPlan == kTwoB && HALVES == 1) {
+      if constexpr (kPlan == kTwoB) {
         n0 = tn * cols;
         if (!leader) pb = &g.b2;
       }
@@ -317,8 +310,7 @@ __global__ void __launch_bounds__(kLThreads, 1)
 #pragma unroll
           for (int h = 0; h < HALVES; ++h) {
             uint8_t* b = a + S::kABytes + h * S::kBBytes;
-            if constexpr (kPlan == kTwoB && HALVES == 2) pb = h == 0 ? &g.b : &g.b2;
-            const int nh = n0 + (kPlan == kTwoB ? 0 : h * bn);
+            const int nh = n0 + h * bn;
             if constexpr (!kBMN) {
 #pragma unroll
               for (int j = 0; j < S::kLK / 64; ++j)
@@ -407,8 +399,8 @@ __global__ void __launch_bounds__(kLThreads, 1)
     TileSlice sl;
     sl.width = kPlan == kTwoB ? cols : bn;
     sl.per = (sl.width + 31) / 32;
-    sl.up_off = HALVES == 1 ? bn / 2 : kBN;
-    const int chunks = kPlan == kTwoB ? sl.per : HALVES * sl.per, first = (chunks + 1) / 2;
+    sl.up_off = bn / 2;
+    const int chunks = HALVES * sl.per, first = (chunks + 1) / 2;
     sl.c_lo = warp < 6 ? 0 : first;
     sl.c_hi = warp < 6 ? first : chunks;
     Staging st{stage + (warp - 2) * kStageBytes, 0};
