@@ -130,7 +130,7 @@ struct Staging {
 
 // What an epilogue warp drains: the 32-column chunks [c_lo, c_hi) of a tile. Chunk c
 // lies in half c / per, `width` output columns wide; a half's last chunk ends with it: where
-// the width is no multiple of 32, that chunk starts early and repeats up to 24 columns
+// the width is no multiple of 32, that chunk starts early and repeats 16 columns
 // with the same values.
 struct TileSlice {
   int c_lo, c_hi, per, width;
