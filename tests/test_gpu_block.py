@@ -127,6 +127,24 @@ def test_linear_strides(M, K, N, pad):
     no_device_error()
 
 
+@pytest.mark.parametrize("N", [66, 131, 258, 1025])
+@pytest.mark.parametrize("M,dtype", [(135, BF16), (300, FP16), (1500, BF16)])
+def test_linear_rows_off_the_16_byte_boundaries(M, N, dtype):
+    """Even and odd counts of columns that are no multiple of 8: the output, the kept slopes and
+    the residual, also when the output is the residual."""
+    check_linear(M, 72, N, "gelu_tanh", dtype=dtype)
+    x, W, b, r, _ = linear_problem(M, 72, N, dtype, True, True)
+    want = F.flce_linear_forward(x, W, b, r, activation="gelu_tanh")
+    for pad, off in ((0, 1), (0, 2), (1, 0), (2, 2), (3, 1)):
+        own = strided(r, pad, off)
+        around = own.as_strided((M, N + pad), (N + pad, 1), own.storage_offset())[:-1, N:].clone()
+        got = F.flce_linear_forward(x, W, b, own, activation="gelu_tanh", out=own)
+        assert got is own and torch.equal(own, want)
+        after = own.as_strided((M, N + pad), (N + pad, 1), own.storage_offset())[:-1, N:]
+        assert torch.equal(after.view(torch.int16), around.view(torch.int16)), "wrote between the rows"
+    no_device_error()
+
+
 def test_linear_output_may_be_the_residual():
     for M in (4, 300):
         x, W, b, r, _ = linear_problem(M, 128, 200, BF16, True, True)
