@@ -185,12 +185,10 @@ const TileShape& best_tile(bool mn, int64_t M, int64_t N, int64_t k64, bool two_
   return *best;
 }
 
-// Products of at most this many tokens go to the few-token kernel (measured: 128 tokens
-// through 4096 x 4096 12.4 us against 15.3 us, 256 17.7 against 15.3; gated 4096 x 14336,
-// 64 tokens 48 us against 51 us, 128 54 against 51).
-constexpr int64_t kSmallTokens = 128, kSmallGatedTokens = 64;
-
-int64_t small_most(bool gated) { return gated ? kSmallGatedTokens : kSmallTokens; }
+// Products of at most this many tokens go to the few-token kernel: of 130 products of 33 to 64
+// tokens it takes 1.03 of the faster kernel's time on average, CTA pairs 1.28 to 1.39. (Of 230
+// of 65 to 128 tokens 1.09 to 1.13 and 1.15 to 1.21, the choice below 1.004 to 1.02.)
+constexpr int64_t kSmallTokens = 64;
 
 // And larger ones with few tiles of a long sum, which that kernel cuts into eight slices:
 // 267 x 376 x 12800 25 us by CTA pairs (four tiles, three slices), 13 us. Its ns for 64 sum
@@ -200,7 +198,7 @@ int64_t small_most(bool gated) { return gated ? kSmallGatedTokens : kSmallTokens
 // eight CTAs 15 run at once, and a second wave of them doubled 251 x 1032 x 1312's time.
 constexpr float kSmallNs = 300.f, kSmallRestNs = 4500.f;
 bool few_tokens(bool mn, int64_t M, int64_t N, int64_t k64, bool two_b) {
-  if (M <= small_most(two_b)) return true;
+  if (M <= kSmallTokens) return true;
   const int slices = small_slices(M, N, static_cast<int>(k64), two_b);
   if (small_tiles(M, N, two_b) > small_clusters(M, slices)) return false;
   const float ns = static_cast<float>((k64 + slices - 1) / slices) * kSmallNs + kSmallRestNs;
