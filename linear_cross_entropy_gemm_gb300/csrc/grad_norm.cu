@@ -6,11 +6,11 @@
 // tensors over one wave of blocks, so a hundred small tensors and one large
 // one load the memory alike. Chunks start on 128-byte lines wherever the tensor does,
 // so that a warp's load touches four lines, not five (2.1 GB of fp32 gradients 32
-// bytes off a line: 324 us from the tensor's start, 296 us = 7.1 TB/s so). The table of tensors travels in the kernel's
-// parameters (no copy to the device, nothing to keep alive). Bound by HBM: the
-// norm reads every element once, clipping reads it again and writes it (60 tensors,
-// 683 MB: 338 us = 6.1 TB/s; chunks of 16 and 64 KiB and blocks of 512 threads took 338 to
-// 390).
+// bytes off a line: 324 us from the tensor's start, 296 us = 7.1 TB/s so). The table of
+// tensors travels in the kernel's parameters (no copy to the device, nothing to keep
+// alive). Bound by HBM: the norm reads every element once, clipping reads it again and
+// writes it (60 tensors, 683 MB: 335 us = 6.1 TB/s; chunks of 16 and 64 KiB and blocks of
+// 512 threads took 338 to 390).
 //
 // The norm pass leaves one fp64 sum per block; whoever needs the norm adds those
 // in one fixed order, so the result does not depend on the blocks' timing.

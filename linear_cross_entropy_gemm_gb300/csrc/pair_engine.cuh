@@ -17,7 +17,7 @@
 //   - The issuing warps stay converged and elect their thread, and a stage of the
 //     HALVES = 1 ring holds 128 sum elements: with 64 and a diverged thread a stage took
 //     550 cycles at any width.
-//   - A long sum with few tiles is split: the 2, 4 pairs of a cluster take a part of one
+//   - A long sum with few tiles is split: the 2 or 3 pairs of a cluster take a part of one
 //     tile's sum each, send one another the fp32 partial sums of a share of its columns
 //     through distributed shared memory and add them in rank order (SPLIT; the result
 //     does not depend on timing).
@@ -55,7 +55,7 @@ struct PairArgs {
   int k_split;           // kTwoK: stages of the first product
   int m_split;           // kTwoA: 256-row tiles of the first A
   int halves, bn;        // accumulator columns of a tile: halves x bn
-  int slices;            // pairs that share a tile's sum: 1, 2 or 4
+  int slices;            // pairs that share a tile's sum: 1, 2 or 3
   int band_m;            // raster: bands of this many row tiles
   int fp16;
   int* dev_err;
