@@ -333,7 +333,8 @@ cudaError_t run_passes(const Grads& g, bool clip, float max_norm, float eps, flo
     e = launch_dependent(square_sums_kernel<CAP>, dim3(grid), kThreadsN, 0, 1, st, t, part + parts);
     parts += static_cast<int>(grid);
   }
-  if (!clip && e == cudaSuccess)
+  // Without elements there is no clip pass to write the norm, 0.
+  if ((!clip || parts == 0) && e == cudaSuccess)
     return launch_dependent(norm_kernel, dim3(1), kThreadsN, 0, 1, st, part, parts, norm);
   for (next = 0; next < g.count && e == cudaSuccess;) {
     if (fill(&t, g, &next) == 0) break;

@@ -1,0 +1,45 @@
+"""The layer operators where they could go wrong unseen: outputs that nothing writes, saturated
+activations, features of very different size, infinities, what a call leaves to autograd."""
+import ctypes
+
+import pytest
+import torch
+
+import linear_cross_entropy_gemm_gb300 as F
+from linear_cross_entropy_gemm_gb300 import _lib
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+# ------------------------------------------------------------------ empty lists
+@pytest.mark.parametrize("count", [0, 1, 3, 70, 300, 1100])
+def test_clip_writes_the_norm_of_no_elements(count):
+    """Through the C ABI, into a norm that holds NaN before the call."""
+    lib = _lib.load()
+    ptrs, numel = (ctypes.c_void_p * max(count, 1))(), (ctypes.c_int64 * max(count, 1))()
+    types = (ctypes.c_int32 * max(count, 1))()
+    ws = torch.empty(lib.flce_grad_norm_workspace_size(count), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    for clip in (False, True):
+        norm = torch.full((), float("nan"), device="cuda")
+        tail = (norm.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+        if clip:
+            status = lib.flce_clip_grads(count, ptrs, None, numel, types, 1.0, 1e-6, *tail)
+        else:
+            status = lib.flce_grad_norm(count, ptrs, numel, types, *tail)
+        assert status == 0 and float(norm) == 0.0
+
+
+def test_clip_of_empty_tensors_returns_zero():
+    """The allocator's small blocks hold NaN when the call takes one for its result."""
+    empty = torch.empty(0, device="cuda")
+    blocks = [torch.full((128,), float("nan"), device="cuda") for _ in range(64)]
+    del blocks
+    assert float(F.flce_clip_grads([empty, empty], 1.0)) == 0.0
+    p = torch.nn.Parameter(torch.empty(0, 4, device="cuda"))
+    p.grad = torch.empty(0, 4, device="cuda")
+    blocks = [torch.full((128,), float("nan"), device="cuda") for _ in range(64)]
+    del blocks
+    assert float(F.clip_grad_norm_([p], 1.0)) == 0.0
