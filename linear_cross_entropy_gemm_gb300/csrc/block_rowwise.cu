@@ -213,10 +213,13 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradArgs a) 
   const size_t at = static_cast<size_t>(i) * 8;
   const bool f16 = a.fp16 != 0;
   float d[8], g[8], u[8];
-  unpack8(__ldg(reinterpret_cast<const uint4*>(a.dh + static_cast<size_t>(row) * a.ld_dh + col)),
-          f16, d);
-  decode_group(__ldg(reinterpret_cast<const uint4*>(a.cross + at)), g);
-  decode_group(__ldg(reinterpret_cast<const uint4*>(a.val + at)), u);
+  // Ordinary loads: the kernel is resident while the one before it still writes these.
+  const uint4 dv = *reinterpret_cast<const uint4*>(a.dh + static_cast<size_t>(row) * a.ld_dh + col);
+  const uint4 gv = *reinterpret_cast<const uint4*>(a.cross + at);
+  const uint4 uv = *reinterpret_cast<const uint4*>(a.val + at);
+  unpack8(dv, f16, d);
+  decode_group(gv, g);
+  decode_group(uv, u);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     g[j] *= d[j];
