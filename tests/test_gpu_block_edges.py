@@ -43,3 +43,29 @@ def test_clip_of_empty_tensors_returns_zero():
     blocks = [torch.full((128,), float("nan"), device="cuda") for _ in range(64)]
     del blocks
     assert float(F.clip_grad_norm_([p], 1.0)) == 0.0
+
+
+# -------------------------------------------------------- saturated activations
+def one_by_one(z, dtype):
+    """x and W whose product holds exactly the values z (rounded to dtype) in column 0."""
+    x = torch.zeros(z.numel(), 8, dtype=dtype, device="cuda")
+    x[:, 0] = z.to(dtype)
+    return x, torch.eye(8, dtype=dtype, device="cuda")
+
+
+def gelu64(z):
+    """z Phi(z), with Phi's tail from erfcx."""
+    x = -z / 2 ** 0.5
+    return z * 0.5 * torch.special.erfcx(x) * torch.exp(-x * x)
+
+
+@pytest.mark.parametrize("rows", ["few", "many"])
+def test_gelu_keeps_its_negative_tail(rows):
+    """bf16 holds gelu(-12) = -2e-32: relative to the output's rounding of 2^-8 (it is below
+    2^-126 only under z = -13), the fit is off by 8e-5 and e^(-z^2 / 2) by the fp32 rounding of
+    an exponent of at most 104, 104 2^-24."""
+    z = torch.linspace(-12, -2, 60 if rows == "few" else 600, device="cuda")
+    x, W = one_by_one(z, BF16)
+    y = F.flce_linear_forward(x, W, activation="gelu")[:, 0].double()
+    want = gelu64(x[:, 0].double())
+    assert bool(((y - want).abs() <= (2.0 ** -8 + 8e-5 + 2 * 104 * 2.0 ** -24) * want.abs()).all())
