@@ -439,7 +439,8 @@ size_t flce_gated_workspace_size(const flce_gated_params_t* p, int which);
 /* Forward. Wg, Wu: [F, K] dense. h: [M, F]. pre: NULL, or a dense buffer of 2 M F 16-bit
  * words that receives what the backward needs: with g = x Wg^T and u = x Wu^T, the
  * values a(g), then u a'(g), each with 15 bits and an exponent that 8 neighbours
- * share. h, pre: 16-byte aligned. */
+ * share (an infinity or NaN reads as NaN and leaves its neighbours as they are). h,
+ * pre: 16-byte aligned. */
 flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, const void* Wg,
                                  const void* Wu, void* h, void* pre, void* workspace,
                                  size_t workspace_bytes, int32_t* dev_err, void* stream);

@@ -69,3 +69,39 @@ def test_gelu_keeps_its_negative_tail(rows):
     y = F.flce_linear_forward(x, W, activation="gelu")[:, 0].double()
     want = gelu64(x[:, 0].double())
     assert bool(((y - want).abs() <= (2.0 ** -8 + 8e-5 + 2 * 104 * 2.0 ** -24) * want.abs()).all())
+
+
+# ---------------------------------------------------- infinities in kept values
+def randn(seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return lambda *shape, std=1.0, dtype=BF16: (
+        torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
+
+
+@pytest.mark.parametrize("M", [5, 50, 300])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")], ids=str)
+def test_a_bad_feature_stays_in_its_row_of_the_weight_gradients(M, value):
+    """A weight row with an infinity or NaN makes u a'(g) of its own feature non-finite in every
+    token, and nothing of its seven neighbours'. Those are compared with 64 bits: each dg and
+    du is off by its rounding and the kept value's 2^-14 of the group's largest."""
+    n = randn(M)
+    x, Wg, Wu, dh = n(M, 64), n(72, 64, std=0.125), n(72, 64, std=0.125), n(M, 72)
+    Wu[11, 5] = value
+    pre = torch.empty(2, M, 72, dtype=BF16, device="cuda")
+    F.flce_gated_forward(x, Wg, Wu, pre=pre)
+    dx, dWg, dWu = F.flce_gated_backward(dh, x, Wg, Wu, pre)
+    good = torch.arange(72, device="cuda") != 11
+    assert not bool(dx.isfinite().any()) and not bool(dWg[11].isfinite().any())
+    x64, d64 = x.double(), dh.double()
+    g, u = x64 @ Wg.double().t(), x64 @ Wu.double().t()
+    p = torch.sigmoid(g)
+    u[:, 11] = 0
+    most = [t.abs().reshape(M, 9, 8).amax(2).repeat_interleave(8, 1)
+            for t in (u * p * (1 + g * (1 - p)), g * p)]
+    for got, kept, size, rows in ((dWg, u * p * (1 + g * (1 - p)), most[0], good),
+                                  (dWu, g * p, most[1], torch.ones_like(good))):
+        d = d64 * kept
+        off = 2.0 ** -8 * d.abs() + 1.01 * 2.0 ** -14 * d64.abs() * size + 2.0 ** -16 * d64.abs()
+        bound = off.t() @ x64.abs() + M * 2.0 ** -23 * (d.abs().t() @ x64.abs())
+        err = (got.double() - d.t() @ x64).abs()
+        assert bool((err <= bound)[rows].all())
