@@ -382,6 +382,13 @@ typedef enum {
   FLCE_ACT_SIGMOID = 5
 } flce_activation_t;
 
+/* How a forward keeps what its backward needs, in 16 bits a value either way.
+ *   FIXED     linear: the slopes a'(z) in steps of 2^-15. A slope below 2^-16 is kept as 0, one
+ *             of 2^-12 within 6 %: units that saturate lose their gradients.
+ *   RELATIVE  linear: the same, but slopes of saturated units (smaller than 2^-6) within 2^-10
+ *             of themselves down to 2^-44, and within 2^-54 below that. */
+typedef enum { FLCE_KEEP_FIXED = 0, FLCE_KEEP_RELATIVE = 1 } flce_keep_t;
+
 /* y = a(z) + r, z = x W^T + b. */
 typedef struct {
   int64_t M;              /* tokens (rows of x); 0 is a valid no-op */
@@ -394,6 +401,7 @@ typedef struct {
   int32_t input_fp16;     /* 0: bf16 operands, 1: fp16 */
   int32_t dW_fp32;        /* backward: 1 = dW in fp32, 0 = in the operands' type */
   int32_t db_fp32;        /* backward: 1 = db in fp32, 0 = in the operands' type */
+  int32_t keep;           /* flce_keep_t of pre, the same in forward and backward */
 } flce_linear_params_t;
 
 /* Workspace bytes: which = 0 forward, 1 backward. 0 for invalid parameters, for
@@ -404,7 +412,7 @@ size_t flce_linear_workspace_size(const flce_linear_params_t* p, int which);
 /* Forward. W: [N, K] dense. y: [M, N]; it may be the residual's own buffer (with
  * the same pitch), which it then replaces. pre: NULL, or a dense buffer of M N 16-bit
  * words, 16-byte aligned, that receives what the backward of a call with an
- * activation needs: the slopes a'(z) in steps of 2^-15. */
+ * activation needs: the slopes a'(z) in the form p->keep. */
 flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, const void* W,
                                   const void* b, const void* residual, void* y, void* pre,
                                   void* workspace, size_t workspace_bytes, int32_t* dev_err,

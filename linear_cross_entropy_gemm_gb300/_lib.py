@@ -47,16 +47,18 @@ class FlceParams(ctypes.Structure):
     ]
 
 
-# flce_activation_t and flce_dtype_t.
+# flce_activation_t, flce_dtype_t.
 ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "sigmoid": 5}
 DTYPES = {"bf16": 0, "fp16": 1, "fp32": 2}
+# flce_keep_t.
+KEEP = {"fixed": 0, "relative": 1}
 
 
 class FlceLinearParams(ctypes.Structure):
     """Mirror of flce_linear_params_t."""
     _fields_ = [(f, ctypes.c_int64) for f in ("M", "K", "N", "ld_x", "ld_res", "ld_y")] + \
         [(f, ctypes.c_int32) for f in ("activation", "has_bias", "has_residual", "input_fp16",
-                                       "dW_fp32", "db_fp32")]
+                                       "dW_fp32", "db_fp32", "keep")]
 
 
 class FlceGatedParams(ctypes.Structure):

@@ -21,7 +21,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import _lib
-from ._lib import ACTIVATIONS
+from ._lib import ACTIVATIONS, KEEP
 
 
 class _On:
@@ -69,8 +69,11 @@ def flce_linear_forward(x: torch.Tensor, W: torch.Tensor, b: Optional[torch.Tens
     x [M, K] and W [N, K] are bf16 or fp16, K a multiple of 8; x's rows may be
     strided (a multiple of 8 elements). b [N]; residual and ``out`` [M, N] with
     rows of any pitch, ``out`` may be the residual itself. ``pre`` (an [M, N]
-    tensor of x's type, by its size alone) receives what flce_linear_backward
-    needs of a layer with an activation: the slopes a'(z), not numbers of x's type. ``workspace``: as in flce_forward."""
+    tensor) receives what flce_linear_backward needs of a layer with an activation:
+    the slopes a'(z), in a form of their own. An int16 tensor takes them with
+    relative precision where units saturate (2^-10 of the slope); one of x's type (by
+    its size alone) in fixed steps of 2^-15, in which slopes below 2^-16 are 0.
+    ``workspace``: as in flce_forward."""
     if stream is not None:
         with _On(x.device, stream):
             return _calls.linear_forward(x, W, b, residual, activation, pre, out, workspace)
@@ -192,14 +195,22 @@ def _usable(t: torch.Tensor) -> torch.Tensor:
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
+def _kept_dtype(x: torch.Tensor, keep: str) -> torch.dtype:
+    if keep not in KEEP:
+        raise ValueError(f"flce: keep must be one of {sorted(KEEP)}, got {keep!r}")
+    return torch.int16 if keep == "relative" else x.dtype
+
+
 class FusedLinearFunction(torch.autograd.Function):
-    """Autograd form of the linear layer. It keeps x, and the slopes of an activation."""
+    """Autograd form of the linear layer. It keeps x, and the slopes of an activation in the
+    form ``keep``."""
 
     @staticmethod
-    def forward(ctx, x, weight, bias, residual, activation):
+    def forward(ctx, x, weight, bias, residual, activation, keep="fixed"):
         pre = None
+        dtype = _kept_dtype(x, keep)
         if activation != "none" and any(ctx.needs_input_grad[:3]):
-            pre = torch.empty(x.shape[0], weight.shape[0], dtype=x.dtype, device=x.device)
+            pre = torch.empty(x.shape[0], weight.shape[0], dtype=dtype, device=x.device)
         y = flce_linear_forward(x, weight, bias, residual, activation=activation, pre=pre)
         ctx.save_for_backward(x, weight, bias, pre)
         ctx.activation = activation
@@ -215,7 +226,7 @@ class FusedLinearFunction(torch.autograd.Function):
             dx, dW, db = flce_linear_backward(d, x, weight, bias, activation=ctx.activation,
                                               pre=pre, dW_dtype=weight.dtype, db_dtype=x.dtype,
                                               needs=ctx.needs_input_grad[:3])
-        return dx, dW, db, dy if ctx.needs_input_grad[3] else None, None
+        return dx, dW, db, dy if ctx.needs_input_grad[3] else None, None, None
 
 
 class GatedLinearFunction(torch.autograd.Function):
@@ -241,17 +252,20 @@ class GatedLinearFunction(torch.autograd.Function):
         return dx, dWg if need_g else None, dWu if need_u else None, None
 
 
-def fused_linear(x, weight, bias=None, residual=None, activation="none"):
+def fused_linear(x, weight, bias=None, residual=None, activation="none", keep="fixed"):
     """activation(x weight^T + bias) + residual with gradients; x [..., K], weight
     [N, K], residual [..., N]. Inputs whose rows the kernels cannot read as they
-    are (flce_linear_forward) are copied first."""
+    are (flce_linear_forward) are copied first. ``keep``: how the slopes of the
+    activation are kept for the backward, "fixed" (steps of 2^-15: a saturated
+    unit's gradient is lost) or "relative" (2^-10 of the slope there); both take
+    two bytes a value."""
     x2 = _usable(x.reshape(-1, x.shape[-1]))
     r2 = None
     if residual is not None:
         r2 = residual.reshape(-1, weight.shape[0])
         if r2.stride(1) != 1 or r2.stride(0) < r2.shape[1]:
             r2 = r2.contiguous()
-    y = FusedLinearFunction.apply(x2, weight, bias, r2, activation)
+    y = FusedLinearFunction.apply(x2, weight, bias, r2, activation, keep)
     return y.reshape(*x.shape[:-1], weight.shape[0])
 
 

@@ -26,6 +26,7 @@ constexpr int64_t kMaxTokens = 1LL << 30, kMaxFeatures = 1LL << 24;
 
 bool act_ok(int32_t a) { return a >= FLCE_ACT_NONE && a <= FLCE_ACT_SIGMOID; }
 bool aligned2(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 1) == 0; }
+bool keep_ok(int32_t k) { return k == FLCE_KEEP_FIXED || k == FLCE_KEEP_RELATIVE; }
 bool flag_ok(int32_t f) { return f == 0 || f == 1; }
 // A row pitch as given (0: dense).
 int64_t pitch(int64_t ld, int64_t dense) { return ld == 0 ? dense : ld; }
@@ -47,7 +48,8 @@ flce_status_t check(const flce_linear_params_t* p) {
   const flce_status_t st = check_sizes(p->M, p->K, p->N);
   if (st != FLCE_OK) return st;
   if (!act_ok(p->activation) || !flag_ok(p->has_bias) || !flag_ok(p->has_residual) ||
-      !flag_ok(p->input_fp16) || !flag_ok(p->dW_fp32) || !flag_ok(p->db_fp32))
+      !flag_ok(p->input_fp16) || !flag_ok(p->dW_fp32) || !flag_ok(p->db_fp32) ||
+      !keep_ok(p->keep))
     return FLCE_ERR_INVALID_ARG;
   if (!pitch_ok(p->ld_x, p->K) || !pitch_ok(p->ld_res, p->N) || !pitch_ok(p->ld_y, p->N))
     return FLCE_ERR_INVALID_ARG;
@@ -420,6 +422,7 @@ flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, 
     sa.ld_res = pitch(p->ld_res, N);
     sa.res_vec = aligned16(residual) && sa.ld_res % 8 == 0 ? 1 : 0;
     sa.keep = static_cast<uint16_t*>(pre);
+    sa.relative = p->keep == FLCE_KEEP_RELATIVE ? 1 : 0;
     sa.act = p->activation;
     return done(launch_small(false, false, sa, static_cast<cudaStream_t>(stream)));
   }
@@ -432,7 +435,7 @@ flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, 
   ea.res_vec = aligned16(residual) && ea.ld_res % 8 == 0 ? 1 : 0;
   ea.act = p->activation;
   ea.fp16 = f16 ? 1 : 0;
-  ea.keep = pre ? 1 : 0;
+  ea.keep = !pre ? 0 : p->keep == FLCE_KEEP_RELATIVE ? 2 : 1;
   ea.M = M;
   ea.N = N;
   PairArgs g = pair_args(M, N, K, 1, false, false, f16, dev_err);
@@ -491,6 +494,7 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
     za.M = M;
     za.N = N;
     za.fp16 = f16 ? 1 : 0;
+    za.tail = p->activation == FLCE_ACT_SIGMOID ? 0x1p82f : -0x1p82f;
     za.vec = dy_rows16 && (!act || N % 8 == 0) ? 1 : 0;
     if (launch_dz(za, s) != cudaSuccess) return FLCE_ERR_CUDA;
     if (db && launch_db_sum(w.part, dz_parts(M, N), N, db, p->db_fp32 != 0, f16, s) != cudaSuccess)

@@ -145,11 +145,17 @@ __device__ __forceinline__ void act_all(int act, float (&v)[N]) {
 }
 
 // ------------------------------------------------------- kept for the backward
-// The backward's error should be that of its own roundings, so what the forward keeps
-// in 16 bits per value has more significant bits than the operands' types.
+// The backward's error should be that of its own roundings. What the forward keeps in 16
+// bits a value takes one of two forms (flce_keep_t).
 //
-// Linear: the slope a'(z), which lies in (-0.2, 1.2) for every activation, as a fixed
-// point number of 2^-15 steps from -0.25 (0 and 1 are exact; 65535: NaN).
+// Linear: the slope a'(z), which lies in (-0.13, 1.13) for every activation, as a fixed
+// point number of 2^-15 steps from -0.25 (0 and 1 are exact; 65535: NaN). Far from 0 that is
+// finer than the operands' types; the slope of a saturated unit is lost in it.
+// FLCE_KEEP_RELATIVE: below 2^-6 the slopes of a saturated unit (sigmoid: all; the others: z
+// under -2) take the codes that the fixed form leaves unused, as floating point numbers of 9
+// bits: 45312 + the bits above the 14th of |a'| 2^-82, which go on with the fixed form's step at
+// 2^-6, are off by 2^-10 of the slope down to 2^-44 and by 2^-54 below. Around the zeros of
+// a' at z = -1.3 .. -0.7 the steps stay fixed. Every other code is that of the fixed form.
 //
 // Gated: a(g) and u a'(g), whose range has no bound, in groups of 8 columns that share
 // an exponent: value = q 2^(eb - 140) 16384 / 16383, q a 15-bit integer, eb the exponent
@@ -167,17 +173,47 @@ __device__ __forceinline__ uint32_t encode_slopes(uint64_t s) {
   return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x5410);
 }
 
+constexpr uint32_t kTailCode = 45312u;  // above the fixed code of any slope, (1.13 + 0.25) 2^15
+template <int ACT>
+__device__ __forceinline__ uint32_t encode_slopes_relative(uint64_t z, uint64_t s) {
+  const uint32_t fixed = encode_slopes(s);
+  if constexpr (ACT == kActNone || ACT == kActRelu) return fixed;
+  constexpr uint64_t kSign = 0x8000000080000000ull;
+  float za, zb, sa, sb, ta, tb;
+  f32x2_split(z, za, zb);
+  f32x2_split(s, sa, sb);
+  f32x2_split(fmul2(s & ~kSign, splat(0x1p-82f)), ta, tb);
+  // Not of a NaN: no comparison holds.
+  const bool low_a = ACT == kActSigmoid ? sa < 0x1p-6f : sa > -0x1p-6f && za < -2.f;
+  const bool low_b = ACT == kActSigmoid ? sb < 0x1p-6f : sb > -0x1p-6f && zb < -2.f;
+  const uint32_t ca = ((__float_as_uint(ta) + 0x2000u) >> 14) + kTailCode;
+  const uint32_t cb = ((__float_as_uint(tb) + 0x2000u) >> 14) + kTailCode;
+  return __byte_perm(low_a ? ca : fixed, low_b ? cb << 16 : fixed, 0x7610);
+}
+
 // v = a(v), and the codes of the slopes.
 template <int N>
-__device__ __forceinline__ void act_keep_slopes(int act, float (&v)[N], uint32_t (&w)[N / 2]) {
+__device__ __forceinline__ void act_keep_slopes(int act, bool relative, float (&v)[N],
+                                                uint32_t (&w)[N / 2]) {
   with_act(act, [&](auto a) {
+    constexpr int kAct = decltype(a)::value;
+    const auto all = [&](auto rel) {
 #pragma unroll
-    for (int j = 0; j < N; j += 2) {
-      uint64_t val, slope;
-      act2<decltype(a)::value>(f32x2(v[j], v[j + 1]), val, slope);
-      w[j / 2] = encode_slopes(slope);
-      f32x2_split(val, v[j], v[j + 1]);
-    }
+      for (int j = 0; j < N; j += 2) {
+        uint64_t val, slope;
+        const uint64_t z = f32x2(v[j], v[j + 1]);
+        act2<kAct>(z, val, slope);
+        if constexpr (decltype(rel)::value)
+          w[j / 2] = encode_slopes_relative<kAct>(z, slope);
+        else
+          w[j / 2] = encode_slopes(slope);
+        f32x2_split(val, v[j], v[j + 1]);
+      }
+    };
+    if (kAct != kActNone && kAct != kActRelu && relative)
+      all(std::true_type());
+    else
+      all(std::false_type());
   });
 }
 // v = a(v), and x = u a'(v).
@@ -193,9 +229,13 @@ __device__ __forceinline__ void act_cross(int act, float (&v)[N], const float (&
     }
   });
 }
-__device__ __forceinline__ float decode_slope(uint32_t code) {
+// A kept slope in either form. tail: 2^82, with the sign that the activation's slope has where
+// the unit is saturated.
+__device__ __forceinline__ float decode_slope(uint32_t code, float tail) {
   const float q = __uint_as_float(0x4B000000u + code) - 8388608.f;
-  return code == 65535u ? __uint_as_float(0x7FFFFFFFu) : fmaf(q, 1.f / 32768.f, -0.25f);
+  const float low = __uint_as_float((code - kTailCode) << 14) * tail;
+  const float v = code >= kTailCode ? low : fmaf(q, 1.f / 32768.f, -0.25f);
+  return code == 65535u ? __uint_as_float(0x7FFFFFFFu) : v;
 }
 
 __device__ __forceinline__ uint32_t largest_bits(const float* v) {
@@ -488,7 +528,8 @@ struct LinearArgs {
   const uint16_t* res;   // [M, ld_res] or null; may be the output itself
   int64_t ld_res;
   int res_vec;           // the residual's rows start on 16-byte boundaries
-  int act, fp16, keep;   // keep: also write the slopes
+  int act, fp16;
+  int keep;              // also write the slopes; 2: in the relative form
   int M, N;
   Out16 y, slope;
 };
@@ -513,7 +554,7 @@ struct LinearEpi {
       if (a.bias) add_row_16(a.bias + col0, a.N - col0, f16, v);
       if (a.keep) {
         uint32_t w[16];
-        act_keep_slopes(a.act, v, w);
+        act_keep_slopes(a.act, a.keep == 2, v, w);
         put_words(a.slope, a.M, a.N, row0, col0, w, st, lane);
       } else {
         act_all(a.act, v);

@@ -73,6 +73,7 @@ struct SmallArgs {
   int64_t ld_res, ld_y;
   int res_vec, y_vec;  // rows start on 16-byte boundaries
   int act, fp16;
+  int relative;    // keep in the relative form
   int M, N;
   int k_blocks, k_split;  // blocks of 64 of the whole sum; those of the first segment
   int slices;             // K slices = cluster size: 1, 2, 4 or 8
@@ -93,6 +94,7 @@ struct DzArgs {
   int64_t ld_dz;
   float* part;         // [dz_parts(M, N), N] column sums of dz, or null
   int M, N, fp16;
+  float tail;          // of decode_slope (block_epilogues.cuh)
   int vec;             // dy, slope and dz rows start on 16-byte boundaries
 };
 int dz_parts(int64_t M, int64_t N);

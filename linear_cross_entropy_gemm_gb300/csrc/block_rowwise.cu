@@ -84,8 +84,8 @@ __global__ void __launch_bounds__(32 * kDzRowGroups) dz_kernel(const DzArgs a, i
           const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            v[2 * j] *= decode_slope(w[j] & 0xFFFFu);
-            v[2 * j + 1] *= decode_slope(w[j] >> 16);
+            v[2 * j] *= decode_slope(w[j] & 0xFFFFu, a.tail);
+            v[2 * j + 1] *= decode_slope(w[j] >> 16, a.tail);
           }
         }
         if (a.dz)
@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(32 * kDzRowGroups) dz_kernel(const DzArgs a, i
         const int c = first + j * step;
         if (c >= a.N) continue;
         float v = unpack_16(a.dy[static_cast<size_t>(r) * a.ld_dy + c], f16);
-        if (a.slope) v *= decode_slope(a.slope[static_cast<size_t>(r) * a.N + c]);
+        if (a.slope) v *= decode_slope(a.slope[static_cast<size_t>(r) * a.N + c], a.tail);
         if (a.dz) a.dz[static_cast<size_t>(r) * a.ld_dz + c] = to16(v, f16);
         sum[j] += v;
       }

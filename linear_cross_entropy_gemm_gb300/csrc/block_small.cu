@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(kSmThreads)
       }
       if (a.keep) {
         uint32_t w[4];
-        act_keep_slopes(a.act, v[0], w);
+        act_keep_slopes(a.act, a.relative != 0, v[0], w);
         uint16_t* k = a.keep + row * a.N + col;
         if (a.N % 8 == 0) {
           *reinterpret_cast<uint4*>(k) = make_uint4(w[0], w[1], w[2], w[3]);

@@ -111,6 +111,19 @@ void dense(const Tensor& t, at::IntArrayRef shape, const Tensor& x, const char* 
     refuse(PyExc_ValueError, "flce: %s must be contiguous and of the call's shape", name);
 }
 
+// The kept values: of x's type in the fixed form, int16 in the relative one.
+int32_t kept(const Tensor& t, at::IntArrayRef shape, const Tensor& x) {
+  if (t.scalar_type() != at::kShort) {
+    dense(t, shape, x, "pre");
+    return FLCE_KEEP_FIXED;
+  }
+  if (!t.is_cuda() || t.get_device() != x.get_device())
+    refuse(PyExc_ValueError, "flce: %s must be on x's device", "pre");
+  if (t.sizes() != shape || !t.is_contiguous())
+    refuse(PyExc_ValueError, "flce: %s must be contiguous and of the call's shape", "pre");
+  return FLCE_KEEP_RELATIVE;
+}
+
 void check_weight(const Tensor& W, const Tensor& x, const char* name) {
   if (W.dim() != 2 || W.size(1) != x.size(1))
     refuse(PyExc_ValueError, "flce: %s must have as many columns as x", name);
@@ -192,7 +205,7 @@ PyObject* linear_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const c10::cuda::CUDAGuard guard(x.device());
     p.has_residual = res ? 1 : 0;
     if (res) p.ld_res = rows_of(*res, p.M, p.N, x, "residual");
-    if (pre) dense(*pre, {p.M, p.N}, x, "pre");
+    if (pre) p.keep = kept(*pre, {p.M, p.N}, x);
     if (out) p.ld_y = rows_of(*out, p.M, p.N, x, "out");
     const Tensor y = out ? *out : at::empty({p.M, p.N}, x.options());
     const Tensor ws = scratch(a[7], flce_linear_workspace_size(&p, 0), x);
@@ -222,7 +235,7 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else {
       if (!pre)
         refuse(PyExc_ValueError, "flce: the backward of a layer with an activation needs %s", "pre=");
-      dense(*pre, {p.M, p.N}, x, "pre");
+      p.keep = kept(*pre, {p.M, p.N}, x);
     }
     Tensor dx, dW, db;
     if (PyObject_IsTrue(a[8])) dx = at::empty({p.M, p.K}, x.options());

@@ -5,12 +5,19 @@ import ctypes
 import pytest
 import torch
 
+import block_reference as R
 import linear_cross_entropy_gemm_gb300 as F
 from linear_cross_entropy_gemm_gb300 import _lib
 
 pytestmark = pytest.mark.gpu
 
 BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+
+
+def randn(seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return lambda *shape, std=1.0, dtype=BF16: (
+        torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
 
 
 # ------------------------------------------------------------------ empty lists
@@ -71,13 +78,98 @@ def test_gelu_keeps_its_negative_tail(rows):
     assert bool(((y - want).abs() <= (2.0 ** -8 + 8e-5 + 2 * 104 * 2.0 ** -24) * want.abs()).all())
 
 
+# Kept slopes in the relative form: off by 2^-10 of the slope (where it is above 2^-6 by 2^-16),
+# by 2^-54 below 2^-44. An activation's slope at a given z is evaluated to 2^-14 of itself there
+# (gelu's fit 8e-5 of a part of it; exponents up to 200 in fp32).
+KEPT, FLOOR, EVAL = 2.0 ** -10, 2.0 ** -54, 2.0 ** -14
+SATURATED = [("silu", -30.0, -2.5), ("sigmoid", -30.0, -2.5), ("gelu", -9.0, -2.5),
+             ("gelu_tanh", -9.0, -2.5)]
+
+
+def slope64(z, act):
+    """a'(z), every term formed without cancellation for z below -1.5 (and for sigmoid anywhere)."""
+    if act == "sigmoid":
+        return torch.sigmoid(z) * torch.sigmoid(-z)
+    if act == "silu":
+        return torch.sigmoid(z) * (1 + z * torch.sigmoid(-z))
+    if act == "gelu":
+        x = -z / 2 ** 0.5
+        return torch.exp(-x * x) * (0.5 * torch.special.erfcx(x) + z / (2 * torch.pi) ** 0.5)
+    c = (2 / torch.pi) ** 0.5
+    w = 2 * c * (z + 0.044715 * z ** 3)
+    p, q = torch.sigmoid(w), torch.sigmoid(-w)
+    return p * (1 + z * q * 2 * c * (1 + 3 * 0.044715 * z * z))
+
+
+@pytest.mark.parametrize("act,lo,hi", SATURATED)
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("M", [40, 700])
+def test_saturated_units_keep_their_gradients(act, lo, hi, dtype, M):
+    x, W = one_by_one(torch.linspace(lo, hi, M, device="cuda"), dtype)
+    z = x[:, 0].double()
+    scale = 512.0  # keeps fp16's gradients away from its smallest numbers
+    dy = torch.full((M, 8), scale, dtype=dtype, device="cuda")
+    want = scale * slope64(z, act)
+    u = R.UNIT[dtype]
+    size, floor = want.abs(), scale * FLOOR
+    pre = torch.empty(M, 8, dtype=torch.int16, device="cuda")
+    F.flce_linear_forward(x, W, W[0], activation=act, pre=pre)
+    x0 = x.clone()
+    x0[:, 0] -= 1  # the bias is 1 in column 0
+    F.flce_linear_forward(x0, W, W[0], activation=act, pre=pre)
+    z0 = x0[:, 0].double() + 1
+    want0 = scale * slope64(z0, act)
+    db = F.flce_linear_backward(dy, x0, W, W[0], activation=act, pre=pre)[2]
+    total = want0.sum()
+    assert abs(float(db[0]) - float(total)) <= float(
+        (KEPT + EVAL + M * 2.0 ** -23) * want0.abs().sum() + M * floor)
+    leaf = x.clone().requires_grad_()
+    y = F.fused_linear(leaf, W, activation=act, keep="relative")
+    y.backward(dy)
+    got = leaf.grad[:, 0].double()
+    # dz, then dx, is rounded.
+    bound = (2 * u + KEPT + EVAL) * (1 + u) * size + floor + 2 * R.TINY[dtype]
+    assert bool(((got - want).abs() <= bound).all())
+
+
+@pytest.mark.parametrize("act", ["silu", "sigmoid", "gelu_tanh"])
+@pytest.mark.parametrize("M", [9, 300])
+def test_units_far_below_zero_train(act, M):
+    """Biases of -14 to -5: dz, dW and db against 64 bits, relative to their own size. z is off by
+    its fp32 sum, and the slope of these activations by at most 12 times as much of itself."""
+    n = randn(M)
+    K, N = 64, 72
+    x, W, dy = n(M, K), n(N, K, std=0.01), n(M, N)
+    b = torch.linspace(-14 if act != "gelu_tanh" else -6, -5, N, device="cuda").to(BF16)
+    pre = torch.empty(M, N, dtype=torch.int16, device="cuda")
+    F.flce_linear_forward(x, W, b, activation=act, pre=pre)
+    dx, dW, db = F.flce_linear_backward(dy, x, W, b, activation=act, pre=pre)
+    z, z_off = R.sums(x, W, b)
+    dz = dy.double() * slope64(z, act)
+    off = (KEPT + EVAL + 12 * z_off) * dz.abs() + FLOOR * dy.double().abs()
+    u = R.UNIT[BF16]
+    assert bool(((db.double() - dz.sum(0)).abs() <= off.sum(0) + M * R.ADD * dz.abs().sum(0)).all())
+    off = off * (1 + u) + u * dz.abs()
+    R.assert_within(dW, R.product(dz.t(), off.t(), x.double(), FP32), "dW")
+    R.assert_within(dx, R.product(dz, off, W.double(), BF16), "dx")
+
+
+def test_kept_forms_agree_where_units_are_not_saturated():
+    """The relative form's codes are the fixed form's, and with them every gradient."""
+    n = randn(3)
+    x, W, dy = n(300, 64), n(77, 64, std=0.125), n(300, 77)
+    x[7, 3] = float("nan")
+    for act in ("silu", "gelu", "gelu_tanh", "relu", "none"):
+        fixed, relative = (torch.empty(300, 77, dtype=t, device="cuda") for t in (BF16, torch.int16))
+        F.flce_linear_forward(x, W, activation=act, pre=fixed)
+        F.flce_linear_forward(x, W, activation=act, pre=relative)
+        slopes = R.kept_slopes(fixed)
+        same = ~((slopes.abs() < 2.0 ** -6) & (x.double() @ W.double().t() < -1.9))
+        assert torch.equal(fixed.view(torch.int16)[same], relative[same]) and bool(same.any())
+        assert bool(R.kept_slopes(relative)[7].isnan().all()) == (act not in ("relu", "none"))
+
+
 # ---------------------------------------------------- infinities in kept values
-def randn(seed):
-    g = torch.Generator(device="cuda").manual_seed(seed)
-    return lambda *shape, std=1.0, dtype=BF16: (
-        torch.randn(shape, generator=g, device="cuda") * std).to(dtype)
-
-
 @pytest.mark.parametrize("M", [5, 50, 300])
 @pytest.mark.parametrize("value", [float("inf"), float("nan")], ids=str)
 def test_a_bad_feature_stays_in_its_row_of_the_weight_gradients(M, value):
