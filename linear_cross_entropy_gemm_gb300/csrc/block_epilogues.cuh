@@ -108,8 +108,17 @@ __device__ __forceinline__ void act2(uint64_t z, uint64_t& val, uint64_t& slope)
     val = fmul2(z, p);
     slope = ffma2(val, ffma2(p, splat(-1.f), splat(1.f)), p);
   } else if constexpr (ACT == kActSigmoid) {
-    val = sigmoid2(z);
-    slope = fmul2(val, ffma2(val, splat(-1.f), splat(1.f)));
+    // With e = e^-|z| and r = 1 / (1 + e): sigmoid is r above 0 and e r below, its slope e r^2 on
+    // both sides. 1 - r would lose it where r rounds to 1.
+    constexpr uint64_t kSign = 0x8000000080000000ull;
+    const uint64_t e = exp2_2(fmul2(z | kSign, splat(kLog2e))), r = rcp2(fadd2(e, splat(1.f)));
+    const uint64_t er = fmul2(e, r);
+    float a, b, ra, rb, ea, eb;
+    f32x2_split(z, a, b);
+    f32x2_split(r, ra, rb);
+    f32x2_split(er, ea, eb);
+    val = f32x2(a < 0.f ? ea : ra, b < 0.f ? eb : rb);
+    slope = fmul2(er, r);
   } else {
     val = z;
     slope = splat(1.f);

@@ -82,7 +82,7 @@ def test_gelu_keeps_its_negative_tail(rows):
 # by 2^-54 below 2^-44. An activation's slope at a given z is evaluated to 2^-14 of itself there
 # (gelu's fit 8e-5 of a part of it; exponents up to 200 in fp32).
 KEPT, FLOOR, EVAL = 2.0 ** -10, 2.0 ** -54, 2.0 ** -14
-SATURATED = [("silu", -30.0, -2.5), ("sigmoid", -30.0, -2.5), ("gelu", -9.0, -2.5),
+SATURATED = [("silu", -30.0, -2.5), ("sigmoid", -30.0, -2.5), ("sigmoid", 2.5, 30.0), ("gelu", -9.0, -2.5),
              ("gelu_tanh", -9.0, -2.5)]
 
 
