@@ -385,8 +385,12 @@ typedef enum {
 /* How a forward keeps what its backward needs, in 16 bits a value either way.
  *   FIXED     linear: the slopes a'(z) in steps of 2^-15. A slope below 2^-16 is kept as 0, one
  *             of 2^-12 within 6 %: units that saturate lose their gradients.
+ *             gated: within 2^-14 of the largest of 8 neighbouring columns: a column 1000 times
+ *             smaller than its neighbour is off by 6 %.
  *   RELATIVE  linear: the same, but slopes of saturated units (smaller than 2^-6) within 2^-10
- *             of themselves down to 2^-44, and within 2^-54 below that. */
+ *             of themselves down to 2^-44, and within 2^-54 below that.
+ *             gated: within 2^-11 of the value itself or, for values under 2^-13 of the largest
+ *             neighbour's, 2^-24 of that. */
 typedef enum { FLCE_KEEP_FIXED = 0, FLCE_KEEP_RELATIVE = 1 } flce_keep_t;
 
 /* y = a(z) + r, z = x W^T + b. */
@@ -440,6 +444,7 @@ typedef struct {
   int32_t activation;  /* flce_activation_t */
   int32_t input_fp16;  /* 0: bf16 operands, 1: fp16 */
   int32_t dW_fp32;     /* backward: 1 = dWg and dWu in fp32, 0 = in the operands' type */
+  int32_t keep;        /* flce_keep_t of pre, the same in forward and backward */
 } flce_gated_params_t;
 
 size_t flce_gated_workspace_size(const flce_gated_params_t* p, int which);
@@ -447,8 +452,8 @@ size_t flce_gated_workspace_size(const flce_gated_params_t* p, int which);
 /* Forward. Wg, Wu: [F, K] dense. h: [M, F]. pre: NULL, or a dense buffer of 2 M F 16-bit
  * words that receives what the backward needs: with g = x Wg^T and u = x Wu^T, the
  * values a(g), then u a'(g), each with 15 bits and an exponent that 8 neighbours
- * share (an infinity or NaN reads as NaN and leaves its neighbours as they are). h,
- * pre: 16-byte aligned. */
+ * share, in the form p->keep (an infinity or NaN reads as NaN and leaves its neighbours as
+ * they are). h, pre: 16-byte aligned. */
 flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, const void* Wg,
                                  const void* Wu, void* h, void* pre, void* workspace,
                                  size_t workspace_bytes, int32_t* dev_err, void* stream);

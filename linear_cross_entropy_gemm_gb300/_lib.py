@@ -64,7 +64,7 @@ class FlceLinearParams(ctypes.Structure):
 class FlceGatedParams(ctypes.Structure):
     """Mirror of flce_gated_params_t."""
     _fields_ = [(f, ctypes.c_int64) for f in ("M", "K", "F", "ld_x", "ld_h")] + \
-        [(f, ctypes.c_int32) for f in ("activation", "input_fp16", "dW_fp32")]
+        [(f, ctypes.c_int32) for f in ("activation", "input_fp16", "dW_fp32", "keep")]
 
 
 class FlceTrace(ctypes.Structure):

@@ -116,8 +116,10 @@ def flce_gated_forward(x: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, *,
 
     x [M, K], Wg and Wu [F, K] are bf16 or fp16, K and F multiples of 8; the rows
     of x and ``out`` may be strided (a multiple of 8 elements). ``pre`` (a
-    [2, M, F] tensor of x's type, by its size alone) receives what
-    flce_gated_backward needs, in a form of its own. ``workspace``: as in flce_forward."""
+    [2, M, F] tensor) receives what flce_gated_backward needs, in a form of its own:
+    an int16 tensor takes it with relative precision (2^-11 of each value), one of
+    x's type (by its size alone) to 2^-14 of the largest of 8 neighbouring columns.
+    ``workspace``: as in flce_forward."""
     if stream is not None:
         with _On(x.device, stream):
             return _calls.gated_forward(x, Wg, Wu, activation, pre, out, workspace)
@@ -230,13 +232,15 @@ class FusedLinearFunction(torch.autograd.Function):
 
 
 class GatedLinearFunction(torch.autograd.Function):
-    """Autograd form of the gated projection. It keeps x and 32 bits for each output."""
+    """Autograd form of the gated projection. It keeps x and 32 bits for each output,
+    in the form ``keep``."""
 
     @staticmethod
-    def forward(ctx, x, gate_weight, up_weight, activation):
+    def forward(ctx, x, gate_weight, up_weight, activation, keep="relative"):
         pre = None
+        dtype = _kept_dtype(x, keep)
         if any(ctx.needs_input_grad[:3]):
-            pre = torch.empty(2, x.shape[0], gate_weight.shape[0], dtype=x.dtype, device=x.device)
+            pre = torch.empty(2, x.shape[0], gate_weight.shape[0], dtype=dtype, device=x.device)
         h = flce_gated_forward(x, gate_weight, up_weight, activation=activation, pre=pre)
         ctx.save_for_backward(x, gate_weight, up_weight, pre)
         ctx.activation = activation
@@ -249,7 +253,7 @@ class GatedLinearFunction(torch.autograd.Function):
         need_x, need_g, need_u = ctx.needs_input_grad[:3]
         dx, dWg, dWu = flce_gated_backward(_usable(dh), x, Wg, Wu, pre, activation=ctx.activation,
                                            dW_dtype=Wg.dtype, needs=(need_x, need_g or need_u))
-        return dx, dWg if need_g else None, dWu if need_u else None, None
+        return dx, dWg if need_g else None, dWu if need_u else None, None, None
 
 
 def fused_linear(x, weight, bias=None, residual=None, activation="none", keep="fixed"):
@@ -269,11 +273,13 @@ def fused_linear(x, weight, bias=None, residual=None, activation="none", keep="f
     return y.reshape(*x.shape[:-1], weight.shape[0])
 
 
-def gated_linear(x, gate_weight, up_weight, activation="silu"):
+def gated_linear(x, gate_weight, up_weight, activation="silu", keep="relative"):
     """activation(x gate_weight^T) * (x up_weight^T) with gradients; x [..., K],
-    the weights [F, K]."""
+    the weights [F, K]. ``keep``: what the backward needs is kept with "relative"
+    precision, or "fixed": to 2^-14 of the largest of 8 neighbouring features, which
+    is finer for features of one size and loses those beside an outlier."""
     x2 = _usable(x.reshape(-1, x.shape[-1]))
-    h = GatedLinearFunction.apply(x2, gate_weight, up_weight, activation)
+    h = GatedLinearFunction.apply(x2, gate_weight, up_weight, activation, keep)
     return h.reshape(*x.shape[:-1], gate_weight.shape[0])
 
 

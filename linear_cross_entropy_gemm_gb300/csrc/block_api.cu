@@ -61,7 +61,8 @@ flce_status_t check(const flce_gated_params_t* p) {
   const flce_status_t st = check_sizes(p->M, p->K, p->F);
   if (st != FLCE_OK) return st;
   if (p->F % 8 != 0) return FLCE_ERR_ALIGNMENT;
-  if (!act_ok(p->activation) || !flag_ok(p->input_fp16) || !flag_ok(p->dW_fp32))
+  if (!act_ok(p->activation) || !flag_ok(p->input_fp16) || !flag_ok(p->dW_fp32) ||
+      !keep_ok(p->keep))
     return FLCE_ERR_INVALID_ARG;
   if (!pitch_ok(p->ld_x, p->K) || !pitch_ok(p->ld_h, p->F)) return FLCE_ERR_INVALID_ARG;
   return p->ld_x % 8 == 0 && p->ld_h % 8 == 0 ? FLCE_OK : FLCE_ERR_ALIGNMENT;
@@ -572,6 +573,7 @@ flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, co
         !k_major(&sa.w, Wg, F, K, K, f16, 64) || !k_major(&sa.w2, Wu, F, K, K, f16, 64))
       return FLCE_ERR_CUDA;
     sa.keep = static_cast<uint16_t*>(pre);
+    sa.relative = p->keep == FLCE_KEEP_RELATIVE ? 1 : 0;
     sa.act = p->activation;
     return done(launch_small(true, false, sa, static_cast<cudaStream_t>(stream)));
   }
@@ -580,7 +582,7 @@ flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, co
   std::memset(&ea, 0, sizeof(ea));
   ea.act = p->activation;
   ea.fp16 = f16 ? 1 : 0;
-  ea.keep = pre ? 1 : 0;
+  ea.keep = !pre ? 0 : p->keep == FLCE_KEEP_RELATIVE ? 2 : 1;
   ea.M = M;
   ea.F = F;
   uint16_t* keep = static_cast<uint16_t*>(pre);
@@ -638,6 +640,7 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
   ga.M = M;
   ga.F = F;
   ga.fp16 = f16 ? 1 : 0;
+  ga.relative = p->keep == FLCE_KEEP_RELATIVE ? 1 : 0;
   if (launch_gated_grad(ga, s) != cudaSuccess) return FLCE_ERR_CUDA;
   cudaError_t e = cudaSuccess;
   if (dx && w.few) {

@@ -171,7 +171,13 @@ __device__ __forceinline__ void act_all(int act, float (&v)[N]) {
 // field of the group's largest magnitude, at least 14. A value's word is 2 q + bit j of
 // eb, j its place in the group, so that a 16-byte load holds all it needs. An infinity or NaN
 // is q = -16384, reads as NaN and leaves its neighbours alone: eb is that of the largest finite
-// one. Off by at most 2^-14 of the largest.
+// one. Off by at most 2^-14 of the largest, whatever their own size.
+// FLCE_KEEP_RELATIVE: the same groups, with value 2^(126 - eb), of magnitude 1 at most, as an fp16
+// number, whose second highest bit is then 0 and makes room for bit j of eb. Off by 2^-11 of
+// the value itself or, under 2^-13 of the group's largest, by 2^-24 of that: the rounding of
+// fp16 operands, an eighth of bf16's. (14 bits of magnitude as steps of 2^-13 above 1/8 and 10-bit
+// numbers below took 10 us more of 55 at 1834 x 512 x 11208 and were 0.2 % off beside a feature
+// 1000 times as large.) An infinity or NaN has 14 low bits of ones.
 constexpr uint32_t kInfBits = 0x7F800000u;
 constexpr float kRound = 12582912.f;  // 1.5 * 2^23: x + kRound holds round(x) in its low bits
 
@@ -185,19 +191,18 @@ __device__ __forceinline__ uint32_t encode_slopes(uint64_t s) {
 constexpr uint32_t kTailCode = 45312u;  // above the fixed code of any slope, (1.13 + 0.25) 2^15
 template <int ACT>
 __device__ __forceinline__ uint32_t encode_slopes_relative(uint64_t z, uint64_t s) {
-  const uint32_t fixed = encode_slopes(s);
-  if constexpr (ACT == kActNone || ACT == kActRelu) return fixed;
   constexpr uint64_t kSign = 0x8000000080000000ull;
-  float za, zb, sa, sb, ta, tb;
+  constexpr uint32_t kAdd = 0x2000u + (kTailCode << 14);  // rounds, and moves to the codes
+  float za, zb, sa, sb, ta, tb, fa, fb;
   f32x2_split(z, za, zb);
   f32x2_split(s, sa, sb);
   f32x2_split(fmul2(s & ~kSign, splat(0x1p-82f)), ta, tb);
+  f32x2_split(ffma2(s, splat(32768.f), splat(kRound + 8192.f)), fa, fb);
   // Not of a NaN: no comparison holds.
   const bool low_a = ACT == kActSigmoid ? sa < 0x1p-6f : sa > -0x1p-6f && za < -2.f;
   const bool low_b = ACT == kActSigmoid ? sb < 0x1p-6f : sb > -0x1p-6f && zb < -2.f;
-  const uint32_t ca = ((__float_as_uint(ta) + 0x2000u) >> 14) + kTailCode;
-  const uint32_t cb = ((__float_as_uint(tb) + 0x2000u) >> 14) + kTailCode;
-  return __byte_perm(low_a ? ca : fixed, low_b ? cb << 16 : fixed, 0x7610);
+  return __byte_perm(low_a ? (__float_as_uint(ta) + kAdd) >> 14 : __float_as_uint(fa),
+                     low_b ? (__float_as_uint(tb) + kAdd) >> 14 : __float_as_uint(fb), 0x5410);
 }
 
 // v = a(v), and the codes of the slopes.
@@ -268,7 +273,26 @@ __device__ __forceinline__ uint4 group_words(const float* v, uint32_t m) {
   }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
-// The same for values that may be infinite or NaN.
+// 2^x of an exponent field f = x + 127, below 1 too (x = -127, -128).
+__device__ __forceinline__ float exp2_of_field(int f) {
+  return __uint_as_float(f > 0 ? static_cast<uint32_t>(f) << 23 : 0x00800000u >> (1 - f));
+}
+// The same in the relative form.
+__device__ __forceinline__ uint4 group_words_relative(const float* v, uint32_t m) {
+  const uint32_t eb = max(m >> 23, 1u);
+  const uint64_t scale = splat(exp2_of_field(253 - static_cast<int>(eb)));
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    f32x2_split(fmul2(f32x2(v[2 * i], v[2 * i + 1]), scale), a, b);
+    const uint32_t t = eb >> (2 * i);
+    w[i] = (pack_f16x2(a, b) & 0xBFFFBFFFu) | ((t & 1u) << 14) | ((t & 2u) << 29);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// A group's words, its exponent that of the largest finite value.
+template <bool RELATIVE>
 __device__ __forceinline__ uint4 group_words_any(const float* v) {
   uint32_t m = 0;
 #pragma unroll
@@ -276,48 +300,68 @@ __device__ __forceinline__ uint4 group_words_any(const float* v) {
     const uint32_t b = __float_as_uint(v[j]) & 0x7FFFFFFFu;
     m = max(m, b < kInfBits ? b : 0u);
   }
-  const uint4 u = group_words(v, m);
+  const uint4 u = RELATIVE ? group_words_relative(v, m) : group_words(v, m);
   uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
-    if ((__float_as_uint(v[j]) & 0x7FFFFFFFu) >= kInfBits)
-      w[j / 2] = (w[j / 2] & ~(0xFFFEu << (16 * (j & 1)))) | (0x8000u << (16 * (j & 1)));
+  for (int j = 0; j < 8; ++j) {
+    if ((__float_as_uint(v[j]) & 0x7FFFFFFFu) < kInfBits) continue;
+    const int at = 16 * (j & 1);
+    w[j / 2] = RELATIVE ? w[j / 2] | (0x3FFFu << at)
+                        : (w[j / 2] & ~(0xFFFEu << at)) | (0x8000u << at);
+  }
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 // The words of N values. One branch for all of them: one for each group kept the groups'
 // instructions apart (1834 x 512 x 11208 with kept values 55 us, 61 us).
-template <int N>
-__device__ __forceinline__ void encode_groups(const float (&v)[N], uint32_t (&w)[N / 2]) {
+template <bool RELATIVE, int N>
+__device__ __forceinline__ void encode_groups_as(const float (&v)[N], uint32_t (&w)[N / 2]) {
   uint32_t m[N / 8], most = 0;
 #pragma unroll
   for (int q = 0; q < N / 8; ++q) {
     m[q] = largest_bits(&v[8 * q]);
     most = max(most, m[q]);
   }
-  const bool finite = most < kInfBits;
-  if (finite) {
+  const auto put = [&](int q, const uint4& u) {
+    w[4 * q] = u.x;
+    w[4 * q + 1] = u.y;
+    w[4 * q + 2] = u.z;
+    w[4 * q + 3] = u.w;
+  };
+  if (most < kInfBits) {
 #pragma unroll
-    for (int q = 0; q < N / 8; ++q) {
-      const uint4 u = group_words(&v[8 * q], m[q]);
-      w[4 * q] = u.x;
-      w[4 * q + 1] = u.y;
-      w[4 * q + 2] = u.z;
-      w[4 * q + 3] = u.w;
-    }
+    for (int q = 0; q < N / 8; ++q)
+      put(q, RELATIVE ? group_words_relative(&v[8 * q], m[q]) : group_words(&v[8 * q], m[q]));
   } else {
 #pragma unroll
-    for (int q = 0; q < N / 8; ++q) {
-      const uint4 u = group_words_any(&v[8 * q]);
-      w[4 * q] = u.x;
-      w[4 * q + 1] = u.y;
-      w[4 * q + 2] = u.z;
-      w[4 * q + 3] = u.w;
-    }
+    for (int q = 0; q < N / 8; ++q) put(q, group_words_any<RELATIVE>(&v[8 * q]));
   }
+}
+template <int N>
+__device__ __forceinline__ void encode_groups(bool relative, const float (&v)[N],
+                                              uint32_t (&w)[N / 2]) {
+  if (relative)
+    encode_groups_as<true>(v, w);
+  else
+    encode_groups_as<false>(v, w);
 }
 // v, or NaN where the word in the upper half of w says so.
 __device__ __forceinline__ float kept_number(uint32_t w, float v) {
   return (w >> 17) == 0x4000u ? __uint_as_float(0x7FFFFFFFu) : v;
+}
+__device__ __forceinline__ void decode_group_relative(const uint4& u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+  uint32_t eb = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) eb |= (((w[i] >> 14) & 1u) | ((w[i] >> 29) & 2u)) << (2 * i);
+  const float scale = __uint_as_float(eb << 23);  // 2^(eb - 127)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t h = w[i] & 0xBFFFBFFFu;
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    const float nan = __uint_as_float(0x7FFFFFFFu);
+    v[2 * i] = (h & 0x3FFFu) == 0x3FFFu ? nan : 2.f * f.x * scale;
+    v[2 * i + 1] = ((h >> 16) & 0x3FFFu) == 0x3FFFu ? nan : 2.f * f.y * scale;
+  }
 }
 __device__ __forceinline__ void decode_group(const uint4& u, float (&v)[8]) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -583,7 +627,8 @@ struct LinearEpi {
 
 // ---------------------------------------------------------- gated: forward
 struct GatedArgs {
-  int act, fp16, keep;  // keep: also write a(g) and u a'(g)
+  int act, fp16;
+  int keep;  // also write a(g) and u a'(g); 2: in the relative form
   int M, F;
   Out16 h, val, cross;
 };
@@ -609,9 +654,9 @@ struct GatedEpi {
         float x[32];  // u a'(g)
         act_cross(a.act, g, u, x);
         uint32_t w[16];
-        encode_groups(g, w);
+        encode_groups(a.keep == 2, g, w);
         staged_block_16(&a.val.map, col0, row0, w, st, lane);
-        encode_groups(x, w);
+        encode_groups(a.keep == 2, x, w);
         staged_block_16(&a.cross.map, col0, row0, w, st, lane);
       } else {
         act_all(a.act, g);

@@ -111,6 +111,7 @@ struct GatedGradArgs {
   uint16_t* du;           // [M, ld]
   int64_t ld;
   int M, F, fp16;
+  int relative;           // val and cross in the relative form
 };
 // A copy of 16-bit rows to another pitch; both on 16-byte boundaries, cols a multiple of 8.
 cudaError_t launch_repack(const uint16_t* src, int64_t ld_src, uint16_t* dst, int64_t ld_dst,

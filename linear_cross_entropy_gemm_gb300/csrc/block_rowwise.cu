@@ -218,8 +218,13 @@ __global__ void __launch_bounds__(256) gated_grad_kernel(const GatedGradArgs a) 
   const uint4 gv = *reinterpret_cast<const uint4*>(a.cross + at);
   const uint4 uv = *reinterpret_cast<const uint4*>(a.val + at);
   unpack8(dv, f16, d);
-  decode_group(gv, g);
-  decode_group(uv, u);
+  if (a.relative != 0) {
+    decode_group_relative(gv, g);
+    decode_group_relative(uv, u);
+  } else {
+    decode_group(gv, g);
+    decode_group(uv, u);
+  }
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     g[j] *= d[j];

@@ -350,9 +350,9 @@ __global__ void __launch_bounds__(kSmThreads)
         act_cross(a.act, v[0], u, x);
         uint16_t* k = a.keep + row * a.N + col;
         uint32_t w[4];
-        encode_groups(v[0], w);
+        encode_groups(a.relative != 0, v[0], w);
         *reinterpret_cast<uint4*>(k) = make_uint4(w[0], w[1], w[2], w[3]);
-        encode_groups(x, w);
+        encode_groups(a.relative != 0, x, w);
         *reinterpret_cast<uint4*>(k + static_cast<size_t>(a.M) * a.N) =
             make_uint4(w[0], w[1], w[2], w[3]);
       } else {

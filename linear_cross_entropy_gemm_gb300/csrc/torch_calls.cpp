@@ -272,7 +272,7 @@ PyObject* gated_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor *pre = optional(a[4], "pre"), *out = optional(a[5], "out");
     flce_gated_params_t p = gated_params(x, Wg, Wu, a[3]);
     const c10::cuda::CUDAGuard guard(x.device());
-    if (pre) dense(*pre, {2, p.M, p.F}, x, "pre");
+    if (pre) p.keep = kept(*pre, {2, p.M, p.F}, x);
     if (out) p.ld_h = rows_of(*out, p.M, p.F, x, "out");
     const Tensor h = out ? *out : at::empty({p.M, p.F}, x.options());
     const Tensor ws = scratch(a[6], flce_gated_workspace_size(&p, 0), x);
@@ -292,7 +292,7 @@ PyObject* gated_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     flce_gated_params_t p = gated_params(x, Wg, Wu, a[5]);
     const c10::cuda::CUDAGuard guard(x.device());
     p.ld_h = rows_of(dh, p.M, p.F, x, "dh");
-    dense(pre, {2, p.M, p.F}, x, "pre");
+    p.keep = kept(pre, {2, p.M, p.F}, x);
     p.dW_fp32 = a[6] == Py_True ? 1 : 0;
     Tensor dx, dWg, dWu;
     if (PyObject_IsTrue(a[7])) dx = at::empty({p.M, p.K}, x.options());

@@ -35,7 +35,17 @@ def test_linear_form_refused(lib, keep):
     assert lib.flce_linear_workspace_size(p, 1) == 0
 
 
+@pytest.mark.parametrize("keep", [-1, 2])
+def test_gated_form_refused(lib, keep):
+    p = ctypes.byref(_lib.FlceGatedParams(M=4, K=64, F=16, activation=4, keep=keep))
+    assert lib.flce_gated_forward(p, AT, AT, AT, AT, AT, None, 0, None, None) == 1
+    assert lib.flce_gated_backward(p, AT, AT, AT, AT, AT, AT, AT, AT, AT, 1 << 40, None, None) == 1
+    assert lib.flce_gated_workspace_size(p, 1) == 0
+
+
 def test_autograd_form_refuses_unknown_names():
     x, W = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(16, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="keep"):
         F.fused_linear(x, W, activation="silu", keep="exact")
+    with pytest.raises(ValueError, match="keep"):
+        F.gated_linear(x, W, W, keep="exact")

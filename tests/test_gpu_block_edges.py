@@ -172,14 +172,16 @@ def test_kept_forms_agree_where_units_are_not_saturated():
 # ---------------------------------------------------- infinities in kept values
 @pytest.mark.parametrize("M", [5, 50, 300])
 @pytest.mark.parametrize("value", [float("inf"), float("nan")], ids=str)
-def test_a_bad_feature_stays_in_its_row_of_the_weight_gradients(M, value):
+@pytest.mark.parametrize("form", [BF16, torch.int16], ids=["fixed", "relative"])
+def test_a_bad_feature_stays_in_its_row_of_the_weight_gradients(M, value, form):
     """A weight row with an infinity or NaN makes u a'(g) of its own feature non-finite in every
     token, and nothing of its seven neighbours'. Those are compared with 64 bits: each dg and
-    du is off by its rounding and the kept value's 2^-14 of the group's largest."""
+    du is off by its rounding and the kept value's 2^-14 of the group's largest (the relative
+    form's 2^-11 of its own size)."""
     n = randn(M)
     x, Wg, Wu, dh = n(M, 64), n(72, 64, std=0.125), n(72, 64, std=0.125), n(M, 72)
     Wu[11, 5] = value
-    pre = torch.empty(2, M, 72, dtype=BF16, device="cuda")
+    pre = torch.empty(2, M, 72, dtype=form, device="cuda")
     F.flce_gated_forward(x, Wg, Wu, pre=pre)
     dx, dWg, dWu = F.flce_gated_backward(dh, x, Wg, Wu, pre)
     good = torch.arange(72, device="cuda") != 11
@@ -193,7 +195,100 @@ def test_a_bad_feature_stays_in_its_row_of_the_weight_gradients(M, value):
     for got, kept, size, rows in ((dWg, u * p * (1 + g * (1 - p)), most[0], good),
                                   (dWu, g * p, most[1], torch.ones_like(good))):
         d = d64 * kept
-        off = 2.0 ** -8 * d.abs() + 1.01 * 2.0 ** -14 * d64.abs() * size + 2.0 ** -16 * d64.abs()
+        kept_off = 2.0 ** -14 * size if form is BF16 else 2.0 ** -11 * kept.abs() + 2.0 ** -24 * size
+        off = 2.0 ** -8 * d.abs() + 1.01 * d64.abs() * kept_off + 2.0 ** -16 * d64.abs()
         bound = off.t() @ x64.abs() + M * 2.0 ** -23 * (d.abs().t() @ x64.abs())
         err = (got.double() - d.t() @ x64).abs()
         assert bool((err <= bound)[rows].all())
+
+
+# ------------------------------------------- kept values of very different size
+def relative_off(v, off):
+    """Bound of a kept value v of the relative form that is off by at most `off` before."""
+    size = v.abs() + off
+    most = size.reshape(-1, 8).amax(1, keepdim=True).expand(-1, 8).reshape(v.shape)
+    return off + 2.0 ** -11 * size + 2.0 ** -24 * most + 2.0 ** -140
+
+
+def gated_relative(x, Wg, Wu, act):
+    """(a(g), bound), (u a'(g), bound) of the kept values in the relative form."""
+    (g, g_off), (u, u_off) = R.sums(x, Wg), R.sums(x, Wu)
+    (a, a_off), (slope, s_off) = R.activated(g, g_off, act)
+    cross = u * slope
+    c_off = s_off * u.abs() + (slope.abs() + s_off) * u_off + R.ADD * cross.abs()
+    return (a, relative_off(a, a_off)), (cross, relative_off(cross, c_off))
+
+
+def check_gated_gradients(got, x, Wg, Wu, dh, act, dW_dtype):
+    """Against 64 bits, not against what the kernels kept."""
+    dt, d = x.dtype, dh.double()
+    (a, a_off), (cross, c_off) = gated_relative(x, Wg, Wu, act)
+    dg, du = d * cross, d * a
+    dg_off = R.rounded(dg, d.abs() * c_off + R.ADD * dg.abs(), dt)
+    du_off = R.rounded(du, d.abs() * a_off + R.ADD * du.abs(), dt)
+    both, both_off = torch.cat((dg, du), 1), torch.cat((dg_off, du_off), 1)
+    R.assert_within(got[0], R.product(both, both_off, torch.cat((Wg, Wu)).double(), dt), "dx")
+    R.assert_within(got[1], R.product(dg.t(), dg_off.t(), x.double(), dW_dtype), "dWg")
+    R.assert_within(got[2], R.product(du.t(), du_off.t(), x.double(), dW_dtype), "dWu")
+    return dg.t() @ x.double(), du.t() @ x.double()
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh", "relu", "sigmoid"])
+@pytest.mark.parametrize("M,K,N", [(1, 64, 8), (5, 64, 72), (50, 136, 264), (300, 200, 136)])
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+def test_gated_gradients_of_the_relative_form(act, M, K, N, dtype):
+    n = randn(M + K + N)
+    x, Wg, Wu = n(M, K, dtype=dtype), n(N, K, std=K ** -0.5, dtype=dtype), n(N, K, std=K ** -0.5, dtype=dtype)
+    dh = n(M, N, std=0.1, dtype=dtype)
+    pre = torch.empty(2, M, N, dtype=torch.int16, device="cuda")
+    h = F.flce_gated_forward(x, Wg, Wu, activation=act, pre=pre)
+    assert torch.equal(h, F.flce_gated_forward(x, Wg, Wu, activation=act))
+    got = F.flce_gated_backward(dh, x, Wg, Wu, pre, activation=act, dW_dtype=dtype)
+    check_gated_gradients(got, x, Wg, Wu, dh, act, dtype)
+    leaves = [t.clone().requires_grad_() for t in (x, Wg, Wu)]
+    F.gated_linear(*leaves, activation=act).backward(dh)
+    for leaf, g in zip(leaves, got):
+        assert torch.equal(leaf.grad, g)
+
+
+@pytest.mark.parametrize("scale", [30.0, 100.0, 1000.0])
+@pytest.mark.parametrize("M", [6, 400])
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+def test_features_beside_an_outlier_keep_their_gradients(scale, M, dtype):
+    """One feature in eight has weights `scale` times as large. Of every other feature each dg and
+    du is off by u and 2^-11 of itself; over the tokens these add like their squares at worst,
+    so a row of dWg or dWu is off by that share of its size. 2^-13 more: a' in fp32, and
+    2^-24 of a neighbour."""
+    n = randn(M)
+    x, dh = n(M, 64, dtype=dtype), n(M, 72, std=0.1, dtype=dtype)
+    Wg, Wu = n(72, 64, std=0.125, dtype=dtype), n(72, 64, std=0.125, dtype=dtype)
+    Wg[2::8] *= scale / 10
+    Wu[5::8] *= scale
+    pre = torch.empty(2, M, 72, dtype=torch.int16, device="cuda")
+    F.flce_gated_forward(x, Wg, Wu, pre=pre)
+    got = F.flce_gated_backward(dh, x, Wg, Wu, pre)
+    if dtype is BF16:
+        want = check_gated_gradients(got, x, Wg, Wu, dh, "silu", FP32)
+    else:
+        g, u, d = x.double() @ Wg.double().t(), x.double() @ Wu.double().t(), dh.double()
+        p = torch.sigmoid(g)
+        want = (d * u * p * (1 + g * torch.sigmoid(-g))).t() @ x.double(), (d * g * p).t() @ x.double()
+    index = torch.arange(72, device="cuda") % 8
+    limit = R.UNIT[dtype] + 2.0 ** -11 + 2.0 ** -13
+    for w, v, out in ((got[1], want[0], 5), (got[2], want[1], 2)):
+        rows = (index != out) & (index != 2)  # a unit with huge g is saturated: its size is its own
+        err = (w.double() - v).norm(dim=1) / v.norm(dim=1)
+        assert float(err[rows].max()) <= limit, float(err[rows].max())
+
+
+@pytest.mark.parametrize("exponent", [-100, -20, 20, 100, 125])
+@pytest.mark.parametrize("M", [5, 200])
+def test_relative_form_at_any_size(exponent, M):
+    """u from 2^-100 to near the largest fp32 number."""
+    n = randn(M)
+    x, Wg, dh = n(M, 64), n(72, 64, std=0.125), n(M, 72, std=0.01)
+    Wu = (n(72, 64, std=0.1, dtype=FP32) * 2.0 ** exponent).to(BF16)
+    pre = torch.empty(2, M, 72, dtype=torch.int16, device="cuda")
+    F.flce_gated_forward(x, Wg, Wu, pre=pre)
+    got = F.flce_gated_backward(dh, x, Wg, Wu, pre)
+    check_gated_gradients(got, x, Wg, Wu, dh, "silu", FP32)
