@@ -468,6 +468,19 @@ flce_status_t flce_gated_backward(const flce_gated_params_t* p, const void* dh, 
                                   void* dWg, void* dWu, void* workspace, size_t workspace_bytes,
                                   int32_t* dev_err, void* stream);
 
+/* Which kernel form a product of a call takes on this library's target; for tests of every
+ * form and for profiles. No device is needed. */
+typedef struct {
+  int32_t few_tokens; /* 16, 32, 64 or 128: tokens of a few-token tile; 0: a GEMM on CTA pairs, with */
+  int32_t halves;     /*   1 or 2 halves */
+  int32_t columns;    /*   of this many accumulator columns */
+  int32_t slices;     /* CTAs (few tokens) or CTA pairs that share a tile's sum */
+} flce_plan_t;
+
+/* product: 0 forward, 1 dx, 2 the weight gradients. M > 0. */
+flce_status_t flce_linear_plan(const flce_linear_params_t* p, int product, flce_plan_t* plan);
+flce_status_t flce_gated_plan(const flce_gated_params_t* p, int product, flce_plan_t* plan);
+
 /* One dense gradient tensor of any shape. */
 typedef enum { FLCE_DTYPE_BF16 = 0, FLCE_DTYPE_FP16 = 1, FLCE_DTYPE_FP32 = 2 } flce_dtype_t;
 

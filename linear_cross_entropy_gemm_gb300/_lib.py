@@ -67,6 +67,11 @@ class FlceGatedParams(ctypes.Structure):
         [(f, ctypes.c_int32) for f in ("activation", "input_fp16", "dW_fp32", "keep")]
 
 
+class FlcePlan(ctypes.Structure):
+    """Mirror of flce_plan_t."""
+    _fields_ = [(f, ctypes.c_int32) for f in ("few_tokens", "halves", "columns", "slices")]
+
+
 class FlceTrace(ctypes.Structure):
     """Mirror of flce_trace_t."""
     _fields_ = [
@@ -166,6 +171,8 @@ def load() -> ctypes.CDLL:
     lib.flce_gated_forward.restype = ctypes.c_int
     lib.flce_gated_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp]
     lib.flce_gated_backward.restype = ctypes.c_int
+    lib.flce_linear_plan.argtypes = lib.flce_gated_plan.argtypes = [vp, ctypes.c_int, vp]
+    lib.flce_linear_plan.restype = lib.flce_gated_plan.restype = ctypes.c_int
     lib.flce_grad_norm_workspace_size.argtypes = [i64]
     lib.flce_grad_norm_workspace_size.restype = sz
     lib.flce_grad_norm.argtypes = [i64, vp, vp, vp, vp, vp, sz, vp]

@@ -378,6 +378,22 @@ size_t carve(const flce_gated_params_t* p, void* base, GatedWs* w) {
   return bytes_of(c);
 }
 
+// What launch of D[M, N] (pair_args, small_args) a product takes.
+flce_plan_t plan_of(bool few, bool mn, int64_t M, int64_t N, int64_t k64, bool two_b) {
+  flce_plan_t r;
+  std::memset(&r, 0, sizeof(r));
+  if (few) {
+    r.few_tokens = small_tokens(M);
+    r.slices = small_slices(M, N, static_cast<int>(k64), two_b);
+    return r;
+  }
+  const TileShape& t = best_tile(mn, M, N, k64, two_b);
+  r.halves = t.halves;
+  r.columns = t.bn;
+  r.slices = t.slices;
+  return r;
+}
+
 bool zero(void* p, size_t bytes, cudaStream_t s) {
   return !p || cudaMemsetAsync(p, 0, bytes, s) == cudaSuccess;
 }
@@ -390,6 +406,17 @@ size_t flce_linear_workspace_size(const flce_linear_params_t* p, int which) {
   if (check(p) != FLCE_OK || p->M == 0 || which < 0 || which > 1) return 0;
   LinearWs w;
   return which == 0 ? carve_forward(p, nullptr, &w) : carve(p, nullptr, &w);
+}
+
+flce_status_t flce_linear_plan(const flce_linear_params_t* p, int product, flce_plan_t* plan) {
+  const flce_status_t st = check(p);
+  if (st != FLCE_OK) return st;
+  if (!plan || product < 0 || product > 2 || p->M == 0) return FLCE_ERR_INVALID_ARG;
+  const int64_t m64 = (p->M + 63) / 64, k64 = (p->K + 63) / 64, n64 = (p->N + 63) / 64;
+  *plan = product == 0 ? plan_of(few_tokens(false, p->M, p->N, k64, false), false, p->M, p->N, k64, false)
+        : product == 1 ? plan_of(few_tokens(true, p->M, p->K, n64, false), true, p->M, p->K, n64, false)
+                       : plan_of(false, true, p->N, p->K, m64, false);
+  return FLCE_OK;
 }
 
 flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, const void* W,
@@ -547,6 +574,18 @@ size_t flce_gated_workspace_size(const flce_gated_params_t* p, int which) {
   if (check(p) != FLCE_OK || p->M == 0 || which < 0 || which > 1) return 0;
   GatedWs w;
   return which == 0 ? carve_forward(p, nullptr, &w) : carve(p, nullptr, &w);
+}
+
+flce_status_t flce_gated_plan(const flce_gated_params_t* p, int product, flce_plan_t* plan) {
+  const flce_status_t st = check(p);
+  if (st != FLCE_OK) return st;
+  if (!plan || product < 0 || product > 2 || p->M == 0) return FLCE_ERR_INVALID_ARG;
+  const int64_t m64 = (p->M + 63) / 64, k64 = (p->K + 63) / 64, f64 = 2 * ((p->F + 63) / 64);
+  const int64_t rows = 2 * ((p->F + 255) / 256) * 256;  // of dWg and dWu, each to whole tiles
+  *plan = product == 0 ? plan_of(few_tokens(false, p->M, p->F, k64, true), false, p->M, p->F, k64, true)
+        : product == 1 ? plan_of(few_tokens(true, p->M, p->K, f64, false), true, p->M, p->K, f64, false)
+                       : plan_of(false, true, rows, p->K, m64, false);
+  return FLCE_OK;
 }
 
 flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, const void* Wg,
