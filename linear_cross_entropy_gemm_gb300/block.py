@@ -176,9 +176,14 @@ def flce_clip_grads(grads: Iterable[torch.Tensor], max_norm: float, *,
     return _calls.clip_grads(grads, out, float(max_norm), eps, workspace)
 
 
-def clip_grad_norm_(parameters, max_norm: float, eps: float = 1e-6) -> torch.Tensor:
+def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0, *,
+                    eps: float = 1e-6) -> torch.Tensor:
     """flce_clip_grads over the ``.grad`` of ``parameters`` (those that have
-    one), in place; the norm before the scaling, 0 where there is no gradient."""
+    one), in place; the norm before the scaling, 0 where there is no gradient.
+    Positional arguments as torch.nn.utils.clip_grad_norm_ has them; ``norm_type``
+    can only be 2."""
+    if float(norm_type) != 2.0:
+        raise ValueError(f"flce: clip_grad_norm_ clips by the 2-norm, got norm_type={norm_type!r}")
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
     grads = [p.grad for p in parameters if p.grad is not None]

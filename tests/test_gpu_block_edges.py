@@ -292,3 +292,20 @@ def test_relative_form_at_any_size(exponent, M):
     F.flce_gated_forward(x, Wg, Wu, pre=pre)
     got = F.flce_gated_backward(dh, x, Wg, Wu, pre)
     check_gated_gradients(got, x, Wg, Wu, dh, "silu", FP32)
+
+
+# ------------------------------------------------------------- clip_grad_norm_
+def test_clip_grad_norm_scales_as_torchs_does():
+    """The third positional argument is the norm's type: the same gradients as torch's, within the
+    rounding of the norm (2^-20) and of the product."""
+    n = randn(12)
+    ours = [torch.nn.Parameter(n(*s, dtype=FP32)) for s in ((40, 7), (3,), (1000,))]
+    torchs = [torch.nn.Parameter(p.detach().clone()) for p in ours]
+    for p, q in zip(ours, torchs):
+        p.grad = n(*p.shape, dtype=FP32)
+        q.grad = p.grad.clone()
+    norm = F.clip_grad_norm_(ours, 0.5, 2.0)
+    want = torch.nn.utils.clip_grad_norm_(torchs, 0.5, 2.0)
+    assert abs(float(norm) - float(want)) <= 2.0 ** -20 * float(want)
+    for p, q in zip(ours, torchs):
+        assert bool(((p.grad - q.grad).abs() <= 2.0 ** -19 * q.grad.abs()).all())
