@@ -147,6 +147,12 @@ size_t bytes(const Tensor& t) { return t.defined() ? static_cast<size_t>(t.numel
 
 void* stream_of(const Tensor& x) { return c10::cuda::getCurrentCUDAStream(x.get_device()).stream(); }
 
+// A call wrote into a tensor of the caller's: autograd refuses a backward that saved the
+// values from before, as with torch's own in-place operations.
+void written(const Tensor& t) {
+  if (t.defined() && !t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
+}
+
 PyObject* wrap(const Tensor& t) {
   if (!t.defined()) Py_RETURN_NONE;
   return THPVariable_Wrap(t);
@@ -213,6 +219,8 @@ PyObject* linear_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
                              bytes(ws), static_cast<int32_t*>(error_word(x.get_device())),
                              stream_of(x)),
          "flce_linear_forward");
+    if (out) written(*out);
+    if (pre) written(*pre);
     return wrap(y);
   });
 }
@@ -279,6 +287,8 @@ PyObject* gated_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     done(flce_gated_forward(&p, data(x), data(Wg), data(Wu), data(h), data(pre), data(ws), bytes(ws),
                             static_cast<int32_t*>(error_word(x.get_device())), stream_of(x)),
          "flce_gated_forward");
+    if (out) written(*out);
+    if (pre) written(*pre);
     return wrap(h);
   });
 }
@@ -377,15 +387,18 @@ PyObject* clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor norm = at::empty({}, first.options().dtype(at::kFloat));
     const Tensor ws = scratch(a[4], flce_grad_norm_workspace_size(count), first);
     float* to = static_cast<float*>(norm.data_ptr());
-    if (a[2] == Py_None)
+    if (a[2] == Py_None) {
       done(flce_grad_norm(count, l.ptrs.data(), l.numel.data(), l.types.data(), to, data(ws),
                           bytes(ws), stream_of(first)),
            "flce_grad_norm");
-    else
+    } else {
       done(flce_clip_grads(count, l.ptrs.data(), l.out.empty() ? nullptr : l.out.data(),
                            l.numel.data(), l.types.data(), static_cast<float>(max_norm),
                            static_cast<float>(eps), to, data(ws), bytes(ws), stream_of(first)),
            "flce_clip_grads");
+      PyObject* list = a[1] == Py_None ? a[0] : a[1];
+      for (int64_t i = 0; i < count; ++i) written(tensor(PyList_GET_ITEM(list, i), "an output"));
+    }
     return wrap(norm);
   });
 }

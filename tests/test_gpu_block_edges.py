@@ -309,3 +309,44 @@ def test_clip_grad_norm_scales_as_torchs_does():
     assert abs(float(norm) - float(want)) <= 2.0 ** -20 * float(want)
     for p, q in zip(ours, torchs):
         assert bool(((p.grad - q.grad).abs() <= 2.0 ** -19 * q.grad.abs()).all())
+
+
+# --------------------------------------------- writes that autograd has to know of
+def test_written_tensors_raise_their_version():
+    n = randn(21)
+    x, W, Wu, r, out = n(4, 64), n(16, 64), n(16, 64), n(4, 16), n(4, 16)
+    pre, both = torch.empty(4, 16, dtype=BF16, device="cuda"), torch.empty(2, 4, 16, dtype=torch.int16, device="cuda")
+    grads = [n(50, dtype=FP32), n(7, 3)]
+    copies = [torch.empty_like(g) for g in grads]
+
+    def raised(call, written, kept=()):
+        before = [t._version for t in written], [t._version for t in kept]
+        call()
+        assert all(t._version > v for t, v in zip(written, before[0]))
+        assert [t._version for t in kept] == before[1]
+
+    raised(lambda: F.flce_linear_forward(x, W, None, r, activation="silu", pre=pre, out=out),
+           [pre, out], [x, W, r])
+    raised(lambda: F.flce_linear_forward(x, W, None, r, out=r), [r], [x, W])
+    raised(lambda: F.flce_gated_forward(x, W, Wu, pre=both, out=out), [both, out], [x, W, Wu])
+    raised(lambda: F.flce_grad_norm(grads), [], grads)
+    raised(lambda: F.flce_clip_grads(grads, 0.1, out=copies), copies, grads)
+    raised(lambda: F.flce_clip_grads(grads, 0.1), grads)
+    p = torch.nn.Parameter(n(9, dtype=FP32))
+    p.grad = n(9, dtype=FP32)
+    raised(lambda: F.clip_grad_norm_([p], 0.1), [p.grad], [p])
+    with torch.inference_mode():
+        t = torch.ones(9, device="cuda")
+    F.flce_clip_grads([t], 0.5)  # has no version
+    assert bool((t < 1).all())
+
+
+def test_autograd_refuses_an_overwritten_saved_residual():
+    n = randn(22)
+    x, W, leaf = n(4, 64), n(16, 64), n(4, 16).requires_grad_()
+    r = leaf * 2
+    s = r.square()  # saves r
+    with torch.no_grad():
+        F.flce_linear_forward(x, W, None, r.detach(), out=r.detach())
+    with pytest.raises(RuntimeError, match="inplace"):
+        s.sum().backward()
