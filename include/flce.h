@@ -408,9 +408,10 @@ typedef struct {
   int32_t keep;           /* flce_keep_t of pre, the same in forward and backward */
 } flce_linear_params_t;
 
-/* Workspace bytes: which = 0 forward, 1 backward. 0 for invalid parameters, for
- * M == 0, and for calls that need none (workspace may then be NULL). A forward needs
- * some where an operand's pitch makes a repacked copy pay. */
+/* Workspace bytes: which = 0 forward, 1 backward, 2 backward with a dy that starts on a
+ * 16-byte boundary (without an activation it then needs no copy of dy). 0 for invalid
+ * parameters, for M == 0, and for forwards that need none (workspace may then be
+ * NULL). A forward needs some where an operand's pitch makes a repacked copy pay. */
 size_t flce_linear_workspace_size(const flce_linear_params_t* p, int which);
 
 /* Forward. W: [N, K] dense. y: [M, N]; it may be the residual's own buffer (with

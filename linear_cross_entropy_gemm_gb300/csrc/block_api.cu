@@ -303,6 +303,7 @@ struct LinearWs {
   float* part;
   int64_t ld_dz, ld_x, ld_w;
   bool repack_dy;  // dy is better copied, even where dz is dy
+  bool copy;       // dz is not dy itself
   bool few;        // forward, dx: by the few-token kernel
 };
 size_t carve_forward(const flce_linear_params_t* p, void* base, LinearWs* w) {
@@ -318,7 +319,7 @@ size_t carve_forward(const flce_linear_params_t* p, void* base, LinearWs* w) {
   w->W = take_rows(&c, p->N, w->ld_w);
   return bytes_of(c);
 }
-size_t carve(const flce_linear_params_t* p, void* base, LinearWs* w) {
+size_t carve(const flce_linear_params_t* p, void* base, bool dy_aligned, LinearWs* w) {
   std::memset(w, 0, sizeof(*w));
   const int64_t n64 = (p->N + 63) / 64;
   w->few = few_tokens(true, p->M, p->K, n64, false);
@@ -329,10 +330,10 @@ size_t carve(const flce_linear_params_t* p, void* base, LinearWs* w) {
   w->ld_dz = scratch_ld(p->M, p->N);
   w->repack_dy = repack_ld(p->M, p->N, pitch(p->ld_y, p->N),
                            {dx.ns + dw.ns, std::max(dx.tiles, dw.tiles)}) != 0;
+  w->copy = p->activation != FLCE_ACT_NONE || w->repack_dy || !dy_aligned ||
+            pitch(p->ld_y, p->N) % 8 != 0;
   Carver c(base, 0);
-  // dy off the 16-byte boundaries also needs a copy: sized for it, since the
-  // pointer is not known here.
-  w->dz = take_rows(&c, p->M, w->ld_dz);
+  w->dz = take_rows(&c, p->M, w->copy ? w->ld_dz : 0);
   w->part = p->has_bias ? c.take<float>(static_cast<size_t>(dz_parts(p->M, p->N)) * p->N) : nullptr;
   w->x = take_rows(&c, p->M, w->ld_x);
   w->W = take_rows(&c, p->N, w->ld_w);
@@ -403,9 +404,9 @@ bool zero(void* p, size_t bytes, cudaStream_t s) {
 extern "C" {
 
 size_t flce_linear_workspace_size(const flce_linear_params_t* p, int which) {
-  if (check(p) != FLCE_OK || p->M == 0 || which < 0 || which > 1) return 0;
+  if (check(p) != FLCE_OK || p->M == 0 || which < 0 || which > 2) return 0;
   LinearWs w;
-  return which == 0 ? carve_forward(p, nullptr, &w) : carve(p, nullptr, &w);
+  return which == 0 ? carve_forward(p, nullptr, &w) : carve(p, nullptr, which == 2, &w);
 }
 
 flce_status_t flce_linear_plan(const flce_linear_params_t* p, int product, flce_plan_t* plan) {
@@ -502,7 +503,8 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
     return FLCE_ERR_ALIGNMENT;
   LinearWs w;
   if (!workspace) return FLCE_ERR_INVALID_ARG;
-  if (workspace_bytes < carve(p, workspace, &w)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace_bytes < carve(p, workspace, aligned16(dy), &w))
+    return FLCE_ERR_WORKSPACE_TOO_SMALL;
   int sms = 0;
   if ((st = device_info(&sms)) != FLCE_OK) return st;
   const bool f16 = p->input_fp16 != 0;
@@ -510,7 +512,7 @@ flce_status_t flce_linear_backward(const flce_linear_params_t* p, const void* dy
 
   const int64_t ld_dy = pitch(p->ld_y, N);
   const bool dy_rows16 = aligned16(dy) && ld_dy % 8 == 0;
-  const bool copy = (act || !dy_rows16 || w.repack_dy) && (dx || dW);
+  const bool copy = w.copy && (dx || dW);
   if (copy || db) {
     DzArgs za;
     za.dy = static_cast<const uint16_t*>(dy);

@@ -145,6 +145,8 @@ void* data(const Tensor* t) { return t && t->defined() ? t->data_ptr() : nullptr
 void* data(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 size_t bytes(const Tensor& t) { return t.defined() ? static_cast<size_t>(t.numel()) : 0; }
 
+bool aligned16(const Tensor& t) { return reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0; }
+
 void* stream_of(const Tensor& x) { return c10::cuda::getCurrentCUDAStream(x.get_device()).stream(); }
 
 // A call wrote into a tensor of the caller's: autograd refuses a backward that saved the
@@ -249,7 +251,7 @@ PyObject* linear_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (PyObject_IsTrue(a[8])) dx = at::empty({p.M, p.K}, x.options());
     if (PyObject_IsTrue(a[9])) dW = at::empty({p.N, p.K}, x.options().dtype(grad_type(p.dW_fp32, x)));
     if (b && PyObject_IsTrue(a[10])) db = at::empty({p.N}, x.options().dtype(grad_type(p.db_fp32, x)));
-    const Tensor ws = scratch(a[11], flce_linear_workspace_size(&p, 1), x);
+    const Tensor ws = scratch(a[11], flce_linear_workspace_size(&p, aligned16(dy) ? 2 : 1), x);
     done(flce_linear_backward(&p, data(dy), data(x), data(W), data(pre), data(dx), data(dW), data(db),
                               data(ws), bytes(ws),
                               static_cast<int32_t*>(error_word(x.get_device())), stream_of(x)),

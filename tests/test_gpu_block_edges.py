@@ -350,3 +350,43 @@ def test_autograd_refuses_an_overwritten_saved_residual():
         F.flce_linear_forward(x, W, None, r.detach(), out=r.detach())
     with pytest.raises(RuntimeError, match="inplace"):
         s.sum().backward()
+
+
+# ------------------------------------------------------ scratch of the backward
+@pytest.mark.parametrize("offset", [0, 8])
+@pytest.mark.parametrize("M,K,N", [(5, 64, 24), (300, 264, 80), (2048, 1032, 1032), (15, 16384, 64)])
+def test_backward_of_an_aligned_dy_stays_inside_the_smaller_workspace(M, K, N, offset):
+    """Without an activation, with exactly the bytes that an aligned dy needs, at any address."""
+    lib, n = _lib.load(), randn(M)
+    x, W, b, dy = n(M, K), n(N, K), n(N), n(M, N)
+    want = F.flce_linear_backward(dy, x, W, b, dW_dtype=BF16, db_dtype=BF16)
+    p = _lib.FlceLinearParams(M=M, K=K, N=N, has_bias=1)
+    at = ctypes.addressof(p)
+    need = lib.flce_linear_workspace_size(at, 2)
+    buf = torch.full((need + offset + 64,), 7, dtype=torch.uint8, device="cuda")
+    got = torch.empty_like(x), torch.empty_like(W), torch.empty_like(b)
+    rest = (x.data_ptr(), W.data_ptr(), None, *(t.data_ptr() for t in got), buf.data_ptr() + offset,
+            need, F.device_error_word("cuda:0").data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert lib.flce_linear_backward(at, dy.data_ptr(), *rest) == 0
+    assert bool((buf[:offset] == 7).all()) and bool((buf[offset + need:] == 7).all())
+    for g, w in zip(got, want):
+        assert torch.equal(g, w)
+    big = torch.empty(M * N + 8, dtype=BF16, device="cuda")
+    shifted = big[1:1 + M * N].view(M, N).copy_(dy)
+    assert lib.flce_linear_backward(at, shifted.data_ptr(), *rest) == \
+        (0 if need == lib.flce_linear_workspace_size(at, 1) else 3)
+    for g, w in zip(F.flce_linear_backward(shifted, x, W, b, dW_dtype=BF16, db_dtype=BF16), want):
+        assert torch.equal(g, w)
+    torch.cuda.synchronize()
+    assert F.flce_read_device_error() == 0
+
+
+def test_backward_without_an_activation_holds_no_copy_of_dy():
+    x, W, dy = (torch.zeros(s, dtype=BF16, device="cuda") for s in ((8192, 512), (4096, 512), (8192, 4096)))
+    F.flce_linear_backward(dy, x, W)
+    torch.cuda.synchronize()
+    torch.cuda.reset_peak_memory_stats()
+    held = torch.cuda.memory_allocated()
+    outputs = F.flce_linear_backward(dy, x, W)
+    size = sum(t.numel() * t.element_size() for t in outputs if t is not None)
+    assert torch.cuda.max_memory_allocated() - held - size < 8192 * 4096 * 2 // 8
