@@ -208,6 +208,14 @@ def _kept_dtype(x: torch.Tensor, keep: str) -> torch.dtype:
     return torch.int16 if keep == "relative" else x.dtype
 
 
+def _dense(t: Optional[torch.Tensor]) -> Optional[torch.Tensor]:
+    """A weight or bias itself where the kernels can read it, else a dense copy."""
+    if t is None:
+        return None
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 class FusedLinearFunction(torch.autograd.Function):
     """Autograd form of the linear layer. It keeps x, and the slopes of an activation in the
     form ``keep``."""
@@ -274,7 +282,7 @@ def fused_linear(x, weight, bias=None, residual=None, activation="none", keep="f
         r2 = residual.reshape(-1, weight.shape[0])
         if r2.stride(1) != 1 or r2.stride(0) < r2.shape[1]:
             r2 = r2.contiguous()
-    y = FusedLinearFunction.apply(x2, weight, bias, r2, activation, keep)
+    y = FusedLinearFunction.apply(x2, _dense(weight), _dense(bias), r2, activation, keep)
     return y.reshape(*x.shape[:-1], weight.shape[0])
 
 
@@ -284,7 +292,7 @@ def gated_linear(x, gate_weight, up_weight, activation="silu", keep="relative"):
     precision, or "fixed": to 2^-14 of the largest of 8 neighbouring features, which
     is finer for features of one size and loses those beside an outlier."""
     x2 = _usable(x.reshape(-1, x.shape[-1]))
-    h = GatedLinearFunction.apply(x2, gate_weight, up_weight, activation, keep)
+    h = GatedLinearFunction.apply(x2, _dense(gate_weight), _dense(up_weight), activation, keep)
     return h.reshape(*x.shape[:-1], gate_weight.shape[0])
 
 

@@ -390,3 +390,28 @@ def test_backward_without_an_activation_holds_no_copy_of_dy():
     outputs = F.flce_linear_backward(dy, x, W)
     size = sum(t.numel() * t.element_size() for t in outputs if t is not None)
     assert torch.cuda.max_memory_allocated() - held - size < 8192 * 4096 * 2 // 8
+
+
+# ------------------------------------- weights and biases the kernels cannot read
+@pytest.mark.parametrize("M", [4, 300])
+def test_autograd_forms_copy_weights_and_biases_too(M):
+    """A transposed weight, and ones that start off the 16-byte boundaries, as views of a flat
+    buffer do: the same results and gradients as of dense copies."""
+    n = randn(M)
+    x = n(M, 64)
+    flat = n(1 + 16 * 64 + 16)
+    cases = [(n(64, 16).t(), n(16)), (flat[1:1 + 16 * 64].view(16, 64), flat[1 + 16 * 64:]),
+             (n(16, 72)[:, :64], n(32)[::2])]
+    for W, b in cases:
+        W, b = W.detach().requires_grad_(), b.detach().requires_grad_()
+        dense = [t.detach().clone(memory_format=torch.contiguous_format).requires_grad_() for t in (W, b)]
+        dy = n(M, 16)
+        for weights in ((W, b), dense):
+            y = F.fused_linear(x, *weights, activation="silu")
+            y.backward(dy)
+            h = F.gated_linear(x, weights[0], weights[0])
+            h.backward(dy)
+            if weights[0] is W:
+                want_y, want_h = y, h
+        assert torch.equal(want_y, y) and torch.equal(want_h, h)
+        assert torch.equal(W.grad, dense[0].grad) and torch.equal(b.grad, dense[1].grad)
