@@ -44,6 +44,13 @@ def _deps():
         glob.glob(os.path.join(CSRC, "*.h")) + glob.glob(os.path.join(INCLUDE, "*.h")) + [CALLS_SRC, __file__]
 
 
+def _calls_wanted() -> bool:
+    """Whether the Python calls can be built: torch and Python's headers are here. The
+    library for C callers needs neither."""
+    headers = os.path.join(sysconfig.get_paths()["include"], "Python.h")
+    return importlib.util.find_spec("torch") is not None and os.path.exists(headers)
+
+
 def _calls_commands(obj: str):
     """g++ commands that compile and link the Python calls against the installed torch."""
     torch = os.path.dirname(importlib.util.find_spec("torch").origin)
@@ -61,9 +68,10 @@ def _calls_commands(obj: str):
 
 
 def up_to_date() -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(CALLS)):
+    made = [LIB, CALLS] if _calls_wanted() else [LIB]
+    if not all(os.path.exists(m) for m in made):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
+    t = min(os.path.getmtime(m) for m in made)
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -82,12 +90,15 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         if verbose:
             print(" ".join(cmd), flush=True)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    calls_obj = os.path.join(BUILD, "torch_calls.o")
-    calls_compile, calls_link = _calls_commands(calls_obj)
-    if verbose:
-        print(" ".join(calls_compile), flush=True)
-    procs.append((CALLS_SRC, subprocess.Popen(calls_compile, stdout=subprocess.PIPE,
-                                              stderr=subprocess.STDOUT)))
+    calls_link = None
+    if _calls_wanted():
+        calls_compile, calls_link = _calls_commands(os.path.join(BUILD, "torch_calls.o"))
+        if verbose:
+            print(" ".join(calls_compile), flush=True)
+        procs.append((CALLS_SRC, subprocess.Popen(calls_compile, stdout=subprocess.PIPE,
+                                                  stderr=subprocess.STDOUT)))
+    else:
+        print("torch or Python.h is missing: building the C library alone", flush=True)
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -104,6 +115,8 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         sys.stdout.write(r.stdout.decode(errors="replace"))
         raise RuntimeError("link of libflce_gb300.so failed")
     os.replace(tmp, LIB)
+    if calls_link is None:
+        return LIB
     r = subprocess.run(calls_link, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if r.returncode != 0:
         sys.stdout.write(r.stdout.decode(errors="replace"))
