@@ -500,7 +500,8 @@ flce_status_t flce_grad_norm(int64_t count, const void* const* ptrs, const int64
 /* The same norm, then out[t] = c ptrs[t] with c = min(1, max_norm / (norm + eps))
  * for every tensor, each product rounded once to the tensor's type. out: HOST array
  * of destinations (an entry may equal its ptrs entry: in place; otherwise the two
- * must not overlap), or NULL for all in place. With c = 1 in-place tensors
+ * must not overlap), or NULL for all in place. No two tensors may overlap (a tied
+ * gradient is given once). With c = 1 in-place tensors
  * are not touched. A NaN norm gives c = NaN, an infinite one c = 0, as the formula
  * says. max_norm >= 0, eps >= 0. Nothing is read back to the host. */
 flce_status_t flce_clip_grads(int64_t count, const void* const* ptrs, void* const* out,

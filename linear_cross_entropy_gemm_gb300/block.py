@@ -181,12 +181,13 @@ def clip_grad_norm_(parameters, max_norm: float, norm_type: float = 2.0, *,
     """flce_clip_grads over the ``.grad`` of ``parameters`` (those that have
     one), in place; the norm before the scaling, 0 where there is no gradient.
     Positional arguments as torch.nn.utils.clip_grad_norm_ has them; ``norm_type``
-    can only be 2."""
+    can only be 2. A parameter that is listed twice counts once."""
     if float(norm_type) != 2.0:
         raise ValueError(f"flce: clip_grad_norm_ clips by the 2-norm, got norm_type={norm_type!r}")
     if isinstance(parameters, torch.Tensor):
         parameters = [parameters]
-    grads = [p.grad for p in parameters if p.grad is not None]
+    # A tied parameter that is listed twice is one: two blocks must not scale the same memory.
+    grads = [p.grad for p in dict.fromkeys(parameters) if p.grad is not None]
     if not grads:
         return torch.zeros(())
     return flce_clip_grads(grads, max_norm, eps=eps)

@@ -6,10 +6,12 @@
 // block.py documents them and handles calls that name a stream.
 #include <Python.h>
 
+#include <algorithm>
 #include <array>
 #include <cstdint>
 #include <cstring>
 #include <exception>
+#include <utility>
 #include <vector>
 
 #include <ATen/ATen.h>
@@ -373,6 +375,22 @@ const Tensor& read_grads(PyObject* grads, PyObject* out, GradList* l) {
   return first;
 }
 
+// Clipped tensors are written by different blocks: none may share memory with another.
+void check_apart(const GradList& l) {
+  std::vector<std::pair<uintptr_t, uintptr_t>> spans;
+  spans.reserve(l.ptrs.size());
+  for (size_t i = 0; i < l.ptrs.size(); ++i) {
+    const void* to = l.out.empty() ? l.ptrs[i] : l.out[i];
+    const uintptr_t begin = reinterpret_cast<uintptr_t>(to);
+    const uintptr_t bytes = static_cast<uintptr_t>(l.numel[i]) * (l.types[i] == FLCE_DTYPE_FP32 ? 4 : 2);
+    if (bytes > 0) spans.emplace_back(begin, begin + bytes);
+  }
+  std::sort(spans.begin(), spans.end());
+  for (size_t i = 1; i < spans.size(); ++i)
+    if (spans[i].first < spans[i - 1].second)
+      refuse(PyExc_ValueError, "flce: %s must not overlap: give each once", "clipped tensors");
+}
+
 // clip_grads(grads, out, max_norm, eps, workspace) -> norm; max_norm None: the norm alone.
 PyObject* clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 5, [&] {
@@ -382,6 +400,7 @@ PyObject* clip_grads(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t count = static_cast<int64_t>(l.ptrs.size());
     double max_norm = 0.0, eps = 0.0;
     if (a[2] != Py_None) {
+      check_apart(l);
       max_norm = PyFloat_AsDouble(a[2]);
       eps = PyFloat_AsDouble(a[3]);
       if (PyErr_Occurred()) throw Refused();

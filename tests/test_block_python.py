@@ -19,3 +19,15 @@ def test_clip_grad_norm_takes_torchs_positional_arguments():
     for norm_type in (1.0, float("inf"), 1e-6):
         with pytest.raises(ValueError, match="norm_type"):
             F.clip_grad_norm_([p], 1.0, norm_type)
+
+
+def test_clip_grad_norm_takes_a_tied_parameter_once(monkeypatch):
+    """In place, a tensor that is given twice would be scaled by two blocks at once."""
+    from linear_cross_entropy_gemm_gb300 import block
+    seen = []
+    monkeypatch.setattr(block, "flce_clip_grads", lambda grads, *a, **k: seen.append(list(grads)))
+    p, q = torch.nn.Parameter(torch.ones(3)), torch.nn.Parameter(torch.ones(3))
+    p.grad, q.grad = torch.ones(3), torch.ones(3)
+    F.clip_grad_norm_(iter([p, q, p, q, torch.nn.Parameter(torch.ones(1))]), 1.0)
+    F.clip_grad_norm_(p, 1.0)
+    assert [[id(g) for g in grads] for grads in seen] == [[id(p.grad), id(q.grad)], [id(p.grad)]]

@@ -415,3 +415,28 @@ def test_autograd_forms_copy_weights_and_biases_too(M):
                 want_y, want_h = y, h
         assert torch.equal(want_y, y) and torch.equal(want_h, h)
         assert torch.equal(W.grad, dense[0].grad) and torch.equal(b.grad, dense[1].grad)
+
+
+# ------------------------------------------------------------ tensors given twice
+def test_clip_refuses_tensors_that_share_memory():
+    n = randn(31)
+    flat = n(100, dtype=FP32)
+    kept = flat.clone()
+    with pytest.raises(ValueError, match="overlap"):
+        F.flce_clip_grads([flat, flat], 0.1)
+    with pytest.raises(ValueError, match="overlap"):
+        F.flce_clip_grads([flat[:60], flat[59:]], 0.1)
+    with pytest.raises(ValueError, match="overlap"):
+        F.flce_clip_grads([flat, kept], 0.1, out=[torch.empty_like(flat)] * 2)
+    assert torch.equal(flat, kept)
+    twice = F.flce_grad_norm([flat, flat])  # the norm only reads
+    assert abs(float(twice) - 2 ** 0.5 * float(flat.double().norm())) <= 1e-5 * float(twice)
+    empty = flat[:0]
+    one = F.flce_clip_grads([flat[:60], flat[60:], empty, empty], 0.1)
+    p = torch.nn.Parameter(kept.clone())
+    p.grad = kept.clone()
+    tied = F.clip_grad_norm_([p, p], 0.1)
+    want = float(kept.double().norm())
+    for norm, g in ((one, flat), (tied, p.grad)):
+        assert abs(float(norm) - want) <= 1e-5 * want
+        assert bool(((g.double() - kept.double() * (0.1 / (want + 1e-6))).abs() <= 1e-5 * kept.double().abs()).all())
