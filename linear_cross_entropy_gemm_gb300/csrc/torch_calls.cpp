@@ -138,6 +138,8 @@ Tensor scratch(PyObject* given, size_t need, const Tensor& x) {
     const Tensor& w = tensor(given, "workspace");
     if (w.scalar_type() != at::kByte || !w.is_cuda() || !w.is_contiguous())
       refuse(PyExc_TypeError, "flce: %s must be a contiguous uint8 CUDA tensor", "workspace");
+    if (w.get_device() != x.get_device())
+      refuse(PyExc_ValueError, "flce: %s must be on x's device", "workspace");
     if (static_cast<size_t>(w.numel()) >= need) return w;
   }
   return at::empty({static_cast<int64_t>(need)}, x.options().dtype(at::kByte));
