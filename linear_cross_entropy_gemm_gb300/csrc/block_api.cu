@@ -452,6 +452,7 @@ flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, 
     sa.res_vec = aligned16(residual) && sa.ld_res % 8 == 0 ? 1 : 0;
     sa.keep = static_cast<uint16_t*>(pre);
     sa.relative = p->keep == FLCE_KEEP_RELATIVE ? 1 : 0;
+    sa.wp = static_cast<const uint16_t*>(W);
     sa.act = p->activation;
     return done(launch_small(false, false, sa, static_cast<cudaStream_t>(stream)));
   }
@@ -467,6 +468,8 @@ flce_status_t flce_linear_forward(const flce_linear_params_t* p, const void* x, 
   ea.keep = !pre ? 0 : p->keep == FLCE_KEEP_RELATIVE ? 2 : 1;
   ea.M = M;
   ea.N = N;
+  ea.sign = {static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(W), ea.bias,
+             pitch(p->ld_x, K), K};
   PairArgs g = pair_args(M, N, K, 1, false, false, f16, dev_err);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaSuccess;
@@ -615,6 +618,7 @@ flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, co
       return FLCE_ERR_CUDA;
     sa.keep = static_cast<uint16_t*>(pre);
     sa.relative = p->keep == FLCE_KEEP_RELATIVE ? 1 : 0;
+    sa.wp = static_cast<const uint16_t*>(Wg);
     sa.act = p->activation;
     return done(launch_small(true, false, sa, static_cast<cudaStream_t>(stream)));
   }
@@ -626,6 +630,8 @@ flce_status_t flce_gated_forward(const flce_gated_params_t* p, const void* x, co
   ea.keep = !pre ? 0 : p->keep == FLCE_KEEP_RELATIVE ? 2 : 1;
   ea.M = M;
   ea.F = F;
+  ea.sign = {static_cast<const uint16_t*>(x), static_cast<const uint16_t*>(Wg), nullptr,
+             pitch(p->ld_x, K), K};
   uint16_t* keep = static_cast<uint16_t*>(pre);
   PairArgs g = pair_args(M, F, K, 1, false, true, f16, dev_err);
   cudaStream_t s = static_cast<cudaStream_t>(stream);

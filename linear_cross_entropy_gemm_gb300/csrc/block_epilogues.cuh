@@ -70,9 +70,11 @@ __device__ __forceinline__ uint64_t gelu_cdf2(uint64_t z, uint64_t& gauss) {
   q = ffma2(t, q, splat(0.109055996f));
   q = ffma2(t, q, splat(0.119156331f));
   q = fmul2(fmul2(q, t), gauss);
-  float a, b;
+  float a, b, qa, qb, ra, rb;
   f32x2_split(z, a, b);
-  return fadd2(q ^ (~z & kSign), f32x2(a < 0.f ? 0.f : 1.f, b < 0.f ? 0.f : 1.f));
+  f32x2_split(q, qa, qb);
+  f32x2_split(ffma2(q, splat(-1.f), splat(1.f)), ra, rb);
+  return f32x2(a < 0.f ? qa : ra, b < 0.f ? qb : rb);
 }
 // gelu_tanh: (1 + tanh w) / 2 = 1 / (1 + e^-2w), w = c (z + 0.044715 z^3).
 __device__ __forceinline__ uint64_t gelu_tanh_gate2(uint64_t z) {
@@ -206,29 +208,19 @@ __device__ __forceinline__ uint32_t encode_slopes_relative(uint64_t z, uint64_t 
 }
 
 // v = a(v), and the codes of the slopes.
-template <int N>
-__device__ __forceinline__ void act_keep_slopes(int act, bool relative, float (&v)[N],
-                                                uint32_t (&w)[N / 2]) {
-  with_act(act, [&](auto a) {
-    constexpr int kAct = decltype(a)::value;
-    const auto all = [&](auto rel) {
+template <int ACT, bool RELATIVE, int N>
+__device__ __forceinline__ void act_keep_slopes(float (&v)[N], uint32_t (&w)[N / 2]) {
 #pragma unroll
-      for (int j = 0; j < N; j += 2) {
-        uint64_t val, slope;
-        const uint64_t z = f32x2(v[j], v[j + 1]);
-        act2<kAct>(z, val, slope);
-        if constexpr (decltype(rel)::value)
-          w[j / 2] = encode_slopes_relative<kAct>(z, slope);
-        else
-          w[j / 2] = encode_slopes(slope);
-        f32x2_split(val, v[j], v[j + 1]);
-      }
-    };
-    if (kAct != kActNone && kAct != kActRelu && relative)
-      all(std::true_type());
+  for (int j = 0; j < N; j += 2) {
+    uint64_t val, slope;
+    const uint64_t z = f32x2(v[j], v[j + 1]);
+    act2<ACT>(z, val, slope);
+    if constexpr (RELATIVE && ACT != kActNone && ACT != kActRelu)
+      w[j / 2] = encode_slopes_relative<ACT>(z, slope);
     else
-      all(std::false_type());
-  });
+      w[j / 2] = encode_slopes(slope);
+    f32x2_split(val, v[j], v[j + 1]);
+  }
 }
 // v = a(v), and x = u a'(v).
 template <int N>
@@ -376,6 +368,126 @@ __device__ __forceinline__ void decode_group(const uint4& u, float (&v)[8]) {
     v[2 * i] = kept_number(w[i] << 16, (__uint_as_float(0x4B400000u + lo) - kRound) * inv);
     v[2 * i + 1] = kept_number(w[i], (__uint_as_float(0x4B400000u + hi) - kRound) * inv);
   }
+}
+
+// --------------------------------------------------------- signs of relu's inputs
+// relu's slope jumps at 0, so there the sign of a sum is the whole gradient. The tensor core
+// drops the low bits of its running sum at every step of 16 products (off by 1.9e-5 of the sums'
+// size after 16384 of them; 1.5e-6 with fp32 adds that round): one element in a million came
+// out on the wrong side of 0, which put fp16 gradients of 5942 x 6456 x 1408 0.0023 of their
+// size from 64 bits, where 32-bit sums are 0.0005 from them. A forward that keeps relu's
+// slopes therefore takes the sign of a sum that is no further from 0 than its own error from
+// the products once more, added in fp32. (Its value is that of the tensor core all the same.)
+//
+// The error: 2^-24 of the largest sum for each step, of this row's sums and of this column's. A
+// warp that still has more than kMaxAgain such sums takes them as they are: they are no accident
+// then, and each costs K products of one warp.
+constexpr int kMaxAgain = 4;
+__device__ __forceinline__ float sum_error(float largest, int K) {
+  return largest * (static_cast<float>(K / 16 + 8) * 0x1p-24f);
+}
+
+template <int N>
+__device__ __forceinline__ float largest_of(const float (&v)[N]) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < N; j += 2) m = fmax3(m, fabsf(v[j]), fabsf(v[j + 1]));
+  return m;
+}
+// Bit j: z[j] is not 0 but within the error of a sum of K products in this row.
+template <int N>
+__device__ __forceinline__ uint32_t near_zero(const float (&z)[N], float largest, int K) {
+  const float off = sum_error(largest, K);
+  float least = off;
+#pragma unroll
+  for (int j = 0; j < N; j += 2) least = fmin3(least, fabsf(z[j]), fabsf(z[j + 1]));
+  uint32_t near = 0;
+  if (least < off) {
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (fabsf(z[j]) < off && z[j] != 0.f) near |= 1u << j;
+  }
+  return near;
+}
+// Clears the bits of sums that are small as all of their column are, whose error is as much
+// smaller. By the whole warp, a row to a lane.
+__device__ __forceinline__ void near_zero_of_column(const float (&z)[32], int K, uint32_t& near) {
+  const uint32_t columns = __reduce_or_sync(0xffffffffu, near);
+#pragma unroll
+  for (int j = 0; j < 32; ++j) {
+    if (((columns >> j) & 1u) == 0) continue;
+    const float size = fabsf(z[j]);
+    const float most = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(size)));
+    if (size >= sum_error(most, K)) near &= ~(1u << j);
+  }
+}
+struct SignArgs {
+  const uint16_t *x, *W;  // [M, ld_x]; [N, K]
+  const uint16_t* bias;   // or null
+  int64_t ld_x;
+  int K;
+};
+// Bit j: the sum of this lane's row and column col + j is above 0, for the bits of `near`, which
+// is cleared where there are too many. By the whole warp.
+__device__ __forceinline__ uint32_t signs_again(const SignArgs& a, bool f16, int row, int col,
+                                                uint32_t& near, int lane) {
+  uint32_t above = 0;
+  if (__reduce_add_sync(0xffffffffu, __popc(near)) > kMaxAgain) near = 0;
+  uint32_t left = near;
+  for (unsigned todo = __ballot_sync(0xffffffffu, left != 0); todo != 0;
+       todo = __ballot_sync(0xffffffffu, left != 0)) {
+    const int src = __ffs(static_cast<int>(todo)) - 1;
+    const int j = __ffs(static_cast<int>(__shfl_sync(0xffffffffu, left, src))) - 1;
+    const int r = __shfl_sync(0xffffffffu, row, src), c = __shfl_sync(0xffffffffu, col, src) + j;
+    const uint16_t* x = a.x + static_cast<size_t>(r) * a.ld_x;
+    const uint16_t* w = a.W + static_cast<size_t>(c) * a.K;
+    float s[4] = {};
+#pragma unroll 2
+    for (int k = lane * 8; k < a.K; k += 256) {
+      const uint4 xv = *reinterpret_cast<const uint4*>(x + k);
+      const uint4 wv = *reinterpret_cast<const uint4*>(w + k);
+      const uint32_t p[4] = {xv.x, xv.y, xv.z, xv.w}, q[4] = {wv.x, wv.y, wv.z, wv.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[e] = fmaf(unpack_16(p[e] & 0xFFFFu, f16), unpack_16(q[e] & 0xFFFFu, f16), s[e]);
+        s[e] = fmaf(unpack_16(p[e] >> 16, f16), unpack_16(q[e] >> 16, f16), s[e]);
+      }
+    }
+    float z = (s[0] + s[1]) + (s[2] + s[3]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+    if (a.bias) z += unpack_16(a.bias[c], f16);
+    if (lane == src) {
+      left &= left - 1;
+      if (z > 0.f) above |= 1u << j;
+    }
+  }
+  return above;
+}
+// The codes of relu's slopes, with those of `near` as `above` says.
+template <int N>
+__device__ __forceinline__ void put_signs(uint32_t near, uint32_t above, uint32_t (&w)[N]) {
+#pragma unroll
+  for (int j = 0; j < 2 * N; ++j)
+    if ((near >> j) & 1u)
+      w[j / 2] = __byte_perm(w[j / 2], ((above >> j) & 1u) ? 0xA000u : 0x2000u,
+                             (j & 1) ? 0x5410 : 0x3254);
+}
+
+// What a forward keeps, as a compile-time constant: the loops over a tile's columns are made for
+// each, so that one's registers and branches do not slow another down. The arguments' `keep`: 0
+// nothing, 1 the fixed form, 2 the relative one.
+enum Keep : int { kKeepNone = 0, kKeepFixed = 1, kKeepRelative = 2, kKeepSigns = 3 };
+template <class Fn>
+__device__ __forceinline__ void with_keep(int keep, int act, Fn f) {
+  if (keep == 0)
+    f(std::integral_constant<int, kKeepNone>());
+  else if (act == kActRelu)
+    f(std::integral_constant<int, kKeepSigns>());  // the slopes 0 and 1 are the same in both forms
+  else if (keep == 2)
+    f(std::integral_constant<int, kKeepRelative>());
+  else
+    f(std::integral_constant<int, kKeepFixed>());
 }
 
 // A 16-bit [rows, cols] output: through a TMA store map of 32 x 32 boxes where
@@ -584,6 +696,7 @@ struct LinearArgs {
   int act, fp16;
   int keep;              // also write the slopes; 2: in the relative form
   int M, N;
+  SignArgs sign;
   Out16 y, slope;
 };
 
@@ -594,6 +707,14 @@ struct LinearEpi {
   template <class Acc>
   __device__ static void tile(const Args& a, const PairArgs&, int, int row0, int col_base, int lane,
                               const Acc& acc, Staging& st, const TileSlice& sl) {
+    with_keep(a.keep, a.act, [&](auto keep) {
+      tile_as<decltype(keep)::value>(a, row0, col_base, lane, acc, st, sl);
+    });
+  }
+  template <int KEEP, class Acc>
+  __device__ __forceinline__ static void tile_as(const Args& a, int row0, int col_base, int lane,
+                                                 const Acc& acc, Staging& st,
+                                                 const TileSlice& sl) {
     const int row = row0 + lane;
     const bool f16 = a.fp16 != 0;
 #pragma unroll 1
@@ -604,13 +725,29 @@ struct LinearEpi {
       if (col0 >= a.N || row0 >= a.M) break;  // uniform over the warp
       float v[32];
       acc.load(acc_col, v);
+      float largest = 0.f;
+      if constexpr (KEEP == kKeepSigns) largest = largest_of(v);
       if (a.bias) add_row_16(a.bias + col0, a.N - col0, f16, v);
-      if (a.keep) {
-        uint32_t w[16];
-        act_keep_slopes(a.act, a.keep == 2, v, w);
-        put_words(a.slope, a.M, a.N, row0, col0, w, st, lane);
-      } else {
+      if constexpr (KEEP == kKeepNone) {
         act_all(a.act, v);
+      } else {
+        uint32_t w[16];
+        if constexpr (KEEP == kKeepSigns) {
+          uint32_t near = row < a.M ? near_zero(v, largest, a.sign.K) : 0u, above = 0;
+          if (a.N - col0 < 32) near &= (1u << (a.N - col0)) - 1u;
+          const bool any = __any_sync(0xffffffffu, near != 0);
+          if (any) {
+            near_zero_of_column(v, a.sign.K, near);
+            above = signs_again(a.sign, f16, row, col0, near, lane);
+          }
+          act_keep_slopes<kActRelu, false>(v, w);
+          if (any) put_signs(near, above, w);
+        } else {
+          with_act(a.act, [&](auto act) {
+            act_keep_slopes<decltype(act)::value, KEEP == kKeepRelative>(v, w);
+          });
+        }
+        put_words(a.slope, a.M, a.N, row0, col0, w, st, lane);
       }
       if (a.res) {
         if (a.res_vec == 0)
@@ -630,6 +767,7 @@ struct GatedArgs {
   int act, fp16;
   int keep;  // also write a(g) and u a'(g); 2: in the relative form
   int M, F;
+  SignArgs sign;
   Out16 h, val, cross;
 };
 
@@ -640,6 +778,14 @@ struct GatedEpi {
   template <class Acc>
   __device__ static void tile(const Args& a, const PairArgs&, int, int row0, int col_base, int lane,
                               const Acc& acc, Staging& st, const TileSlice& sl) {
+    with_keep(a.keep, a.act, [&](auto keep) {
+      tile_as<decltype(keep)::value>(a, row0, col_base, lane, acc, st, sl);
+    });
+  }
+  template <int KEEP, class Acc>
+  __device__ __forceinline__ static void tile_as(const Args& a, int row0, int col_base, int lane,
+                                                 const Acc& acc, Staging& st,
+                                                 const TileSlice& sl) {
     const bool f16 = a.fp16 != 0;
 #pragma unroll 1
     for (int c = sl.c_lo; c < sl.c_hi; ++c) {
@@ -650,16 +796,38 @@ struct GatedEpi {
       float g[32], u[32];
       acc.load(acc_col, g);
       acc.load(sl.up_off + acc_col, u);
-      if (a.keep) {
-        float x[32];  // u a'(g)
-        act_cross(a.act, g, u, x);
-        uint32_t w[16];
-        encode_groups(a.keep == 2, g, w);
-        staged_block_16(&a.val.map, col0, row0, w, st, lane);
-        encode_groups(a.keep == 2, x, w);
-        staged_block_16(&a.cross.map, col0, row0, w, st, lane);
-      } else {
+      if constexpr (KEEP == kKeepNone) {
         act_all(a.act, g);
+      } else {
+        float x[32];  // u a'(g)
+        if constexpr (KEEP == kKeepSigns) {
+          uint32_t near = row0 + lane < a.M ? near_zero(g, largest_of(g), a.sign.K) : 0u, above = 0;
+          if (a.F - col0 < 32) near &= (1u << (a.F - col0)) - 1u;
+          const bool any = __any_sync(0xffffffffu, near != 0);
+          if (any) {
+            near_zero_of_column(g, a.sign.K, near);
+            above = signs_again(a.sign, f16, row0 + lane, col0, near, lane);
+          }
+          act_cross(kActRelu, g, u, x);
+          if (any) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if ((near >> j) & 1u) x[j] = ((above >> j) & 1u) ? u[j] : 0.f;
+          }
+        } else {
+          act_cross(a.act, g, u, x);
+        }
+        uint32_t w[16];
+        const auto encode_as = [&](const float (&v)[32], uint32_t (&out)[16]) {
+          if constexpr (KEEP == kKeepSigns)  // of either form
+            encode_groups(a.keep == 2, v, out);
+          else
+            encode_groups_as<KEEP == kKeepRelative>(v, out);
+        };
+        encode_as(g, w);
+        staged_block_16(&a.val.map, col0, row0, w, st, lane);
+        encode_as(x, w);
+        staged_block_16(&a.cross.map, col0, row0, w, st, lane);
       }
 #pragma unroll
       for (int j = 0; j < 32; j += 2)

@@ -64,6 +64,7 @@ cudaError_t launch_grad_w(bool two, const PairArgs& g, const GradWArgs& ea, int 
 struct SmallArgs {
   CUtensorMap w, w2, x, x2;  // x, x2: above 32 tokens only
   const uint16_t *xp, *xp2;  // x and the second segment's, [M, ld_x]
+  const uint16_t* wp;        // weights [N, k_len] of the activation's argument, with keep
   int64_t ld_x;
   int k_len;                 // sum elements of a segment
   const uint16_t* bias;

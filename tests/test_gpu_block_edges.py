@@ -440,3 +440,72 @@ def test_clip_refuses_tensors_that_share_memory():
     for norm, g in ((one, flat), (tied, p.grad)):
         assert abs(float(norm) - want) <= 1e-5 * want
         assert bool(((g.double() - kept.double() * (0.1 / (want + 1e-6))).abs() <= 1e-5 * kept.double().abs()).all())
+
+
+# ------------------------------------------------------------ signs of relu's inputs
+def relu_signs(M, K, N, dtype, gated, seed):
+    """(kept slopes above 0, z in 64 bits)."""
+    n = randn(seed)
+    x, W = n(M, K, dtype=dtype), n(N, K, std=K ** -0.5, dtype=dtype)
+    z = x.double() @ W.double().t()
+    if gated:
+        # u = 1 everywhere: the kept u a'(g) is the slope.
+        x[:, 0] = 1
+        Wu = torch.zeros(N, K, dtype=dtype, device="cuda")
+        Wu[:, 0] = 1
+        z = x.double() @ W.double().t()
+        pre = torch.empty(2, M, N, dtype=torch.int16, device="cuda")
+        F.flce_gated_forward(x, W, Wu, activation="relu", pre=pre)
+        return (pre[1] & 0x3FFF) > 0, z
+    b = n(N, std=0.1, dtype=dtype)
+    pre = torch.empty(M, N, dtype=dtype, device="cuda")
+    F.flce_linear_forward(x, W, b, activation="relu", pre=pre)
+    return R.kept_slopes(pre) > 0.5, z + b.double()
+
+
+@pytest.mark.parametrize("M,K,N", [(2048, 16384, 2048), (1000, 8192, 4100), (64, 16384, 16384), (20, 12808, 30000)])
+@pytest.mark.parametrize("gated", [False, True], ids=["linear", "gated"])
+@pytest.mark.parametrize("dtype", [BF16, FP16], ids=["bf16", "fp16"])
+def test_relu_takes_the_sign_of_an_accurate_sum(M, K, N, gated, dtype):
+    """z has size 1. The tensor core's sums are off by 1e-5 to 2e-5 here (root mean square), fp32 adds
+    of K / 128 products and then of 128 partial sums by 3.4e-7: ten times that, 2^-18, leaves no
+    wrong sign, of which the tensor core's sums alone have several in each of these."""
+    above, z = relu_signs(M, K, -(-N // 8) * 8 if gated else N, dtype, gated, 5)
+    wrong = (above != (z > 0)) & (z.abs() > 2.0 ** -18)
+    assert int(wrong.sum()) == 0
+
+
+def test_relu_with_rows_and_weights_far_smaller_than_their_neighbours():
+    """Zero tokens, zero weights and tiny weights: more sums near 0 than are looked at again.
+    Outside the tensor core's error (2^-24 of the row's largest sum for each 16 products, four
+    times) every sign is right."""
+    n = randn(6)
+    M, K, N = 600, 4096, 520
+    x, W = n(M, K), n(N, K, std=K ** -0.5)
+    x[::3] = 0
+    W[::5] = 0
+    W[1::5] = (W[1::5].float() * 2.0 ** -14).to(BF16)
+    pre = torch.empty(M, N, dtype=BF16, device="cuda")
+    y = F.flce_linear_forward(x, W, activation="relu", pre=pre)
+    z = x.double() @ W.double().t()
+    error = 4 * (K / 16 + 8) * 2.0 ** -24 * z.abs().amax(1, keepdim=True)
+    above = R.kept_slopes(pre) > 0.5
+    assert bool((above == (z > 0))[z.abs() > error].all())
+    assert not bool(above[::3].any()) and not bool(above[:, ::5].any())
+    assert torch.equal(y, F.flce_linear_forward(x, W, activation="relu"))
+
+
+@pytest.mark.parametrize("M,K,N", [(5942, 6456, 1408), (64, 11112, 12368)])
+def test_relu_gradients_are_those_of_an_accurate_sum(M, K, N):
+    """fp16: dz without a wrong sign is exact, so dx and dW are off by their rounding alone, and by
+    what signs inside 2^-18 can do: a share of 2^-18 of the elements, sqrt(2^-17) if all were wrong,
+    of which the fp32 sum's 3.4e-7 leaves a tenth of the share."""
+    n = randn(9)
+    x, W, dy = n(M, K, dtype=FP16), n(N, K, std=K ** -0.5, dtype=FP16), n(M, N, std=0.01, dtype=FP16)
+    pre = torch.empty(M, N, dtype=FP16, device="cuda")
+    F.flce_linear_forward(x, W, activation="relu", pre=pre)
+    dx, dW, _ = F.flce_linear_backward(dy, x, W, activation="relu", pre=pre)
+    dz = dy.double() * (x.double() @ W.double().t() > 0)
+    for got, want, u in ((dx, dz @ W.double(), 2.0 ** -11), (dW, dz.t() @ x.double(), 0.0)):
+        err = float((got.double() - want).norm() / want.norm())
+        assert err <= u + 2.0 ** -23 * (max(M, N) / 16) + (0.1 * 2.0 ** -17) ** 0.5, err
