@@ -49,9 +49,10 @@ __device__ __forceinline__ uint64_t exp2_2(uint64_t x) {
   f32x2_split(x, a, b);
   return f32x2(fast_exp2(a), fast_exp2(b));
 }
-// 1 / (1 + e^-z) from ex2 and the approximate reciprocal: relative error a few 2^-22,
-// far below the 16-bit rounding of anything made from it. e^-z overflows to +inf for
-// z < -88, and the reciprocal is then 0, its limit.
+// 1 / (1 + e^-z) from ex2 and the approximate reciprocal: relative error (|z| + 4) 2^-24 for
+// negative z, whose exponent is rounded to fp32 (5e-6 at z = -87), and 2^-22 above, far
+// below the 16-bit rounding of anything made from it. 0 under z = -87.3, where fp32's normal
+// numbers end (e^-z overflows to +inf soon after, and its reciprocal is 0).
 __device__ __forceinline__ uint64_t sigmoid2(uint64_t z) {
   return rcp2(fadd2(exp2_2(fmul2(z, splat(-kLog2e))), splat(1.f)));
 }

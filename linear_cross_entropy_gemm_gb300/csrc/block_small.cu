@@ -4,9 +4,10 @@
 // weights from HBM, so the weights take the MMA's 128 rows (TMEM lanes) and the
 // tokens its columns:
 //
-//   D[f, m] = sum_k Wt[f, k] x[m, k],   128 features x NT tokens, NT = 16 .. 128
+//   D[f, m] = sum_k Wt[f, k] x[m, k],   128 features x NT tokens, NT = 16, 32, 64, 128
 //
-// and a tile wastes at most 15 of the columns it computes. A tile of the gated
+// and a tile computes up to half of its columns for nothing (33 tokens take 64, 129 two
+// tiles of 128), which the stream of weights hides. A tile of the gated
 // projection has 64 rows of each weight, so that its ring stage is no larger. One CTA per tile and K
 // slice: the slices of a tile form a cluster (1, 2, 4 or 8 CTAs), so that even a
 // narrow layer keeps every SM streaming. The slices join through distributed shared
@@ -130,6 +131,8 @@ __device__ __forceinline__ void fetch_x(const SmallArgs& a, int kb, int m0, int 
 // dz), else its rows are the features. TWO: two weight tensors with one x (gated
 // forward); rows 0 .. 63 of a tile are the first's, 64 .. 127 the second's. The
 // two-segment sum of the gated dx is `k_split` < `k_blocks`.
+// The bound of one block is for ptxas, which otherwise stops at 64 registers and spills (32 x
+// 14336 x 4096 23.45 us, 22.99 us); two blocks of 114 fit an SM.
 template <int NT, bool TWO, bool W_MN>
 __global__ void __launch_bounds__(kSmThreads, 1)
     small_gemm_kernel(const __grid_constant__ SmallArgs a) {
