@@ -132,7 +132,7 @@ __device__ __forceinline__ void fetch_x(const SmallArgs& a, int kb, int m0, int 
 // forward); rows 0 .. 63 of a tile are the first's, 64 .. 127 the second's. The
 // two-segment sum of the gated dx is `k_split` < `k_blocks`.
 // The bound of one block is for ptxas, which otherwise stops at 64 registers and spills (32 x
-// 14336 x 4096 23.45 us, 22.99 us); two blocks of 114 fit an SM.
+// 14336 x 4096 23.45 us, 22.99 us); two blocks of 148 fit an SM.
 template <int NT, bool TWO, bool W_MN>
 __global__ void __launch_bounds__(kSmThreads, 1)
     small_gemm_kernel(const __grid_constant__ SmallArgs a) {
@@ -318,108 +318,120 @@ __global__ void __launch_bounds__(kSmThreads, 1)
   // This CTA's features: [rank * own, rank * own + own) of the tile, 8 at a time.
   const int groups = own / 8;
   const bool f16 = a.fp16 != 0;
-  // relu's signs (signs_again) are looked at by whole warps.
-  const bool signs = !W_MN && a.keep && a.act == kActRelu;
-  for (int i0 = warp * 32; i0 < tokens * groups; i0 += kSmThreads) {
-    const int i = i0 + lane, t = i / groups, gl = i - t * groups;
-    const int col = f0 + rank * own + gl * 8, n = a.N - col;
-    const bool mine = i < tokens * groups && n > 0;
-    if (!mine && !signs) continue;
-    float v[kProducts][8];
-    const size_t row = static_cast<size_t>(m0 + t);
-    uint32_t near = 0, above = 0;
-    if (mine) {
+  // relu's signs (signs_again) are looked at by whole warps, in a loop of its own.
+  const auto finish = [&](auto with_signs) {
+    constexpr bool kSigns = decltype(with_signs)::value;
+    for (int i0 = warp * 32; i0 < tokens * groups; i0 += kSmThreads) {
+      const int i = i0 + lane, t = i / groups, gl = i - t * groups;
+      const int col = f0 + rank * own + gl * 8, n = a.N - col;
+      const bool mine = i < tokens * groups && n > 0;
+      if (!mine && !kSigns) continue;
+      float v[kProducts][8];
+      const size_t row = static_cast<size_t>(m0 + t);
+      uint32_t near = 0, above = 0;
+      if (mine) {
 #pragma unroll
-      for (int h = 0; h < kProducts; ++h) {
-        const float* p = part + (h * NT + t) * own + gl * 8;
-        const int step = kProducts * NT * own;
+        for (int h = 0; h < kProducts; ++h) {
+          const float* p = part + (h * NT + t) * own + gl * 8;
+          const int step = kProducts * NT * own;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[h][j] = p[j];
+          for (int j = 0; j < 8; ++j) v[h][j] = p[j];
 #pragma unroll
-        for (int r = 1; r < 8; ++r) {
-          if (r < slices) {
-            const float4 q0 = *reinterpret_cast<const float4*>(p + r * step);
-            const float4 q1 = *reinterpret_cast<const float4*>(p + r * step + 4);
-            v[h][0] += q0.x;
-            v[h][1] += q0.y;
-            v[h][2] += q0.z;
-            v[h][3] += q0.w;
-            v[h][4] += q1.x;
-            v[h][5] += q1.y;
-            v[h][6] += q1.z;
-            v[h][7] += q1.w;
+          for (int r = 1; r < 8; ++r) {
+            if (r < slices) {
+              const float4 q0 = *reinterpret_cast<const float4*>(p + r * step);
+              const float4 q1 = *reinterpret_cast<const float4*>(p + r * step + 4);
+              v[h][0] += q0.x;
+              v[h][1] += q0.y;
+              v[h][2] += q0.z;
+              v[h][3] += q0.w;
+              v[h][4] += q1.x;
+              v[h][5] += q1.y;
+              v[h][6] += q1.z;
+              v[h][7] += q1.w;
+            }
           }
         }
-      }
-      const float largest = signs ? largest_of(v[0]) : 0.f;
-      if (!TWO && a.bias) {
-        float b[8];
-        load8(a.bias + col, n, true, f16, b);
+        float largest = 0.f;
+        if constexpr (kSigns) largest = largest_of(v[0]);
+        if (!TWO && a.bias) {
+          float b[8];
+          load8(a.bias + col, n, true, f16, b);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[0][j] += b[j];
-      }
-      if (signs) {
-        near = near_zero(v[0], largest, a.k_len);
-        if (n < 8) near &= (1u << n) - 1u;
-      }
-    }
-    if (signs && __any_sync(0xffffffffu, near != 0))
-      above = signs_again(SignArgs{a.xp, a.wp, a.bias, a.ld_x, a.k_len}, f16,
-                          static_cast<int>(row), col, near, lane);
-    if (!mine) continue;
-    if constexpr (TWO) {
-      float (&u)[8] = v[kProducts - 1];
-      if (a.keep) {
-        float x[8];
-        act_cross(a.act, v[0], u, x);
-        if (signs) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if ((near >> j) & 1u) x[j] = ((above >> j) & 1u) ? u[j] : 0.f;
+          for (int j = 0; j < 8; ++j) v[0][j] += b[j];
         }
-        uint16_t* k = a.keep + row * a.N + col;
-        uint32_t w[4];
-        encode_groups(a.relative != 0, v[0], w);
-        *reinterpret_cast<uint4*>(k) = make_uint4(w[0], w[1], w[2], w[3]);
-        encode_groups(a.relative != 0, x, w);
-        *reinterpret_cast<uint4*>(k + static_cast<size_t>(a.M) * a.N) =
-            make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-        act_all(a.act, v[0]);
+        if constexpr (kSigns) {
+          near = near_zero(v[0], largest, a.k_len);
+          if (n < 8) near &= (1u << n) - 1u;
+        }
       }
+      if constexpr (kSigns) {
+        if (__any_sync(0xffffffffu, near != 0))
+          above = signs_again(SignArgs{a.xp, a.wp, a.bias, a.ld_x, a.k_len}, f16,
+                              static_cast<int>(row), col, near, lane);
+        if (!mine) continue;
+      }
+      if constexpr (TWO) {
+        float (&u)[8] = v[kProducts - 1];
+        if (a.keep) {
+          float x[8];
+          act_cross(a.act, v[0], u, x);
+          if constexpr (kSigns) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[0][j] *= u[j];
-    } else {
-      if (a.keep) {
-        uint32_t w[4];
-        with_act(a.act, [&](auto act) {
-          constexpr int kAct = decltype(act)::value;
-          if (a.relative != 0)
-            act_keep_slopes<kAct, true>(v[0], w);
-          else
-            act_keep_slopes<kAct, false>(v[0], w);
-        });
-        if (signs) put_signs(near, above, w);
-        uint16_t* k = a.keep + row * a.N + col;
-        if (a.N % 8 == 0) {
+            for (int j = 0; j < 8; ++j)
+              if ((near >> j) & 1u) x[j] = ((above >> j) & 1u) ? u[j] : 0.f;
+          }
+          uint16_t* k = a.keep + row * a.N + col;
+          uint32_t w[4];
+          encode_groups(a.relative != 0, v[0], w);
           *reinterpret_cast<uint4*>(k) = make_uint4(w[0], w[1], w[2], w[3]);
+          encode_groups(a.relative != 0, x, w);
+          *reinterpret_cast<uint4*>(k + static_cast<size_t>(a.M) * a.N) =
+              make_uint4(w[0], w[1], w[2], w[3]);
         } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            if (j < n) k[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+          act_all(a.act, v[0]);
         }
-      } else {
-        act_all(a.act, v[0]);
-      }
-      if (a.res) {
-        float r[8];
-        load8(a.res + row * a.ld_res + col, n, a.res_vec != 0, f16, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[0][j] += r[j];
+        for (int j = 0; j < 8; ++j) v[0][j] *= u[j];
+      } else {
+        if (a.keep) {
+          uint32_t w[4];
+          with_act(a.act, [&](auto act) {
+            constexpr int kAct = decltype(act)::value;
+            if (a.relative != 0)
+              act_keep_slopes<kAct, true>(v[0], w);
+            else
+              act_keep_slopes<kAct, false>(v[0], w);
+          });
+          if constexpr (kSigns) put_signs(near, above, w);
+          uint16_t* k = a.keep + row * a.N + col;
+          if (a.N % 8 == 0) {
+            *reinterpret_cast<uint4*>(k) = make_uint4(w[0], w[1], w[2], w[3]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j < n) k[j] = static_cast<uint16_t>(w[j >> 1] >> (16 * (j & 1)));
+          }
+        } else {
+          act_all(a.act, v[0]);
+        }
+        if (a.res) {
+          float r[8];
+          load8(a.res + row * a.ld_res + col, n, a.res_vec != 0, f16, r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) v[0][j] += r[j];
+        }
       }
+      store8(a.y + row * a.ld_y + col, n, a.y_vec != 0, f16, v[0]);
     }
-    store8(a.y + row * a.ld_y + col, n, a.y_vec != 0, f16, v[0]);
+  };
+  if constexpr (!W_MN) {
+    if (a.keep && a.act == kActRelu) {
+      finish(std::true_type());
+      return;
+    }
   }
+  finish(std::false_type());
 }
 
 template <int NT, bool TWO, bool W_MN>
