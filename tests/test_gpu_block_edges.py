@@ -509,3 +509,20 @@ def test_relu_gradients_are_those_of_an_accurate_sum(M, K, N):
     for got, want, u in ((dx, dz @ W.double(), 2.0 ** -11), (dW, dz.t() @ x.double(), 0.0)):
         err = float((got.double() - want).norm() / want.norm())
         assert err <= u + 2.0 ** -23 * (max(M, N) / 16) + (0.1 * 2.0 ** -17) ** 0.5, err
+
+
+# ------------------------------------------------ the autograd functions by themselves
+def test_autograd_functions_take_their_arguments_without_a_form():
+    """`keep` is the last argument of both and may be left out."""
+    n = randn(41)
+    x, W, Wu, b, r = (t.requires_grad_() for t in (n(9, 64), n(16, 64), n(16, 64), n(16), n(9, 16)))
+    dy = n(9, 16)
+    F.FusedLinearFunction.apply(x, W, b, r, "silu").backward(dy)
+    F.GatedLinearFunction.apply(x, W, Wu, "silu").backward(dy)
+    short = [t.grad for t in (x, W, Wu, b, r)]
+    for t in (x, W, Wu, b, r):
+        t.grad = None
+    F.FusedLinearFunction.apply(x, W, b, r, "silu", "fixed").backward(dy)
+    F.GatedLinearFunction.apply(x, W, Wu, "silu", "relative").backward(dy)
+    for t, g in zip((x, W, Wu, b, r), short):
+        assert torch.equal(t.grad, g)
