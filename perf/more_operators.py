@@ -145,8 +145,8 @@ def _own_norm(s, c):
     rstd = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
     y, h = F.flce_rms_norm_forward(x, w, r, eps=EPS, dropout=c["p"], seed=s["seed"], rstd=rstd)
     dx, dr, dw = F.flce_rms_norm_backward(s["dy"], h, w, rstd, s["dh"], dropout=c["p"], seed=s["seed"],
-                                          dW_dtype=x.dtype)
-    return y, h, dx, dr if r is not None else None, dw
+                                          dW_dtype=x.dtype, needs=(True, r is not None, True))
+    return y, h, dx, dr, dw
 
 
 def _own_norm8(s, c):
