@@ -509,6 +509,112 @@ flce_status_t flce_clip_grads(int64_t count, const void* const* ptrs, void* cons
                               float eps, float* norm, void* workspace, size_t workspace_bytes,
                               void* stream);
 
+/*
+ * Operators between a block, the loss head and a served token: the root-mean-square norm
+ * of the residual stream, dropout on the branch that joins it, and sampling from the
+ * head's logits. The conventions at the top of this file hold. Operands are bf16, fp16 or
+ * fp32 (flce_dtype_t); row pitches (ld_*) are in elements, 0 meaning dense rows; sizes,
+ * pitches and alignments are free, and rows that all start on 16-byte boundaries with a
+ * multiple of 8 columns are read 16 bytes at a time. The pages have no counterpart.
+ *
+ * Dropout D(x): an element is dropped (0, whatever it held) where its 16 random bits are
+ * below t = floor(65536 p + 1/2), else scaled by 65536 / (65536 - t). The bits of (row, column)
+ * are the half-word (column mod 8), lowest first, of Philox4x32-10 with the counter
+ * (column / 8, row, offset low, offset high) and the key (seed low, seed high): the mask
+ * depends on nothing else, is stored nowhere, and is the same in every call. `seed`, where
+ * a call takes one, is a device int64 that is read when the kernel runs, instead of the
+ * parameters' (for captured graphs); NULL: the parameters'.
+ */
+typedef enum {
+  FLCE_SCALES_NONE = 0,  /* y in the operands' type */
+  FLCE_SCALES_ROW = 1,   /* y in e4m3, a scale for each row */
+  FLCE_SCALES_BLOCK = 2  /* y in e4m3, a scale for each 128 columns of a row */
+} flce_scales_t;
+
+#define FLCE_RMS_NORM_MAX_H 32768
+
+/* h = r + D(x), y = weight h rstd, rstd = 1 / sqrt(mean(h^2) + eps). */
+typedef struct {
+  int64_t M;             /* rows; 0 is a valid no-op */
+  int64_t H;             /* columns, 1 .. FLCE_RMS_NORM_MAX_H */
+  int64_t ld_x, ld_res, ld_h, ld_y; /* pitches of x, of the residual (backward: of dh), of h, of y (backward: of dy) */
+  int64_t seed, offset;  /* of the dropout */
+  double dropout;        /* p in [0, 1]; 0: none */
+  float eps;             /* >= 0 */
+  int32_t dtype;         /* flce_dtype_t of x and y, dy and dx */
+  int32_t stream_dtype;  /* of the residual and h, dh and dresidual: dtype or FLCE_DTYPE_FP32 */
+  int32_t weight_dtype;  /* dtype or FLCE_DTYPE_FP32 */
+  int32_t scales;        /* flce_scales_t (forward) */
+  int32_t dW_fp32;       /* backward: 1 = dW in fp32, 0 = in dtype */
+} flce_rms_norm_params_t;
+
+/* Forward. weight: [H], or NULL for ones. residual: [M, H], or NULL for zeros. h: [M, H] receives
+ * the sum (rounded; the norm is of the unrounded one), or NULL. rstd: [M], what the backward
+ * needs beside h, or NULL. With scales, y is e4m3 (448 the largest) and scales [M] or [M, ceil(H / 128)]
+ * receives largest |y| / 448, which y8 times gives y (a scale below 2^-126 is 0, and so
+ * are its values); NULL otherwise. y may be x's own buffer, and h the residual's, with the
+ * same pitch. Squares are summed in fp32: beyond its range (|h| above 1.8e19) rstd is 0. */
+flce_status_t flce_rms_norm_forward(const flce_rms_norm_params_t* p, const void* x, const void* weight,
+                                    const void* residual, const int64_t* seed, void* y, void* h,
+                                    float* rstd, float* scales, void* stream);
+
+/* Backward from h as the forward left it (x itself without a residual and dropout, its pitch
+ * ld_h): with xhat = h rstd and g = dy weight,
+ *   dresidual = dh + rstd (g - xhat mean(g xhat)),  dx = D(dresidual),  dW = sum over rows of dy xhat.
+ * dh: the gradient that reaches h along the stream, or NULL for zeros. dx, dresidual: [M, H] dense;
+ * dW: [H]. Each may be NULL: not computed. Without dropout and with one type dx and
+ * dresidual are equal and may be one buffer. dW's shares are added in a fixed order. Only dW needs the
+ * workspace; with M == 0 it is zeroed. */
+size_t flce_rms_norm_workspace_size(const flce_rms_norm_params_t* p);
+flce_status_t flce_rms_norm_backward(const flce_rms_norm_params_t* p, const void* dy, const void* h,
+                                     const void* weight, const float* rstd, const void* dh,
+                                     const int64_t* seed, void* dx, void* dresidual, void* dW,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* y = residual + D(x) over [M, H]; the gradient of x is the same call on dy. */
+typedef struct {
+  int64_t M, H;                /* rows, columns; 0 is a valid no-op */
+  int64_t ld_x, ld_res, ld_y;
+  int64_t seed, offset;
+  double dropout;              /* p in [0, 1] */
+  int32_t dtype;               /* flce_dtype_t of x */
+  int32_t out_dtype;           /* of y and the residual: dtype, or one of the two is FLCE_DTYPE_FP32 */
+} flce_dropout_params_t;
+
+/* residual: [M, H], or NULL for zeros. y may be the buffer of x (of the same type) or of the
+ * residual, with the same pitch. */
+flce_status_t flce_dropout(const flce_dropout_params_t* p, const void* x, const void* residual,
+                           const int64_t* seed, void* y, void* stream);
+
+/* One token for each row z of logits, from one random number u in [0, 1) for each row.
+ * With w_i = exp((z_i - max z) / temperature) and the order by falling z, equal ones by index:
+ *   top_k   the first k elements (0, or V and more: all)
+ *   top_p   of those, the ones before which less than p of their sum lies (1: all)
+ *   min_p   of those, the ones with w_i >= min_p (0: all)
+ *   token   the lowest index i at which the w of what is left, summed up to and including i,
+ *           exceed u times their sum
+ * The first element of the order is always left. temperature 0 (k = 1, p = 0): that element. A
+ * logit of -infinity is never chosen, one of +infinity leaves the others no weight, a row with
+ * a NaN or without any logit above -infinity gives -1. u below 0 or NaN counts as 0, u of 1
+ * and more as just below it. Weights are whole numbers of 2^-43 (smaller ones are 0): their sums are exact, so
+ * a row's token does not depend on the batch around it. */
+#define FLCE_SAMPLE_MAX_V (1 << 20)
+typedef struct {
+  int64_t B;             /* rows; 0 is a valid no-op */
+  int64_t V;             /* logits of a row, 1 .. FLCE_SAMPLE_MAX_V */
+  int64_t ld;            /* row pitch */
+  int32_t dtype;         /* flce_dtype_t of the logits */
+  int32_t top_k;         /* these four for all rows, */
+  float temperature, top_p, min_p;
+} flce_sample_params_t;
+
+/* temperatures, top_ks, top_ps, min_ps: device arrays [B] with a value for each row, or NULL for the
+ * parameters'. Values in them count as follows: a temperature that is not above 0 as 0, a negative k
+ * as 0, p above 1 as 1, p not above 0 as 0, min_p outside [0, 1] as the nearer end, NaN as 0. */
+flce_status_t flce_sample(const flce_sample_params_t* p, const void* logits, const float* u,
+                          const float* temperatures, const int32_t* top_ks, const float* top_ps,
+                          const float* min_ps, int64_t* tokens, void* stream);
+
 /* Failure-detection self-test: launches one kernel that waits, through the
  * same bounded mbarrier wait the GEMM pipelines use, on a barrier nothing
  * arrives on. After limit_cycles (1 .. 2^32 SM clock cycles) the wait gives

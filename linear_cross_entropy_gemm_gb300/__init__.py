@@ -31,7 +31,10 @@ __all__ = [
     "ACTIVATIONS", "flce_linear_forward", "flce_linear_backward", "flce_gated_forward",
     "flce_gated_backward", "flce_grad_norm", "flce_clip_grads", "clip_grad_norm_",
     "FusedLinearFunction", "GatedLinearFunction", "fused_linear", "gated_linear",
-    "GatedFeedForward",
+    "GatedFeedForward", "flce_rms_norm_forward", "flce_rms_norm_quantized",
+    "flce_rms_norm_backward", "flce_dropout", "flce_sample", "FusedRMSNormFunction",
+    "FusedDropoutFunction", "FusedRMSNorm", "fused_rms_norm", "fused_dropout",
+    "fused_linear_sample",
 ]
 
 _err_words = {}
@@ -446,3 +449,7 @@ from .block import (ACTIVATIONS, FusedLinearFunction, GatedFeedForward,  # noqa:
                     GatedLinearFunction, clip_grad_norm_, flce_clip_grads, flce_gated_backward,
                     flce_gated_forward, flce_grad_norm, flce_linear_backward, flce_linear_forward,
                     fused_linear, gated_linear)
+from .residual import (FusedDropoutFunction, FusedRMSNorm, FusedRMSNormFunction,  # noqa: E402
+                       flce_dropout, flce_rms_norm_backward, flce_rms_norm_forward,
+                       flce_rms_norm_quantized, fused_dropout, fused_rms_norm)
+from .sampling import flce_sample, fused_linear_sample  # noqa: E402

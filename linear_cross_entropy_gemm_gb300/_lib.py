@@ -72,6 +72,31 @@ class FlcePlan(ctypes.Structure):
     _fields_ = [(f, ctypes.c_int32) for f in ("few_tokens", "halves", "columns", "slices")]
 
 
+# flce_scales_t.
+SCALES = {"none": 0, "row": 1, "block": 2}
+
+
+class FlceRmsNormParams(ctypes.Structure):
+    """Mirror of flce_rms_norm_params_t."""
+    _fields_ = [(f, ctypes.c_int64) for f in ("M", "H", "ld_x", "ld_res", "ld_h", "ld_y", "seed",
+                                              "offset")] + \
+        [("dropout", ctypes.c_double), ("eps", ctypes.c_float)] + \
+        [(f, ctypes.c_int32) for f in ("dtype", "stream_dtype", "weight_dtype", "scales", "dW_fp32")]
+
+
+class FlceDropoutParams(ctypes.Structure):
+    """Mirror of flce_dropout_params_t."""
+    _fields_ = [(f, ctypes.c_int64) for f in ("M", "H", "ld_x", "ld_res", "ld_y", "seed", "offset")] + \
+        [("dropout", ctypes.c_double), ("dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class FlceSampleParams(ctypes.Structure):
+    """Mirror of flce_sample_params_t."""
+    _fields_ = [(f, ctypes.c_int64) for f in ("B", "V", "ld")] + \
+        [("dtype", ctypes.c_int32), ("top_k", ctypes.c_int32)] + \
+        [(f, ctypes.c_float) for f in ("temperature", "top_p", "min_p")]
+
+
 class FlceTrace(ctypes.Structure):
     """Mirror of flce_trace_t."""
     _fields_ = [
@@ -180,6 +205,16 @@ def load() -> ctypes.CDLL:
     lib.flce_clip_grads.argtypes = [i64, vp, vp, vp, vp, ctypes.c_float, ctypes.c_float, vp, vp,
                                     sz, vp]
     lib.flce_clip_grads.restype = ctypes.c_int
+    lib.flce_rms_norm_workspace_size.argtypes = [vp]
+    lib.flce_rms_norm_workspace_size.restype = sz
+    lib.flce_rms_norm_forward.argtypes = [vp] * 10
+    lib.flce_rms_norm_forward.restype = ctypes.c_int
+    lib.flce_rms_norm_backward.argtypes = [vp] * 11 + [sz, vp]
+    lib.flce_rms_norm_backward.restype = ctypes.c_int
+    lib.flce_dropout.argtypes = [vp] * 6
+    lib.flce_dropout.restype = ctypes.c_int
+    lib.flce_sample.argtypes = [vp] * 9
+    lib.flce_sample.restype = ctypes.c_int
     lib.flce_status_string.argtypes = [ctypes.c_int]
     lib.flce_status_string.restype = ctypes.c_char_p
     lib.flce_version.argtypes = []

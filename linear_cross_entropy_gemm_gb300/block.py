@@ -51,7 +51,8 @@ class _Late:
     def __getattr__(self, name):
         calls = _lib.calls(_error_word)
         for n in ("linear_forward", "linear_backward", "gated_forward", "gated_backward",
-                  "clip_grads"):
+                  "clip_grads", "rms_norm_forward", "rms_norm_quantized", "rms_norm_backward",
+                  "dropout", "sample"):
             setattr(self, n, getattr(calls, n))
         return getattr(calls, name)
 
@@ -298,17 +299,21 @@ def gated_linear(x, gate_weight, up_weight, activation="silu", keep="relative"):
 
 
 class GatedFeedForward(torch.nn.Module):
-    """x + W_down (a(W_gate x) * (W_up x)): the gated projection and the down
-    projection that adds the residual stream, two kernels forward. ``inputs``
-    (by default x) is what the block reads, such as the normed residual stream."""
+    """x + D(W_down (a(W_gate n) * (W_up n))): the gated projection and the down
+    projection that adds the residual stream, two kernels forward. n is ``inputs``,
+    by default x or, with ``norm_eps``, x's root-mean-square norm (``norm``, a
+    FusedRMSNorm). D: dropout with probability ``dropout`` in training, which adds the
+    stream in a kernel of its own."""
 
     def __init__(self, hidden: int, features: int, activation: str = "silu",
-                 dtype=torch.bfloat16, device=None):
+                 dtype=torch.bfloat16, device=None, *, norm_eps: Optional[float] = None,
+                 dropout: float = 0.0):
         super().__init__()
         if activation not in ACTIVATIONS:
             raise ValueError(f"flce: activation must be one of {sorted(ACTIVATIONS)}, "
                              f"got {activation!r}")
         self.activation = activation
+        self.dropout = _probability(dropout)
 
         def weight(rows, cols):
             w = torch.empty(rows, cols, dtype=dtype, device=device)
@@ -316,7 +321,17 @@ class GatedFeedForward(torch.nn.Module):
 
         self.gate, self.up = weight(features, hidden), weight(features, hidden)
         self.down = weight(hidden, features)
+        self.norm = None
+        if norm_eps is not None:
+            self.norm = FusedRMSNorm(hidden, norm_eps, dtype=dtype, device=device)
 
     def forward(self, x, inputs=None):
-        h = gated_linear(x if inputs is None else inputs, self.gate, self.up, self.activation)
+        if inputs is None:
+            inputs = x if self.norm is None else self.norm(x)
+        h = gated_linear(inputs, self.gate, self.up, self.activation)
+        if self.training and self.dropout > 0:
+            return fused_dropout(fused_linear(h, self.down), self.dropout, residual=x)
         return fused_linear(h, self.down, residual=x)
+
+
+from .residual import FusedRMSNorm, _probability, fused_dropout  # noqa: E402  (they use this module)

@@ -23,7 +23,7 @@ __device__ __forceinline__ void griddep_launch() {
 }
 
 template <class... P, class... A>
-static cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
+static cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem,
                                     int cluster, cudaStream_t st, const A&... args) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[2];
@@ -34,7 +34,7 @@ static cudaError_t launch_dependent(void (*kernel)(P...), dim3 grid, int threads
   attr[1].val.clusterDim.y = 1;
   attr[1].val.clusterDim.z = 1;
   cfg.gridDim = grid;
-  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.blockDim = block;
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cfg.attrs = attr;
