@@ -27,14 +27,24 @@ namespace cg = cooperative_groups;
 namespace flce {
 namespace {
 
-constexpr int kThreadsS = 512, kWarpsS = kThreadsS / 32;
+constexpr int kThreadsS = 256, kWarpsS = kThreadsS / 32;
+constexpr int kPerSm = 4;                  // blocks of an SM
 constexpr int kMaxCluster = 8;
 constexpr int kFrac = 43;                  // fraction bits of a weight
 constexpr uint64_t kOne = 1ull << kFrac;
 constexpr int kTable = 1024;               // 2^(i / kTable)
-constexpr int kPerOctave = 64;             // histogram bins to a factor of 2
-constexpr int kBins = 46 * kPerOctave;     // weights below 2^-44 are 0
-constexpr int kList = 2048;                // elements that are sorted
+constexpr int kTableFrac = 55;
+constexpr int kAhead = 4;                  // loads of a thread in flight,
+constexpr int kStep = kAhead * 256;        //   elements of a warp's
+constexpr int kParts = 32;                 // sums of a warp's stretch, at most
+constexpr int kList = 1536;                // elements that are listed,
+constexpr int kSort = 1024;                //   or sorted
+constexpr int kMostK = 1000;               // top-k up to this goes by the list
+constexpr int kWanted = 512;               // the list's least length where only p says how much is needed
+constexpr int kNear = 8, kNearBins = 512;  // bins to a factor of 2 and bins: of the loads' largest,
+constexpr int kFew = 16, kFewBins = 46 * kFew;       //   of the list,
+constexpr int kPerOctave = 64, kBins = 46 * kPerOctave;  // of all elements; weights below 2^-44 are 0
+constexpr int kPairs = kThreadsS / 2;      // lists up to this length are compared in pairs
 constexpr uint64_t kAll = ~0ull;
 
 struct Table {
@@ -49,7 +59,7 @@ constexpr Table make_table() {
       term *= x / k;
       sum += term;
     }
-    t.v[i] = static_cast<uint64_t>(sum * static_cast<double>(kOne) + 0.5);
+    t.v[i] = static_cast<uint64_t>(sum * static_cast<double>(1ull << kTableFrac) + 0.5);
   }
   return t;
 }
@@ -61,31 +71,49 @@ struct SampleArgs {
   const int32_t* top_ks;
   int64_t* tokens;
   int64_t ld;
-  int B, V, cluster, stretch;  // stretch: elements of a warp, a multiple of 8
+  int B, V, cluster, stretch, part;  // elements of a warp, a multiple of 8; of a part of them, of kStep
   float temperature, top_p, min_p;
   int top_k;
 };
 
+// Two arrays of a block share memory where one of them is done with when the other is made.
 struct Shared {
-  uint64_t table[kTable];
-  uint32_t hist[kBins];
-  uint64_t list[kList];
+  union {
+    uint32_t hist[kBins];
+    struct {
+      uint64_t few_mass[kFewBins];
+      uint32_t few_hist[kFewBins];
+    };
+    uint64_t bucket[kThreadsS];
+    uint32_t near_hist[kNearBins];
+  };
+  uint64_t list[kList];      // places; in the first block those of all blocks, kList / cluster for each
+  union {
+    uint64_t table[kTable];  // without a list
+    uint64_t item[kList];    // the list, one after another,
+  };
+  uint64_t heft[kList];      //   and its weights
+  uint16_t few[kList];       // items of one bin or bucket
   uint64_t red[kWarpsS][2];
   uint64_t peers[2][kMaxCluster][2];
-  uint64_t warp_sum[kWarpsS];
+  uint64_t warp_sum[kWarpsS], warp_kept[kWarpsS];
+  uint64_t kept[kWarpsS][kParts];  // weights that are kept, by parts of the warps' stretches
+  uint64_t cut, cut_mass;    // the last place that is kept, the weight up to and including it
+  uint64_t x_before, list_mass;
+  uint64_t rests[kMaxCluster];
+  uint32_t owns[kMaxCluster];
+  float thresholds[kMaxCluster][2];
   uint32_t scan[kWarpsS];
-  float scan_mass[kWarpsS], within[2];
-  uint32_t listed;
-  uint64_t cut;
+  float scan_mass[kWarpsS], within[2], mine[2];
+  uint32_t owned, few_n, x_count, above;
+  int x_bin, verdict;
   int bins[2];
   float c_hi, c_lo;
-  double p;
 };
+enum Verdict { kDone = 0, kInexact = 1, kTooShort = 2 };
 
 // A row's order as a number: larger for larger z, and for the lower index among equals.
-// A NaN is above everything.
 __device__ __forceinline__ uint32_t order_of(float z) {
-  if (z != z) return 0xFFFFFFFFu;
   const uint32_t b = __float_as_uint(z + 0.f);  // -0 and 0 are equal
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
@@ -95,9 +123,97 @@ __device__ __forceinline__ float value_of(uint32_t order) {
 __device__ __forceinline__ uint64_t place_of(float z, int index) {
   return static_cast<uint64_t>(order_of(z)) << 32 | (0xFFFFFFFFu - static_cast<uint32_t>(index));
 }
+__device__ __forceinline__ float place_value(uint64_t place) {
+  return value_of(static_cast<uint32_t>(place >> 32));
+}
+__device__ __forceinline__ int place_index(uint64_t place) {
+  return static_cast<int>(0xFFFFFFFFu - static_cast<uint32_t>(place));
+}
+
+// The last index that is at or above a place, among those of its logit.
+__device__ __forceinline__ uint32_t place_last(uint64_t place) {
+  return 0xFFFFFFFFu - static_cast<uint32_t>(place);
+}
 
 __device__ __forceinline__ uint64_t shfl64(uint64_t v, int mask) {
   return __shfl_xor_sync(0xffffffffu, v, mask);
+}
+
+// x f, rounded down or up to a whole number, exactly: f in [0, 1).
+template <bool UP>
+__device__ __forceinline__ uint64_t times(uint64_t x, float f) {
+  const uint32_t b = __float_as_uint(f);
+  const int e = static_cast<int>(b >> 23);
+  const uint64_t m = (b & 0x7FFFFFu) | (e > 0 ? 0x800000u : 0u);
+  const int down = 150 - (e > 0 ? e : 1);  // f = m 2^-down, at least 24
+  const uint64_t lo = x * m, hi = __umul64hi(x, m);
+  uint64_t whole, rest;
+  if (down < 64) {
+    whole = hi << (64 - down) | lo >> down;
+    rest = lo << (64 - down);
+  } else if (down < 128) {
+    whole = down == 64 ? hi : hi >> (down - 64);
+    rest = lo | (down == 64 ? 0 : hi << (128 - down));
+  } else {
+    whole = 0;
+    rest = lo | hi;
+  }
+  return whole + (UP && rest != 0 ? 1 : 0);
+}
+
+// The weight before which elements are kept: p `of`, and the first one always.
+__device__ __forceinline__ uint64_t share_of(uint64_t of, float p) {
+  const uint64_t m = times<true>(of, p);
+  return m > 0 ? m : 1;
+}
+
+// The largest of eight; a NaN if there is one.
+template <int TYPE>
+__device__ __forceinline__ float largest(const Raw8<TYPE>& r) {
+  if constexpr (TYPE == kFp32) {
+    float v[8];
+    unpack8<TYPE>(r, v);
+    return max_nan(max_nan(max_nan(v[0], v[1]), max_nan(v[2], v[3])),
+                   max_nan(max_nan(v[4], v[5]), max_nan(v[6], v[7])));
+  } else {
+    const uint4& w = r.w[0];
+    uint32_t m;
+    if constexpr (TYPE == kBf16)
+      asm("{.reg .b32 a, b;\n max.NaN.bf16x2 a, %1, %2;\n max.NaN.bf16x2 b, %3, %4;\n"
+          " max.NaN.bf16x2 %0, a, b;}" : "=r"(m) : "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w));
+    else
+      asm("{.reg .b32 a, b;\n max.NaN.f16x2 a, %1, %2;\n max.NaN.f16x2 b, %3, %4;\n"
+          " max.NaN.f16x2 %0, a, b;}" : "=r"(m) : "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w));
+    return max_nan(unpack_16(m & 0xFFFFu, TYPE == kFp16), unpack_16(m >> 16, TYPE == kFp16));
+  }
+}
+template <int TYPE>
+__device__ __forceinline__ Raw8<TYPE> nothing() {
+  const uint32_t w = TYPE == kFp32 ? 0xFF800000u : TYPE == kBf16 ? 0xFF80FF80u : 0xFC00FC00u;
+  Raw8<TYPE> r;
+  for (auto& x : r.w) x = make_uint4(w, w, w, w);
+  return r;
+}
+
+// exp((z - top) / T) in units of 2^-43, for z / T of any size: (z - top) log2(e) / T as a pair of
+// floats is right to 2^-42, and then as in Row::weight_near.
+__device__ __noinline__ uint64_t weight_far(float v, float top, float c_hi, float c_lo, const uint64_t* table) {
+  if (v == top) return kOne;
+  const float d = v - top;
+  const float hi = __fmul_rn(d, c_hi);
+  if (!(hi > -45.f)) return 0;
+  const float back = d - v;
+  const float err = (v - (d - back)) + (-top - back);
+  const float lo = __fmaf_rn(d, c_hi, -hi) + __fmaf_rn(d, c_lo, __fmul_rn(err, c_hi));
+  const float near = hi + 12288.f;
+  const int k = __float_as_int(near) - 0x46400000;
+  const float r = (hi - (near - 12288.f)) + lo;
+  const uint64_t t = table[k & (kTable - 1)];
+  const float part = __int_as_float(static_cast<int>(t >> 32) + 0x3F000000) *
+                     (r * __fmaf_rn(r, 0.24022651f * 0x1p40f, 0.69314718f * 0x1p40f));
+  const uint64_t w = t + static_cast<int64_t>(__float2int_rn(part)) * 32768;
+  const int down = (kTableFrac - kFrac) - (k >> 10);
+  return (w + (1ull << (down - 1))) >> down;
 }
 
 template <int TYPE>
@@ -108,7 +224,9 @@ struct Row {
   int shift;          // its first element's distance from a 16-byte boundary, in elements
   int rank, first, last;  // this warp's positions, index + shift
   int lane, warp, turn;
-  float top, c_hi, c_lo, bin_scale;
+  float top, c_hi, c_lo, lowest;
+  int octave;         // weights are 2^(z log2(e) / T - octave)
+  bool far;           // z log2(e) / T is too large for weight_near
 
   __device__ void sync() const {
     if (a.cluster == 1)
@@ -116,22 +234,74 @@ struct Row {
     else
       cg::this_cluster().sync();
   }
+  template <class T>
+  __device__ T* of_block(T* p, int r) const {
+    return a.cluster == 1 ? p : cg::this_cluster().map_shared_rank(p, r);
+  }
 
-  // f(index of the first, 8 values) over this warp's stretch; -inf where there is no element.
-  template <class F>
-  __device__ __forceinline__ void each(F f) const {
-    for (int at = first + lane * 8; at < last; at += 256) {
-      const int i = at - shift;
-      float v[8];
-      if (i >= 0 && i + 8 <= a.V) {
-        unpack8<TYPE>(load8<TYPE, true>(z, i, a.V), v);
-      } else {
+  __device__ __forceinline__ Raw8<TYPE> group(int at) const {
+    const int i = at - shift;
+    if (at >= last) return nothing<TYPE>();
+    if (i >= 0 && i + 8 <= a.V) return load8<TYPE, true>(z, i, a.V);
+    float v[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          v[e] = i + e >= 0 && i + e < a.V ? load_value<TYPE>(z, i + e) : -INFINITY;
+    for (int e = 0; e < 8; ++e)
+      v[e] = i + e >= 0 && i + e < a.V ? load_value<TYPE>(z, i + e) : -INFINITY;
+    return pack8<TYPE>(v);
+  }
+  // f(which of the loads, index of the first, 8 values as they are) over this warp's stretch;
+  // -inf where there is no element.
+  template <class F>
+  __device__ __forceinline__ void each_raw(F f) const {
+    each_step([&](int base) {
+      const int at = base + lane * 8;
+      Raw8<TYPE> r[kAhead];
+#pragma unroll
+      for (int g = 0; g < kAhead; ++g) r[g] = group(at + g * 256);
+#pragma unroll
+      for (int g = 0; g < kAhead; ++g) f(g, at + g * 256 - shift, r[g]);
+    });
+  }
+  template <class F>
+  __device__ __forceinline__ void each_step(F f) const {
+    for (int base = first; base < last; base += kStep) f(base);
+  }
+  // f(index, value) for the groups of 8 that hold one of at least `least`.
+  template <class F>
+  __device__ __forceinline__ void each(float least, F f) const {
+    each_raw([&](int, int i, const Raw8<TYPE>& raw) {
+      if (!(largest<TYPE>(raw) >= least)) return;
+      float v[8];
+      unpack8<TYPE>(raw, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f(i + e, v[e]);
+    });
+  }
+  // each, f returning a weight: they are added to s.kept, by parts of this warp's stretch.
+  template <class F>
+  __device__ __forceinline__ void each_kept(float least, F f) const {
+    uint64_t sum = 0;
+    each_step([&](int base) {
+      const int at = base + lane * 8;
+      Raw8<TYPE> r[kAhead];
+#pragma unroll
+      for (int g = 0; g < kAhead; ++g) r[g] = group(at + g * 256);
+#pragma unroll
+      for (int g = 0; g < kAhead; ++g) {
+        if (!(largest<TYPE>(r[g]) >= least)) continue;
+        float v[8];
+        unpack8<TYPE>(r[g], v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += f(at + g * 256 - shift + e, v[e]);
       }
-      f(i, v);
-    }
+      const int part = (base - first) / a.part;
+      if (base + kStep >= last || (base + kStep - first) / a.part != part) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) sum += shfl64(sum, o);
+        if (lane == 0) s.kept[warp][part] += sum;
+        sum = 0;
+      }
+    });
   }
 
   // The sums (or the largest) of two numbers over the cluster, in every thread.
@@ -158,8 +328,7 @@ struct Row {
         y = MAX ? max(y, q) : y + q;
       }
       if (lane < a.cluster) {
-        uint64_t* to = a.cluster == 1 ? s.peers[turn][0]
-                                      : cg::this_cluster().map_shared_rank(s.peers[turn][rank], lane);
+        uint64_t* to = of_block(s.peers[turn][rank], lane);
         to[0] = x;
         to[1] = y;
       }
@@ -173,51 +342,66 @@ struct Row {
     turn ^= 1;
   }
 
-  // exp((z - top) / T) in units of 2^-43. (z - top) log2(e) / T as a pair of floats is right
-  // to 2^-42; the table takes its first 10 fraction bits, a polynomial the rest.
-  __device__ __forceinline__ uint64_t weight(float v) const {
-    if (v == top) return kOne;
-    const float d = v - top;
-    const float hi = __fmul_rn(d, c_hi);
-    if (!(hi > -45.f)) return 0;
-    const float back = d - v;
-    const float err = (v - (d - back)) + (-top - back);
-    const float lo = __fmaf_rn(d, c_hi, -hi) + __fmaf_rn(d, c_lo, __fmul_rn(err, c_hi));
-    const float magic = 12288.f;  // its last bit is 2^-10
-    const float near = hi + magic;
-    const int k = __float_as_int(near) - __float_as_int(magic);
-    const float r = (hi - (near - magic)) + lo;
-    const float q = r * fmaf(r, fmaf(r, 0.05550411f, 0.24022651f), 0.69314718f);
-    const uint64_t base = s.table[k & (kTable - 1)];
-    const float part = static_cast<float>(static_cast<uint32_t>(base >> 20)) * q * 131072.f;
-    const int64_t w = static_cast<int64_t>(base) + (static_cast<int64_t>(__float2int_rn(part)) << 3);
-    const int down = -(k >> 10);
-    return (static_cast<uint64_t>(w) + ((1ull << down) >> 1)) >> down;
+  // 2^(z log2(e) / T - octave) in units of 2^-43, octave being the largest's. Adding 12288 rounds
+  // z log2(e) / T to 10 fraction bits, for which there is the table; what is left, at most
+  // 2^-11, is exact to 2^-35, and a polynomial of two terms gives the rest to 2^-37.
+  __device__ __forceinline__ uint64_t weight_near(float v, const uint64_t* table) const {
+    const float x = fmaxf(v, lowest);
+    const float near = __fmaf_rn(x, c_hi, 12288.f);
+    const float r = __fmaf_rn(x, c_lo, __fmaf_rn(x, c_hi, 12288.f - near));
+    const int k = __float_as_int(near);
+    const uint64_t t = table[k & (kTable - 1)];
+    const float part = __int_as_float(static_cast<int>(t >> 32) + 0x3F000000) *  // 1 .. 2
+                       (r * __fmaf_rn(r, 0.24022651f * 0x1p40f, 0.69314718f * 0x1p40f));
+    const uint64_t w = t + static_cast<int64_t>(__float2int_rn(part)) * 32768;
+    const int down = (kTableFrac - kFrac) + octave + (0x46400000 >> 10) - (k >> 10);
+    return (w + (1ull << (down - 1))) >> down;
   }
-  // The histogram bin, kBins where the weight is 0: falls with the logit.
-  __device__ __forceinline__ int bin(float v) const {
-    const float d = v == top ? 0.f : (top - v) * bin_scale;
-    return d < static_cast<float>(kBins) ? static_cast<int>(d) : kBins;
+  template <bool FAR>
+  __device__ __forceinline__ uint64_t weight(float v, const uint64_t* table) const {
+    return FAR ? weight_far(v, top, c_hi, c_lo, table) : weight_near(v, table);
+  }
+  __device__ uint64_t any_weight(float v, const uint64_t* table) const {
+    return far ? weight<true>(v, table) : weight<false>(v, table);
   }
 
+  // A bin of `per` to a factor of 2, `bins` where it is beyond the last: falls with the logit.
+  __device__ __forceinline__ int bin(float v, float per, int bins) const {
+    const float d = v == top ? 0.f : (top - v) * (c_hi * per);
+    return d < static_cast<float>(bins) ? static_cast<int>(d) : bins;
+  }
+  __device__ __forceinline__ int bin(float v) const { return bin(v, kPerOctave, kBins); }
+  // The least logit whose bin is below b, to the bit; a NaN, which none reaches, for b = 0.
+  __device__ float above_bin(int b) const {
+    if (b <= 0) return __int_as_float(0x7FC00000);
+    uint32_t lo = order_of(-INFINITY), hi = order_of(top);
+    while (lo < hi) {
+      const uint32_t mid = lo + (hi - lo) / 2;
+      if (bin(value_of(mid)) < b)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    return value_of(hi);
+  }
+
+  // ---- the whole row: a histogram of all elements, merged in the first block
+
   __device__ void histogram() {
+    __syncthreads();
     for (int i = threadIdx.x; i < kBins; i += kThreadsS) s.hist[i] = 0;
     __syncthreads();
-    each([&](int, const float* v) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int b = bin(v[e]);
-        if (b < kBins) atomicAdd(&s.hist[b], 1u);
-      }
+    each(-INFINITY, [&](int, float v) {
+      const int b = bin(v);
+      if (b < kBins) atomicAdd(&s.hist[b], 1u);
     });
     sync();
     if (a.cluster > 1) {
       // Block r adds its share of the bins over all blocks, into the first block's copy.
-      auto cl = cg::this_cluster();
       for (int i = rank * kThreadsS + threadIdx.x; i < kBins; i += a.cluster * kThreadsS) {
         uint32_t n = 0;
-        for (int r = 0; r < a.cluster; ++r) n += cl.map_shared_rank(s.hist, r)[i];
-        cl.map_shared_rank(s.hist, 0)[i] = n;
+        for (int r = 0; r < a.cluster; ++r) n += of_block(s.hist, r)[i];
+        of_block(s.hist, 0)[i] = n;
       }
       sync();
     }
@@ -257,7 +441,10 @@ struct Row {
         s.scan[warp] = n_scan;
         s.scan_mass[warp] = m_scan;
       }
-      if (threadIdx.x == 0) s.bins[0] = s.bins[1] = kBins - 1;
+      if (threadIdx.x == 0) {
+        s.bins[0] = s.bins[1] = kBins - 1;
+        s.above = 0;
+      }
       __syncthreads();
       uint32_t n_before = n_scan - n;
       float m_before = m_scan - m, total = 0.f;
@@ -280,6 +467,7 @@ struct Row {
           c += s.hist[i++];
         }
         if (p >= 1.f) s.bins[0] = s.bins[1] = i;
+        s.above = c;
         s.within[0] = x;
         s.within[1] = x + static_cast<float>(s.hist[i]) * bin_weight(i);
       }
@@ -294,97 +482,183 @@ struct Row {
         }
       }
     }
+    share_bins();
+  }
+
+  // The same once the weight above s.bins[0] is known: `needed` more reaches the cut, in units of
+  // `heaviest`, the largest's weight.
+  __device__ void narrow(uint64_t needed, uint64_t heaviest) {
+    if (rank == 0) {
+      constexpr int kEach = (kBins + kThreadsS - 1) / kThreadsS;
+      const int b0 = s.bins[0], b1 = s.bins[1];
+      const int b = max(static_cast<int>(threadIdx.x) * kEach, b0);
+      const int b_end = min(static_cast<int>(threadIdx.x + 1) * kEach, b1 + 1);
+      float m = 0.f;
+      for (int i = b; i < b_end; ++i) m += static_cast<float>(s.hist[i]) * bin_weight(i);
+      float m_scan = m;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float y = __shfl_up_sync(0xffffffffu, m_scan, o);
+        if (lane >= o) m_scan += y;
+      }
+      if (lane == 31) s.scan_mass[warp] = m_scan;
+      __syncthreads();  // the bins have been read
+      if (threadIdx.x == 0) s.bins[0] = s.bins[1] = b1;
+      float x = m_scan - m;
+      for (int w = 0; w < warp; ++w) x += s.scan_mass[w];
+      __syncthreads();
+      const float to = static_cast<float>(needed) / static_cast<float>(heaviest);
+      for (int i = b; i < b_end; ++i) {
+        x += static_cast<float>(s.hist[i]) * bin_weight(i);
+        if (x >= to * 0.993f) atomicMin(&s.bins[0], i);
+        if (x >= to * 1.007f) atomicMin(&s.bins[1], i);
+      }
+    }
+    share_bins();
+  }
+
+  // s.bins and s.above of the first block to all.
+  __device__ void share_bins() {
     if (a.cluster > 1 && rank == 0) {
       __syncthreads();
       if (threadIdx.x > 0 && threadIdx.x < a.cluster) {
-        int* to = cg::this_cluster().map_shared_rank(s.bins, threadIdx.x);
+        int* to = of_block(s.bins, threadIdx.x);
         to[0] = s.bins[0];
         to[1] = s.bins[1];
+        *of_block(&s.above, threadIdx.x) = s.above;
       }
     }
     sync();
   }
 
-  // The cut: the lowest place that is kept, where at most k elements and those before which
-  // less than `mass` lies are. Elements below `floor` do not count. k, mass: kAll for none.
-  __device__ uint64_t find_cut(uint64_t k, uint64_t mass, uint64_t floor, int b0, int b1) {
-    // What lies above the bracket, and what is in it.
+  // Notes a place, in this block's s.heft.
+  __device__ __forceinline__ void own(uint64_t place) {
+    const uint32_t n = atomicAdd(&s.owned, 1u);
+    if (n < kList) s.heft[n] = place;
+  }
+  // The blocks' places into the first one's list. Their number, the same in every thread; above
+  // kSort nothing is listed. sum: over the cluster.
+  __device__ uint64_t gather(uint64_t& sum) {
+    __syncthreads();
+    const uint32_t mine = s.owned;
+    uint64_t n = threadIdx.x == 0 ? mine : 0;
+    const int at = turn;
+    reduce<false>(sum, n);
+    if (n > kSort) return n;
+    uint32_t before = 0;
+    for (int r = 0; r < rank; ++r) before += static_cast<uint32_t>(s.peers[at][r][1]);
+    uint64_t* list = of_block(s.list, 0);
+    for (uint32_t i = threadIdx.x; i < mine; i += kThreadsS) list[before + i] = s.heft[i];
+    sync();
+    return n;
+  }
+
+  // The cut within places [lo, hi), which hold it: the last place before which less than k and less
+  // than `mass` lie, above_n and above_m of them at or above hi. n: how many there are; listed: whether
+  // they are in the list. moved: whether more elements than those above hi and of the list are kept.
+  template <bool FAR>
+  __device__ uint64_t cut_between(uint64_t lo, uint64_t hi, uint64_t n, bool listed, uint64_t k, uint64_t mass,
+                                  uint64_t above_n, uint64_t above_m, bool& moved) {
     const bool weigh = mass != kAll;
-    uint64_t above_n = 0, above_m = 0, in_lo = kAll, in_hi = 0, in_n = 0, none = 0;
-    each([&](int i, const float* v) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int b = bin(v[e]);
-        if (b > b1) continue;
-        const uint64_t at = place_of(v[e], i + e);
-        if (at < floor) continue;
-        if (b < b0) {
-          above_n += 1;
-          if (weigh) above_m += weight(v[e]);
-        } else {
-          in_n += 1;
-          in_lo = min(in_lo, at);
-          in_hi = max(in_hi, at);
-        }
-      }
-    });
-    reduce<false>(above_n, above_m);
-    reduce<false>(in_n, none);
-    in_lo = ~in_lo;
-    reduce<true>(in_lo, in_hi);
-    in_lo = ~in_lo;
-    if (in_n == 0) return floor;
-    uint64_t lo = in_lo, hi = in_hi + 1;  // the bracket [lo, hi)
-    while (in_n > kList) {
-      const uint64_t mid = lo + (hi - lo) / 2;
-      uint64_t n = 0, m = 0;
-      each([&](int i, const float* v) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint64_t at = place_of(v[e], i + e);
+    uint64_t none = 0;
+    while (!listed) {
+      while (n > kSort) {
+        const uint64_t mid = lo + (hi - lo) / 2;
+        uint64_t c = 0, m = 0;
+        each(place_value(mid), [&](int i, float v) {
+          const uint64_t at = place_of(v, i);
           if (at >= mid && at < hi) {
-            n += 1;
-            if (weigh) m += weight(v[e]);
+            c += 1;
+            if (weigh) m += weight<FAR>(v, s.table);
           }
+        });
+        reduce<false>(c, m);
+        if (above_n + c < k && above_m + m < mass) {
+          above_n += c;
+          above_m += m;
+          moved |= c > 0;
+          hi = mid;
+          n -= c;
+        } else {
+          lo = mid;
+          n = c;
         }
-      });
-      reduce<false>(n, m);
-      if (above_n + n < k && above_m + m < mass) {
-        above_n += n;
-        above_m += m;
-        hi = mid;
-        in_n -= n;
-      } else {
-        lo = mid;
-        in_n = n;
       }
-    }
-    if (rank == 0 && threadIdx.x == 0) s.listed = 0;
-    sync();
-    {
-      uint32_t* listed = a.cluster == 1 ? &s.listed : cg::this_cluster().map_shared_rank(&s.listed, 0);
-      uint64_t* list = a.cluster == 1 ? s.list : cg::this_cluster().map_shared_rank(s.list, 0);
-      each([&](int i, const float* v) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint64_t at = place_of(v[e], i + e);
-          if (at >= lo && at < hi) {
-            const uint32_t n = atomicAdd(listed, 1u);
-            if (n < kList) list[n] = at;
-          }
-        }
+      if (threadIdx.x == 0) s.owned = 0;
+      __syncthreads();
+      each(place_value(lo), [&](int i, float v) {
+        const uint64_t at = place_of(v, i);
+        if (at >= lo && at < hi) own(at);
       });
+      n = gather(none);
+      listed = n <= kSort;
     }
-    sync();
     if (rank == 0) {
-      const int n = min(static_cast<int>(s.listed), kList);
-      sort_list(n);
-      cut_list(n, k, mass, above_n, above_m, hi);
-      if (threadIdx.x < a.cluster && a.cluster > 1)
-        *cg::this_cluster().map_shared_rank(&s.cut, threadIdx.x) = s.cut;
+      sort_list(static_cast<int>(n));
+      cut_list<FAR>(static_cast<int>(n), k, mass, above_n, above_m, hi);
+      if (threadIdx.x < a.cluster && a.cluster > 1) *of_block(&s.cut, threadIdx.x) = s.cut;
     }
     sync();
     return s.cut;
+  }
+
+  // The place of the k-th element, from the histogram.
+  __device__ uint64_t cut_by_count(uint64_t k) {
+    bracket(k, 1.f);
+    const float from = above_bin(s.bins[0] + 1), to = above_bin(s.bins[0]);
+    const uint64_t lo = static_cast<uint64_t>(order_of(from)) << 32;
+    const uint64_t hi = s.bins[0] == 0 ? kAll : static_cast<uint64_t>(order_of(to)) << 32;
+    if (threadIdx.x == 0) s.owned = 0;
+    __syncthreads();
+    each(from, [&](int i, float v) {
+      if (v >= from && !(v >= to)) own(place_of(v, i));
+    });
+    uint64_t none = 0;
+    const uint64_t n = gather(none);
+    bool moved = false;
+    return cut_between<false>(lo, hi, n, n <= kSort, k, kAll, s.above, 0, moved);
+  }
+
+  // The last place of those at or above `floor`, the k-th one's, before which less than p of their
+  // weight lies. s.kept is what is at or above it, unless `moved`.
+  template <bool FAR>
+  __device__ uint64_t cut_by_mass(uint64_t k, float p, uint64_t floor, uint64_t heaviest, bool& moved) {
+    bracket(k, p);
+    const float above = above_bin(s.bins[0]), least = floor > 0 ? place_value(floor) : -INFINITY;
+    const uint32_t least_index = place_last(floor);
+    clear_kept();
+    uint64_t all = 0, sum = 0;
+    each_kept(least, [&](int i, float v) {
+      uint64_t w = weight<FAR>(v, s.table);
+      w = v > least || (v == least && static_cast<uint32_t>(i) <= least_index) ? w : 0;
+      all += w;
+      w = v >= above ? w : 0;
+      sum += w;
+      return w;
+    });
+    reduce<false>(all, sum);
+    const uint64_t mass = share_of(all, p);
+    narrow(mass - sum, heaviest);
+    const float upper = above_bin(s.bins[0]), lower = fmaxf(above_bin(s.bins[1] + 1), least);
+    const uint64_t lo = static_cast<uint64_t>(order_of(lower)) << 32;
+    const uint64_t hi = s.bins[0] == 0 ? kAll : static_cast<uint64_t>(order_of(upper)) << 32;
+    if (threadIdx.x == 0) s.owned = 0;
+    __syncthreads();
+    uint64_t more = 0;
+    each(lower, [&](int i, float v) {
+      if (v < lower || v >= above) return;
+      if (v == least && static_cast<uint32_t>(i) > least_index) return;
+      if (v >= upper) {
+        const uint64_t w = weight<FAR>(v, s.table);
+        more += w;
+        const int part = (i + shift - first) / a.part;
+        atomicAdd(reinterpret_cast<unsigned long long*>(&s.kept[warp][part]), static_cast<unsigned long long>(w));
+      } else {
+        own(place_of(v, i));
+      }
+    });
+    const uint64_t n = gather(more);
+    return cut_between<FAR>(floor > lo ? floor : lo, hi, n, n <= kSort, kAll, mass, 0, sum + more, moved);
   }
 
   // The list by falling place, in this block.
@@ -408,69 +682,132 @@ struct Row {
     }
   }
 
-  // s.cut from the sorted list: the last place that is kept, or `hi` where none is.
-  __device__ void cut_list(int n, uint64_t k, uint64_t mass, uint64_t above_n, uint64_t above_m,
-                           uint64_t hi) {
-    constexpr int kEach = kList / kThreadsS;
+  // s.cut from the sorted list: the last place that is kept, or `hi` where none is. With weights,
+  // the kept ones' go to their parts of s.kept.
+  template <bool FAR>
+  __device__ void cut_list(int n, uint64_t k, uint64_t mass, uint64_t above_n, uint64_t above_m, uint64_t hi) {
+    constexpr int kEach = kSort / kThreadsS;
+    const bool weigh = mass != kAll;
     uint64_t w[kEach], sum = 0;
 #pragma unroll
     for (int e = 0; e < kEach; ++e) {
       const int i = threadIdx.x * kEach + e;
-      w[e] = i < n && mass != kAll ? weight(value_of(static_cast<uint32_t>(s.list[i] >> 32))) : 0;
+      w[e] = i < n && weigh ? weight<FAR>(place_value(s.list[i]), s.table) : 0;
       sum += w[e];
     }
-    uint64_t scan = sum;
+    uint32_t none, none_all;
+    uint64_t before, all;
+    if (threadIdx.x == 0) s.cut = hi;
+    scan(0, sum, none, before, none_all, all);
+    before += above_m;
+    int kept = -1;
+#pragma unroll
+    for (int e = 0; e < kEach; ++e) {
+      const int i = threadIdx.x * kEach + e;
+      if (i < n && above_n + i < k && before < mass) {
+        kept = i;
+        if (weigh) {
+          const int at = place_index(s.list[i]) + shift, w_at = at / a.stretch;
+          uint64_t* to = &s.kept[w_at % kWarpsS][at % a.stretch / a.part];
+          atomicAdd(reinterpret_cast<unsigned long long*>(of_block(to, w_at / kWarpsS)),
+                    static_cast<unsigned long long>(w[e]));
+        }
+      }
+      before += w[e];
+    }
+    // What is kept is a prefix.
+    if (kept >= 0)
+      atomicMin(reinterpret_cast<unsigned long long*>(&s.cut), static_cast<unsigned long long>(s.list[kept]));
+    __syncthreads();
+  }
+
+  // u all, rounded down: the sums are whole, and one is above u all where it is above this.
+  __device__ static uint64_t target_of(uint64_t all, float u) {
+    if (!(u > 0.f)) return 0;
+    return u < 1.f ? times<false>(all, u) : all - 1;
+  }
+
+  // Exclusive sums of (n, m) over the block's threads, and the totals.
+  __device__ void scan(uint32_t n, uint64_t m, uint32_t& n_before, uint64_t& m_before, uint32_t& n_all,
+                       uint64_t& m_all) {
+    uint32_t sn = n;
+    uint64_t sm = m;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, sn, o);
+      const uint64_t y = __shfl_up_sync(0xffffffffu, sm, o);
+      if (lane >= o) {
+        sn += x;
+        sm += y;
+      }
+    }
+    __syncthreads();  // the last scan has been read
+    if (lane == 31) {
+      s.scan[warp] = sn;
+      s.warp_sum[warp] = sm;
+    }
+    __syncthreads();
+    n_before = sn - n;
+    m_before = sm - m;
+    n_all = 0;
+    m_all = 0;
+#pragma unroll
+    for (int w = 0; w < kWarpsS; ++w) {
+      const uint32_t x = s.scan[w];
+      const uint64_t y = s.warp_sum[w];
+      if (w < warp) {
+        n_before += x;
+        m_before += y;
+      }
+      n_all += x;
+      m_all += y;
+    }
+  }
+
+  __device__ void clear_kept() {
+    static_assert(kParts == 32, "one for each lane");
+    s.kept[warp][lane] = 0;
+    __syncwarp();
+  }
+  // The elements at or above `cut` that weigh at least `least` into s.kept; those below `low` are
+  // known to weigh less.
+  template <bool FAR>
+  __device__ void weigh_kept(uint64_t cut, uint64_t least, float low) {
+    const float edge = cut > 0 ? place_value(cut) : -INFINITY;
+    const uint32_t edge_index = place_last(cut);
+    clear_kept();
+    if (cut == 0 && least == 0) {
+      each_kept(-INFINITY, [&](int, float v) { return weight<FAR>(v, s.table); });
+      return;
+    }
+    each_kept(fmaxf(low, edge), [&](int i, float v) {
+      const uint64_t w = weight<FAR>(v, s.table);
+      return (v > edge || (v == edge && static_cast<uint32_t>(i) <= edge_index)) && w >= least ? w : 0;
+    });
+  }
+  // Draws from them.
+  template <bool FAR>
+  __device__ void draw(uint64_t cut, uint64_t least, float low, float u, int64_t* token) {
+    const float edge = cut > 0 ? place_value(cut) : -INFINITY;
+    const uint32_t edge_index = place_last(cut);
+    __syncwarp();
+    const uint64_t part = s.kept[warp][lane];
+    uint64_t scan = part;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const uint64_t x = __shfl_up_sync(0xffffffffu, scan, o);
       if (lane >= o) scan += x;
     }
-    if (lane == 31) s.warp_sum[warp] = scan;
-    if (threadIdx.x == 0) s.cut = hi;
-    __syncthreads();
-    uint64_t before = above_m + scan - sum;
-    for (int i = 0; i < warp; ++i) before += s.warp_sum[i];
-    int kept = -1;
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const int i = threadIdx.x * kEach + e;
-      if (i < n && above_n + i < k && before < mass) kept = i;
-      before += w[e];
-    }
-    // What is kept is a prefix: the last one's thread sees that the next is not.
-    if (kept >= 0) {
-      const uint64_t at = s.list[kept];
-      atomicMin(reinterpret_cast<unsigned long long*>(&s.cut), static_cast<unsigned long long>(at));
-    }
-    __syncthreads();
-  }
-
-  // Draws from the elements at or above `cut` whose weight is at least `least`.
-  __device__ void draw(uint64_t cut, uint64_t least, float u, int64_t* token) {
-    uint64_t sum = 0;
-    each([&](int i, const float* v) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (v[e] == -INFINITY || place_of(v[e], i + e) < cut) continue;
-        const uint64_t w = weight(v[e]);
-        if (w >= least) sum += w;
-      }
-    });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += shfl64(sum, o);
-    if (lane == 0) s.warp_sum[warp] = sum;
+    if (lane == 31) s.warp_kept[warp] = scan;
     __syncthreads();
     uint64_t block = 0, before = 0;
+#pragma unroll
     for (int i = 0; i < kWarpsS; ++i) {
-      if (i < warp) before += s.warp_sum[i];
-      block += s.warp_sum[i];
+      if (i < warp) before += s.warp_kept[i];
+      block += s.warp_kept[i];
     }
-    if (threadIdx.x < a.cluster) {
-      uint64_t* to = a.cluster == 1
-                         ? s.peers[turn][0]
-                         : cg::this_cluster().map_shared_rank(s.peers[turn][rank], threadIdx.x);
-      to[0] = block;
-    }
+    const uint64_t sum = s.warp_kept[warp];
+    if (threadIdx.x < a.cluster) *of_block(s.peers[turn][rank], threadIdx.x) = block;
     sync();
     uint64_t all = 0;
     for (int i = 0; i < a.cluster; ++i) {
@@ -478,30 +815,24 @@ struct Row {
       all += s.peers[turn][i][0];
     }
     turn ^= 1;
-    // The sums are whole: one is above u all where it is above the whole part of that.
-    uint64_t target = 0;
-    if (lane == 0 && u > 0.f) {
-      const double t = static_cast<double>(u) * static_cast<double>(all);
-      target = t < static_cast<double>(all) ? static_cast<uint64_t>(t) : all - 1;
-      if (target >= all) target = all - 1;
-    }
-    target = __shfl_sync(0xffffffffu, target, 0);
+    const uint64_t target = target_of(all, u);
     if (target < before || target >= before + sum) return;
-    // This warp's stretch holds it.
-    for (int at = first; at < last; at += 256) {
+    // This warp's stretch holds it, and this part of it.
+    const uint64_t part_before = before + scan - part;
+    const uint32_t holds = __ballot_sync(0xffffffffu, target >= part_before && target < part_before + part);
+    const int which = __ffs(holds) - 1;
+    before = __shfl_sync(0xffffffffu, part_before, which);
+    const int end = min(first + (which + 1) * a.part, last);
+    for (int at = first + which * a.part; at < end; at += 256) {
       const int i = at + lane * 8 - shift;
+      float v[8];
+      unpack8<TYPE>(group(at + lane * 8), v);
       uint64_t w[8], mine = 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int j = i + e;
-        w[e] = 0;
-        if (j >= 0 && j < a.V && at + lane * 8 < last) {
-          const float v = load_value<TYPE>(z, j);
-          if (v != -INFINITY && place_of(v, j) >= cut) {
-            const uint64_t x = weight(v);
-            if (x >= least) w[e] = x;
-          }
-        }
+        w[e] = weight<FAR>(v[e], s.table);
+        const bool in = v[e] >= low && (v[e] > edge || (v[e] == edge && static_cast<uint32_t>(i + e) <= edge_index)) && w[e] >= least;
+        w[e] = in ? w[e] : 0;
         mine += w[e];
       }
       uint64_t scan = mine;
@@ -527,73 +858,476 @@ struct Row {
     }
   }
 
+  // Everything from passes over the row.
+  template <bool FAR>
+  __device__ void from_row(int64_t top_k, float p, uint64_t heaviest, uint64_t least, float low, float u,
+                           int64_t* token) {
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTable; i += kThreadsS) s.table[i] = kExp2.v[i];
+    __syncthreads();
+    const bool by_k = top_k < a.V, by_p = p < 1.f;
+    uint64_t cut = 0;
+    if (by_k || by_p) histogram();
+    if (by_k) cut = cut_by_count(top_k);
+    bool moved = false;
+    if (by_p) cut = cut_by_mass<FAR>(top_k, p, cut, heaviest, moved);
+    if (!by_p || least > 0 || moved) weigh_kept<FAR>(cut, least, low);
+    draw<FAR>(cut, least, low, u, token);
+  }
+
+  // ---- the list of candidates: all elements that reach a logit
+
+  // This block's largest logit of each thread's loads is m. Finds the row's largest (its order, or
+  // 0xFFFFFFFF for a NaN), and where `wanted` is not 0 a logit that at least so many elements
+  // reach, from the m's: each block offers the one that `wanted` of its own reach, and the one that
+  // its share of them reach. The highest of the former will do, and the lowest of the latter.
+  __device__ uint32_t find_top(const float (&m)[kAhead], uint32_t wanted, float& threshold) {
+    float most = max_nan(max_nan(m[0], m[1]), max_nan(m[2], m[3]));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = max_nan(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (lane == 0) s.scan_mass[warp] = most;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarpsS; ++w) most = max_nan(most, s.scan_mass[w]);
+    c_hi = s.c_hi;
+    c_lo = s.c_lo;
+    if (wanted > 0) {
+      const float scale = c_hi * kNear;
+      // What is beyond the last bin has no weight.
+      if (threadIdx.x < 2) s.mine[threadIdx.x] = (most - kNearBins / scale) - fabsf(most) * 1e-6f;
+#pragma unroll
+      for (int g = 0; g < kAhead; ++g) {
+        const float d = m[g] == most ? 0.f : (most - m[g]) * scale;
+        if (d < static_cast<float>(kNearBins) && most > -INFINITY) atomicAdd(&s.near_hist[static_cast<int>(d)], 1u);
+      }
+      __syncthreads();
+      static_assert(kNearBins == 2 * kThreadsS, "two bins for a thread");
+      const uint32_t n0 = s.near_hist[2 * threadIdx.x], n = n0 + s.near_hist[2 * threadIdx.x + 1];
+      uint32_t sum = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+      }
+      if (lane == 31) s.scan[warp] = sum;
+      __syncthreads();
+      uint32_t before = sum - n;
+      for (int w = 0; w < warp; ++w) before += s.scan[w];
+      const uint32_t share = (wanted + a.cluster - 1) / a.cluster;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint32_t k = i == 0 ? wanted : share;
+        if (before < k && k <= before + n) {
+          // The bins' edges are rounded: a little further.
+          const float b = static_cast<float>(2 * threadIdx.x + (before + n0 < k ? 1 : 0)) + 1.01f;
+          s.mine[i] = (most - b / scale) - fabsf(most) * 1e-6f;
+        }
+      }
+      __syncthreads();
+    }
+    if (threadIdx.x < a.cluster) {
+      of_block(s.peers[turn][rank], threadIdx.x)[0] = most != most ? 0xFFFFFFFFull : order_of(most);
+      float* to = of_block(s.thresholds[rank], threadIdx.x);
+      to[0] = wanted > 0 ? s.mine[0] : -INFINITY;
+      to[1] = wanted > 0 ? s.mine[1] : -INFINITY;
+    }
+    sync();
+    uint64_t best = 0;
+    float one = -INFINITY, each_one = INFINITY;
+    for (int r = 0; r < a.cluster; ++r) {
+      best = max(best, s.peers[turn][r][0]);
+      one = fmaxf(one, s.thresholds[r][0]);
+      each_one = fminf(each_one, s.thresholds[r][1]);
+    }
+    turn ^= 1;
+    threshold = fmaxf(one, each_one);
+    return static_cast<uint32_t>(best);
+  }
+
+  // Lists the elements that reach `threshold`, in the first block. `weigh`: the weight of all
+  // others, by the hardware's 2^x, in the weights' units. Their number, the same in every thread; above
+  // kList they are not listed.
+  __device__ int list_above(float threshold, bool weigh, uint64_t heaviest) {
+    const uint32_t room = kList / a.cluster;
+    uint64_t* list = of_block(s.list, 0);
+    const float shift_by = top * c_hi;
+    float sum = 0.f;
+    each_raw([&](int, int i, const Raw8<TYPE>& raw) {
+      float v[8];
+      if (weigh) {
+        float w[8];
+        unpack8<TYPE>(raw, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w[e]) : "f"(fmaf(v[e], c_hi, -shift_by)));
+          w[e] = v[e] >= threshold ? 0.f : w[e];
+        }
+        sum += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+      }
+      if (largest<TYPE>(raw) >= threshold) {
+        unpack8<TYPE>(raw, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          if (v[e] >= threshold && v[e] != -INFINITY) {
+            const uint32_t n = atomicAdd(&s.owned, 1u);
+            if (n < room) list[rank * room + n] = place_of(v[e], i + e);
+            if (n < kList) s.heft[n] = place_of(v[e], i + e);
+          }
+        }
+      }
+    });
+    uint64_t rest = 0;
+    if (weigh) {
+      rest = __float2ull_rn(sum * static_cast<float>(heaviest));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) rest += shfl64(rest, o);
+      if (lane == 0) s.red[warp][0] = rest;
+    }
+    __syncthreads();
+    if (threadIdx.x < a.cluster) {
+      rest = 0;
+      if (weigh)
+        for (int w = 0; w < kWarpsS; ++w) rest += s.red[w][0];
+      *of_block(&s.rests[rank], threadIdx.x) = rest;
+      *of_block(&s.owns[rank], threadIdx.x) = s.owned;
+    }
+    sync();
+    uint32_t n = 0, before = 0, most = 0;
+    for (int r = 0; r < a.cluster; ++r) {
+      if (r < rank) before += min(s.owns[r], kList + 0u);
+      n += min(s.owns[r], kList + 1u);
+      most = max(most, s.owns[r]);
+    }
+    if (n <= kList && most > room) {
+      // More than a block's room: once more, one block's after the other's.
+      const uint32_t mine = s.owns[rank];
+      for (uint32_t i = threadIdx.x; i < mine; i += kThreadsS) list[before + i] = s.heft[i];
+      sync();
+    }
+    return static_cast<int>(n);
+  }
+
+  // In the first block: the items and their weights from the list.
+  __device__ void take_list(uint64_t& rest) {
+    uint32_t room = kList / a.cluster, most = 0;
+    for (int r = 0; r < a.cluster; ++r) most = max(most, s.owns[r]);
+    int n = 0;
+    rest = 0;
+    for (int r = 0; r < a.cluster; ++r) {
+      const uint32_t m = s.owns[r], from = most > room ? n : r * room;
+      rest += s.rests[r];
+      for (uint32_t i = threadIdx.x; i < m; i += kThreadsS) s.item[n + i] = s.list[from + i];
+      n += static_cast<int>(m);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreadsS) s.heft[i] = any_weight(place_value(s.item[i]), kExp2.v);
+    __syncthreads();
+  }
+
+  // The token from a list of up to kPairs items: two threads compare an item with the others.
+  __device__ int draw_pairs(int n, uint64_t k, float p, uint64_t rest, uint64_t error, uint64_t least, float u,
+                            int64_t* token) {
+    const int mine = threadIdx.x >> 1, half = threadIdx.x & 1;
+    const bool on = mine < n;
+    const uint64_t at = on ? s.item[mine] : 0, w = on ? s.heft[mine] : 0;
+    uint32_t count = 0;
+    uint64_t before = 0;
+    for (int j = half; j < n; j += 2) {
+      const bool above = s.item[j] > at;
+      count += above ? 1 : 0;
+      before += above ? s.heft[j] : 0;
+    }
+    count += __shfl_xor_sync(0xffffffffu, count, 1);
+    before += shfl64(before, 1);
+    bool kept = on && count < k;
+    if (p < 1.f) {
+      uint64_t sum = kept && half == 0 ? w : 0;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) sum += shfl64(sum, o);
+      if (lane == 0) s.warp_sum[warp] = sum;
+      __syncthreads();
+      uint64_t listed = 0;
+#pragma unroll
+      for (int i = 0; i < kWarpsS; ++i) listed += s.warp_sum[i];
+      const uint64_t of = listed + rest;
+      const uint64_t mass = share_of(of - (of < error ? of : error), p), most = share_of(of + error, p);
+      if (most > listed) return kTooShort;
+      if (__syncthreads_or(kept && before >= mass && before < most)) return kInexact;
+      kept = kept && before < mass;
+    }
+    kept = kept && w >= least;
+    if (half == 0) s.list[mine] = kept ? w : 0;
+    __syncthreads();
+    uint64_t all = 0, c = 0;
+    const uint32_t index = static_cast<uint32_t>(at);  // falls with the index
+    for (int j = half; j < n; j += 2) {
+      const uint64_t x = s.list[j];
+      all += x;
+      c += static_cast<uint32_t>(s.item[j]) > index ? x : 0;
+    }
+    all += shfl64(all, 1);
+    c += shfl64(c, 1);
+    const uint64_t target = target_of(all, u);
+    if (kept && half == 0 && target >= c && target < c + w) *token = place_index(at);
+    return kDone;
+  }
+
+  // Longer lists: by bins of the logit, then the items of one bin with each other.
+  __device__ int few_bin(uint64_t place) const { return bin(place_value(place), kFew, kFewBins); }
+  __device__ void fill_bins(int n) {
+    for (int i = threadIdx.x; i < kFewBins; i += kThreadsS) {
+      s.few_hist[i] = 0;
+      s.few_mass[i] = 0;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreadsS) {
+      const int b = few_bin(s.item[i]);
+      if (b == kFewBins) continue;
+      atomicAdd(&s.few_hist[b], 1u);
+      atomicAdd(reinterpret_cast<unsigned long long*>(&s.few_mass[b]),
+                static_cast<unsigned long long>(s.heft[i]));
+    }
+    __syncthreads();
+  }
+  // s.cut: the last place of which less than k and less than `mass` lie before; s.cut_mass: the weight
+  // up to it. Everything (cut 0) where the list ends before both.
+  __device__ void cut_bins(int n, uint64_t k, uint64_t mass) {
+    constexpr int kEach = (kFewBins + kThreadsS - 1) / kThreadsS;
+    const int b = min(static_cast<int>(threadIdx.x) * kEach, kFewBins), b_end = min(b + kEach, kFewBins);
+    uint32_t c = 0, c_before, c_all;
+    uint64_t m = 0, m_before, m_all;
+    for (int i = b; i < b_end; ++i) {
+      c += s.few_hist[i];
+      m += s.few_mass[i];
+    }
+    if (threadIdx.x == 0) {
+      s.x_bin = -1;
+      s.few_n = 0;
+    }
+    scan(c, m, c_before, m_before, c_all, m_all);
+    if (threadIdx.x == 0) {
+      s.cut = 0;
+      s.cut_mass = s.list_mass = m_all;
+    }
+    if (c_before < k && m_before < mass && (c_before + c >= k || m_before + m >= mass)) {
+      int i = b;
+      while (c_before + s.few_hist[i] < k && m_before + s.few_mass[i] < mass) {
+        c_before += s.few_hist[i];
+        m_before += s.few_mass[i++];
+      }
+      s.x_bin = i;
+      s.x_count = c_before;
+      s.x_before = m_before;
+    }
+    __syncthreads();
+    const int x = s.x_bin;
+    if (x < 0) return;
+    for (int i = threadIdx.x; i < n; i += kThreadsS)
+      if (few_bin(s.item[i]) == x) s.few[atomicAdd(&s.few_n, 1u)] = static_cast<uint16_t>(i);
+    __syncthreads();
+    const uint32_t few = s.few_n;
+    for (uint32_t i = threadIdx.x; i < few; i += kThreadsS) {
+      const uint64_t at = s.item[s.few[i]], w = s.heft[s.few[i]];
+      uint64_t before = s.x_before, count = s.x_count;
+      for (uint32_t j = 0; j < few; ++j) {
+        const bool above = s.item[s.few[j]] > at;
+        before += above ? s.heft[s.few[j]] : 0;
+        count += above ? 1 : 0;
+      }
+      if (count < k && before < mass && (count + 1 >= k || before + w >= mass)) {
+        s.cut = at;
+        s.cut_mass = before + w;
+      }
+    }
+    __syncthreads();
+  }
+  // The token, from the items at or above s.cut with weights of at least `least`: by buckets of
+  // neighbouring indices.
+  __device__ void draw_buckets(int n, uint64_t least, float u, int64_t* token) {
+    int down = 0;
+    while (((a.V - 1) >> down) >= kThreadsS) ++down;
+    const uint64_t cut = s.cut;
+    s.bucket[threadIdx.x] = 0;
+    if (threadIdx.x == 0) s.few_n = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += kThreadsS) {
+      const uint64_t at = s.item[i], w = s.heft[i];
+      if (at >= cut && w >= least)
+        atomicAdd(reinterpret_cast<unsigned long long*>(&s.bucket[place_index(at) >> down]),
+                  static_cast<unsigned long long>(w));
+    }
+    __syncthreads();
+    uint32_t none, none_all;
+    uint64_t before, all;
+    const uint64_t mine = s.bucket[threadIdx.x];
+    scan(0, mine, none, before, none_all, all);
+    const uint64_t target = target_of(all, u);
+    if (target >= before && target < before + mine) {
+      s.x_bin = threadIdx.x;
+      s.x_before = before;
+    }
+    __syncthreads();
+    const int x = s.x_bin;
+    for (int i = threadIdx.x; i < n; i += kThreadsS) {
+      const uint64_t at = s.item[i];
+      if (at >= cut && place_index(at) >> down == x && s.heft[i] >= least)
+        s.few[atomicAdd(&s.few_n, 1u)] = static_cast<uint16_t>(i);
+    }
+    __syncthreads();
+    const uint32_t few = s.few_n;
+    for (uint32_t i = threadIdx.x; i < few; i += kThreadsS) {
+      const int index = place_index(s.item[s.few[i]]);
+      uint64_t c = s.x_before;
+      for (uint32_t j = 0; j < few; ++j)
+        c += place_index(s.item[s.few[j]]) < index ? s.heft[s.few[j]] : 0;
+      if (target >= c && target < c + s.heft[s.few[i]]) *token = index;
+    }
+  }
+
+  // The token from the list, where it holds all that is kept. Otherwise the cut hangs on what `rest` is
+  // within `error` (kInexact), or on elements that are not listed (kTooShort). again: the items
+  // have been through this.
+  __device__ int from_items(int n, bool again, uint64_t k, float p, uint64_t rest, uint64_t error,
+                            uint64_t least, float u, int64_t* token) {
+    if (n <= kPairs) return draw_pairs(n, k, p, rest, error, least, u, token);
+    if (!again) fill_bins(n);
+    if (k != kAll) {
+      cut_bins(n, k, kAll);
+    } else {
+      uint32_t none, none_all;
+      uint64_t m = 0, before, all;
+      for (int i = threadIdx.x; i < n; i += kThreadsS) m += s.heft[i];
+      scan(0, m, none, before, none_all, all);
+      if (threadIdx.x == 0) s.cut_mass = s.list_mass = all;
+      __syncthreads();
+    }
+    if (p < 1.f) {
+      const uint64_t of = s.cut_mass + rest;
+      __syncthreads();
+      const uint64_t mass = share_of(of - (of < error ? of : error), p), most = share_of(of + error, p);
+      if (most > s.list_mass) return kTooShort;
+      cut_bins(n, k, mass);
+      if (s.cut_mass < most) return kInexact;
+    }
+    draw_buckets(n, least, u, token);
+    return kDone;
+  }
+  // Whether the token was drawn from the elements that reach `threshold`.
+  __device__ bool from_list(float threshold, bool again, int64_t top_k, float p, uint64_t heaviest, uint64_t least,
+                            float u, int64_t* token) {
+    const bool by_k = top_k < a.V;
+    const uint64_t k = by_k ? top_k : kAll;
+    if (again) {
+      if (threadIdx.x == 0) s.owned = 0;
+      __syncthreads();
+    }
+    const int n = list_above(threshold, !by_k, heaviest);
+    if (n > kList) return false;
+    int verdict = kTooShort;
+    uint64_t rest = 0;
+    if (rank == 0) {
+      take_list(rest);
+      // The hardware's 2^x and its argument, a thread's sums, and top c, whose rounding grows with
+      // it; each weight is rounded by half a unit.
+      const float off = 0x1p-18f + (fabsf(top * c_hi) + static_cast<float>(a.stretch / 256 + 8)) * 0x1p-24f;
+      const uint64_t error = by_k ? 0 : static_cast<uint64_t>(static_cast<float>(rest) * off) + a.V;
+      verdict = from_items(n, false, k, p, rest, error, least, u, token);
+      if (threadIdx.x < a.cluster) *of_block(&s.verdict, threadIdx.x) = verdict;
+    }
+    sync();
+    if (s.verdict == kInexact) {
+      // The others' weight once more, as whole numbers.
+      rest = 0;
+      uint64_t none = 0;
+      each(-INFINITY, [&](int, float v) {
+        if (v < threshold) rest += any_weight(v, kExp2.v);
+      });
+      reduce<false>(rest, none);
+      if (rank == 0) {
+        verdict = from_items(n, true, k, p, rest, 0, least, u, token);
+        if (threadIdx.x < a.cluster) *of_block(&s.verdict, threadIdx.x) = verdict;
+      }
+      sync();
+    }
+    return s.verdict == kDone;
+  }
+
   __device__ void run(int row) {
     const float temperature = a.temperatures ? a.temperatures[row] : a.temperature;
     int64_t top_k = a.top_ks ? a.top_ks[row] : a.top_k;
-    float p = a.top_ps ? a.top_ps[row] : a.top_p;
+    const float p = a.top_ps ? a.top_ps[row] : a.top_p;
     const float min_p = a.min_ps ? a.min_ps[row] : a.min_p;
+    const float u = a.u[row];
     if (threadIdx.x == 0) {
       const double c = 1.4426950408889634074 / fmax(static_cast<double>(temperature), 1e-30);
       s.c_hi = static_cast<float>(c);
       s.c_lo = static_cast<float>(c - static_cast<double>(s.c_hi));
     }
-    for (int i = threadIdx.x; i < kTable; i += kThreadsS) s.table[i] = kExp2.v[i];
-    uint64_t best = 0, none = 0;
-    each([&](int i, const float* v) {
+    if (top_k <= 0 || top_k > a.V) top_k = a.V;
+    const bool greedy = !(temperature > 0.f) || top_k == 1 || !(p > 0.f);
+    const bool by_k = top_k < a.V, by_p = p < 1.f;
+    const bool list = !greedy && (by_k ? top_k <= kMostK : by_p) && temperature < 1e30f;
+    // The loads' largest tell where the list begins if there are enough of them.
+    const int loads = min(a.cluster * kThreadsS * kAhead, a.V / 8);
+    const int wanted = by_k ? static_cast<int>(min(top_k, static_cast<int64_t>(kMostK))) : min(loads / 2, kWanted);
+    const bool near = list && wanted > 0 && loads >= 2 * wanted;
+    float m[kAhead];
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (v[e] != -INFINITY) best = max(best, place_of(v[e], i + e));
-    });
-    reduce<true>(best, none);
-    c_hi = s.c_hi;
-    c_lo = s.c_lo;
-    bin_scale = c_hi * kPerOctave;
-    const uint32_t order = static_cast<uint32_t>(best >> 32);
+    for (int g = 0; g < kAhead; ++g) m[g] = -INFINITY;
+    each_raw([&](int g, int, const Raw8<TYPE>& raw) { m[g] = max_nan(m[g], largest<TYPE>(raw)); });
+    float threshold;
+    const uint32_t order = find_top(m, near ? wanted : 0, threshold);
     int64_t* token = a.tokens + row;
-    if (best == 0 || order == 0xFFFFFFFFu) {  // nothing to choose from, or a NaN
+    top = value_of(order);
+    if (order == 0xFFFFFFFFu || top == -INFINITY) {  // a NaN, or nothing to choose from
       if (rank == 0 && threadIdx.x == 0) *token = -1;
       return;
     }
-    top = value_of(order);
-    if (top_k <= 0 || top_k > a.V) top_k = a.V;
-    const bool greedy = !(temperature > 0.f) || top_k == 1 || !(p > 0.f);
     if (greedy) {
-      if (rank == 0 && threadIdx.x == 0)
-        *token = static_cast<int64_t>(0xFFFFFFFFu - static_cast<uint32_t>(best));
+      uint64_t at = 0, none = 0;
+      each(top, [&](int i, float v) {
+        if (v == top) at = max(at, place_of(top, i));
+      });
+      reduce<true>(at, none);
+      if (rank == 0 && threadIdx.x == 0) *token = place_index(at);
       return;
     }
-    const bool by_k = top_k < a.V, by_p = p < 1.f;
-    uint64_t cut = 0;
-    if (by_k || by_p) histogram();
-    if (by_k) {
-      bracket(top_k, 1.f);
-      cut = find_cut(top_k, kAll, 0, s.bins[0], s.bins[1]);
-    }
-    if (by_p) {
-      uint64_t all = 0, zero = 0;
-      each([&](int i, const float* v) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (v[e] != -INFINITY && place_of(v[e], i + e) >= cut) all += weight(v[e]);
-      });
-      reduce<false>(all, zero);
-      if (threadIdx.x == 0) s.p = ceil(static_cast<double>(p) * static_cast<double>(all));
-      bracket(top_k, p);
-      const uint64_t mass = static_cast<uint64_t>(s.p);
-      cut = find_cut(kAll, mass < 1 ? 1 : mass, cut, s.bins[0], s.bins[1]);
-    }
-    // min_p above 1 keeps the largest.
+    const float high = top * c_hi;
+    far = !(fabsf(high) < 3900.f) || c_hi < 1e-30f;
+    octave = far ? 0 : static_cast<int>(ceilf(high));
+    lowest = far ? -INFINITY : top - 47.f / c_hi;
+    // min_p above 1 keeps the largest. Elements well below the limit need no weight.
     const float share = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;
-    // share 2^43 is exact in 32 bits' mantissa; the least whole number at or above it.
-    const uint64_t least = static_cast<uint64_t>(__float2ull_ru(share * static_cast<float>(kOne)));
-    draw(cut, least, a.u[row], token);
+    const uint64_t heaviest = any_weight(top, kExp2.v);
+    const uint64_t least = share < 1.f ? times<true>(heaviest, share) : heaviest;
+    const float low =
+        share > 0.f && c_hi > 1e-30f ? top + (log2f(share) - 0.01f) / c_hi - fabsf(top) * 1e-6f : -INFINITY;
+    if (list) {
+      if (near || a.V <= kList / a.cluster) {
+        if (!near) threshold = -INFINITY;
+        if (from_list(threshold, false, top_k, p, heaviest, least, u, token)) return;
+      }
+      if (by_k) {
+        histogram();
+        bracket(wanted, 1.f);
+        threshold = above_bin(s.bins[0] + 1);
+        if (from_list(threshold, true, top_k, p, heaviest, least, u, token)) return;
+      }
+    }
+    if (far)
+      from_row<true>(top_k, p, heaviest, least, low, u, token);
+    else
+      from_row<false>(top_k, p, heaviest, least, low, u, token);
   }
 };
 
 template <int TYPE>
-__global__ void __launch_bounds__(kThreadsS) sample_kernel(const __grid_constant__ SampleArgs a) {
+__global__ void __launch_bounds__(kThreadsS, kPerSm) sample_kernel(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   griddep_launch();
+  Shared& s = *reinterpret_cast<Shared*>(smem);
+  for (int i = threadIdx.x; i < kNearBins; i += kThreadsS) s.near_hist[i] = 0;
+  if (threadIdx.x == 0) s.owned = 0;
   griddep_wait();
   const int row = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
   const uint8_t* z = static_cast<const uint8_t*>(a.logits) + row * a.ld * type_size(TYPE);
@@ -601,8 +1335,7 @@ __global__ void __launch_bounds__(kThreadsS) sample_kernel(const __grid_constant
   const int shift = static_cast<int>(reinterpret_cast<uintptr_t>(z) % 16) / type_size(TYPE);
   const int64_t begin = static_cast<int64_t>(rank * kWarpsS + warp) * a.stretch;
   const int64_t end = min(begin + a.stretch, static_cast<int64_t>(a.V) + shift);
-  Row<TYPE> r{a, *reinterpret_cast<Shared*>(smem), z, shift, rank,
-              static_cast<int>(min(begin, end)), static_cast<int>(end), lane, warp, 0};
+  Row<TYPE> r{a, s, z, shift, rank, static_cast<int>(min(begin, end)), static_cast<int>(end), lane, warp, 0};
   r.run(row);
   // No block leaves while another may still write into its memory.
   r.sync();
@@ -656,12 +1389,16 @@ extern "C" flce_status_t flce_sample(const flce_sample_params_t* p, const void* 
   a.top_k = p->top_k;
   a.top_p = p->top_p;
   a.min_p = p->min_p;
-  // Blocks for a row: as many as fill the GPU, each with 4096 elements at least.
+  // Blocks for a row: as many as give two waves of them, each with 16 KiB at least.
   int cluster = 1;
-  while (cluster < kMaxCluster && 2 * cluster * p->B <= 2 * sms && p->V >= 2 * cluster * 4096) cluster *= 2;
+  while (cluster < kMaxCluster && 2 * cluster * p->B <= 2 * kPerSm * sms &&
+         p->V * type_size(p->dtype) >= 2 * cluster * 16384)
+    cluster *= 2;
   a.cluster = cluster;
   const int64_t warps = static_cast<int64_t>(cluster) * kWarpsS;
   a.stretch = static_cast<int>(((p->V + 8 + warps - 1) / warps + 7) / 8 * 8);
+  const int steps = (a.stretch + kStep - 1) / kStep;
+  a.part = (steps + kParts - 1) / kParts * kStep;
   const cudaError_t e = launch_sample(a, p->dtype, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
