@@ -20,53 +20,73 @@ struct DropArgs {
   Dropout drop;
 };
 
-// A thread takes 8 columns of a row: one counter's words.
-template <int XT, int YT, bool VEC, class Index>
-__global__ void __launch_bounds__(256) dropout_kernel(const __grid_constant__ DropArgs a) {
+// A thread takes the same group of 8 columns, one counter's words, of kRows rows, blockDim.y apart: their
+// loads are in flight together, and the generator's keys are made once for all of them.
+constexpr int kRows = 4, kThreads = 256;
+
+template <int XT, int YT, bool WIDE>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropArgs a, uint32_t across) {
   griddep_launch();
   griddep_wait();
-  const Index groups = static_cast<Index>((a.H + 7) / 8);
-  const Index i = static_cast<Index>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= groups * static_cast<Index>(a.M)) return;
-  const int64_t row = static_cast<int64_t>(i / groups);
-  const uint32_t group = static_cast<uint32_t>(i - static_cast<Index>(row) * groups);
-  const int64_t col = static_cast<int64_t>(group) * 8;
-  const uint8_t* x = static_cast<const uint8_t*>(a.x) + row * a.ld_x * type_size(XT);
-  const uint8_t* r = static_cast<const uint8_t*>(a.r) + row * a.ld_r * type_size(YT);
-  uint8_t* y = static_cast<uint8_t*>(a.y) + row * a.ld_y * type_size(YT);
-  const Raw8<XT> xr = load8<XT, VEC>(x, col, a.H);
-  Raw8<YT> rr = {};
-  if (a.r) rr = load8<YT, VEC>(r, col, a.H);
-  float v[8], u[8];
-  unpack8<XT>(xr, v);
-  unpack8<YT>(rr, u);
-  if (a.drop.threshold != 0) drop8(a.drop, dropout_key(a.drop), static_cast<uint32_t>(row), group, v);
-  if (a.r) {
+  const uint32_t down = blockIdx.x / across;
+  const int64_t group = static_cast<int64_t>(blockIdx.x - down * across) * blockDim.x + threadIdx.x;
+  const int64_t col = group * 8, first = static_cast<int64_t>(down) * (blockDim.y * kRows) + threadIdx.y;
+  if (col >= a.H) return;
+  const auto row_of = [](const void* p, int64_t row, int64_t ld, int size) {
+    return static_cast<const uint8_t*>(p) + row * ld * size;
+  };
+  Raw8<XT> xr[kRows];
+  Raw8<YT> rr[kRows];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[e] += u[e];
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t row = first + i * blockDim.y;
+    rr[i] = {};
+    if (row >= a.M) break;
+    xr[i] = load8<XT, WIDE>(row_of(a.x, row, a.ld_x, type_size(XT)), col, a.H);
+    if (a.r) rr[i] = load8<YT, WIDE>(row_of(a.r, row, a.ld_r, type_size(YT)), col, a.H);
   }
-  store8<YT, VEC>(y, col, a.H, v);
+  Keys keys;
+  if (a.drop.threshold != 0) keys = dropout_keys(a.drop);
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t row = first + i * blockDim.y;
+    if (row >= a.M) break;
+    float v[8];
+    unpack8<XT>(xr[i], v);
+    if (a.drop.threshold != 0)
+      drop8(a.drop, keys, static_cast<uint32_t>(row), static_cast<uint32_t>(group), v);
+    if (a.r) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        f32x2_split(fadd2(f32x2(v[2 * e], v[2 * e + 1]), pair_of(rr[i], e)), v[2 * e], v[2 * e + 1]);
+    }
+    store8<YT, WIDE>(static_cast<uint8_t*>(a.y) + row * a.ld_y * type_size(YT), col, a.H, v);
+  }
 }
 
 template <int XT, int YT>
-cudaError_t launch_drop(const DropArgs& a, bool vec, cudaStream_t st) {
-  const uint64_t n = static_cast<uint64_t>(a.M) * static_cast<uint64_t>((a.H + 7) / 8);
-  const uint64_t blocks = (n + 255) / 256;
-  if (blocks > 0x7FFFFFFFull) return cudaErrorInvalidValue;
-  const bool small = n < (1ull << 32) - 256;
-  auto kernel = vec ? small ? dropout_kernel<XT, YT, true, uint32_t> : dropout_kernel<XT, YT, true, uint64_t>
-                    : small ? dropout_kernel<XT, YT, false, uint32_t> : dropout_kernel<XT, YT, false, uint64_t>;
-  return launch_dependent(kernel, dim3(static_cast<unsigned>(blocks)), 256, 0, 1, st, a);
+cudaError_t launch_drop(const DropArgs& a, bool wide, cudaStream_t st) {
+  const int64_t groups = (a.H + 7) / 8;
+  // Blocks across a row, all of nearly the same width.
+  const int64_t across = (groups + kThreads - 1) / kThreads;
+  const int64_t even = (groups + across - 1) / across;
+  const unsigned x = even <= 16 ? static_cast<unsigned>(even) : static_cast<unsigned>((even + 31) / 32 * 32);
+  const unsigned y = kThreads / x;
+  const int64_t down = (a.M + y * kRows - 1) / (y * kRows);
+  if (across > 0x7FFFFFFF / down) return cudaErrorInvalidValue;
+  auto kernel = wide ? dropout_kernel<XT, YT, true> : dropout_kernel<XT, YT, false>;
+  return launch_dependent(kernel, dim3(static_cast<unsigned>(across * down)), dim3(x, y), 0, 1, st, a,
+                          static_cast<uint32_t>(across));
 }
 
-cudaError_t dispatch(const DropArgs& a, int xt, int yt, bool vec, cudaStream_t st) {
+cudaError_t dispatch(const DropArgs& a, int xt, int yt, bool wide, cudaStream_t st) {
   if (xt == kFp32)
-    return yt == kFp32   ? launch_drop<kFp32, kFp32>(a, vec, st)
-           : yt == kBf16 ? launch_drop<kFp32, kBf16>(a, vec, st)
-                         : launch_drop<kFp32, kFp16>(a, vec, st);
+    return yt == kFp32   ? launch_drop<kFp32, kFp32>(a, wide, st)
+           : yt == kBf16 ? launch_drop<kFp32, kBf16>(a, wide, st)
+                         : launch_drop<kFp32, kFp16>(a, wide, st);
   if (xt == kBf16)
-    return yt == kFp32 ? launch_drop<kBf16, kFp32>(a, vec, st) : launch_drop<kBf16, kBf16>(a, vec, st);
-  return yt == kFp32 ? launch_drop<kFp16, kFp32>(a, vec, st) : launch_drop<kFp16, kFp16>(a, vec, st);
+    return yt == kFp32 ? launch_drop<kBf16, kFp32>(a, wide, st) : launch_drop<kBf16, kBf16>(a, wide, st);
+  return yt == kFp32 ? launch_drop<kFp16, kFp32>(a, wide, st) : launch_drop<kFp16, kFp16>(a, wide, st);
 }
 
 }  // namespace
@@ -83,9 +103,10 @@ extern "C" flce_status_t flce_dropout(const flce_dropout_params_t* p, const void
     if (!pitch_ok(ld, p->H)) return FLCE_ERR_INVALID_ARG;
   DropArgs a;
   if (!make_dropout(p->dropout, p->seed, p->offset, seed, &a.drop)) return FLCE_ERR_INVALID_ARG;
-  // A counter holds the row and the group of columns in 32 bits each, and the grid its blocks in 31.
+  // A counter holds the row and the group of columns in 32 bits each; the grid has fewer than 2^31
+  // blocks of 4 rows or more and half of 256 groups or more, or of 64 rows and more.
   if (p->M > (1LL << 31) || p->H > (1LL << 34) ||
-      (p->H > 0 && p->M > 0 && (p->H + 7) / 8 > ((1LL << 31) - 1) * 256 / p->M))
+      (p->H > 0 && p->M > 0 && (p->H + 7) / 8 > (1LL << 31) * 256 / p->M))
     return FLCE_ERR_UNSUPPORTED;
   if (p->M == 0 || p->H == 0) return FLCE_OK;
   if (!x || !y) return FLCE_ERR_INVALID_ARG;
@@ -103,8 +124,8 @@ extern "C" flce_status_t flce_dropout(const flce_dropout_params_t* p, const void
   a.ld_y = pitch_of(p->ld_y, p->H);
   a.M = p->M;
   a.H = p->H;
-  const bool vec = p->H % 8 == 0 && rows16(x, a.ld_x, p->M, p->dtype) &&
+  const bool wide = p->H % 8 == 0 && rows16(x, a.ld_x, p->M, p->dtype) &&
                    rows16(residual, a.ld_r, p->M, p->out_dtype) && rows16(y, a.ld_y, p->M, p->out_dtype);
-  const cudaError_t e = dispatch(a, p->dtype, p->out_dtype, vec, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = dispatch(a, p->dtype, p->out_dtype, wide, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }

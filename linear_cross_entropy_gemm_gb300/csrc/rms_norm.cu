@@ -1,194 +1,67 @@
-// The root-mean-square norm with the residual's addition, dropout on the branch that joins
-// it, and an output in the operands' type or in 8 bits with scales.
+// C ABI of the root-mean-square norm with the residual's addition, dropout on the branch that joins
+// it, and an output in the operands' type or in 8 bits with scales (declared in include/flce.h).
 //
 //   h = r + D(x),   rstd = (mean_c h^2 + eps)^(-1/2),   y = w h rstd
 //   8 bits: s = max |y| / 448 over the row or over 128 columns,  y8 = e4m3(y / s)
-//
-// One pass: a row stays in its threads' registers from the loads to the stores, so x and r
-// are read once and h and y written once. The norm is of the unrounded h: rounding it to
-// 16 bits first would put 2^-9 of error into each y for nothing.
-#include <cuda_fp8.h>
+//   backward, g = dy w, xhat = h rstd:  e = dh + rstd (g - xhat mean_c(g xhat))
+//   dr = e,   dx = D(e),   dw = sum_m dy xhat
+#include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
 #include "block_internal.h"
 #include "flce_host.h"
+#include "rms_norm.h"
 #include "stream_host.h"
-#include "stream_ops.cuh"
 
 namespace flce {
+
 namespace {
 
-struct NormArgs {
-  const void *x, *w, *r;
-  void *y, *h;
-  float *rstd, *scales;
-  int64_t ld_x, ld_r, ld_h, ld_y;
-  int M, H;
-  int w_fp32, blocks;  // blocks: scales of 128 columns, not of a row
-  float eps;
-  Dropout drop;
-};
-
-__device__ __forceinline__ uint2 to_e4m3(const float* y, float inv) {
-  uint32_t q[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    q[e] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * e] * inv, y[2 * e + 1] * inv), __NV_SATFINITE,
-                                    __NV_E4M3);
-  return make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
-}
-
-// Scales below the smallest normal number are 0, and the values under them too: their
-// inverses need not be finite.
-__device__ __forceinline__ float scale_of(float largest, float* inv) {
-  float s = __fdiv_rn(largest, 448.f);
-  if (s < 1.17549435e-38f) s = 0.f;
-  *inv = s == 0.f ? 0.f : __frcp_rn(s);
-  return s;
-}
-
-// blockDim.x threads for a row, blockDim.y rows (one, unless a warp holds a row); a thread
-// holds NV groups of 8 columns, blockDim.x groups apart.
-template <int XT, int ST, int NV, bool VEC, bool Q>
-__global__ void __launch_bounds__(1024) norm_kernel(const __grid_constant__ NormArgs a) {
-  __shared__ float s_sum[32], s_max[32];
-  griddep_launch();
+// dw = the ordered sum of the blocks' shares: a cluster of up to 8 blocks takes 32 columns, each of its
+// warps every so many'th share; the warps of a block and then the blocks add up in their order.
+constexpr int kSumThreads = 512, kSumBlocks = 8;
+__global__ void __launch_bounds__(kSumThreads)
+    share_sum_kernel(const float* part, int parts, int n, void* out, int type, int blocks) {
+  __shared__ float s_sum[kSumThreads / 32][32], s_all[kSumBlocks][32];
   griddep_wait();
-  const int row = blockIdx.x * blockDim.y + threadIdx.y, T = blockDim.x, t = threadIdx.x;
-  if (row >= a.M) return;
-  const uint8_t* x = static_cast<const uint8_t*>(a.x) + row * a.ld_x * type_size(XT);
-  const uint8_t* r = static_cast<const uint8_t*>(a.r) + row * a.ld_r * type_size(ST);
-  const int n = a.H;
-  float h[NV * 8];
-  Raw8<ST> rr[NV];
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int col = (j * T + t) * 8;
-    Raw8<XT> xr = {};
-    rr[j] = {};
-    if (col < n) {
-      xr = load8<XT, VEC>(x, col, n);
-      if (a.r) rr[j] = load8<ST, VEC>(r, col, n);
-    }
-    unpack8<XT>(xr, h + 8 * j);
-  }
-  if (a.drop.threshold != 0) {
-    const Key key = dropout_key(a.drop);
-#pragma unroll
-    for (int j = 0; j < NV; ++j) drop8(a.drop, key, row, j * T + t, h + 8 * j);
-  }
+  const int rank = blockIdx.x % blocks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int col = static_cast<int>(blockIdx.x / blocks) * 32 + lane, apart = blocks * (kSumThreads / 32);
   float sum = 0.f;
-#pragma unroll
-  for (int j = 0; j < NV; ++j) {
+  for (int i = rank * (kSumThreads / 32) + warp; i < parts; i += 8 * apart) {
     float v[8];
-    unpack8<ST>(rr[j], v);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      h[8 * j + e] += v[e];
-      sum = fmaf(h[8 * j + e], h[8 * j + e], sum);
-    }
+    for (int k = 0; k < 8; ++k)
+      v[k] = col < n && i + k * apart < parts ? part[static_cast<int64_t>(i + k * apart) * n + col] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += v[k];
   }
-  sum = row_reduce<false>(sum, s_sum);
-  const float rstd = rsqrtf(sum / static_cast<float>(n) + a.eps);
-  if (a.rstd && t == 0) a.rstd[row] = rstd;
-  uint8_t* ho = static_cast<uint8_t*>(a.h) + row * a.ld_h * type_size(ST);
-  uint8_t* yo = static_cast<uint8_t*>(a.y) + row * a.ld_y * (Q ? 1 : type_size(XT));
-  float most = 0.f;
+  griddep_launch();
+  s_sum[warp][lane] = sum;
+  __syncthreads();
+  if (warp == 0) {
+    sum = 0.f;
 #pragma unroll
-  for (int j = 0; j < NV; ++j) {
-    const int col = (j * T + t) * 8;
-    if (col < n) {
-      if (a.h) store8<ST, VEC>(ho, col, n, h + 8 * j);
-      float w[8];
-      if (a.w == nullptr) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = 1.f;
-      } else if (a.w_fp32) {
-        unpack8<kFp32>(load8<kFp32, VEC>(a.w, col, n), w);
-      } else {
-        unpack8<XT>(load8<XT, VEC>(a.w, col, n), w);
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) h[8 * j + e] *= rstd * w[e];
-    }
-    if constexpr (!Q) {
-      if (col < n) store8<XT, VEC>(yo, col, n, h + 8 * j);
-    } else {
-      float m = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) m = max_nan(m, fabsf(h[8 * j + e]));
-      if (a.blocks) {
-        // 16 neighbouring threads hold 128 columns.
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
-        float inv;
-        const float s = scale_of(m, &inv);
-        if (col < n) {
-          if ((t & 15) == 0) a.scales[static_cast<int64_t>(row) * ((n + 127) / 128) + col / 128] = s;
-          const uint2 q = to_e4m3(h + 8 * j, inv);
-          if constexpr (VEC) {
-            *reinterpret_cast<uint2*>(yo + col) = q;
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              if (col + e < n)
-                yo[col + e] = static_cast<uint8_t>((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
-          }
-        }
-      }
-      most = max_nan(most, m);
-    }
+    for (int w = 0; w < kSumThreads / 32; ++w) sum += s_sum[w][lane];
+    if (blocks > 1)
+      cooperative_groups::this_cluster().map_shared_rank(s_all[rank], 0)[lane] = sum;
   }
-  if constexpr (Q) {
-    if (a.blocks) return;
-    most = row_reduce<true>(most, s_max);
-    float inv;
-    const float s = scale_of(most, &inv);
-    if (t == 0) a.scales[row] = s;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      const int col = (j * T + t) * 8;
-      if (col >= n) continue;
-      const uint2 q = to_e4m3(h + 8 * j, inv);
-      if constexpr (VEC) {
-        *reinterpret_cast<uint2*>(yo + col) = q;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (col + e < n) yo[col + e] = static_cast<uint8_t>((e < 4 ? q.x : q.y) >> (8 * (e & 3)));
-      }
-    }
+  if (blocks > 1) {
+    cooperative_groups::this_cluster().sync();
+    sum = 0.f;
+    for (int r = 0; r < blocks; ++r) sum += s_all[r][lane];
   }
+  if (rank != 0 || warp != 0 || col >= n) return;
+  if (type == kFp32)
+    static_cast<float*>(out)[col] = sum;
+  else
+    static_cast<uint16_t*>(out)[col] = static_cast<uint16_t>(pack_16x2(sum, 0.f, type == kFp16) & 0xFFFFu);
 }
 
-template <int XT, int ST, int NV, bool VEC>
-cudaError_t launch_q(const NormArgs& a, dim3 grid, dim3 block, cudaStream_t st) {
-  return a.scales ? launch_dependent(norm_kernel<XT, ST, NV, VEC, true>, grid, block, 0, 1, st, a)
-                  : launch_dependent(norm_kernel<XT, ST, NV, VEC, false>, grid, block, 0, 1, st, a);
-}
-template <int XT, int ST, int NV>
-cudaError_t launch_vec(const NormArgs& a, bool vec, dim3 grid, dim3 block, cudaStream_t st) {
-  return vec ? launch_q<XT, ST, NV, true>(a, grid, block, st)
-             : launch_q<XT, ST, NV, false>(a, grid, block, st);
-}
-template <int XT, int ST>
-cudaError_t launch_norm(const NormArgs& a, bool vec, cudaStream_t st) {
-  const int groups = (a.H + 7) / 8;
-  const int nv = groups <= 1024 ? 1 : groups <= 2048 ? 2 : 4;
-  const int threads = ((groups + nv - 1) / nv + 31) / 32 * 32;
-  const int rows = threads == 32 ? 4 : 1;
-  const dim3 block(static_cast<unsigned>(threads), static_cast<unsigned>(rows));
-  const dim3 grid(static_cast<unsigned>((a.M + rows - 1) / rows));
-  return nv == 1   ? launch_vec<XT, ST, 1>(a, vec, grid, block, st)
-         : nv == 2 ? launch_vec<XT, ST, 2>(a, vec, grid, block, st)
-                   : launch_vec<XT, ST, 4>(a, vec, grid, block, st);
-}
-
-cudaError_t dispatch(const NormArgs& a, int xt, int st_type, bool vec, cudaStream_t st) {
-  if (xt == kFp32) return launch_norm<kFp32, kFp32>(a, vec, st);
-  if (xt == kBf16)
-    return st_type == kFp32 ? launch_norm<kBf16, kFp32>(a, vec, st) : launch_norm<kBf16, kBf16>(a, vec, st);
-  return st_type == kFp32 ? launch_norm<kFp16, kFp32>(a, vec, st) : launch_norm<kFp16, kFp16>(a, vec, st);
+cudaError_t launch_share_sum(const float* part, int parts, int n, void* out, int type, cudaStream_t st) {
+  int blocks = 1;
+  while (blocks < kSumBlocks && parts > blocks * 160) blocks *= 2;
+  return launch_dependent(share_sum_kernel, dim3((n + 31) / 32 * blocks), kSumThreads, 0, blocks, st, part, parts, n,
+                          out, type, blocks);
 }
 
 }  // namespace
@@ -207,6 +80,48 @@ flce_status_t check_norm(const flce_rms_norm_params_t* p) {
   return FLCE_OK;
 }
 
+namespace {
+
+// The registers of a row's threads, its ring and the time of its one sum decide. 8192 x 4096: 2 groups
+// of 256 threads with 128 registers and two blocks on an SM 42.9 us, 3 blocks with 80 registers 52,
+// 4 groups 69, 1 group of 512 threads 56.
+GradShape grad_shape(int64_t M, int64_t H, int x_size, int stream_size) {
+  constexpr size_t kMemory = 220 * 1024;
+  const int groups = static_cast<int>((H + 7) / 8);
+  const auto with = [&](int nv) {
+    GradShape s;
+    s.nv = nv;
+    s.threads = ((groups + nv - 1) / nv + 31) / 32 * 32;
+    s.rows = nv == 1 && s.threads == 32 ? kBlockRows : 1;
+    const int by_threads = (nv == 1 ? 1024 : 512) / (s.threads * s.rows);
+    const int by_ring = static_cast<int>(kMemory / (grad_ring(s, x_size, stream_size) + 1024));
+    s.blocks = by_threads < by_ring ? by_threads : by_ring;  // of an SM
+    return s;
+  };
+  GradShape s = with(8);
+  if (groups <= 256) {
+    s = with(1);
+  } else {
+    const GradShape two = with(2), four = with(4);
+    if (two.threads <= kRowThreads && two.blocks > 0)
+      s = two;
+    else if (four.threads <= kRowThreads && four.blocks > 0)
+      s = four;
+  }
+  const int64_t all = 152 * static_cast<int64_t>(s.blocks > 0 ? s.blocks : 1), need = (M + s.rows - 1) / s.rows;
+  s.blocks = static_cast<int>(need < all ? need : all);
+  return s;
+}
+GradShape grad_shape(const flce_rms_norm_params_t* p) {
+  return grad_shape(p->M, p->H, type_size(p->dtype), type_size(p->stream_dtype));
+}
+
+size_t grad_workspace(const flce_rms_norm_params_t* p) {
+  const GradShape s = grad_shape(p);
+  return static_cast<size_t>(s.blocks) * p->H * sizeof(float) + kAlign;
+}
+
+}  // namespace
 }  // namespace flce
 
 extern "C" flce_status_t flce_rms_norm_forward(const flce_rms_norm_params_t* p, const void* x,
@@ -248,9 +163,86 @@ extern "C" flce_status_t flce_rms_norm_forward(const flce_rms_norm_params_t* p, 
   if (!make_dropout(p->dropout, p->seed, p->offset, seed, &a.drop)) return FLCE_ERR_INVALID_ARG;
   const bool y16 = quantized ? aligned_to(y, 8) && (p->M <= 1 || a.ld_y % 8 == 0)
                              : rows16(y, a.ld_y, p->M, p->dtype);
-  const bool vec = p->H % 8 == 0 && y16 && rows16(x, a.ld_x, p->M, p->dtype) &&
+  const bool wide = p->H % 8 == 0 && y16 && rows16(x, a.ld_x, p->M, p->dtype) &&
                    rows16(residual, a.ld_r, p->M, p->stream_dtype) &&
                    rows16(h, a.ld_h, p->M, p->stream_dtype) && aligned_to(weight, 16);
-  const cudaError_t e = dispatch(a, p->dtype, p->stream_dtype, vec, static_cast<cudaStream_t>(stream));
+  const bool stream_fp32 = p->stream_dtype == FLCE_DTYPE_FP32;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = p->dtype == FLCE_DTYPE_BF16   ? norm_bf16(a, stream_fp32, wide, st)
+                        : p->dtype == FLCE_DTYPE_FP16 ? norm_fp16(a, stream_fp32, wide, st)
+                                                      : norm_fp32(a, stream_fp32, wide, st);
   return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
 }
+
+extern "C" {
+
+size_t flce_rms_norm_workspace_size(const flce_rms_norm_params_t* p) {
+  if (flce::check_norm(p) != FLCE_OK || p->M == 0) return 0;
+  return flce::grad_workspace(p);
+}
+
+flce_status_t flce_rms_norm_backward(const flce_rms_norm_params_t* p, const void* dy, const void* h,
+                                     const void* weight, const float* rstd, const void* dh,
+                                     const int64_t* seed, void* dx, void* dresidual, void* dW,
+                                     void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace flce;
+  NvtxRange nvtx_range("flce_rms_norm_backward");
+  const flce_status_t bad = check_norm(p);
+  if (bad != FLCE_OK) return bad;
+  if (p->scales != FLCE_SCALES_NONE) return FLCE_ERR_INVALID_ARG;
+  const int xb = type_size(p->dtype), sb = type_size(p->stream_dtype), wb = p->dW_fp32 ? 4 : xb;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!aligned_to(dW, wb)) return FLCE_ERR_ALIGNMENT;
+  if (p->M == 0) {
+    if (dW && cudaMemsetAsync(dW, 0, static_cast<size_t>(p->H) * wb, st) != cudaSuccess)
+      return FLCE_ERR_CUDA;
+    return FLCE_OK;
+  }
+  if (!dx && !dresidual && !dW) return FLCE_OK;
+  if (!dy || !h || !rstd) return FLCE_ERR_INVALID_ARG;
+  // One buffer for both gradients: where they are equal.
+  if (dx && dx == dresidual) {
+    if (p->dropout != 0.0 || p->dtype != p->stream_dtype) return FLCE_ERR_INVALID_ARG;
+    dresidual = nullptr;
+  }
+  if (!aligned_to(dy, xb) || !aligned_to(h, sb) || !aligned_to(weight, type_size(p->weight_dtype)) ||
+      !aligned_to(dh, sb) || !aligned_to(rstd, 4) || !aligned_to(dx, xb) || !aligned_to(dresidual, sb) ||
+      !aligned_to(seed, 8))
+    return FLCE_ERR_ALIGNMENT;
+  if (dW && !workspace) return FLCE_ERR_INVALID_ARG;
+  if (dW && workspace_bytes < grad_workspace(p)) return FLCE_ERR_WORKSPACE_TOO_SMALL;
+  int sms = 0;
+  const flce_status_t ds = device_info(&sms);
+  if (ds != FLCE_OK) return ds;
+  const GradShape s = grad_shape(p);
+  Carver cv(workspace, workspace_bytes);
+  NormGradArgs a;
+  a.dy = dy;
+  a.h = h;
+  a.w = weight;
+  a.dh = dh;
+  a.rstd = rstd;
+  a.dx = dx;
+  a.dr = dresidual;
+  a.part = dW ? cv.take<float>(0) : nullptr;
+  a.ld_dy = pitch_of(p->ld_y, p->H);
+  a.ld_h = pitch_of(p->ld_h, p->H);
+  a.ld_dh = pitch_of(p->ld_res, p->H);
+  a.M = static_cast<int>(p->M);
+  a.H = static_cast<int>(p->H);
+  a.w_fp32 = p->weight_dtype == FLCE_DTYPE_FP32 ? 1 : 0;
+  if (!make_dropout(p->dropout, p->seed, p->offset, seed, &a.drop)) return FLCE_ERR_INVALID_ARG;
+  const bool wide = p->H % 8 == 0 && rows16(dy, a.ld_dy, p->M, p->dtype) &&
+                   rows16(h, a.ld_h, p->M, p->stream_dtype) &&
+                   rows16(dh, a.ld_dh, p->M, p->stream_dtype) && aligned_to(weight, 16) &&
+                   aligned_to(dx, 16) && aligned_to(dresidual, 16);
+  const bool stream_fp32 = p->stream_dtype == FLCE_DTYPE_FP32;
+  cudaError_t e = p->dtype == FLCE_DTYPE_BF16   ? norm_grad_bf16(a, stream_fp32, wide, s, st)
+                  : p->dtype == FLCE_DTYPE_FP16 ? norm_grad_fp16(a, stream_fp32, wide, s, st)
+                                                : norm_grad_fp32(a, stream_fp32, wide, s, st);
+  if (e == cudaSuccess && dW)
+    e = launch_share_sum(a.part, s.blocks, a.H, dW, p->dW_fp32 ? FLCE_DTYPE_FP32 : p->dtype, st);
+  return e == cudaSuccess ? FLCE_OK : FLCE_ERR_CUDA;
+}
+
+}  // extern "C"

@@ -1,0 +1,7 @@
+// The backward of the root-mean-square norm of fp16 rows.
+#include "rms_norm_grad.cuh"
+
+cudaError_t flce::norm_grad_fp16(const NormGradArgs& a, bool stream_fp32, bool wide, const GradShape& s, cudaStream_t st) {
+  return stream_fp32 ? launch_grad<kFp16, kFp32>(a, wide, s, st)
+                     : launch_grad<kFp16, kFp16>(a, wide, s, st);
+}

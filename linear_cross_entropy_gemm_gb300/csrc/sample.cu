@@ -1324,7 +1324,6 @@ struct Row {
 template <int TYPE>
 __global__ void __launch_bounds__(kThreadsS, kPerSm) sample_kernel(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
-  griddep_launch();
   Shared& s = *reinterpret_cast<Shared*>(smem);
   for (int i = threadIdx.x; i < kNearBins; i += kThreadsS) s.near_hist[i] = 0;
   if (threadIdx.x == 0) s.owned = 0;
@@ -1337,6 +1336,8 @@ __global__ void __launch_bounds__(kThreadsS, kPerSm) sample_kernel(const __grid_
   const int64_t end = min(begin + a.stretch, static_cast<int64_t>(a.V) + shift);
   Row<TYPE> r{a, s, z, shift, rank, static_cast<int>(min(begin, end)), static_cast<int>(end), lane, warp, 0};
   r.run(row);
+  // Not before: blocks of the next kernel that wait on an SM keep this one's from it.
+  griddep_launch();
   // No block leaves while another may still write into its memory.
   r.sync();
 }

@@ -66,6 +66,43 @@ __device__ __forceinline__ Raw8<TYPE> pack8(const float* v) {
   return r;
 }
 
+// Values 2 i and 2 i + 1 as a packed pair of floats, on which one instruction does two sums or
+// products.
+template <int TYPE>
+__device__ __forceinline__ uint64_t pair_of(const Raw8<TYPE>& r, int i) {
+  const uint4& u = r.w[TYPE == kFp32 ? i / 2 : 0];
+  if constexpr (TYPE == kFp32) {
+    return i % 2 ? f32x2(__uint_as_float(u.z), __uint_as_float(u.w))
+                 : f32x2(__uint_as_float(u.x), __uint_as_float(u.y));
+  } else {
+    const uint32_t w = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
+    return f32x2(unpack_16(w & 0xFFFFu, TYPE == kFp16), unpack_16(w >> 16, TYPE == kFp16));
+  }
+}
+
+// a b of values 2 i and 2 i + 1 of two groups, exact in fp32 for 16-bit types: the products
+// take the halves of a word as they are.
+template <int TYPE>
+__device__ __forceinline__ uint64_t pair_product(const Raw8<TYPE>& a, const Raw8<TYPE>& b, int i) {
+  if constexpr (TYPE == kFp32) {
+    return fmul2(pair_of(a, i), pair_of(b, i));
+  } else {
+    const uint4 &u = a.w[0], &v = b.w[0];
+    const uint32_t x = i == 0 ? u.x : i == 1 ? u.y : i == 2 ? u.z : u.w;
+    const uint32_t y = i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+    float lo, hi;
+    if constexpr (TYPE == kBf16)
+      asm("{.reg .b16 a, b, c, d;\n mov.b32 {a, b}, %2;\n mov.b32 {c, d}, %3;\n"
+          " fma.rn.f32.bf16 %0, a, c, 0f00000000;\n fma.rn.f32.bf16 %1, b, d, 0f00000000;}"
+          : "=f"(lo), "=f"(hi) : "r"(x), "r"(y));
+    else
+      asm("{.reg .b16 a, b, c, d;\n mov.b32 {a, b}, %2;\n mov.b32 {c, d}, %3;\n"
+          " fma.rn.f32.f16 %0, a, c, 0f00000000;\n fma.rn.f32.f16 %1, b, d, 0f00000000;}"
+          : "=f"(lo), "=f"(hi) : "r"(x), "r"(y));
+    return f32x2(lo, hi);
+  }
+}
+
 // Columns col .. col + 7 of a row. VEC: the row starts on a 16-byte boundary and n is a
 // multiple of 8; otherwise value by value, and values at or past n read as 0.
 template <int TYPE, bool VEC>
@@ -98,57 +135,105 @@ __device__ __forceinline__ void store8(void* row, int64_t col, int64_t n, const 
   }
 }
 
+// How a thread's groups of 8 columns lie. kWide: 8 neighbours, moved 16 bytes at a time; rows off
+// the 16-byte boundaries go value by value, either with a warp's accesses next to each other
+// (kStrided), or, where a scale covers 128 columns, as in kWide (kNarrow).
+enum Layout { kWide, kStrided, kNarrow };
+
+template <Layout L>
+__device__ __forceinline__ int column(int j, int e, int T, int t) {
+  return L == kStrided ? (j * 8 + e) * T + t : (j * T + t) * 8 + e;
+}
+template <int TYPE, Layout L>
+__device__ __forceinline__ Raw8<TYPE> load_group(const void* row, int j, int T, int t, int n) {
+  if constexpr (L == kWide) {
+    if (column<L>(j, 0, T, t) >= n) return {};
+    return load8<TYPE, true>(row, column<L>(j, 0, T, t), n);
+  } else {
+    float v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int col = column<L>(j, e, T, t);
+      v[e] = col < n ? load_value<TYPE>(row, col) : 0.f;
+    }
+    return pack8<TYPE>(v);
+  }
+}
+template <int TYPE, Layout L>
+__device__ __forceinline__ void store_group(void* row, int j, int T, int t, int n, const float* v) {
+  if constexpr (L == kWide) {
+    if (column<L>(j, 0, T, t) < n) store8<TYPE, true>(row, column<L>(j, 0, T, t), n, v);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int col = column<L>(j, e, T, t);
+      if (col < n) store_value<TYPE>(row, col, v[e]);
+    }
+  }
+}
+
 // Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as easy as 1, 2,
-// 3", 2011): four random words for a counter of four words and a key of two.
-__device__ __forceinline__ uint4 philox(uint4 c, uint32_t k0, uint32_t k1) {
+// 3", 2011): four random words for a counter of four words and a key of two. The ten rounds'
+// keys are the same for all counters of a call: a thread makes them once (in shared
+// memory they cost more: 8192 x 4096 forward 48 us for 43).
+struct Keys {
+  uint32_t k0[10], k1[10];
+};
+__device__ __forceinline__ Keys philox_keys(uint64_t seed) {
+  Keys k;
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    k.k0[i] = static_cast<uint32_t>(seed) + i * 0x9E3779B9u;
+    k.k1[i] = static_cast<uint32_t>(seed >> 32) + i * 0xBB67AE85u;
+  }
+  return k;
+}
+__device__ __forceinline__ uint4 philox(uint4 c, const Keys& k) {
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
     const uint64_t a = static_cast<uint64_t>(c.x) * 0xD2511F53u;
     const uint64_t b = static_cast<uint64_t>(c.z) * 0xCD9E8D57u;
-    c = make_uint4(static_cast<uint32_t>(b >> 32) ^ c.y ^ k0, static_cast<uint32_t>(b),
-                   static_cast<uint32_t>(a >> 32) ^ c.w ^ k1, static_cast<uint32_t>(a));
-    k0 += 0x9E3779B9u;
-    k1 += 0xBB67AE85u;
+    c = make_uint4(static_cast<uint32_t>(b >> 32) ^ c.y ^ k.k0[i], static_cast<uint32_t>(b),
+                   static_cast<uint32_t>(a >> 32) ^ c.w ^ k.k1[i], static_cast<uint32_t>(a));
   }
   return c;
 }
 
 // The dropout of a call: an element is dropped where its 16 random bits are below
 // `threshold`, and scaled otherwise. Sixteen bits for an element, not 32: the generator's ten
-// rounds are two products and two three-way XORs each, which for a counter of four words
-// would cost as much time as the memory does; p is kept to 2^-16, and the scale is the
-// exact inverse of what is kept, so that the mean is right for the p that is drawn.
+// rounds take some 60 instructions for a counter's four words, which with 32 bits would be
+// more time than the memory takes; p is kept to 2^-16, and the scale is the exact inverse of
+// what is kept, so that the mean is right for the p that is drawn.
 struct Dropout {
   uint32_t threshold;  // 0: no dropout, 65536: everything
   float scale;         // 65536 / (65536 - threshold), 0 where everything is dropped
   uint64_t seed, offset;
   const int64_t* seed_at;  // the seed in device memory instead, or null
 };
-struct Key {
-  uint32_t k0, k1;
-};
-__device__ __forceinline__ Key dropout_key(const Dropout& d) {
-  uint64_t s = d.seed;
-  if (d.threshold != 0 && d.seed_at) s = static_cast<uint64_t>(*d.seed_at);
-  return {static_cast<uint32_t>(s), static_cast<uint32_t>(s >> 32)};
+__device__ __forceinline__ Keys dropout_keys(const Dropout& d) {
+  return philox_keys(d.seed_at ? static_cast<uint64_t>(*d.seed_at) : d.seed);
 }
-// v[e] = D(v[e]) of columns 8 group .. 8 group + 7 of a row.
-__device__ __forceinline__ void drop8(const Dropout& d, Key k, uint32_t row, uint32_t group, float* v) {
-  const uint4 r = philox(make_uint4(group, row, static_cast<uint32_t>(d.offset),
-                                    static_cast<uint32_t>(d.offset >> 32)), k.k0, k.k1);
+// The random bits of columns 8 group .. 8 group + 7 of a row, two in a word, the lower first.
+__device__ __forceinline__ uint4 drop_bits(const Dropout& d, const Keys& k, uint32_t row, uint32_t group) {
+  return philox(make_uint4(group, row, static_cast<uint32_t>(d.offset), static_cast<uint32_t>(d.offset >> 32)),
+                k);
+}
+// v[e] = D(v[e]) of those columns. A half is compared where it is, or in the upper place.
+__device__ __forceinline__ void drop8(const Dropout& d, const Keys& k, uint32_t row, uint32_t group, float* v) {
+  const uint4 r = drop_bits(d, k, row, group);
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  // At least the threshold: above the last word whose upper half is below it.
+  const uint32_t last = (d.threshold - 1) << 16 | 0xFFFFu;
+  const uint64_t scale = f32x2(d.scale, d.scale);
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    v[2 * e] = (w[e] & 0xFFFFu) >= d.threshold ? v[2 * e] * d.scale : 0.f;
-    v[2 * e + 1] = (w[e] >> 16) >= d.threshold ? v[2 * e + 1] * d.scale : 0.f;
+    float lo, hi;
+    f32x2_split(fmul2(f32x2(v[2 * e], v[2 * e + 1]), scale), lo, hi);
+    v[2 * e] = (w[e] << 16) > last ? lo : 0.f;
+    v[2 * e + 1] = w[e] > last ? hi : 0.f;
   }
 }
 
-__device__ __forceinline__ float warp_add(float v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
 // The larger one; a NaN if there is one.
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
