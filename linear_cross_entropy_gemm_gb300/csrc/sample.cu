@@ -37,13 +37,13 @@ constexpr int kTableFrac = 55;
 constexpr int kAhead = 4;                  // loads of a thread in flight,
 constexpr int kStep = kAhead * 256;        //   elements of a warp's
 constexpr int kParts = 32;                 // sums of a warp's stretch, at most
-constexpr int kList = 1536;                // elements that are listed,
-constexpr int kSort = 1024;                //   or sorted
+constexpr int kList = 1536;                // elements that are listed
 constexpr int kMostK = 1000;               // top-k up to this goes by the list
 constexpr int kWanted = 512;               // the list's least length where only p says how much is needed
 constexpr int kNear = 8, kNearBins = 512;  // bins to a factor of 2 and bins: of the loads' largest,
-constexpr int kFew = 16, kFewBins = 46 * kFew;       //   of the list,
-constexpr int kPerOctave = 64, kBins = 46 * kPerOctave;  // of all elements; weights below 2^-44 are 0
+constexpr int kPerOctave = 64, kBins = 46 * kPerOctave;  //   of all elements; weights below 2^-44 are 0
+constexpr int kItemBits = 9;               // bins of a list
+constexpr int kFew = 64;                   // items that are compared with each other
 constexpr int kPairs = kThreadsS / 2;      // lists up to this length are compared in pairs
 constexpr uint64_t kAll = ~0ull;
 
@@ -80,12 +80,12 @@ struct SampleArgs {
 struct Shared {
   union {
     uint32_t hist[kBins];
+    uint32_t near_hist[kNearBins];
     struct {
-      uint64_t few_mass[kFewBins];
-      uint32_t few_hist[kFewBins];
+      uint64_t item_mass[1 << kItemBits];
+      uint32_t item_hist[1 << kItemBits];
     };
     uint64_t bucket[kThreadsS];
-    uint32_t near_hist[kNearBins];
   };
   uint64_t list[kList];      // places; in the first block those of all blocks, kList / cluster for each
   union {
@@ -99,13 +99,13 @@ struct Shared {
   uint64_t warp_sum[kWarpsS], warp_kept[kWarpsS];
   uint64_t kept[kWarpsS][kParts];  // weights that are kept, by parts of the warps' stretches
   uint64_t cut, cut_mass;    // the last place that is kept, the weight up to and including it
-  uint64_t x_before, list_mass;
+  uint64_t x_before, x_count, list_mass;
   uint64_t rests[kMaxCluster];
   uint32_t owns[kMaxCluster];
   float thresholds[kMaxCluster][2];
   uint32_t scan[kWarpsS];
   float scan_mass[kWarpsS], within[2], mine[2];
-  uint32_t owned, few_n, x_count, above;
+  uint32_t owned, few_n, above;
   int x_bin, verdict;
   int bins[2];
   float c_hi, c_lo;
@@ -537,14 +537,14 @@ struct Row {
     if (n < kList) s.heft[n] = place;
   }
   // The blocks' places into the first one's list. Their number, the same in every thread; above
-  // kSort nothing is listed. sum: over the cluster.
+  // kList nothing is listed. sum: over the cluster.
   __device__ uint64_t gather(uint64_t& sum) {
     __syncthreads();
     const uint32_t mine = s.owned;
     uint64_t n = threadIdx.x == 0 ? mine : 0;
     const int at = turn;
     reduce<false>(sum, n);
-    if (n > kSort) return n;
+    if (n > kList) return n;
     uint32_t before = 0;
     for (int r = 0; r < rank; ++r) before += static_cast<uint32_t>(s.peers[at][r][1]);
     uint64_t* list = of_block(s.list, 0);
@@ -562,7 +562,7 @@ struct Row {
     const bool weigh = mass != kAll;
     uint64_t none = 0;
     while (!listed) {
-      while (n > kSort) {
+      while (n > kList) {
         const uint64_t mid = lo + (hi - lo) / 2;
         uint64_t c = 0, m = 0;
         each(place_value(mid), [&](int i, float v) {
@@ -591,11 +591,26 @@ struct Row {
         if (at >= lo && at < hi) own(at);
       });
       n = gather(none);
-      listed = n <= kSort;
+      listed = n <= kList;
     }
     if (rank == 0) {
-      sort_list(static_cast<int>(n));
-      cut_list<FAR>(static_cast<int>(n), k, mass, above_n, above_m, hi);
+      const int listed_n = static_cast<int>(n);
+      if (weigh) {
+        for (int i = threadIdx.x; i < listed_n; i += kThreadsS)
+          s.heft[i] = weight<FAR>(place_value(s.list[i]), s.table);
+        __syncthreads();
+      }
+      cut_items(s.list, listed_n, lo, hi, k, mass, above_n, above_m);
+      if (weigh) {
+        // The kept ones' weights, to their parts of s.kept.
+        for (int i = threadIdx.x; i < listed_n; i += kThreadsS) {
+          if (s.list[i] < s.cut) continue;
+          const int at = place_index(s.list[i]) + shift, w_at = at / a.stretch;
+          uint64_t* to = &s.kept[w_at % kWarpsS][at % a.stretch / a.part];
+          atomicAdd(reinterpret_cast<unsigned long long*>(of_block(to, w_at / kWarpsS)),
+                    static_cast<unsigned long long>(s.heft[i]));
+        }
+      }
       if (threadIdx.x < a.cluster && a.cluster > 1) *of_block(&s.cut, threadIdx.x) = s.cut;
     }
     sync();
@@ -616,7 +631,7 @@ struct Row {
     uint64_t none = 0;
     const uint64_t n = gather(none);
     bool moved = false;
-    return cut_between<false>(lo, hi, n, n <= kSort, k, kAll, s.above, 0, moved);
+    return cut_between<false>(lo, hi, n, n <= kList, k, kAll, s.above, 0, moved);
   }
 
   // The last place of those at or above `floor`, the k-th one's, before which less than p of their
@@ -658,67 +673,7 @@ struct Row {
       }
     });
     const uint64_t n = gather(more);
-    return cut_between<FAR>(floor > lo ? floor : lo, hi, n, n <= kSort, kAll, mass, 0, sum + more, moved);
-  }
-
-  // The list by falling place, in this block.
-  __device__ void sort_list(int n) {
-    int size = 1;
-    while (size < n) size <<= 1;
-    for (int i = n + threadIdx.x; i < size; i += kThreadsS) s.list[i] = 0;
-    __syncthreads();
-    for (int k = 2; k <= size; k <<= 1) {
-      for (int j = k >> 1; j > 0; j >>= 1) {
-        for (int t = threadIdx.x; t < size / 2; t += kThreadsS) {
-          const int x = 2 * t - (t & (j - 1)), y = x + j;
-          const uint64_t p = s.list[x], q = s.list[y];
-          if ((p < q) == ((x & k) == 0)) {
-            s.list[x] = q;
-            s.list[y] = p;
-          }
-        }
-        __syncthreads();
-      }
-    }
-  }
-
-  // s.cut from the sorted list: the last place that is kept, or `hi` where none is. With weights,
-  // the kept ones' go to their parts of s.kept.
-  template <bool FAR>
-  __device__ void cut_list(int n, uint64_t k, uint64_t mass, uint64_t above_n, uint64_t above_m, uint64_t hi) {
-    constexpr int kEach = kSort / kThreadsS;
-    const bool weigh = mass != kAll;
-    uint64_t w[kEach], sum = 0;
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const int i = threadIdx.x * kEach + e;
-      w[e] = i < n && weigh ? weight<FAR>(place_value(s.list[i]), s.table) : 0;
-      sum += w[e];
-    }
-    uint32_t none, none_all;
-    uint64_t before, all;
-    if (threadIdx.x == 0) s.cut = hi;
-    scan(0, sum, none, before, none_all, all);
-    before += above_m;
-    int kept = -1;
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) {
-      const int i = threadIdx.x * kEach + e;
-      if (i < n && above_n + i < k && before < mass) {
-        kept = i;
-        if (weigh) {
-          const int at = place_index(s.list[i]) + shift, w_at = at / a.stretch;
-          uint64_t* to = &s.kept[w_at % kWarpsS][at % a.stretch / a.part];
-          atomicAdd(reinterpret_cast<unsigned long long*>(of_block(to, w_at / kWarpsS)),
-                    static_cast<unsigned long long>(w[e]));
-        }
-      }
-      before += w[e];
-    }
-    // What is kept is a prefix.
-    if (kept >= 0)
-      atomicMin(reinterpret_cast<unsigned long long*>(&s.cut), static_cast<unsigned long long>(s.list[kept]));
-    __syncthreads();
+    return cut_between<FAR>(floor > lo ? floor : lo, hi, n, n <= kList, kAll, mass, 0, sum + more, moved);
   }
 
   // u all, rounded down: the sums are whole, and one is above u all where it is above this.
@@ -762,6 +717,80 @@ struct Row {
       n_all += x;
       m_all += y;
     }
+  }
+
+  // Among n items, with their weights in s.heft (not read with mass kAll), those in [lo, hi): s.cut is
+  // the last place before which less than k and less than `mass` lie, above_n and above_m of them at or
+  // above hi; s.cut_mass the weight up to it. lo, and all the weight, where the items end before both
+  // are reached. By bins of equal stretches of places, then those of one bin.
+  __device__ void cut_items(const uint64_t* items, int n, uint64_t lo, uint64_t hi, uint64_t k, uint64_t mass,
+                            uint64_t above_n, uint64_t above_m) {
+    const bool weigh = mass != kAll;
+    while (true) {
+      const int top_bit = 63 - __clzll(static_cast<long long>(hi - lo - 1 | 1));
+      const int down = max(0, top_bit + 1 - kItemBits);
+      s.item_mass[threadIdx.x] = s.item_mass[threadIdx.x + kThreadsS] = 0;
+      s.item_hist[threadIdx.x] = s.item_hist[threadIdx.x + kThreadsS] = 0;
+      if (threadIdx.x == 0) {
+        s.x_bin = -1;
+        s.few_n = 0;
+      }
+      __syncthreads();
+      for (int i = threadIdx.x; i < n; i += kThreadsS) {
+        const uint64_t at = items[i];
+        if (at < lo || at >= hi) continue;
+        const int b = static_cast<int>((hi - 1 - at) >> down);
+        atomicAdd(&s.item_hist[b], 1u);
+        if (weigh)
+          atomicAdd(reinterpret_cast<unsigned long long*>(&s.item_mass[b]),
+                    static_cast<unsigned long long>(s.heft[i]));
+      }
+      __syncthreads();
+      const int b = 2 * threadIdx.x;
+      uint32_t c0 = s.item_hist[b], c = c0 + s.item_hist[b + 1], c_before, c_all;
+      uint64_t m0 = s.item_mass[b], m = m0 + s.item_mass[b + 1], m_before, m_all;
+      scan(c, m, c_before, m_before, c_all, m_all);
+      uint64_t x_n = above_n + c_before, x_m = above_m + m_before;
+      if (threadIdx.x == 0) {
+        s.cut = lo;
+        s.cut_mass = above_m + m_all;
+      }
+      __syncthreads();
+      if (x_n < k && x_m < mass && (x_n + c >= k || x_m + m >= mass)) {
+        const bool second = x_n + c0 < k && x_m + m0 < mass;
+        s.x_bin = b + (second ? 1 : 0);
+        s.x_count = second ? x_n + c0 : x_n;
+        s.x_before = second ? x_m + m0 : x_m;
+      }
+      __syncthreads();
+      const int x = s.x_bin;
+      if (x < 0) return;
+      above_n = s.x_count;
+      above_m = s.x_before;
+      const uint32_t in_bin = s.item_hist[x];
+      hi -= static_cast<uint64_t>(x) << down;
+      if (hi - lo > 1ull << down) lo = hi - (1ull << down);
+      if (in_bin <= kFew) break;
+      __syncthreads();
+    }
+    for (int i = threadIdx.x; i < n; i += kThreadsS)
+      if (items[i] >= lo && items[i] < hi) s.few[atomicAdd(&s.few_n, 1u)] = static_cast<uint16_t>(i);
+    __syncthreads();
+    const uint32_t few = s.few_n;
+    if (threadIdx.x < few) {
+      const uint64_t at = items[s.few[threadIdx.x]], w = weigh ? s.heft[s.few[threadIdx.x]] : 0;
+      uint64_t before = above_m, count = above_n;
+      for (uint32_t j = 0; j < few; ++j) {
+        const bool above = items[s.few[j]] > at;
+        if (weigh) before += above ? s.heft[s.few[j]] : 0;
+        count += above ? 1 : 0;
+      }
+      if (count < k && before < mass && (count + 1 >= k || before + w >= mass)) {
+        s.cut = at;
+        s.cut_mass = before + w;
+      }
+    }
+    __syncthreads();
   }
 
   __device__ void clear_kept() {
@@ -870,6 +899,7 @@ struct Row {
     if (by_k || by_p) histogram();
     if (by_k) cut = cut_by_count(top_k);
     bool moved = false;
+    if (by_k && by_p) histogram();  // its place has been in use
     if (by_p) cut = cut_by_mass<FAR>(top_k, p, cut, heaviest, moved);
     if (!by_p || least > 0 || moved) weigh_kept<FAR>(cut, least, low);
     draw<FAR>(cut, least, low, u, token);
@@ -1072,75 +1102,6 @@ struct Row {
     return kDone;
   }
 
-  // Longer lists: by bins of the logit, then the items of one bin with each other.
-  __device__ int few_bin(uint64_t place) const { return bin(place_value(place), kFew, kFewBins); }
-  __device__ void fill_bins(int n) {
-    for (int i = threadIdx.x; i < kFewBins; i += kThreadsS) {
-      s.few_hist[i] = 0;
-      s.few_mass[i] = 0;
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += kThreadsS) {
-      const int b = few_bin(s.item[i]);
-      if (b == kFewBins) continue;
-      atomicAdd(&s.few_hist[b], 1u);
-      atomicAdd(reinterpret_cast<unsigned long long*>(&s.few_mass[b]),
-                static_cast<unsigned long long>(s.heft[i]));
-    }
-    __syncthreads();
-  }
-  // s.cut: the last place of which less than k and less than `mass` lie before; s.cut_mass: the weight
-  // up to it. Everything (cut 0) where the list ends before both.
-  __device__ void cut_bins(int n, uint64_t k, uint64_t mass) {
-    constexpr int kEach = (kFewBins + kThreadsS - 1) / kThreadsS;
-    const int b = min(static_cast<int>(threadIdx.x) * kEach, kFewBins), b_end = min(b + kEach, kFewBins);
-    uint32_t c = 0, c_before, c_all;
-    uint64_t m = 0, m_before, m_all;
-    for (int i = b; i < b_end; ++i) {
-      c += s.few_hist[i];
-      m += s.few_mass[i];
-    }
-    if (threadIdx.x == 0) {
-      s.x_bin = -1;
-      s.few_n = 0;
-    }
-    scan(c, m, c_before, m_before, c_all, m_all);
-    if (threadIdx.x == 0) {
-      s.cut = 0;
-      s.cut_mass = s.list_mass = m_all;
-    }
-    if (c_before < k && m_before < mass && (c_before + c >= k || m_before + m >= mass)) {
-      int i = b;
-      while (c_before + s.few_hist[i] < k && m_before + s.few_mass[i] < mass) {
-        c_before += s.few_hist[i];
-        m_before += s.few_mass[i++];
-      }
-      s.x_bin = i;
-      s.x_count = c_before;
-      s.x_before = m_before;
-    }
-    __syncthreads();
-    const int x = s.x_bin;
-    if (x < 0) return;
-    for (int i = threadIdx.x; i < n; i += kThreadsS)
-      if (few_bin(s.item[i]) == x) s.few[atomicAdd(&s.few_n, 1u)] = static_cast<uint16_t>(i);
-    __syncthreads();
-    const uint32_t few = s.few_n;
-    for (uint32_t i = threadIdx.x; i < few; i += kThreadsS) {
-      const uint64_t at = s.item[s.few[i]], w = s.heft[s.few[i]];
-      uint64_t before = s.x_before, count = s.x_count;
-      for (uint32_t j = 0; j < few; ++j) {
-        const bool above = s.item[s.few[j]] > at;
-        before += above ? s.heft[s.few[j]] : 0;
-        count += above ? 1 : 0;
-      }
-      if (count < k && before < mass && (count + 1 >= k || before + w >= mass)) {
-        s.cut = at;
-        s.cut_mass = before + w;
-      }
-    }
-    __syncthreads();
-  }
   // The token, from the items at or above s.cut with weights of at least `least`: by buckets of
   // neighbouring indices.
   __device__ void draw_buckets(int n, uint64_t least, float u, int64_t* token) {
@@ -1185,28 +1146,29 @@ struct Row {
   }
 
   // The token from the list, where it holds all that is kept. Otherwise the cut hangs on what `rest` is
-  // within `error` (kInexact), or on elements that are not listed (kTooShort). again: the items
-  // have been through this.
-  __device__ int from_items(int n, bool again, uint64_t k, float p, uint64_t rest, uint64_t error,
+  // within `error` (kInexact), or on elements that are not listed (kTooShort).
+  __device__ int from_items(int n, float threshold, uint64_t k, float p, uint64_t rest, uint64_t error,
                             uint64_t least, float u, int64_t* token) {
     if (n <= kPairs) return draw_pairs(n, k, p, rest, error, least, u, token);
-    if (!again) fill_bins(n);
-    if (k != kAll) {
-      cut_bins(n, k, kAll);
-    } else {
+    const uint64_t lo = static_cast<uint64_t>(order_of(threshold)) << 32;
+    const uint64_t hi = static_cast<uint64_t>(order_of(top) + 1) << 32;
+    uint64_t listed = 0, cut = lo;
+    if (k == kAll) {
       uint32_t none, none_all;
-      uint64_t m = 0, before, all;
+      uint64_t m = 0, before;
       for (int i = threadIdx.x; i < n; i += kThreadsS) m += s.heft[i];
-      scan(0, m, none, before, none_all, all);
-      if (threadIdx.x == 0) s.cut_mass = s.list_mass = all;
-      __syncthreads();
+      scan(0, m, none, before, none_all, listed);
+    } else {
+      cut_items(s.item, n, lo, hi, k, p < 1.f ? kAll - 1 : kAll, 0, 0);
+      listed = s.cut_mass;
+      cut = s.cut;
     }
     if (p < 1.f) {
-      const uint64_t of = s.cut_mass + rest;
-      __syncthreads();
+      const uint64_t of = listed + rest;
       const uint64_t mass = share_of(of - (of < error ? of : error), p), most = share_of(of + error, p);
-      if (most > s.list_mass) return kTooShort;
-      cut_bins(n, k, mass);
+      if (most > listed) return kTooShort;
+      __syncthreads();
+      cut_items(s.item, n, cut, hi, kAll, mass, 0, 0);
       if (s.cut_mass < most) return kInexact;
     }
     draw_buckets(n, least, u, token);
@@ -1231,7 +1193,7 @@ struct Row {
       // it; each weight is rounded by half a unit.
       const float off = 0x1p-18f + (fabsf(top * c_hi) + static_cast<float>(a.stretch / 256 + 8)) * 0x1p-24f;
       const uint64_t error = by_k ? 0 : static_cast<uint64_t>(static_cast<float>(rest) * off) + a.V;
-      verdict = from_items(n, false, k, p, rest, error, least, u, token);
+      verdict = from_items(n, threshold, k, p, rest, error, least, u, token);
       if (threadIdx.x < a.cluster) *of_block(&s.verdict, threadIdx.x) = verdict;
     }
     sync();
@@ -1244,7 +1206,7 @@ struct Row {
       });
       reduce<false>(rest, none);
       if (rank == 0) {
-        verdict = from_items(n, true, k, p, rest, 0, least, u, token);
+        verdict = from_items(n, threshold, k, p, rest, 0, least, u, token);
         if (threadIdx.x < a.cluster) *of_block(&s.verdict, threadIdx.x) = verdict;
       }
       sync();
@@ -1320,6 +1282,8 @@ struct Row {
       from_row<false>(top_k, p, heaviest, least, low, u, token);
   }
 };
+
+static_assert(kPerSm * (sizeof(Shared) + 1024) <= 227 * 1024, "as many blocks as an SM is to hold");
 
 template <int TYPE>
 __global__ void __launch_bounds__(kThreadsS, kPerSm) sample_kernel(const __grid_constant__ SampleArgs a) {
