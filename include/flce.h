@@ -535,7 +535,7 @@ typedef enum {
 
 /* h = r + D(x), y = weight h rstd, rstd = 1 / sqrt(mean(h^2) + eps). */
 typedef struct {
-  int64_t M;             /* rows; 0 is a valid no-op */
+  int64_t M;             /* rows, up to 2^30; 0 is a valid no-op */
   int64_t H;             /* columns, 1 .. FLCE_RMS_NORM_MAX_H */
   int64_t ld_x, ld_res, ld_h, ld_y; /* pitches of x, of the residual (backward: of dh), of h, of y (backward: of dy) */
   int64_t seed, offset;  /* of the dropout */

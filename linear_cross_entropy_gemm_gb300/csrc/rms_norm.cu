@@ -68,7 +68,7 @@ cudaError_t launch_share_sum(const float* part, int parts, int n, void* out, int
 
 flce_status_t check_norm(const flce_rms_norm_params_t* p) {
   if (!p || p->M < 0 || p->H <= 0) return FLCE_ERR_INVALID_ARG;
-  if (p->M > (1LL << 31) - 8 || p->H > FLCE_RMS_NORM_MAX_H) return FLCE_ERR_UNSUPPORTED;
+  if (p->M > (1LL << 30) || p->H > FLCE_RMS_NORM_MAX_H) return FLCE_ERR_UNSUPPORTED;
   if (!float_type_ok(p->dtype) || !wider_ok(p->stream_dtype, p->dtype) ||
       !wider_ok(p->weight_dtype, p->dtype) || p->scales < FLCE_SCALES_NONE ||
       p->scales > FLCE_SCALES_BLOCK || (p->dW_fp32 != 0 && p->dW_fp32 != 1))

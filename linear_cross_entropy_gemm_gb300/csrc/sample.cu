@@ -38,10 +38,12 @@ constexpr int kAhead = 4;                  // loads of a thread in flight,
 constexpr int kStep = kAhead * 256;        //   elements of a warp's
 constexpr int kParts = 32;                 // sums of a warp's stretch, at most
 constexpr int kList = 1536;                // elements that are listed
+constexpr int kNotes = 2 * kList;          // groups that are looked at again
 constexpr int kMostK = 1000;               // top-k up to this goes by the list
 constexpr int kWanted = 512;               // the list's least length where only p says how much is needed
 constexpr int kNear = 8, kNearBins = 512;  // bins to a factor of 2 and bins: of the loads' largest,
 constexpr int kPerOctave = 64, kBins = 46 * kPerOctave;  //   of all elements; weights below 2^-44 are 0
+constexpr float kSureSlack = 0.016f, kLikelySlack = 0.0004f;
 constexpr int kItemBits = 9;               // bins of a list
 constexpr int kFew = 64;                   // items that are compared with each other
 constexpr int kPairs = kThreadsS / 2;      // lists up to this length are compared in pairs
@@ -105,7 +107,7 @@ struct Shared {
   float thresholds[kMaxCluster][2];
   uint32_t scan[kWarpsS];
   float scan_mass[kWarpsS], within[2], mine[2];
-  uint32_t owned, few_n, above;
+  uint32_t owned, noted, few_n, above;
   int x_bin, verdict;
   int bins[2];
   float c_hi, c_lo;
@@ -239,9 +241,12 @@ struct Row {
     return a.cluster == 1 ? p : cg::this_cluster().map_shared_rank(p, r);
   }
 
+  // The 8 values at a position, -inf where there is no element; `group`: of this warp's stretch.
   __device__ __forceinline__ Raw8<TYPE> group(int at) const {
+    return at >= last ? nothing<TYPE>() : any_group(at);
+  }
+  __device__ __forceinline__ Raw8<TYPE> any_group(int at) const {
     const int i = at - shift;
-    if (at >= last) return nothing<TYPE>();
     if (i >= 0 && i + 8 <= a.V) return load8<TYPE, true>(z, i, a.V);
     float v[8];
 #pragma unroll
@@ -249,57 +254,63 @@ struct Row {
       v[e] = i + e >= 0 && i + e < a.V ? load_value<TYPE>(z, i + e) : -INFINITY;
     return pack8<TYPE>(v);
   }
-  // f(which of the loads, index of the first, 8 values as they are) over this warp's stretch;
-  // -inf where there is no element.
+  // f(which of the loads, position, 8 values as they are) over this warp's stretch.
   template <class F>
   __device__ __forceinline__ void each_raw(F f) const {
-    each_step([&](int base) {
+    for (int base = first; base < last; base += kStep) {
       const int at = base + lane * 8;
       Raw8<TYPE> r[kAhead];
 #pragma unroll
       for (int g = 0; g < kAhead; ++g) r[g] = group(at + g * 256);
 #pragma unroll
-      for (int g = 0; g < kAhead; ++g) f(g, at + g * 256 - shift, r[g]);
-    });
+      for (int g = 0; g < kAhead; ++g) f(g, at + g * 256, r[g]);
+    }
   }
+  // f(position, 8 values as they are), the next ones on their way: a body that is long is not
+  // repeated for each of several loads, which the instruction cache would not hold.
   template <class F>
-  __device__ __forceinline__ void each_step(F f) const {
-    for (int base = first; base < last; base += kStep) f(base);
+  __device__ __forceinline__ void each_group(F f) const {
+    Raw8<TYPE> next = group(first + lane * 8);
+#pragma unroll 1
+    for (int base = first; base < last; base += 256) {
+      const Raw8<TYPE> r = next;
+      next = group(base + 256 + lane * 8);
+      f(base + lane * 8, r);
+    }
   }
-  // f(index, value) for the groups of 8 that hold one of at least `least`.
+  // f(index, value) for the groups that hold one of at least `least`.
   template <class F>
   __device__ __forceinline__ void each(float least, F f) const {
-    each_raw([&](int, int i, const Raw8<TYPE>& raw) {
-      if (!(largest<TYPE>(raw) >= least)) return;
+    each_group([&](int at, const Raw8<TYPE>& r) {
+      if (!(largest<TYPE>(r) >= least)) return;
       float v[8];
-      unpack8<TYPE>(raw, v);
+      unpack8<TYPE>(r, v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f(i + e, v[e]);
+      for (int e = 0; e < 8; ++e) f(at - shift + e, v[e]);
     });
   }
-  // each, f returning a weight: they are added to s.kept, by parts of this warp's stretch.
-  template <class F>
-  __device__ __forceinline__ void each_kept(float least, F f) const {
+  // The same, f returning weights: they go to s.kept, by parts of this warp's stretch. after(position)
+  // follows each group.
+  template <class F, class G>
+  __device__ __forceinline__ void each_kept(float least, F f, G after) const {
     uint64_t sum = 0;
-    each_step([&](int base) {
-      const int at = base + lane * 8;
-      Raw8<TYPE> r[kAhead];
-#pragma unroll
-      for (int g = 0; g < kAhead; ++g) r[g] = group(at + g * 256);
-#pragma unroll
-      for (int g = 0; g < kAhead; ++g) {
-        if (!(largest<TYPE>(r[g]) >= least)) continue;
+    int part = 0, left = a.part;
+    each_group([&](int at, const Raw8<TYPE>& r) {
+      if (largest<TYPE>(r) >= least) {
         float v[8];
-        unpack8<TYPE>(r[g], v);
+        unpack8<TYPE>(r, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += f(at + g * 256 - shift + e, v[e]);
+        for (int e = 0; e < 8; ++e) sum += f(at - shift + e, v[e]);
+        after(at);
       }
-      const int part = (base - first) / a.part;
-      if (base + kStep >= last || (base + kStep - first) / a.part != part) {
+      left -= 256;
+      if (left == 0 || at - lane * 8 + 256 >= last) {
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) sum += shfl64(sum, o);
-        if (lane == 0) s.kept[warp][part] += sum;
+        if (lane == 0) s.kept[warp][part] = sum;
         sum = 0;
+        ++part;
+        left = a.part;
       }
     });
   }
@@ -371,16 +382,21 @@ struct Row {
     return d < static_cast<float>(bins) ? static_cast<int>(d) : bins;
   }
   __device__ __forceinline__ int bin(float v) const { return bin(v, kPerOctave, kBins); }
-  // The least logit whose bin is below b, to the bit; a NaN, which none reaches, for b = 0.
+  // The least logit whose bin is below b, to the bit; a NaN, which none reaches, for b = 0. By a
+  // whole warp: its lanes try 32 places between the ends.
   __device__ float above_bin(int b) const {
     if (b <= 0) return __int_as_float(0x7FC00000);
     uint32_t lo = order_of(-INFINITY), hi = order_of(top);
     while (lo < hi) {
-      const uint32_t mid = lo + (hi - lo) / 2;
-      if (bin(value_of(mid)) < b)
-        hi = mid;
-      else
-        lo = mid + 1;
+      const uint32_t step = (hi - lo) / 32 + 1, probe = min(lo + lane * step, hi);
+      const uint32_t below = __ballot_sync(0xffffffffu, bin(value_of(probe)) < b);
+      if (below == 0) {
+        lo = min(lo + 31 * step, hi - 1) + 1;
+      } else {
+        const int at = __ffs(below) - 1;
+        hi = min(lo + at * step, hi);
+        if (at > 0) lo = min(lo + (at - 1) * step + 1, hi);
+      }
     }
     return value_of(hi);
   }
@@ -407,16 +423,27 @@ struct Row {
     }
   }
 
-  __device__ static float bin_weight(int i) {
-    return exp2f(-(static_cast<float>(i) + 0.5f) / kPerOctave);
+  // The weight of a bin's elements, relative to the largest: of its middle, or, as 16-bit logits are
+  // few in a bin or none, of the middle of those that it can hold.
+  __device__ float bin_weight(int i) const {
+    if (c_hi < 1e-30f) return exp2f(-(static_cast<float>(i) + 0.5f) / kPerOctave);
+    const float scale = c_hi * kPerOctave, upper = top - static_cast<float>(i) / scale;
+    float z = upper - 0.5f / scale;
+    if constexpr (TYPE != kFp32) {
+      constexpr uint32_t kBelow = TYPE == kBf16 ? 0xFFFFu : 0x1FFFu;  // the bits that fp32 has below
+      const uint32_t u = order_of(upper), l = order_of(upper - 1.f / scale);
+      const uint32_t high = u & 0x80000000u ? u & ~kBelow : ((u + 1) & ~kBelow) - 1;
+      const uint32_t low = l & 0x80000000u ? (l + kBelow) & ~kBelow : l | kBelow;
+      if (low <= high) z = 0.5f * (value_of(low) + value_of(high));
+    }
+    return exp2f((z - top) * c_hi);
   }
 
   // In the first block: the bins [s.bins[0], s.bins[1]] in which the cut must lie: the one that
   // holds the k-th element, or, with p < 1, those where the weight before an element can
   // reach p of the sum over the first k. A bin's weight is known from its count to half a
-  // bin's width, 0.55 %; two such sums are compared, and `slack` is more than both errors.
-  __device__ void bracket(uint64_t k, float p) {
-    constexpr float slack = 0.016f;
+  // bin's width, 0.55 %; two such sums are compared, and kSureSlack is more than both errors.
+  __device__ void bracket(uint64_t k, float p, float slack = kSureSlack) {
     if (rank == 0) {
       constexpr int kEach = (kBins + kThreadsS - 1) / kThreadsS;
       const int b = min(static_cast<int>(threadIdx.x) * kEach, kBins), b_end = min(b + kEach, kBins);
@@ -531,6 +558,31 @@ struct Row {
     sync();
   }
 
+  // Groups that are looked at again once a pass is over, by as many threads as there are: in the pass a
+  // warp would go through the code for each value of a few of its lanes.
+  __device__ void clear_notes() {
+    if (threadIdx.x == 0) s.owned = s.noted = 0;
+    __syncthreads();
+  }
+  __device__ __forceinline__ void note(uint32_t* notes, int at) {
+    const uint32_t n = atomicAdd(&s.noted, 1u);
+    if (n < kNotes) notes[n] = at;
+  }
+  // f(index, value) of the groups noted; s.owned is more than kList where they were too many.
+  template <class F>
+  __device__ __forceinline__ void look_again(const uint32_t* notes, F f) {
+    __syncthreads();
+    const uint32_t n = s.noted;
+    if (n > kNotes && threadIdx.x == 0) s.owned = kList + 1;
+    for (uint32_t i = threadIdx.x; i < (n <= kNotes ? n : 0); i += kThreadsS) {
+      const int at = notes[i];
+      float v[8];
+      unpack8<TYPE>(any_group(at), v);
+#pragma unroll 1
+      for (int e = 0; e < 8; ++e) f(at - shift + e, v[e]);
+    }
+  }
+
   // Notes a place, in this block's s.heft.
   __device__ __forceinline__ void own(uint64_t place) {
     const uint32_t n = atomicAdd(&s.owned, 1u);
@@ -562,7 +614,7 @@ struct Row {
     const bool weigh = mass != kAll;
     uint64_t none = 0;
     while (!listed) {
-      while (n > kList) {
+      while (n > kList && hi - lo > 1) {
         const uint64_t mid = lo + (hi - lo) / 2;
         uint64_t c = 0, m = 0;
         each(place_value(mid), [&](int i, float v) {
@@ -611,7 +663,10 @@ struct Row {
                     static_cast<unsigned long long>(s.heft[i]));
         }
       }
-      if (threadIdx.x < a.cluster && a.cluster > 1) *of_block(&s.cut, threadIdx.x) = s.cut;
+      if (threadIdx.x < a.cluster && a.cluster > 1) {
+        *of_block(&s.cut, threadIdx.x) = s.cut;
+        *of_block(&s.cut_mass, threadIdx.x) = s.cut_mass;
+      }
     }
     sync();
     return s.cut;
@@ -638,21 +693,54 @@ struct Row {
   // weight lies. s.kept is what is at or above it, unless `moved`.
   template <bool FAR>
   __device__ uint64_t cut_by_mass(uint64_t k, float p, uint64_t floor, uint64_t heaviest, bool& moved) {
-    bracket(k, p);
-    const float above = above_bin(s.bins[0]), least = floor > 0 ? place_value(floor) : -INFINITY;
+    const float least = floor > 0 ? place_value(floor) : -INFINITY;
     const uint32_t least_index = place_last(floor);
-    clear_kept();
-    uint64_t all = 0, sum = 0;
-    each_kept(least, [&](int i, float v) {
-      uint64_t w = weight<FAR>(v, s.table);
-      w = v > least || (v == least && static_cast<uint32_t>(i) <= least_index) ? w : 0;
-      all += w;
-      w = v >= above ? w : 0;
-      sum += w;
-      return w;
-    });
-    reduce<false>(all, sum);
-    const uint64_t mass = share_of(all, p);
+    // The bins' middles are nearer to the truth than they have to be: first a bracket that is likely to
+    // hold the cut, which the exact sums confirm or refute.
+    for (float slack = kLikelySlack;; slack = kSureSlack) {
+      bracket(k, p, slack);
+      const float above = above_bin(s.bins[0]), lower = fmaxf(above_bin(s.bins[1] + 1), least);
+      clear_kept();
+      clear_notes();
+      uint64_t all = 0, none = 0;
+      uint32_t* notes = reinterpret_cast<uint32_t*>(s.list);
+      bool hit = false;
+      each_kept(
+          least,
+          [&](int i, float v) {
+            uint64_t w = weight<FAR>(v, s.table);
+            if (floor > 0) w = v > least || (v == least && static_cast<uint32_t>(i) <= least_index) ? w : 0;
+            all += w;
+            hit |= v >= lower && !(v >= above);
+            return v >= above ? w : 0;
+          },
+          [&](int at) {
+            if (hit && at < last) note(notes, at);
+            hit = false;
+          });
+      look_again(notes, [&](int i, float v) {
+        if (v >= lower && !(v >= above) && !(v == least && static_cast<uint32_t>(i) > least_index))
+          own(place_of(v, i));
+      });
+      uint64_t sum = s.kept[warp][lane];
+      reduce<false>(all, sum);
+      const uint64_t mass = share_of(all, p), n = gather(none);
+      const uint64_t lo = static_cast<uint64_t>(order_of(lower)) << 32;
+      const uint64_t hi = s.bins[0] == 0 ? kAll : static_cast<uint64_t>(order_of(above)) << 32;
+      const bool sure = slack == kSureSlack;
+      if (sum < mass && n <= kList) {
+        const uint64_t cut =
+            cut_between<FAR>(floor > lo ? floor : lo, hi, n, true, kAll, mass, 0, sum, moved);
+        if (sure || s.cut_mass >= mass) return cut;
+      } else if (sure) {
+        return narrow_cut<FAR>(above, least, least_index, floor, mass, sum, heaviest, moved);
+      }
+    }
+  }
+  // The same where the bracket holds too many: once more, from the weight above it.
+  template <bool FAR>
+  __device__ uint64_t narrow_cut(float above, float least, uint32_t least_index, uint64_t floor, uint64_t mass,
+                                 uint64_t sum, uint64_t heaviest, bool& moved) {
     narrow(mass - sum, heaviest);
     const float upper = above_bin(s.bins[0]), lower = fmaxf(above_bin(s.bins[1] + 1), least);
     const uint64_t lo = static_cast<uint64_t>(order_of(lower)) << 32;
@@ -663,15 +751,12 @@ struct Row {
     each(lower, [&](int i, float v) {
       if (v < lower || v >= above) return;
       if (v == least && static_cast<uint32_t>(i) > least_index) return;
-      if (v >= upper) {
-        const uint64_t w = weight<FAR>(v, s.table);
-        more += w;
-        const int part = (i + shift - first) / a.part;
-        atomicAdd(reinterpret_cast<unsigned long long*>(&s.kept[warp][part]), static_cast<unsigned long long>(w));
-      } else {
+      if (v >= upper)
+        more += weight<FAR>(v, s.table);
+      else
         own(place_of(v, i));
-      }
     });
+    moved |= true;  // s.kept lacks these
     const uint64_t n = gather(more);
     return cut_between<FAR>(floor > lo ? floor : lo, hi, n, n <= kList, kAll, mass, 0, sum + more, moved);
   }
@@ -805,14 +890,18 @@ struct Row {
     const float edge = cut > 0 ? place_value(cut) : -INFINITY;
     const uint32_t edge_index = place_last(cut);
     clear_kept();
+    const auto nothing_more = [](int) {};
     if (cut == 0 && least == 0) {
-      each_kept(-INFINITY, [&](int, float v) { return weight<FAR>(v, s.table); });
+      each_kept(-INFINITY, [&](int, float v) { return weight<FAR>(v, s.table); }, nothing_more);
       return;
     }
-    each_kept(fmaxf(low, edge), [&](int i, float v) {
-      const uint64_t w = weight<FAR>(v, s.table);
-      return (v > edge || (v == edge && static_cast<uint32_t>(i) <= edge_index)) && w >= least ? w : 0;
-    });
+    each_kept(
+        fmaxf(low, edge),
+        [&](int i, float v) {
+          const uint64_t w = weight<FAR>(v, s.table);
+          return (v > edge || (v == edge && static_cast<uint32_t>(i) <= edge_index)) && w >= least ? w : 0;
+        },
+        nothing_more);
   }
   // Draws from them.
   template <bool FAR>
@@ -982,10 +1071,11 @@ struct Row {
     uint64_t* list = of_block(s.list, 0);
     const float shift_by = top * c_hi;
     float sum = 0.f;
-    each_raw([&](int, int i, const Raw8<TYPE>& raw) {
-      float v[8];
+    clear_notes();
+    uint32_t* notes = reinterpret_cast<uint32_t*>(s.item);
+    each_raw([&](int, int at, const Raw8<TYPE>& raw) {
       if (weigh) {
-        float w[8];
+        float v[8], w[8];
         unpack8<TYPE>(raw, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -994,16 +1084,13 @@ struct Row {
         }
         sum += ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
       }
-      if (largest<TYPE>(raw) >= threshold) {
-        unpack8<TYPE>(raw, v);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          if (v[e] >= threshold && v[e] != -INFINITY) {
-            const uint32_t n = atomicAdd(&s.owned, 1u);
-            if (n < room) list[rank * room + n] = place_of(v[e], i + e);
-            if (n < kList) s.heft[n] = place_of(v[e], i + e);
-          }
-        }
+      if (largest<TYPE>(raw) >= threshold && at < last) note(notes, at);
+    });
+    look_again(notes, [&](int i, float v) {
+      if (v >= threshold && v != -INFINITY) {
+        const uint32_t n = atomicAdd(&s.owned, 1u);
+        if (n < room) list[rank * room + n] = place_of(v, i);
+        if (n < kList) s.heft[n] = place_of(v, i);
       }
     });
     uint64_t rest = 0;
@@ -1175,14 +1262,10 @@ struct Row {
     return kDone;
   }
   // Whether the token was drawn from the elements that reach `threshold`.
-  __device__ bool from_list(float threshold, bool again, int64_t top_k, float p, uint64_t heaviest, uint64_t least,
+  __device__ bool from_list(float threshold, int64_t top_k, float p, uint64_t heaviest, uint64_t least,
                             float u, int64_t* token) {
     const bool by_k = top_k < a.V;
     const uint64_t k = by_k ? top_k : kAll;
-    if (again) {
-      if (threadIdx.x == 0) s.owned = 0;
-      __syncthreads();
-    }
     const int n = list_above(threshold, !by_k, heaviest);
     if (n > kList) return false;
     int verdict = kTooShort;
@@ -1267,13 +1350,13 @@ struct Row {
     if (list) {
       if (near || a.V <= kList / a.cluster) {
         if (!near) threshold = -INFINITY;
-        if (from_list(threshold, false, top_k, p, heaviest, least, u, token)) return;
+        if (from_list(threshold, top_k, p, heaviest, least, u, token)) return;
       }
       if (by_k) {
         histogram();
         bracket(wanted, 1.f);
         threshold = above_bin(s.bins[0] + 1);
-        if (from_list(threshold, true, top_k, p, heaviest, least, u, token)) return;
+        if (from_list(threshold, top_k, p, heaviest, least, u, token)) return;
       }
     }
     if (far)
@@ -1290,7 +1373,6 @@ __global__ void __launch_bounds__(kThreadsS, kPerSm) sample_kernel(const __grid_
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
   for (int i = threadIdx.x; i < kNearBins; i += kThreadsS) s.near_hist[i] = 0;
-  if (threadIdx.x == 0) s.owned = 0;
   griddep_wait();
   const int row = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
   const uint8_t* z = static_cast<const uint8_t*>(a.logits) + row * a.ld * type_size(TYPE);

@@ -75,7 +75,7 @@ def backward(lib, p, dy=AT, h=AT, w=AT, rstd=AT, dh=AT, seed=None, dx=AT, dr=Non
 
 
 NORM_BAD = [(dict(M=-1), INVALID), (dict(H=0), INVALID), (dict(H=32769), UNSUPPORTED),
-            (dict(M=1 << 31), UNSUPPORTED), (dict(dtype=3), INVALID), (dict(dtype=-1), INVALID),
+            (dict(M=(1 << 30) + 1), UNSUPPORTED), (dict(dtype=3), INVALID), (dict(dtype=-1), INVALID),
             (dict(dtype=0, stream_dtype=1), INVALID), (dict(dtype=2, stream_dtype=0), INVALID),
             (dict(dtype=1, weight_dtype=0), INVALID), (dict(ld_x=63), INVALID), (dict(ld_res=-64), INVALID),
             (dict(ld_h=8), INVALID), (dict(ld_y=63), INVALID), (dict(eps=-1e-6), INVALID),
