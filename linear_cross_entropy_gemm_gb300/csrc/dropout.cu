@@ -24,7 +24,7 @@ struct DropArgs {
 // loads are in flight together, and the generator's keys are made once for all of them.
 constexpr int kRows = 4, kThreads = 256;
 
-template <int XT, int YT, bool WIDE>
+template <int XT, int YT>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant__ DropArgs a, uint32_t across) {
   griddep_launch();
   griddep_wait();
@@ -42,8 +42,8 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
     const int64_t row = first + i * blockDim.y;
     rr[i] = {};
     if (row >= a.M) break;
-    xr[i] = load8<XT, WIDE>(row_of(a.x, row, a.ld_x, type_size(XT)), col, a.H);
-    if (a.r) rr[i] = load8<YT, WIDE>(row_of(a.r, row, a.ld_r, type_size(YT)), col, a.H);
+    xr[i] = load8<XT, true>(row_of(a.x, row, a.ld_x, type_size(XT)), col, a.H);
+    if (a.r) rr[i] = load8<YT, true>(row_of(a.r, row, a.ld_r, type_size(YT)), col, a.H);
   }
   Keys keys;
   if (a.drop.threshold != 0) keys = dropout_keys(a.drop);
@@ -60,13 +60,68 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
       for (int e = 0; e < 4; ++e)
         f32x2_split(fadd2(f32x2(v[2 * e], v[2 * e + 1]), pair_of(rr[i], e)), v[2 * e], v[2 * e + 1]);
     }
-    store8<YT, WIDE>(static_cast<uint8_t*>(a.y) + row * a.ld_y * type_size(YT), col, a.H, v);
+    store8<YT, true>(static_cast<uint8_t*>(a.y) + row * a.ld_y * type_size(YT), col, a.H, v);
+  }
+}
+
+// Rows off the 16-byte boundaries go value by value: a warp takes 256 columns of kRows rows, its
+// accesses next to each other; a lane makes the random bits of a group, and takes those of the columns
+// that it moves.
+template <int XT, int YT>
+__global__ void __launch_bounds__(kThreads)
+    dropout_strided_kernel(const __grid_constant__ DropArgs a, uint32_t segments, int64_t warps) {
+  __shared__ uint4 s_bits[kThreads / 32][32];
+  griddep_launch();
+  griddep_wait();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + warp;
+  if (id >= warps) return;
+  const int64_t down = id / segments, segment = id - down * segments, col = segment * 256 + lane;
+  const int left = static_cast<int>(a.H - segment * 256 < 256 ? a.H - segment * 256 : 256) - lane;
+  const uint32_t group = static_cast<uint32_t>(segment) * 32 + lane;
+  const uint16_t* bits = reinterpret_cast<const uint16_t*>(s_bits[warp]) + lane;
+  Keys keys;
+  if (a.drop.threshold != 0) keys = dropout_keys(a.drop);
+#pragma unroll 2
+  for (int i = 0; i < kRows; ++i) {
+    const int64_t row = down * kRows + i;
+    if (row >= a.M) return;
+    const uint8_t* x = static_cast<const uint8_t*>(a.x) + (row * a.ld_x + col) * type_size(XT);
+    const uint8_t* r = static_cast<const uint8_t*>(a.r) + (row * a.ld_r + col) * type_size(YT);
+    uint8_t* y = static_cast<uint8_t*>(a.y) + (row * a.ld_y + col) * type_size(YT);
+    float v[8], u[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      v[e] = 32 * e < left ? load_value<XT>(x, 32 * e) : 0.f;
+      u[e] = 0.f;
+    }
+    if (a.r) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = 32 * e < left ? load_value<YT>(r, 32 * e) : 0.f;
+    }
+    if (a.drop.threshold != 0) {
+      s_bits[warp][lane] = drop_bits(a.drop, keys, static_cast<uint32_t>(row), group);
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[e] = bits[32 * e] >= a.drop.threshold ? v[e] * a.drop.scale : 0.f;
+      __syncwarp();
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (32 * e < left) store_value<YT>(y, 32 * e, a.r ? v[e] + u[e] : v[e]);
   }
 }
 
 template <int XT, int YT>
 cudaError_t launch_drop(const DropArgs& a, bool wide, cudaStream_t st) {
   const int64_t groups = (a.H + 7) / 8;
+  if (!wide) {
+    const int64_t segments = (groups + 31) / 32, warps = segments * ((a.M + kRows - 1) / kRows);
+    const int64_t blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
+    if (blocks > 0x7FFFFFFF) return cudaErrorInvalidValue;
+    return launch_dependent(dropout_strided_kernel<XT, YT>, dim3(static_cast<unsigned>(blocks)), kThreads, 0, 1, st,
+                            a, static_cast<uint32_t>(segments), warps);
+  }
   // Blocks across a row, all of nearly the same width.
   const int64_t across = (groups + kThreads - 1) / kThreads;
   const int64_t even = (groups + across - 1) / across;
@@ -74,8 +129,7 @@ cudaError_t launch_drop(const DropArgs& a, bool wide, cudaStream_t st) {
   const unsigned y = kThreads / x;
   const int64_t down = (a.M + y * kRows - 1) / (y * kRows);
   if (across > 0x7FFFFFFF / down) return cudaErrorInvalidValue;
-  auto kernel = wide ? dropout_kernel<XT, YT, true> : dropout_kernel<XT, YT, false>;
-  return launch_dependent(kernel, dim3(static_cast<unsigned>(across * down)), dim3(x, y), 0, 1, st, a,
+  return launch_dependent(dropout_kernel<XT, YT>, dim3(static_cast<unsigned>(across * down)), dim3(x, y), 0, 1, st, a,
                           static_cast<uint32_t>(across));
 }
 

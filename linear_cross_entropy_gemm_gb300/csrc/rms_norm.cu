@@ -85,7 +85,7 @@ namespace {
 // The registers of a row's threads, its ring and the time of its one sum decide. 8192 x 4096: 2 groups
 // of 256 threads with 128 registers and two blocks on an SM 42.9 us, 3 blocks with 80 registers 52,
 // 4 groups 69, 1 group of 512 threads 56.
-GradShape grad_shape(int64_t M, int64_t H, int x_size, int stream_size) {
+GradShape grad_shape(int64_t M, int64_t H, int x_size, int stream_size, bool wide) {
   constexpr size_t kMemory = 220 * 1024;
   const int groups = static_cast<int>((H + 7) / 8);
   const auto with = [&](int nv) {
@@ -99,7 +99,11 @@ GradShape grad_shape(int64_t M, int64_t H, int x_size, int stream_size) {
     return s;
   };
   GradShape s = with(8);
-  if (groups <= 256) {
+  if (!wide) {
+    // Value by value, many threads carry the accesses.
+    s = with(groups <= 1024 ? 1 : groups <= 2048 ? 2 : 4);
+    s.blocks = 1024 / (s.threads * s.rows);
+  } else if (groups <= 256) {
     s = with(1);
   } else {
     const GradShape two = with(2), four = with(4);
@@ -112,13 +116,14 @@ GradShape grad_shape(int64_t M, int64_t H, int x_size, int stream_size) {
   s.blocks = static_cast<int>(need < all ? need : all);
   return s;
 }
-GradShape grad_shape(const flce_rms_norm_params_t* p) {
-  return grad_shape(p->M, p->H, type_size(p->dtype), type_size(p->stream_dtype));
+GradShape grad_shape(const flce_rms_norm_params_t* p, bool wide) {
+  return grad_shape(p->M, p->H, type_size(p->dtype), type_size(p->stream_dtype), wide);
 }
 
 size_t grad_workspace(const flce_rms_norm_params_t* p) {
-  const GradShape s = grad_shape(p);
-  return static_cast<size_t>(s.blocks) * p->H * sizeof(float) + kAlign;
+  // Whichever of the two the tensors' alignment asks for.
+  const int wide = grad_shape(p, true).blocks, narrow = grad_shape(p, false).blocks;
+  return static_cast<size_t>(wide > narrow ? wide : narrow) * p->H * sizeof(float) + kAlign;
 }
 
 }  // namespace
@@ -214,7 +219,6 @@ flce_status_t flce_rms_norm_backward(const flce_rms_norm_params_t* p, const void
   int sms = 0;
   const flce_status_t ds = device_info(&sms);
   if (ds != FLCE_OK) return ds;
-  const GradShape s = grad_shape(p);
   Carver cv(workspace, workspace_bytes);
   NormGradArgs a;
   a.dy = dy;
@@ -236,6 +240,7 @@ flce_status_t flce_rms_norm_backward(const flce_rms_norm_params_t* p, const void
                    rows16(h, a.ld_h, p->M, p->stream_dtype) &&
                    rows16(dh, a.ld_dh, p->M, p->stream_dtype) && aligned_to(weight, 16) &&
                    aligned_to(dx, 16) && aligned_to(dresidual, 16);
+  const GradShape s = grad_shape(p, wide);
   const bool stream_fp32 = p->stream_dtype == FLCE_DTYPE_FP32;
   cudaError_t e = p->dtype == FLCE_DTYPE_BF16   ? norm_grad_bf16(a, stream_fp32, wide, s, st)
                   : p->dtype == FLCE_DTYPE_FP16 ? norm_grad_fp16(a, stream_fp32, wide, s, st)

@@ -15,7 +15,6 @@
 namespace flce {
 namespace {
 
-
 __device__ __forceinline__ uint2 to_e4m3(const float* y, float inv) {
   uint32_t q[4];
 #pragma unroll
@@ -52,7 +51,7 @@ __device__ __forceinline__ void store_e4m3(uint8_t* row, int j, int T, int t, in
 // blockDim.x threads for a row, blockDim.y rows (one, unless a warp holds a row); a thread
 // holds NV groups of 8 columns.
 template <int XT, int ST, int NV, Layout L, bool Q>
-__global__ void __launch_bounds__(kRowThreads) norm_kernel(const __grid_constant__ NormArgs a) {
+__global__ void __launch_bounds__(L == kStrided ? 1024 : kRowThreads) norm_kernel(const __grid_constant__ NormArgs a) {
   __shared__ float s_sum[32], s_max[32];
   extern __shared__ __align__(16) uint8_t smem[];  // kStrided: the dropout's random bits
   griddep_launch();
@@ -163,10 +162,11 @@ cudaError_t launch_q(const NormArgs& a, dim3 grid, dim3 block, size_t smem, cuda
 }
 template <int XT, int ST, Layout L>
 cudaError_t launch_nv(const NormArgs& a, int nv, dim3 grid, dim3 block, size_t smem, cudaStream_t st) {
+  if constexpr (L == kWide)
+    if (nv == 8) return launch_q<XT, ST, 8, L>(a, grid, block, smem, st);
   return nv == 1   ? launch_q<XT, ST, 1, L>(a, grid, block, smem, st)
          : nv == 2 ? launch_q<XT, ST, 2, L>(a, grid, block, smem, st)
-         : nv == 4 ? launch_q<XT, ST, 4, L>(a, grid, block, smem, st)
-                   : launch_q<XT, ST, 8, L>(a, grid, block, smem, st);
+                   : launch_q<XT, ST, 4, L>(a, grid, block, smem, st);
 }
 template <int XT, int ST>
 cudaError_t launch_norm(const NormArgs& a, bool wide, cudaStream_t st) {
@@ -178,8 +178,9 @@ cudaError_t launch_norm(const NormArgs& a, bool wide, cudaStream_t st) {
   // 8; 65536 x 256 20.5 us with 1, 24.4 with 2. Value by value the accesses are many and small,
   // and more threads carry them; so do a few rows.
   int nv = groups <= 64 ? 1 : groups <= 256 ? 2 : groups <= (XT == kFp32 ? 2048 : 1024) ? 4 : 8;
-  if (layout == kStrided || (a.M <= 256 && layout == kWide))
+  if (layout == kWide && a.M <= 256)
     nv = groups <= 512 ? 1 : groups <= 1024 ? 2 : groups <= (XT == kFp32 ? 2048 : 1024) ? 4 : 8;
+  if (layout == kStrided) nv = groups <= 1024 ? 1 : groups <= 2048 ? 2 : 4;
   if (layout == kNarrow) nv = 8;
   const int threads = ((groups + nv - 1) / nv + 31) / 32 * 32;
   const int rows = threads == 32 ? kBlockRows : 1;

@@ -31,7 +31,7 @@ __device__ __forceinline__ void copies_wait() {
 // blockDim.x threads for a row, blockDim.y rows at a time (one, unless a warp holds a row); a thread
 // holds NV groups of 8 columns.
 template <int XT, int ST, int NV, Layout L, bool DROP>
-__global__ void __launch_bounds__(NV == 1 ? 256 : kRowThreads, NV == 1 ? 4 : 1)
+__global__ void __launch_bounds__(L == kStrided ? 1024 : NV == 1 ? 256 : kRowThreads, L == kWide && NV == 1 ? 4 : 1)
     norm_grad_kernel(const __grid_constant__ NormGradArgs a) {
   constexpr bool kRing = L == kWide && grad_has_ring(NV, type_size(ST));
   constexpr int kStages = grad_stages(NV);
@@ -42,8 +42,14 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : kRowThreads, NV == 1 ? 4 : 1)
   griddep_wait();
   const int T = blockDim.x, t = threadIdx.x, n = a.H;
   const int first = blockIdx.x * blockDim.y + threadIdx.y, step = gridDim.x * blockDim.y;
+  // The generator's keys: value by value, in shared memory, as the registers are few.
+  __shared__ Keys s_keys;
   Keys keys;
-  if constexpr (DROP) keys = dropout_keys(a.drop);
+  if constexpr (DROP && L == kWide) keys = dropout_keys(a.drop);
+  if constexpr (DROP && L != kWide) {
+    if (threadIdx.y * T + t == 0) s_keys = dropout_keys(a.drop);
+    __syncthreads();
+  }
   Raw8<XT> wr[NV];
   uint64_t acc[NV * 4];  // pairs of columns
 #pragma unroll
@@ -161,7 +167,7 @@ __global__ void __launch_bounds__(NV == 1 ? 256 : kRowThreads, NV == 1 ? 4 : 1)
       uint4* made = reinterpret_cast<uint4*>(smem) + threadIdx.y * (NV * T);
       T == 32 ? __syncwarp() : __syncthreads();
 #pragma unroll
-      for (int j = 0; j < NV; ++j) made[j * T + t] = drop_bits(a.drop, keys, row, j * T + t);
+      for (int j = 0; j < NV; ++j) made[j * T + t] = drop_bits(a.drop, s_keys, row, j * T + t);
       T == 32 ? __syncwarp() : __syncthreads();
       bits = reinterpret_cast<const uint16_t*>(made);
     }
@@ -220,7 +226,9 @@ template <int XT, int ST, int NV, bool DROP>
 cudaError_t launch_nv(const NormGradArgs& a, bool wide, const GradShape& s, cudaStream_t st) {
   const dim3 grid(static_cast<unsigned>(s.blocks));
   const dim3 block(static_cast<unsigned>(s.threads), static_cast<unsigned>(s.rows));
-  auto kernel = wide ? norm_grad_kernel<XT, ST, NV, kWide, DROP> : norm_grad_kernel<XT, ST, NV, kStrided, DROP>;
+  auto kernel = norm_grad_kernel<XT, ST, NV, kWide, DROP>;
+  if constexpr (NV <= 4)
+    if (!wide) kernel = norm_grad_kernel<XT, ST, NV, kStrided, DROP>;
   const size_t smem = wide ? grad_ring(s, type_size(XT), type_size(ST))
                       : DROP ? static_cast<size_t>(NV) * s.threads * s.rows * 16 : 0;
   if (smem > 48 * 1024) {

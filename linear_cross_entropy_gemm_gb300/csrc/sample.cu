@@ -933,56 +933,56 @@ struct Row {
       all += s.peers[turn][i][0];
     }
     turn ^= 1;
-    const uint64_t target = target_of(all, u);
-    if (target < before || target >= before + sum) return;
-    // This warp's stretch holds it, and this part of it.
-    const uint64_t part_before = before + scan - part;
-    const uint32_t holds = __ballot_sync(0xffffffffu, target >= part_before && target < part_before + part);
-    const int which = __ffs(holds) - 1;
-    before = __shfl_sync(0xffffffffu, part_before, which);
-    const int end = min(first + (which + 1) * a.part, last);
-    for (int at = first + which * a.part; at < end; at += 256) {
-      const int i = at + lane * 8 - shift;
-      float v[8];
-      unpack8<TYPE>(group(at + lane * 8), v);
-      uint64_t w[8], mine = 0;
+    const uint64_t target = target_of(all, u), part_before = before + scan - part;
+    if (target >= part_before && target < part_before + part) {
+      s.x_bin = warp * kParts + lane;
+      s.x_before = part_before;
+    }
+    if (!__syncthreads_or(target >= before && target < before + sum)) return;
+    // This block holds it, in this part of a warp's stretch.
+    const int stretch_begin = (rank * kWarpsS + s.x_bin / kParts) * a.stretch;
+    const int begin = stretch_begin + s.x_bin % kParts * a.part;
+    const int end = min(min(begin + a.part, stretch_begin + a.stretch), a.V + shift);
+    before = s.x_before;
+    constexpr int kMine = 4;
+    for (int at = begin; at < end; at += kThreadsS * kMine) {
+      const int i = at + static_cast<int>(threadIdx.x) * kMine - shift;
+      uint64_t w[kMine], mine = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        w[e] = weight<FAR>(v[e], s.table);
-        const bool in = v[e] >= low && (v[e] > edge || (v[e] == edge && static_cast<uint32_t>(i + e) <= edge_index)) && w[e] >= least;
+      for (int e = 0; e < kMine; ++e) {
+        const bool on = i + e >= 0 && i + e + shift < end;
+        const float v = on ? load_value<TYPE>(z, i + e) : -INFINITY;
+        w[e] = weight<FAR>(v, s.table);
+        const bool in =
+            on && v >= low && (v > edge || (v == edge && static_cast<uint32_t>(i + e) <= edge_index)) && w[e] >= least;
         w[e] = in ? w[e] : 0;
         mine += w[e];
       }
-      uint64_t scan = mine;
+      uint32_t none, none_all;
+      uint64_t c, total;
+      this->scan(0, mine, none, c, none_all, total);
+      c += before;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t x = __shfl_up_sync(0xffffffffu, scan, o);
-        if (lane >= o) scan += x;
+      for (int e = 0; e < kMine; ++e) {
+        if (target >= c && target < c + w[e]) *token = i + e;
+        c += w[e];
       }
-      uint64_t c = before + scan - mine;
-      if (target >= c && target < c + mine) {
-        int e = 0;
-#pragma unroll
-        for (int k = 0; k < 7; ++k) {
-          if (e == k && target >= c + w[k]) {
-            c += w[k];
-            e = k + 1;
-          }
-        }
-        *token = i + e;
-      }
-      before += __shfl_sync(0xffffffffu, scan, 31);
-      if (target < before) return;
+      before += total;
     }
   }
 
-  // Everything from passes over the row.
-  template <bool FAR>
-  __device__ void from_row(int64_t top_k, float p, uint64_t heaviest, uint64_t least, float low, float u,
-                           int64_t* token) {
-    __syncthreads();
+  __device__ void fill_table() {
     for (int i = threadIdx.x; i < kTable; i += kThreadsS) s.table[i] = kExp2.v[i];
-    __syncthreads();
+  }
+  // Everything from passes over the row. by_list: the list has had the table's place.
+  template <bool FAR>
+  __device__ void from_row(bool by_list, int64_t top_k, float p, uint64_t heaviest, uint64_t least, float low,
+                           float u, int64_t* token) {
+    if (by_list) {
+      __syncthreads();
+      fill_table();
+      __syncthreads();
+    }
     const bool by_k = top_k < a.V, by_p = p < 1.f;
     uint64_t cut = 0;
     if (by_k || by_p) histogram();
@@ -1316,6 +1316,7 @@ struct Row {
     const int loads = min(a.cluster * kThreadsS * kAhead, a.V / 8);
     const int wanted = by_k ? static_cast<int>(min(top_k, static_cast<int64_t>(kMostK))) : min(loads / 2, kWanted);
     const bool near = list && wanted > 0 && loads >= 2 * wanted;
+    if (!list && !greedy) fill_table();
     float m[kAhead];
 #pragma unroll
     for (int g = 0; g < kAhead; ++g) m[g] = -INFINITY;
@@ -1343,8 +1344,8 @@ struct Row {
     lowest = far ? -INFINITY : top - 47.f / c_hi;
     // min_p above 1 keeps the largest. Elements well below the limit need no weight.
     const float share = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;
-    const uint64_t heaviest = any_weight(top, kExp2.v);
-    const uint64_t least = share < 1.f ? times<true>(heaviest, share) : heaviest;
+    const uint64_t heaviest = share > 0.f || by_p ? any_weight(top, kExp2.v) : 0;
+    const uint64_t least = share < 1.f ? times<true>(heaviest, share) : heaviest;  // 0 where all weigh enough
     const float low =
         share > 0.f && c_hi > 1e-30f ? top + (log2f(share) - 0.01f) / c_hi - fabsf(top) * 1e-6f : -INFINITY;
     if (list) {
@@ -1360,9 +1361,9 @@ struct Row {
       }
     }
     if (far)
-      from_row<true>(top_k, p, heaviest, least, low, u, token);
+      from_row<true>(list, top_k, p, heaviest, least, low, u, token);
     else
-      from_row<false>(top_k, p, heaviest, least, low, u, token);
+      from_row<false>(list, top_k, p, heaviest, least, low, u, token);
   }
 };
 
