@@ -137,6 +137,14 @@ __device__ __forceinline__ uint32_t place_last(uint64_t place) {
   return 0xFFFFFFFFu - static_cast<uint32_t>(place);
 }
 
+// To a sum of 64 bits in shared memory, in two halves: there is no such instruction for the whole.
+__device__ __forceinline__ void add64(uint64_t* sum, uint64_t v) {
+  uint32_t* half = reinterpret_cast<uint32_t*>(sum);
+  const uint32_t low = static_cast<uint32_t>(v), old = atomicAdd(half, low);
+  const uint32_t high = static_cast<uint32_t>(v >> 32) + (old + low < old ? 1 : 0);
+  if (high != 0) atomicAdd(half + 1, high);
+}
+
 __device__ __forceinline__ uint64_t shfl64(uint64_t v, int mask) {
   return __shfl_xor_sync(0xffffffffu, v, mask);
 }
@@ -229,6 +237,8 @@ struct Row {
   float top, c_hi, c_lo, lowest;
   int octave;         // weights are 2^(z log2(e) / T - octave)
   bool far;           // z log2(e) / T is too large for weight_near
+  int index_bits;     // of the largest index,
+  uint32_t place_mask;  //   all of them set
 
   __device__ void sync() const {
     if (a.cluster == 1)
@@ -448,10 +458,13 @@ struct Row {
       constexpr int kEach = (kBins + kThreadsS - 1) / kThreadsS;
       const int b = min(static_cast<int>(threadIdx.x) * kEach, kBins), b_end = min(b + kEach, kBins);
       uint32_t n = 0;
-      float m = 0.f;
-      for (int i = b; i < b_end; ++i) {
-        n += s.hist[i];
-        m += static_cast<float>(s.hist[i]) * bin_weight(i);
+      float m = 0.f, in_bin[kEach];
+#pragma unroll
+      for (int j = 0; j < kEach; ++j) {
+        const uint32_t c = b + j < b_end ? s.hist[b + j] : 0;
+        in_bin[j] = c > 0 ? static_cast<float>(c) * bin_weight(b + j) : 0.f;
+        n += c;
+        m += in_bin[j];
       }
       uint32_t n_scan = n;
       float m_scan = m;
@@ -488,25 +501,33 @@ struct Row {
       if (n_before < k && k <= n_before + n) {
         uint32_t c = n_before;
         float x = m_before;
-        int i = b;
-        while (c + s.hist[i] < k) {
-          x += static_cast<float>(s.hist[i]) * bin_weight(i);
-          c += s.hist[i++];
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          const uint32_t h = b + j < b_end ? s.hist[b + j] : 0;
+          if (c < k && k <= c + h) {
+            if (p >= 1.f) s.bins[0] = s.bins[1] = b + j;
+            s.above = c;
+            s.within[0] = x;
+            s.within[1] = x + in_bin[j];
+          }
+          c += h;
+          x += in_bin[j];
         }
-        if (p >= 1.f) s.bins[0] = s.bins[1] = i;
-        s.above = c;
-        s.within[0] = x;
-        s.within[1] = x + static_cast<float>(s.hist[i]) * bin_weight(i);
       }
       __syncthreads();
       if (p < 1.f) {
         const float low = p * s.within[0] * (1.f - slack), high = p * s.within[1] * (1.f + slack);
         float x = m_before;
-        for (int i = b; i < b_end; ++i) {
-          x += static_cast<float>(s.hist[i]) * bin_weight(i);
-          if (x >= low) atomicMin(&s.bins[0], i);
-          if (x >= high) atomicMin(&s.bins[1], i);
+        int at_low = kBins, at_high = kBins;
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+          x += in_bin[j];
+          if (b + j >= b_end) continue;
+          if (x >= low) at_low = min(at_low, b + j);
+          if (x >= high) at_high = min(at_high, b + j);
         }
+        if (at_low < kBins) atomicMin(&s.bins[0], at_low);
+        if (at_high < kBins) atomicMin(&s.bins[1], at_high);
       }
     }
     share_bins();
@@ -574,11 +595,20 @@ struct Row {
     __syncthreads();
     const uint32_t n = s.noted;
     if (n > kNotes && threadIdx.x == 0) s.owned = kList + 1;
-    for (uint32_t i = threadIdx.x; i < (n <= kNotes ? n : 0); i += kThreadsS) {
-      const int at = notes[i];
-      float v[8];
-      unpack8<TYPE>(any_group(at), v);
+    const uint32_t end = n <= kNotes ? n : 0;
+    if (threadIdx.x >= end) return;
+    int next_at = notes[threadIdx.x];
+    Raw8<TYPE> next = any_group(next_at);
 #pragma unroll 1
+    for (uint32_t i = threadIdx.x; i < end; i += kThreadsS) {
+      const int at = next_at;
+      float v[8];
+      unpack8<TYPE>(next, v);
+      if (i + kThreadsS < end) {
+        next_at = notes[i + kThreadsS];
+        next = any_group(next_at);
+      }
+#pragma unroll
       for (int e = 0; e < 8; ++e) f(at - shift + e, v[e]);
     }
   }
@@ -691,9 +721,9 @@ struct Row {
 
   // The last place of those at or above `floor`, the k-th one's, before which less than p of their
   // weight lies. s.kept is what is at or above it, unless `moved`.
-  template <bool FAR>
+  template <bool FAR, bool FLOOR>
   __device__ uint64_t cut_by_mass(uint64_t k, float p, uint64_t floor, uint64_t heaviest, bool& moved) {
-    const float least = floor > 0 ? place_value(floor) : -INFINITY;
+    const float least = FLOOR ? place_value(floor) : -INFINITY;
     const uint32_t least_index = place_last(floor);
     // The bins' middles are nearer to the truth than they have to be: first a bracket that is likely to
     // hold the cut, which the exact sums confirm or refute.
@@ -709,7 +739,7 @@ struct Row {
           least,
           [&](int i, float v) {
             uint64_t w = weight<FAR>(v, s.table);
-            if (floor > 0) w = v > least || (v == least && static_cast<uint32_t>(i) <= least_index) ? w : 0;
+            if (FLOOR) w = v > least || (v == least && static_cast<uint32_t>(i) <= least_index) ? w : 0;
             all += w;
             hit |= v >= lower && !(v >= above);
             return v >= above ? w : 0;
@@ -719,7 +749,7 @@ struct Row {
             hit = false;
           });
       look_again(notes, [&](int i, float v) {
-        if (v >= lower && !(v >= above) && !(v == least && static_cast<uint32_t>(i) > least_index))
+        if (v >= lower && !(v >= above) && !(FLOOR && v == least && static_cast<uint32_t>(i) > least_index))
           own(place_of(v, i));
       });
       uint64_t sum = s.kept[warp][lane];
@@ -804,15 +834,26 @@ struct Row {
     }
   }
 
+  // A place without the bits in which no two differ: those that a 16-bit logit lacks, and those above
+  // the largest index. Rises with the places of elements.
+  __device__ __forceinline__ uint64_t key_of(uint64_t place) const {
+    constexpr int kLacks = TYPE == kBf16 ? 16 : TYPE == kFp16 ? 13 : 0;
+    const uint32_t order = static_cast<uint32_t>(place >> 32) >> kLacks, index = place_last(place);
+    return static_cast<uint64_t>(order) << index_bits | (place_mask - min(index, place_mask));
+  }
+
   // Among n items, with their weights in s.heft (not read with mass kAll), those in [lo, hi): s.cut is
   // the last place before which less than k and less than `mass` lie, above_n and above_m of them at or
   // above hi; s.cut_mass the weight up to it. lo, and all the weight, where the items end before both
-  // are reached. By bins of equal stretches of places, then those of one bin.
+  // are reached. By bins of equal stretches of keys, then those of one bin.
   __device__ void cut_items(const uint64_t* items, int n, uint64_t lo, uint64_t hi, uint64_t k, uint64_t mass,
                             uint64_t above_n, uint64_t above_m) {
     const bool weigh = mass != kAll;
+    // The ends need not be elements' places: outwards, to a logit's first and last key.
+    uint64_t key_lo = key_of(lo) >> index_bits << index_bits, key_hi = key_of(hi - 1) | place_mask;
+    ++key_hi;
     while (true) {
-      const int top_bit = 63 - __clzll(static_cast<long long>(hi - lo - 1 | 1));
+      const int top_bit = 63 - __clzll(static_cast<long long>(key_hi - key_lo - 1 | 1));
       const int down = max(0, top_bit + 1 - kItemBits);
       s.item_mass[threadIdx.x] = s.item_mass[threadIdx.x + kThreadsS] = 0;
       s.item_hist[threadIdx.x] = s.item_hist[threadIdx.x + kThreadsS] = 0;
@@ -822,13 +863,11 @@ struct Row {
       }
       __syncthreads();
       for (int i = threadIdx.x; i < n; i += kThreadsS) {
-        const uint64_t at = items[i];
-        if (at < lo || at >= hi) continue;
-        const int b = static_cast<int>((hi - 1 - at) >> down);
+        const uint64_t at = items[i], key = key_of(at);
+        if (at < lo || at >= hi || key < key_lo || key >= key_hi) continue;
+        const int b = static_cast<int>((key_hi - 1 - key) >> down);
         atomicAdd(&s.item_hist[b], 1u);
-        if (weigh)
-          atomicAdd(reinterpret_cast<unsigned long long*>(&s.item_mass[b]),
-                    static_cast<unsigned long long>(s.heft[i]));
+        if (weigh) add64(&s.item_mass[b], s.heft[i]);
       }
       __syncthreads();
       const int b = 2 * threadIdx.x;
@@ -853,13 +892,15 @@ struct Row {
       above_n = s.x_count;
       above_m = s.x_before;
       const uint32_t in_bin = s.item_hist[x];
-      hi -= static_cast<uint64_t>(x) << down;
-      if (hi - lo > 1ull << down) lo = hi - (1ull << down);
+      key_hi -= static_cast<uint64_t>(x) << down;
+      if (key_hi - key_lo > 1ull << down) key_lo = key_hi - (1ull << down);
       if (in_bin <= kFew) break;
       __syncthreads();
     }
-    for (int i = threadIdx.x; i < n; i += kThreadsS)
-      if (items[i] >= lo && items[i] < hi) s.few[atomicAdd(&s.few_n, 1u)] = static_cast<uint16_t>(i);
+    for (int i = threadIdx.x; i < n; i += kThreadsS) {
+      const uint64_t at = items[i], key = key_of(at);
+      if (at >= lo && at < hi && key >= key_lo && key < key_hi) s.few[atomicAdd(&s.few_n, 1u)] = static_cast<uint16_t>(i);
+    }
     __syncthreads();
     const uint32_t few = s.few_n;
     if (threadIdx.x < few) {
@@ -989,7 +1030,9 @@ struct Row {
     if (by_k) cut = cut_by_count(top_k);
     bool moved = false;
     if (by_k && by_p) histogram();  // its place has been in use
-    if (by_p) cut = cut_by_mass<FAR>(top_k, p, cut, heaviest, moved);
+    if (by_p)
+      cut = by_k ? cut_by_mass<FAR, true>(top_k, p, cut, heaviest, moved)
+                 : cut_by_mass<FAR, false>(top_k, p, 0, heaviest, moved);
     if (!by_p || least > 0 || moved) weigh_kept<FAR>(cut, least, low);
     draw<FAR>(cut, least, low, u, token);
   }
@@ -1061,6 +1104,29 @@ struct Row {
     turn ^= 1;
     threshold = fmaxf(one, each_one);
     return static_cast<uint32_t>(best);
+  }
+
+  // 2^((z - top) log2(e) / T), by the hardware's.
+  __device__ __forceinline__ float about(float v) const {
+    float w;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"((v - top) * c_hi));
+    return w;
+  }
+  // Whether those that reach `threshold` seem to weigh less than p of all: from the loads' largest, and from
+  // the middle of each warp's stretch. The list would be for nothing (512 rows of 128256, p = 0.95: 27 of
+  // 166 us that a block of a flat row takes); asking takes 3.
+  __device__ bool seems_flat(const float (&m)[kAhead], float threshold, float p) {
+    float listed = 0.f, rest = 0.f, v[8];
+#pragma unroll
+    for (int g = 0; g < kAhead; ++g) listed += m[g] >= threshold ? about(m[g]) : 0.f;
+    const int steps = (last - first) / 256;
+    unpack8<TYPE>(group(first + steps / 2 * 256 + lane * 8), v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) rest += v[e] >= threshold ? 0.f : about(v[e]);
+    uint64_t x = static_cast<uint64_t>(listed * 0x1p20f);
+    uint64_t y = static_cast<uint64_t>(rest * static_cast<float>(steps + 1) * 0x1p20f);
+    reduce<false>(x, y);
+    return 2.f * static_cast<float>(x) * (1.f - p) < static_cast<float>(y) * p;
   }
 
   // Lists the elements that reach `threshold`, in the first block. `weigh`: the weight of all
@@ -1201,8 +1267,7 @@ struct Row {
     for (int i = threadIdx.x; i < n; i += kThreadsS) {
       const uint64_t at = s.item[i], w = s.heft[i];
       if (at >= cut && w >= least)
-        atomicAdd(reinterpret_cast<unsigned long long*>(&s.bucket[place_index(at) >> down]),
-                  static_cast<unsigned long long>(w));
+        add64(&s.bucket[place_index(at) >> down], w);
     }
     __syncthreads();
     uint32_t none, none_all;
@@ -1338,6 +1403,8 @@ struct Row {
       if (rank == 0 && threadIdx.x == 0) *token = place_index(at);
       return;
     }
+    index_bits = 32 - __clz(a.V);
+    place_mask = (1u << index_bits) - 1;
     const float high = top * c_hi;
     far = !(fabsf(high) < 3900.f) || c_hi < 1e-30f;
     octave = far ? 0 : static_cast<int>(ceilf(high));
@@ -1349,8 +1416,9 @@ struct Row {
     const float low =
         share > 0.f && c_hi > 1e-30f ? top + (log2f(share) - 0.01f) / c_hi - fabsf(top) * 1e-6f : -INFINITY;
     if (list) {
-      if (near || a.V <= kList / a.cluster) {
-        if (!near) threshold = -INFINITY;
+      const bool in_vain = near && !by_k && seems_flat(m, threshold, p);
+      if ((near && !in_vain) || a.V <= kList / a.cluster) {
+        if (!near || in_vain) threshold = -INFINITY;
         if (from_list(threshold, top_k, p, heaviest, least, u, token)) return;
       }
       if (by_k) {
