@@ -13,6 +13,7 @@
 #include <cstdint>
 #include <cstring>
 #include <exception>
+#include <initializer_list>
 #include <utility>
 #include <vector>
 
@@ -511,6 +512,10 @@ void apart(const Tensor& out, const Tensor* in, bool same, const char* name) {
   refuse(PyExc_ValueError, "flce: %s must not overlap another tensor of the call", name);
 }
 
+void apart_from(const Tensor& out, std::initializer_list<const Tensor*> others, const char* name) {
+  for (const Tensor* t : others) apart(out, t, false, name);
+}
+
 double number(PyObject* o, const char* name) {
   const double v = PyFloat_AsDouble(o);
   if (v == -1.0 && PyErr_Occurred()) {
@@ -603,6 +608,7 @@ PyObject* rms_norm_forward(PyObject*, PyObject* const* a, Py_ssize_t n) {
       apart(*out, w, false, "out");
       if (c.write_h) apart(*out, &c.h, false, "out");
     }
+    if (rstd) apart_from(*rstd, {&x, w, r, &c.h, out}, "rstd");
     const Tensor y = out ? *out : at::empty(x.sizes(), x.options());
     done(flce_rms_norm_forward(&c.p, data(x), data(w), data(r), c.seed, data(y),
                                c.write_h ? data(c.h) : nullptr, static_cast<float*>(data(rstd)), nullptr,
@@ -635,7 +641,10 @@ PyObject* rms_norm_quantized(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     std::vector<int64_t> shape(x.sizes().begin(), x.sizes().end() - 1);
     if (c.p.scales == FLCE_SCALES_BLOCK) shape.push_back((c.p.H + 127) / 128);
-    if (given) flat(*given, at::kFloat, shape, x, "scale");
+    if (given) {
+      flat(*given, at::kFloat, shape, x, "scale");
+      apart_from(*given, {&x, w, r, &c.h, out}, "scale");
+    }
     const Tensor y = out ? *out : at::empty(x.sizes(), x.options().dtype(at::kFloat8_e4m3fn));
     const Tensor scale = given ? *given : at::empty(shape, x.options().dtype(at::kFloat));
     done(flce_rms_norm_forward(&c.p, data(x), data(w), data(r), c.seed, data(y),
@@ -766,7 +775,12 @@ PyObject* sample(PyObject*, PyObject* const* a, Py_ssize_t n) {
     p.top_p = static_cast<float>(top_p);
     p.min_p = static_cast<float>(min_p);
     const c10::cuda::CUDAGuard guard(z.device());
-    if (out) flat(*out, at::kLong, {p.B}, z, "out");
+    if (out) {
+      flat(*out, at::kLong, {p.B}, z, "out");
+      apart_from(*out, {&z, &u}, "out");
+      for (PyObject* o : {a[2], a[3], a[4], a[5]})
+        if (THPVariable_Check(o)) apart(*out, &THPVariable_Unpack(o), false, "out");
+    }
     const Tensor tokens = out ? *out : at::empty({p.B}, z.options().dtype(at::kLong));
     done(flce_sample(&p, data(z), static_cast<const float*>(data(u)), temperatures, top_ks, top_ps, min_ps,
                      static_cast<int64_t*>(data(tokens)), stream_of(z)),

@@ -73,7 +73,8 @@ def flce_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: Optional[t
                            dW_dtype: torch.dtype = torch.float32, needs=(True, True, True),
                            workspace: Optional[torch.Tensor] = None, stream=None):
     """dx in dy's type, dresidual in h's and dW [H] (fp32 or dy's type; None without a
-    weight) of flce_rms_norm_forward, which gave h and ``rstd``.
+    weight) of flce_rms_norm_forward, which gave h and ``rstd``. h is read as it is stored:
+    in 16 bits its rounding reaches dW, about as much again as rounding dW to 16 bits.
 
     ``dh``: the gradient that reaches h along the residual stream, of h's type, or None.
     dropout, seed and offset are the forward's. Without dropout and with one type dx and
@@ -133,6 +134,17 @@ def _rows(t: torch.Tensor) -> torch.Tensor:
     return t.contiguous()
 
 
+def _keep(ctx, seed, *tensors):
+    """Keeps tensors and the seed; a seed tensor that is written before the backward is an error then."""
+    ctx.seed = None if torch.is_tensor(seed) else seed
+    ctx.save_for_backward(seed if torch.is_tensor(seed) else None, *tensors)
+
+
+def _kept(ctx):
+    seed, *tensors = ctx.saved_tensors
+    return (ctx.seed if seed is None else seed, *tensors)
+
+
 class FusedRMSNormFunction(torch.autograd.Function):
     """Autograd form of the norm: (y, h). It keeps h, one number for each row, and the seed."""
 
@@ -143,20 +155,20 @@ class FusedRMSNormFunction(torch.autograd.Function):
             rstd = torch.empty(x.shape[:-1].numel(), dtype=torch.float32, device=x.device)
         y, h = flce_rms_norm_forward(x, weight, residual, eps=eps, dropout=dropout, seed=seed, rstd=rstd)
         ctx.set_materialize_grads(False)
-        ctx.dropout, ctx.seed, ctx.x_dtype = dropout, seed, x.dtype
-        ctx.save_for_backward(h, weight, rstd)
+        ctx.dropout, ctx.x_dtype = dropout, x.dtype
+        _keep(ctx, seed, h, weight, rstd)
         return y, (None if h is x else h)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy, dh):
-        h, weight, rstd = ctx.saved_tensors
+        seed, h, weight, rstd = _kept(ctx)
         need_x, need_w, need_r = ctx.needs_input_grad[:3]
         dx = dr = dW = None
         if dy is not None:
             dh = None if dh is None else _rows(dh)
             dx, dr, dW = flce_rms_norm_backward(
-                _rows(dy), h, weight, rstd, dh, dropout=ctx.dropout, seed=ctx.seed,
+                _rows(dy), h, weight, rstd, dh, dropout=ctx.dropout, seed=seed,
                 dW_dtype=torch.float32 if weight is None else weight.dtype,
                 needs=(need_x, need_r, need_w))
         elif dh is not None:
@@ -164,7 +176,7 @@ class FusedRMSNormFunction(torch.autograd.Function):
             dr = dh if need_r else None
             if need_x:
                 like = torch.empty(0, dtype=ctx.x_dtype, device=dh.device)
-                dx = flce_dropout(_rows(dh), ctx.dropout, ctx.seed, like=like)
+                dx = flce_dropout(_rows(dh), ctx.dropout, seed, like=like)
             dW = torch.zeros_like(weight) if need_w else None
         return dx, dW, dr, None, None, None
 
@@ -174,15 +186,17 @@ class FusedDropoutFunction(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, x, residual, p, seed):
-        ctx.p, ctx.seed, ctx.like = p, seed, x.new_empty(0)
+        ctx.p, ctx.like = p, x.new_empty(0)
+        _keep(ctx, seed)
         return flce_dropout(x, p, seed, residual=residual)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
         dx = None
+        (seed,) = _kept(ctx)
         if ctx.needs_input_grad[0]:
-            dx = flce_dropout(_rows(dy), ctx.p, ctx.seed, like=ctx.like)
+            dx = flce_dropout(_rows(dy), ctx.p, seed, like=ctx.like)
         return dx, dy if ctx.needs_input_grad[1] else None, None, None
 
 

@@ -248,3 +248,28 @@ def test_the_heads_serving_side():
                           for v in range(0, V, 97)])
     mine = F.flce_forward(y, W, b, best, reduction="none")[0]
     assert bool((mine <= losses.amin(0) + 2e-2).all())  # the logits are rounded to bf16, of up to 16
+
+
+def test_tokens_share_no_memory_with_the_inputs():
+    z, both = torch.zeros(4, 100, device="cuda"), torch.zeros(8, dtype=torch.int64, device="cuda")
+    u = both.view(torch.float32)[6:10]
+    with pytest.raises(ValueError, match="overlap"):
+        F.flce_sample(z, u, out=both[:4])
+    with pytest.raises(ValueError, match="overlap"):
+        F.flce_sample(z, torch.zeros(4, device="cuda"), top_p=u, out=both[:4])
+    assert F.flce_sample(z, both.view(torch.float32)[8:12], out=both[:4]).data_ptr() == both.data_ptr()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("values", [1, 2, 7, 40])
+def test_lists_full_of_equal_logits(dtype, values):
+    """A list whose items are of few values, over the signs: the cut lies among equal ones."""
+    V = 1 << 17
+    g = torch.Generator(device="cuda").manual_seed(values)
+    z = torch.full((6, V), -30.0, device="cuda")
+    at = torch.randperm(V, generator=g, device="cuda")[:1200]
+    z[:, at] = torch.linspace(-0.02, 0.02, values, device="cuda").repeat(1200 // values + 1)[:1200]
+    z = z.to(dtype)
+    u = torch.tensor([0.0, 0.2, 0.5, 0.7, 0.9, 0.999999], device="cuda")
+    for kw in (dict(top_p=0.5), dict(top_p=0.999), dict(top_k=600), dict(top_k=999, top_p=0.3)):
+        check(z, u, **kw)

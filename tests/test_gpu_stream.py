@@ -589,3 +589,50 @@ def test_training_step_through_norm_and_loss_head():
     total = sum(float(p.grad.double().square().sum()) for p in params) ** 0.5
     got = F.clip_grad_norm_(params, 1e-3)
     assert float(got) == pytest.approx(total, rel=1e-5)
+
+
+def test_numbers_of_rows_share_no_memory_with_the_rows():
+    buf = torch.zeros(8 * 64 + 8, dtype=FP32, device="cuda")
+    x, tail = buf[:512].view(8, 64), buf[508:516]
+    for call in (lambda: F.flce_rms_norm_forward(x, None, rstd=tail), lambda: F.flce_rms_norm_quantized(x, None, scale=tail),
+                 lambda: F.flce_rms_norm_forward(torch.ones_like(x), None, out=x, rstd=tail)):
+        with pytest.raises(ValueError, match="overlap"):
+            call()
+    F.flce_rms_norm_forward(x[:7], None, rstd=buf[512:519])
+
+
+def test_a_seed_that_is_written_before_the_backward_is_an_error():
+    """The gradients would be of another mask."""
+    x = torch.randn(8, 64, device="cuda", requires_grad=True)
+    w = torch.ones(64, device="cuda")
+    seed = torch.zeros(1, dtype=torch.int64, device="cuda")
+    for call in (lambda: F.fused_dropout(x, 0.5, seed=seed), lambda: F.fused_rms_norm(x, w, dropout=0.5, seed=seed)[0]):
+        y = call()
+        seed.add_(1)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.sum().backward()
+        call().sum().backward()
+
+
+@pytest.mark.parametrize("H", [257, 2049, 4100, 8193, 9000, 16388])
+def test_wide_odd_rows_draw_the_same_masks(H):
+    """Rows off 16-byte boundaries, of each number of threads and groups: the masks and sums of
+    64 bits, in the norm, its backward and dropout by itself."""
+    M, p, seed = 5, 0.25, 77
+    g = torch.Generator(device="cuda").manual_seed(H)
+    x, r, dy = (torch.randn(M, H, device="cuda", generator=g) for _ in range(3))
+    f = R.factors(M, H, p, seed)
+    rstd = torch.empty(M, device="cuda")
+    y, h = F.flce_rms_norm_forward(x, None, r, dropout=p, seed=seed, rstd=rstd)
+    h64 = r.double() + x.double() * f
+    # One product and one sum, each rounded by half a step of up to 2 |x| + |r| < 16.
+    assert float((h.double() - h64).abs().max()) <= 2 * 16 * 2.0 ** -24
+    assert torch.equal(h, F.flce_dropout(x, p, seed, residual=r))
+    n64 = h64 * (h64.square().mean(-1, keepdim=True) + 1e-6).rsqrt()
+    # The root of the mean: a thread's sum of 32 terms, its tree and rsqrt, under 2^-18 together; |y| < 16.
+    assert float((y.double() - n64).abs().max()) <= 16 * 2.0 ** -18
+    dx, dr, _ = F.flce_rms_norm_backward(dy, h, None, rstd, dropout=p, seed=seed)
+    assert torch.equal(dx == 0, f == 0)
+    kept = f != 0
+    scale = float(f.max())
+    assert torch.equal(dx[kept], (dr * scale)[kept])
