@@ -1,7 +1,8 @@
 // Dropout from a counter-based generator, with the residual's addition:  y = r + D(x).
 //
 // The mask is a function of (seed, offset, row, column), so it is never stored: the backward,
-// dx = D(dy), is the same call on dy.
+// dx = D(dy), is the same call on dy. Bound by HBM, and by the generator's instructions (10 rounds for 8
+// columns) close behind: 8192 x 14336 bf16 85 us (5.5 TB/s; a copy of it 72).
 #include <cuda_runtime.h>
 
 #include "block_internal.h"
@@ -66,7 +67,7 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const __grid_constant
 
 // Rows off the 16-byte boundaries go value by value: a warp takes 256 columns of kRows rows, its
 // accesses next to each other; a lane makes the random bits of a group, and takes those of the columns
-// that it moves.
+// that it moves. 8192 x 4095 bf16 37 us; 89 with a thread for 8 neighbouring columns.
 template <int XT, int YT>
 __global__ void __launch_bounds__(kThreads)
     dropout_strided_kernel(const __grid_constant__ DropArgs a, uint32_t segments, int64_t warps) {

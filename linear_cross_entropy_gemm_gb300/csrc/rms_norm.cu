@@ -18,7 +18,8 @@ namespace flce {
 namespace {
 
 // dw = the ordered sum of the blocks' shares: a cluster of up to 8 blocks takes 32 columns, each of its
-// warps every so many'th share; the warps of a block and then the blocks add up in their order.
+// warps every so many'th share; the warps of a block and then the blocks add up in their order. 608 shares
+// of 2048 columns: the backward 11.5 us with 4 blocks, 12.6 with one; 304 of 4096 alike.
 constexpr int kSumThreads = 512, kSumBlocks = 8;
 __global__ void __launch_bounds__(kSumThreads)
     share_sum_kernel(const float* part, int parts, int n, void* out, int type, int blocks) {

@@ -5,15 +5,26 @@
 //   S = { i in S_p : w_i >= min_p }.  token = lowest i with  sum_{j <= i, j in S} w_j > u sum(S)
 //
 // A token is a comparison of two long sums, so a rounding anywhere in a row of 100000 terms
-// could move it. The weights are therefore whole numbers of 2^-43 of the largest, each right to
-// 2^-35 of itself: their sums are exact in any order, and the same for any split of a row
-// over threads and blocks.
+// could move it. The weights are therefore whole numbers of 2^-43 of the power of two at or above the
+// largest (of the largest itself where z / T is far from 0), each right to 2^-35 of itself: their
+// sums are exact in any order, and the same for any split of a row over threads and blocks.
 //
 // A cluster of blocks takes a row, each warp a contiguous stretch of it. All three limits keep a
-// prefix of the same order, so one cut, a (logit, index) pair, says what is kept. It is
-// found from a histogram of the logits' distance from the largest, whose bins bracket it, and
-// then by sorting the few elements of the bracket; a bracket that holds too many (equal
-// logits, flat distributions) is halved until it does not.
+// prefix of the same order, so one cut, a (logit, index) pair, says what is kept.
+//   One pass finds the largest, and from the threads' largest a logit that enough elements reach.
+//   The list: a second pass lists those that reach it (and adds up the others' weight, by the hardware's
+//   2^x, where p alone limits); cut and draw are among the listed. Where the error of that sum could
+//   move the cut it is made again in whole numbers.
+//   The row: where k is large or the kept ones are many, a histogram of the distances from the largest
+//   brackets the cut, one pass of exact weights sums what lies above the bracket and lists what lies in
+//   it, and a bracket with too many (equal logits) is halved until it has not. Sums of parts of the
+//   warps' stretches say where the draw falls.
+//
+// The bytes are the logits once (512 x 128256 bf16: 131 MB, 19.4 us), but the second pass comes from L2
+// at best, and an exact weight takes about 35 instructions. Measured at that size: the largest
+// alone 48 us, top-k 50 61, the whole distribution 106, p = 0.95 112 where some hundreds of
+// words matter and 240 where 40000 do. One row of 128256: 6.5, 13, 12, 18 and 41 us: the clusters'
+// exchanges and the first block's work on the list, each a few us of waiting.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>
 
@@ -28,7 +39,7 @@ namespace flce {
 namespace {
 
 constexpr int kThreadsS = 256, kWarpsS = kThreadsS / 32;
-constexpr int kPerSm = 4;                  // blocks of an SM
+constexpr int kPerSm = 4;                  // blocks of an SM: 64 registers for a thread
 constexpr int kMaxCluster = 8;
 constexpr int kFrac = 43;                  // fraction bits of a weight
 constexpr uint64_t kOne = 1ull << kFrac;
@@ -101,7 +112,7 @@ struct Shared {
   uint64_t warp_sum[kWarpsS], warp_kept[kWarpsS];
   uint64_t kept[kWarpsS][kParts];  // weights that are kept, by parts of the warps' stretches
   uint64_t cut, cut_mass;    // the last place that is kept, the weight up to and including it
-  uint64_t x_before, x_count, list_mass;
+  uint64_t x_before, x_count;
   uint64_t rests[kMaxCluster];
   uint32_t owns[kMaxCluster];
   float thresholds[kMaxCluster][2];
@@ -1505,7 +1516,8 @@ extern "C" flce_status_t flce_sample(const flce_sample_params_t* p, const void* 
   a.top_k = p->top_k;
   a.top_p = p->top_p;
   a.min_p = p->min_p;
-  // Blocks for a row: as many as give two waves of them, each with 16 KiB at least.
+  // Blocks for a row: as many as give two waves of them, each with 16 KiB at least. 512 x 128256, p = 0.95,
+  // rows of mixed certainty: 1 block 241 us, 2 234, 4 258; 1 x 128256 with 8.
   int cluster = 1;
   while (cluster < kMaxCluster && 2 * cluster * p->B <= 2 * kPerSm * sms &&
          p->V * type_size(p->dtype) >= 2 * cluster * 16384)
