@@ -636,3 +636,24 @@ def test_wide_odd_rows_draw_the_same_masks(H):
     kept = f != 0
     scale = float(f.max())
     assert torch.equal(dx[kept], (dr * scale)[kept])
+
+
+def test_equal_gradients_of_two_leaves_stay_apart():
+    """dx and dresidual are one tensor where they are equal: the leaves' gradients are not, and a
+    tensor that is both gets their sum."""
+    x, w, r, dy, _ = problem(6, 64, FP32, FP32)
+    x, r, w = (t.clone().requires_grad_() for t in (x, r, w))
+    for times in (1, 2):
+        y, h = F.fused_rms_norm(x, w, r)
+        (y * dy + h).sum().backward()
+        assert torch.equal(x.grad, r.grad)
+    assert x.grad.data_ptr() != r.grad.data_ptr()
+    kept = r.grad.clone()
+    x.grad.zero_()
+    assert torch.equal(r.grad, kept)
+    y, h = F.fused_rms_norm(r, w, r)
+    (both,) = torch.autograd.grad((y * dy + h).sum(), r)
+    x2, r2 = r.detach().clone().requires_grad_(), r.detach().clone().requires_grad_()
+    y, h = F.fused_rms_norm(x2, w, r2)
+    (y * dy + h).sum().backward()
+    assert torch.equal(both, x2.grad + r2.grad)
