@@ -24,6 +24,7 @@ constexpr int kSumThreads = 512, kSumBlocks = 8;
 __global__ void __launch_bounds__(kSumThreads)
     share_sum_kernel(const float* part, int parts, int n, void* out, int type, int blocks) {
   __shared__ float s_sum[kSumThreads / 32][32], s_all[kSumBlocks][32];
+  if (blocks > 1) cluster_arrive();
   griddep_wait();
   const int rank = blockIdx.x % blocks, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = static_cast<int>(blockIdx.x / blocks) * 32 + lane, apart = blocks * (kSumThreads / 32);
@@ -39,6 +40,7 @@ __global__ void __launch_bounds__(kSumThreads)
   griddep_launch();
   s_sum[warp][lane] = sum;
   __syncthreads();
+  if (blocks > 1) cluster_wait();  // the first block runs: its memory may be written
   if (warp == 0) {
     sum = 0.f;
 #pragma unroll
