@@ -1098,6 +1098,7 @@ struct Row {
       }
       __syncthreads();
     }
+    if (a.cluster > 1) cluster_wait();  // all blocks run: their memory may be written
     if (threadIdx.x < a.cluster) {
       of_block(s.peers[turn][rank], threadIdx.x)[0] = most != most ? 0xFFFFFFFFull : order_of(most);
       float* to = of_block(s.thresholds[rank], threadIdx.x);
@@ -1452,6 +1453,7 @@ template <int TYPE>
 __global__ void __launch_bounds__(kThreadsS, kPerSm) sample_kernel(const __grid_constant__ SampleArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];
   Shared& s = *reinterpret_cast<Shared*>(smem);
+  if (a.cluster > 1) cluster_arrive();
   for (int i = threadIdx.x; i < kNearBins; i += kThreadsS) s.near_hist[i] = 0;
   griddep_wait();
   const int row = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
