@@ -1421,12 +1421,13 @@ struct Row {
     far = !(fabsf(high) < 3900.f) || c_hi < 1e-30f;
     octave = far ? 0 : static_cast<int>(ceilf(high));
     lowest = far ? -INFINITY : top - 47.f / c_hi;
-    // min_p above 1 keeps the largest. Elements well below the limit need no weight.
+    // min_p above 1 keeps the largest. Elements well below the limit need no weight; below +infinity no
+    // logit says how far.
     const float share = min_p > 0.f ? fminf(min_p, 1.f) : 0.f;
     const uint64_t heaviest = share > 0.f || by_p ? any_weight(top, kExp2.v) : 0;
     const uint64_t least = share < 1.f ? times<true>(heaviest, share) : heaviest;  // 0 where all weigh enough
-    const float low =
-        share > 0.f && c_hi > 1e-30f ? top + (log2f(share) - 0.01f) / c_hi - fabsf(top) * 1e-6f : -INFINITY;
+    const float low = share > 0.f && c_hi > 1e-30f && top < INFINITY
+                          ? top + (log2f(share) - 0.01f) / c_hi - fabsf(top) * 1e-6f : -INFINITY;
     if (list) {
       const bool in_vain = near && !by_k && seems_flat(m, threshold, p);
       if ((near && !in_vain) || a.V <= kList / a.cluster) {

@@ -1,0 +1,55 @@
+"""Sampling where a comparison hangs on little: rows of infinities, distributions that the middles of
+the histogram's bins misjudge, weights that cross a limit in their last bits. The same tokens as
+the definition in 64 bits."""
+
+import pytest
+import torch
+
+import linear_cross_entropy_gemm_gb300 as F
+import stream_reference as R
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP16, FP32 = torch.bfloat16, torch.float16, torch.float32
+INF = float("inf")
+UNWRITTEN = -7
+
+
+def tokens_of(z, u, **kw):
+    """The call's tokens, in a buffer that tells a token that was not written."""
+    out = torch.full((z.shape[0],), UNWRITTEN, dtype=torch.int64, device="cuda")
+    return F.flce_sample(z, u, out=out, **kw).tolist()
+
+
+def check(z, u, **kw):
+    zs = z.float().cpu()
+    assert tokens_of(z, u, **kw) == [R.sample(zs[b], float(u[b]), **kw) for b in range(z.shape[0])]
+
+
+def randoms(n, seed=0):
+    return torch.rand(n, generator=torch.Generator(device="cuda").manual_seed(seed), device="cuda")
+
+
+# ---------------------------------------------------------------- infinities
+def infinite_rows(B, V, infinities, dtype, seed=1):
+    """Rows with so many +infinities at random places; and the rows whose weights they have."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    z = torch.randn(B, V, generator=g, device="cuda") * 3
+    z[:, ::7] = -INF
+    at = torch.stack([torch.randperm(V, generator=g, device="cuda")[:infinities] for _ in range(B)])
+    z.scatter_(1, at, INF)
+    return z.to(dtype), torch.where(z == INF, 0.0, -INF)
+
+
+# One block for a row, and a cluster of them.
+@pytest.mark.parametrize("B,V", [(1, 1), (4, 300), (2, 70000), (1, 1 << 18), (330, 2000)], ids=str)
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
+def test_infinities_with_min_p(B, V, dtype):
+    """+infinity leaves the others no weight, whatever min_p is."""
+    for infinities in sorted({1, min(3, V), min(V, 1000)}):
+        z, flat = infinite_rows(B, V, infinities, dtype)
+        u = randoms(B, 2)
+        for kw in (dict(min_p=0.05), dict(min_p=1.0), dict(min_p=1e-6, temperature=30.0)):
+            want = tokens_of(flat, u)
+            assert tokens_of(z, u, **kw) == want and UNWRITTEN not in want
+        check(z[:4], u[:4], min_p=0.3, top_k=1200)
