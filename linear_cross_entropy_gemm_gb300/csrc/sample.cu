@@ -447,6 +447,7 @@ struct Row {
   // The weight of a bin's elements, relative to the largest: of its middle, or, as 16-bit logits are
   // few in a bin or none, of the middle of those that it can hold.
   __device__ float bin_weight(int i) const {
+    if (!(top < INFINITY)) return 1.f;  // only the infinities are in a bin, in the first
     if (c_hi < 1e-30f) return exp2f(-(static_cast<float>(i) + 0.5f) / kPerOctave);
     const float scale = c_hi * kPerOctave, upper = top - static_cast<float>(i) / scale;
     float z = upper - 0.5f / scale;

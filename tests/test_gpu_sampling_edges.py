@@ -53,3 +53,20 @@ def test_infinities_with_min_p(B, V, dtype):
             want = tokens_of(flat, u)
             assert tokens_of(z, u, **kw) == want and UNWRITTEN not in want
         check(z[:4], u[:4], min_p=0.3, top_k=1200)
+
+
+@pytest.mark.parametrize("infinities", [2, 40, 1500, 5000])
+@pytest.mark.parametrize("B,V", [(330, 7000), (2, 131072)], ids=str)
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
+def test_infinities_with_top_k_and_top_p(B, V, infinities, dtype):
+    """They are equal weights: the limits keep the first ones of them."""
+    z, flat = infinite_rows(B, V, infinities, dtype)
+    u = randoms(B, 3)
+    u[:2] = 1 - 2.0 ** -24
+    for kw in (dict(top_p=0.5), dict(top_k=1200, top_p=0.5), dict(top_k=3000, top_p=0.25), dict(top_k=6000),
+               dict(top_p=0.9, min_p=0.1), dict(top_p=0.01), dict(top_k=900, top_p=0.75)):
+        check(z[:3], u[:3], **kw)
+        want = tokens_of(flat, u, **kw)
+        assert tokens_of(z, u, **kw) == want
+        # A temperature above all changes nothing among equals.
+        assert tokens_of(z, u, temperature=INF, **kw) == want
