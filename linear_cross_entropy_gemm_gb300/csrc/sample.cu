@@ -774,6 +774,7 @@ struct Row {
         const uint64_t cut =
             cut_between<FAR>(floor > lo ? floor : lo, hi, n, true, kAll, mass, 0, sum, moved);
         if (sure || s.cut_mass >= mass) return cut;
+        histogram();  // the items' sums have had its place
       } else if (sure) {
         return narrow_cut<FAR>(above, least, least_index, floor, mass, sum, heaviest, moved);
       }

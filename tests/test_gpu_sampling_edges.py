@@ -1,7 +1,9 @@
 """Sampling where a comparison hangs on little: rows of infinities, distributions that the middles of
 the histogram's bins misjudge, weights that cross a limit in their last bits. The same tokens as
 the definition in 64 bits."""
+import math
 
+import numpy as np
 import pytest
 import torch
 
@@ -70,3 +72,44 @@ def test_infinities_with_top_k_and_top_p(B, V, infinities, dtype):
         assert tokens_of(z, u, **kw) == want
         # A temperature above all changes nothing among equals.
         assert tokens_of(z, u, temperature=INF, **kw) == want
+
+
+# ---------------------------------------------------------- misjudged bins
+def groups_row(groups, V, dtype, seed=4):
+    """A row of (value, count) groups; the values of each at places of their own, in random order."""
+    assert sum(n for _, n in groups) == V
+    z = torch.cat([torch.full((n,), v, dtype=torch.float64) for v, n in groups]).to(dtype)
+    assert all(float(torch.tensor(v, dtype=torch.float64).to(dtype).double()) == v for v, _ in groups) or dtype == FP32
+    return z[torch.randperm(V, generator=torch.Generator().manual_seed(seed))].cuda()
+
+
+def bins_apart(dtype):
+    """Values in three neighbouring bins of 1/64 of a factor of 2, the first at its bin's low end, whose
+    weight the bin's middle overestimates; (largest, the three, value of the rest, temperature)."""
+    if dtype == FP32:
+        b = math.log(2) / 64
+        return 0.0, (-64.97 * b, -65.5 * b, -66.03 * b), -20.0, 1.0
+    top, step, T = (1.0, 2.0 ** -8, 4.0) if dtype == BF16 else (8.0, 2.0 ** -8, 2.0)
+    of_bin = {}
+    for j in range(1, 100):
+        of_bin.setdefault(int((top - (top - j * step)) * 64 / (T * math.log(2))), []).append(top - j * step)
+    return top, (of_bin[3][-1], of_bin[4][len(of_bin[4]) // 2], of_bin[5][0]), -20.0 * T, T
+
+
+@pytest.mark.parametrize("V,many,few", [(131072, 60000, 300), (8000, 3500, 100)], ids=str)
+@pytest.mark.parametrize("top_k", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
+def test_a_bracket_that_is_too_high(dtype, top_k, V, many, few):
+    """Between two groups of thousands lie a few words: the first guess of where the cut lies is just
+    they, and the exact sums refute it. A few hundred of the second group are kept, not all."""
+    top, (a, b, c), rest, T = bins_apart(dtype)
+    groups = [(top, 1), (a, many), (b, few), (c, many), (rest, V - 1 - 2 * many - few)]
+    z = groups_row(groups, V, dtype)
+    k = 1 + 2 * many + few + (V - 1 - 2 * many - few) // 2 if top_k else 0
+    value = [float(z.double().max()), *sorted(set(z.double().tolist()), reverse=True)[1:]]
+    weights = [n * math.exp((v - value[0]) / T) for v, (_, n) in zip(value, groups)]
+    if top_k:
+        weights[-1] /= 2
+    p = float(np.float32((sum(weights[:3]) + 0.001 * sum(weights)) / sum(weights)))
+    u = torch.tensor([1 - 2.0 ** -24, 0.9999, 0.999, 0.75, 0.5, 0.25], device="cuda")
+    check(z.expand(6, V).contiguous(), u, top_k=k, top_p=p, temperature=T)
