@@ -113,3 +113,17 @@ def test_a_bracket_that_is_too_high(dtype, top_k, V, many, few):
     p = float(np.float32((sum(weights[:3]) + 0.001 * sum(weights)) / sum(weights)))
     u = torch.tensor([1 - 2.0 ** -24, 0.9999, 0.999, 0.75, 0.5, 0.25], device="cuda")
     check(z.expand(6, V).contiguous(), u, top_k=k, top_p=p, temperature=T)
+
+
+def test_bins_narrower_than_a_step_of_the_logits():
+    """Large logits at a small temperature: a step of fp32 is nearly two bins wide, and a bin's weight
+    is that of its own middle, not of a logit rounded from it. The cut lies 32 words into the second group."""
+    V, many, top, T = 131072, 10000, 127.0, 0.0003646422701422125
+    step = 2.0 ** -17  # of fp32 in [64, 128)
+    groups = [(top, 1), (top - 15 * step, many), (top - 16 * step, V - 1 - many)]
+    z = torch.cat([torch.full((n,), v, dtype=FP32) for v, n in groups]).cuda()
+    weights = [n * math.exp((v - top) / float(np.float32(T))) for v, n in groups]
+    p = float(np.float32((weights[0] + 1.003 * weights[1]) / sum(weights)))
+    u = torch.tensor([1 - 2.0 ** -24, 0.9995, 0.998, 0.5], device="cuda")
+    check(z.expand(4, V).contiguous(), u, top_p=p, temperature=T)
+    check(z.expand(4, V).contiguous(), u, top_k=V - 5, top_p=p, temperature=T)
