@@ -1429,7 +1429,9 @@ struct Row {
     const uint64_t least = share < 1.f ? times<true>(heaviest, share) : heaviest;  // 0 where all weigh enough
     const float low = share > 0.f && c_hi > 1e-30f && top < INFINITY
                           ? top + (log2f(share) - 0.01f) / c_hi - fabsf(top) * 1e-6f : -INFINITY;
-    if (list) {
+    // Where p alone limits, the others' weight is by the hardware's 2^x, whose argument must be right to
+    // less than 1: from_list's bound on its error is linear in the argument's. Else from the row.
+    if (list && (by_k || fabsf(high) < 0x1p24f)) {
       const bool in_vain = near && !by_k && seems_flat(m, threshold, p);
       if ((near && !in_vain) || a.V <= kList / a.cluster) {
         if (!near || in_vain) threshold = -INFINITY;

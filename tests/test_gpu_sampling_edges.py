@@ -127,3 +127,25 @@ def test_bins_narrower_than_a_step_of_the_logits():
     u = torch.tensor([1 - 2.0 ** -24, 0.9995, 0.998, 0.5], device="cuda")
     check(z.expand(4, V).contiguous(), u, top_p=p, temperature=T)
     check(z.expand(4, V).contiguous(), u, top_k=V - 5, top_p=p, temperature=T)
+
+
+def test_sums_by_2_to_the_x_far_from_0():
+    """z / T of 2^25: the exponents of the words outside the list are off by up to 2, so their sum by
+    the hardware's 2^x is not what decides. p is so near a multiple of one word's share that the others'
+    weight of 2^-37 each keeps one word more."""
+    V, listed = 1 << 20, 701
+    top, T = np.float32(10.33804988861084), np.float32(4.428887336871412e-07)
+    step = 2.0 ** -20  # of fp32 in [8, 16)
+    low = float(top) - 12 * step
+    z = torch.full((V,), low, dtype=FP32)
+    at = torch.arange(listed) * (V // listed) + 5
+    z[at] = float(top)
+    others = (V - listed) * math.exp((low - float(top)) / float(T))
+    # j words and a little less lie before p of the sum: word j is kept.
+    found = [(j, p) for j in range(50, listed - 1) for p in [float(np.float32(j / (listed + 0.9 * others)))]
+             if 0.03 * p * others < p * (listed + others) - j < 0.17 * p * others]
+    assert len(found) >= 4
+    u = torch.full((1,), 1 - 2.0 ** -24, device="cuda")
+    for j, p in found[:8]:
+        assert R.sample(z, float(u), temperature=float(T), top_p=p) == int(at[j])
+        assert tokens_of(z.cuda()[None], u, temperature=float(T), top_p=p) == [int(at[j])]
