@@ -236,9 +236,13 @@ cudaError_t launch_nv(const NormGradArgs& a, bool wide, const GradShape& s, cuda
     if (!wide) kernel = norm_grad_kernel<XT, ST, NV, kStrided, DROP>;
   const size_t smem = wide ? grad_ring(s, type_size(XT), type_size(ST))
                       : DROP ? static_cast<size_t>(NV) * s.threads * s.rows * 16 : 0;
-  if (smem > 48 * 1024) {
+  // Beyond 48 KiB, of which the kernel's own arrays take under 4, it is asked for: always the most that this
+  // kernel can need, so that no call lowers what another is about to launch with.
+  if (smem > 44 * 1024) {
+    const size_t most = wide ? grad_ring({NV, NV == 1 ? 256 : kRowThreads, 1, 1}, type_size(XT), type_size(ST))
+                             : static_cast<size_t>(NV) * 1024 * 16;
     const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most));
     if (e != cudaSuccess) return e;
   }
   return launch_dependent(kernel, grid, block, smem, 1, st, a);

@@ -1,0 +1,41 @@
+"""Norm and dropout in the calls that depend on what the process did before, and in the forms that
+the module and the calls document."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+
+WIDE_ODD = """
+import sys
+sys.path[:0] = [%r, %r]
+import torch
+import linear_cross_entropy_gemm_gb300 as F
+import stream_reference as R
+H, pad, p, seed = %d, %d, 0.25, 77
+g = torch.Generator(device="cuda").manual_seed(H)
+M = 3
+rows = lambda: torch.randn(M, H + pad, device="cuda", generator=g)[:, :H]
+x, r, dy = rows(), rows(), rows()
+f = R.factors(M, H, p, seed)
+rstd = torch.empty(M, device="cuda")
+y, h = F.flce_rms_norm_forward(x, None, r, dropout=p, seed=seed, rstd=rstd)
+dx, dr, _ = F.flce_rms_norm_backward(dy, h, None, rstd, dropout=p, seed=seed)
+e, e_err, d, d_err, _, _ = R.norm_grad(dy, h, None, rstd, None, f)
+R.assert_near(dr, e, e_err, "dresidual")
+R.assert_near(dx, d, d_err, "dx")
+"""
+
+
+@pytest.mark.parametrize("H,pad", [(23553, 0), (24001, 0), (24575, 0), (24576, 1), (24577, 0), (32767, 0)])
+def test_wide_odd_rows_as_a_processs_first_call(H, pad):
+    """The backward with dropout off the 16-byte boundaries takes 48 KiB of shared memory for the random
+    bits at 23553 .. 24576 columns, beside what it always has: the opt-in above 48 KiB counts both. In a
+    process of its own: a wider call before would have opted in."""
+    run = subprocess.run([sys.executable, "-c", WIDE_ODD % (os.path.dirname(HERE), HERE, H, pad)],
+                         capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, run.stderr[-2000:]
