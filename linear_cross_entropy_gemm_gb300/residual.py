@@ -37,7 +37,7 @@ def flce_rms_norm_forward(x: torch.Tensor, weight: Optional[torch.Tensor],
     pitch; H up to 32768. weight [H] (None: ones) is of x's type or fp32, and so is the
     residual, of x's shape; h has its type. Without a residual and dropout h is x. A
     tensor ``h`` receives the sum (it may be the residual itself, which it then
-    replaces), False leaves it out (x is returned in its place). ``out`` may be x.
+    replaces), False leaves it out (None is returned for it). ``out`` may be x.
     ``rstd`` ([rows] fp32) receives what flce_rms_norm_backward needs beside h.
 
     D is the dropout of flce_dropout, with its ``seed`` and ``offset``."""

@@ -5,6 +5,9 @@ import subprocess
 import sys
 
 import pytest
+import torch
+
+import linear_cross_entropy_gemm_gb300 as F
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +42,15 @@ def test_wide_odd_rows_as_a_processs_first_call(H, pad):
     run = subprocess.run([sys.executable, "-c", WIDE_ODD % (os.path.dirname(HERE), HERE, H, pad)],
                          capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, run.stderr[-2000:]
+
+
+def test_h_false_returns_none():
+    x = torch.randn(5, 64, device="cuda")
+    for kw in (dict(), dict(residual=x.clone()), dict(dropout=0.5, seed=1)):
+        want = F.flce_rms_norm_forward(x, None, **kw)
+        y, h = F.flce_rms_norm_forward(x, None, h=False, **kw)
+        assert h is None and torch.equal(y, want[0])
+        want = F.flce_rms_norm_quantized(x, None, **kw)
+        y8, scale, h = F.flce_rms_norm_quantized(x, None, h=False, **kw)
+        assert h is None and torch.equal(y8.float(), want[0].float()) and torch.equal(scale, want[1])
+    assert F.flce_rms_norm_forward(x, None)[1] is x
