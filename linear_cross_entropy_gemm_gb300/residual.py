@@ -234,4 +234,6 @@ class FusedRMSNorm(torch.nn.Module):
 
     def forward(self, x, residual=None):
         p = self.dropout if self.training else 0.0
-        return fused_rms_norm(x, self.weight, residual, self.eps, p)
+        out = fused_rms_norm(x, self.weight, residual, self.eps, p)
+        # With dropout the function returns the sum too; without a residual there is no stream to carry on.
+        return out[0] if residual is None and p > 0 else out

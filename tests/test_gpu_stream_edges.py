@@ -54,3 +54,21 @@ def test_h_false_returns_none():
         y8, scale, h = F.flce_rms_norm_quantized(x, None, h=False, **kw)
         assert h is None and torch.equal(y8.float(), want[0].float()) and torch.equal(scale, want[1])
     assert F.flce_rms_norm_forward(x, None)[1] is x
+
+
+def test_the_module_without_a_residual_gives_y_alone():
+    """In training with dropout as in evaluation: what norm(x) returns is of one kind."""
+    norm = F.FusedRMSNorm(64, dropout=0.5, dtype=torch.float32, device="cuda")
+    x = torch.randn(6, 64, device="cuda", requires_grad=True)
+    torch.manual_seed(3)
+    y = norm(x)
+    assert torch.is_tensor(y) and y.shape == x.shape
+    torch.manual_seed(3)
+    want, h = F.fused_rms_norm(x, norm.weight, None, norm.eps, 0.5)
+    assert torch.equal(y, want) and bool((h == 0).any())
+    dy = torch.randn_like(y)
+    (got,) = torch.autograd.grad(y, x, dy)
+    assert torch.equal(got, torch.autograd.grad(want, x, dy)[0])
+    assert len(norm(x, x)) == 2
+    norm.eval()
+    assert torch.is_tensor(norm(x)) and torch.equal(norm(x), F.fused_rms_norm(x, norm.weight, eps=norm.eps))
