@@ -597,7 +597,7 @@ flce_status_t flce_dropout(const flce_dropout_params_t* p, const void* x, const 
  * logit of -infinity is never chosen, one of +infinity leaves the others no weight, a row with
  * a NaN or without any logit above -infinity gives -1. u below 0 or NaN counts as 0, u of 1
  * and more as just below it. Weights are whole numbers of a unit of 2^-43 to 2^-42 of the largest
- * (those under half of it are 0), each right to 2^-35 of itself: their sums are exact, so a row's token
+ * (those under half of it are 0), each right to 2^-32 of itself: their sums are exact, so a row's token
  * does not depend on the batch around it. */
 #define FLCE_SAMPLE_MAX_V (1 << 20)
 typedef struct {

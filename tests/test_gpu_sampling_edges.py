@@ -1,6 +1,7 @@
 """Sampling where a comparison hangs on little: rows of infinities, distributions that the middles of
 the histogram's bins misjudge, weights that cross a limit in their last bits. The same tokens as
 the definition in 64 bits."""
+import decimal
 import math
 
 import numpy as np
@@ -149,3 +150,52 @@ def test_sums_by_2_to_the_x_far_from_0():
     for j, p in found[:8]:
         assert R.sample(z, float(u), temperature=float(T), top_p=p) == int(at[j])
         assert tokens_of(z.cuda()[None], u, temperature=float(T), top_p=p) == [int(at[j])]
+
+
+# ------------------------------------------------------------ the weights
+def nearly_equal(gap, most):
+    """(m, n) up to `most` with m and n e^-gap nearly equal, and whether m is the larger: the best
+    whose distance is above 2^-30 of them."""
+    with decimal.localcontext() as ctx:
+        ctx.prec = 60
+        r, best = (-decimal.Decimal(gap)).exp(), None
+        x, (p0, q0), (p1, q1) = r, (0, 1), (1, 0)
+        for _ in range(30):  # the continued fraction of e^-gap, and what lies between two of its terms
+            a = int(x)
+            for i in range(1, a + 1) if a < 50 else (1, a):
+                m, n = i * p1 + p0, i * q1 + q0
+                if m < 1 or m + n > most:
+                    continue
+                off = abs(m / (n * r) - 1)
+                if off > decimal.Decimal(2) ** -30 and (best is None or off < best[0]):
+                    best = off, m, n, m > n * r
+            (p0, q0), (p1, q1) = (p1, q1), (a * p1 + p0, a * q1 + q0)
+            if x == a or q1 > most:
+                break
+            x = 1 / (x - a)
+    return best
+
+
+@pytest.mark.parametrize("top,T", [(0.0, 1.0), (7.5, 1.0), (-3.25, 0.75), (900.0, 1.0), (9000.0, 1.0), (2.5, 0.000244140625)],
+                         ids=str)
+def test_a_weights_precision(top, T):
+    """m words of one logit, then n of another, with sums apart by as little as 2^-30 of themselves: half
+    of the whole lies on the right side. Each weight is right to 2^-32 of itself, two
+    of them to 2^-31."""
+    step = abs(float(np.spacing(np.float32(top if top else 1.0))))
+    gaps = [round(g * T / step) * step for g in (0.011, 0.07, 0.3, 0.69, 0.7, 1.1, 1.9, 2.3)]
+    tried = 0
+    for gap in gaps:
+        lower = np.float32(top - gap)
+        found = nearly_equal(decimal.Decimal(float(top) - float(lower)) / decimal.Decimal(T), 1 << 20)
+        if found is None or found[0] > decimal.Decimal(2) ** -26:
+            continue
+        tried += 1
+        _, m, n, above = found
+        z = torch.cat((torch.full((m,), top), torch.full((n,), float(lower)))).cuda()[None]
+        got = tokens_of(z, torch.tensor([0.5], device="cuda"), temperature=T)
+        assert got == [m - 1 if above else m], (gap, m, n)
+        # The other way round.
+        got = tokens_of(z.flip(1), torch.tensor([0.5], device="cuda"), temperature=T)
+        assert got == [n if above else n - 1], (gap, m, n)
+    assert tried >= 4
