@@ -447,20 +447,23 @@ struct Row {
     }
   }
 
+  // The same by a call, where it is rarely needed: inlined once more it costs the callers registers.
+  __device__ __noinline__ static void histogram_apart(Row r) { r.histogram(); }
+
   // The weight of a bin's elements, relative to the largest: of its middle, or, as 16-bit logits are
   // few in a bin or none, of the middle of those that it can hold. The bin's middle is not by way of a
   // logit: where z / T is far from 0, fp32's step is as wide as a bin, and rounding to it puts 2 % on a weight.
   __device__ float bin_weight(int i) const {
-    if (!(top < INFINITY)) return 1.f;  // only the infinities are in a bin, in the first
+    float x = -(static_cast<float>(i) + 0.5f) / kPerOctave;
     if (TYPE != kFp32 && c_hi >= 1e-30f) {
       constexpr uint32_t kBelow = TYPE == kBf16 ? 0xFFFFu : 0x1FFFu;  // the bits that fp32 has below
       const float scale = c_hi * kPerOctave, upper = top - static_cast<float>(i) / scale;
       const uint32_t u = order_of(upper), l = order_of(upper - 1.f / scale);
       const uint32_t high = u & 0x80000000u ? u & ~kBelow : ((u + 1) & ~kBelow) - 1;
       const uint32_t low = l & 0x80000000u ? (l + kBelow) & ~kBelow : l | kBelow;
-      if (low <= high) return exp2f((0.5f * (value_of(low) + value_of(high)) - top) * c_hi);
+      if (low <= high) x = (0.5f * (value_of(low) + value_of(high)) - top) * c_hi;
     }
-    return exp2f(-(static_cast<float>(i) + 0.5f) / kPerOctave);
+    return top < INFINITY ? exp2f(x) : 1.f;  // below +infinity no element is in a bin
   }
 
   // In the first block: the bins [s.bins[0], s.bins[1]] in which the cut must lie: the one that
@@ -776,7 +779,7 @@ struct Row {
         const uint64_t cut =
             cut_between<FAR>(floor > lo ? floor : lo, hi, n, true, kAll, mass, 0, sum, moved);
         if (sure || s.cut_mass >= mass) return cut;
-        histogram();  // the items' sums have had its place
+        histogram_apart(*this);  // the items' sums have had its place
       } else if (sure) {
         return narrow_cut<FAR>(above, least, least_index, floor, mass, sum, heaviest, moved);
       }
