@@ -6,8 +6,8 @@
 // their way into shared memory, each thread its own part and for itself alone, while one is
 // worked on. The blocks' shares are added in a fixed order by a second kernel. Bound by HBM, and
 // by instructions close behind: the arithmetic is on packed pairs, and products of 16-bit values
-// take them as they are. 8192 x 4096 bf16 with dh 45 us (6.0 TB/s, dw's sum 5 of it), with dropout
-// 57 (the generator's ten rounds for 8 columns), fp32 85. Rows off the 16-byte boundaries go value
+// take them as they are. 8192 x 4096 bf16 with dh 45 to 47 us (6.0 TB/s, dw's sum 5 of it), with dropout
+// 57 (the generator's ten rounds for 8 columns), fp32 84. Rows off the 16-byte boundaries go value
 // by value, by up to 1024 threads: 8192 x 4095 86 us (512 threads with twice the columns 118).
 //
 // dw takes h as it is stored: in 16 bits its rounding adds as much error to dw as dw's own to 16 bits.

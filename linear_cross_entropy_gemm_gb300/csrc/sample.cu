@@ -22,8 +22,8 @@
 //
 // The bytes are the logits once (512 x 128256 bf16: 131 MB, 19.4 us), but the second pass comes from L2
 // at best, and an exact weight takes about 35 instructions. Measured at that size: the largest
-// alone 48 us, top-k 50 61, the whole distribution 106, p = 0.95 112 where some hundreds of
-// words matter and 240 where 40000 do. One row of 128256: 6.5, 13, 12, 18 and 41 us: the clusters'
+// alone 48 us, top-k 50 59, the whole distribution 106, p = 0.95 83 where some tens of words
+// matter and 237 where 106000 do. One row of 128256: 6, 13, 12, 18 and 39 us: the clusters'
 // exchanges and the first block's work on the list, each a few us of waiting.
 #include <cooperative_groups.h>
 #include <cuda_runtime.h>

@@ -33,7 +33,8 @@ def flce_sample(logits: torch.Tensor, u: torch.Tensor, *, temperature: Setting =
 
     Each setting is a number, or a tensor [B] with one for each row (fp32; top_k int32).
     A logit of -inf is never chosen; a row without any other, or with a NaN, gives -1. The
-    sums are exact, so a row's token does not depend on the batch."""
+    sums are exact, so a row's token does not depend on the batch. Numbers
+    of torch.rand are multiples of 2^-24: a word whose stretch of the sum holds none is never drawn."""
     if stream is not None:
         with _On(logits.device, stream):
             return _calls.sample(logits, u, temperature, top_k, top_p, min_p, out)
