@@ -75,6 +75,25 @@ def test_infinities_with_top_k_and_top_p(B, V, infinities, dtype):
         assert tokens_of(z, u, temperature=INF, **kw) == want
 
 
+@pytest.mark.parametrize("B,V", [(330, 2000), (3, 70000)], ids=str)
+@pytest.mark.parametrize("dtype", [BF16, FP16, FP32], ids=str)
+def test_min_p_beside_masks(B, V, dtype):
+    """min_p alone, from passes over the row: -infinity and the type's lowest value in most places, a row
+    with one word left, one with nothing."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    z = torch.randn(B, V, generator=g, device="cuda") * 2
+    z[torch.rand(B, V, generator=g, device="cuda") < 0.9] = -INF
+    z[:, ::5] = torch.finfo(dtype).min
+    z[0] = -INF
+    z[1] = -INF
+    z[1, V - 3] = -40.0
+    z, u = z.to(dtype), randoms(B, 6)
+    for kw in (dict(min_p=0.05), dict(min_p=1.0), dict(min_p=1e-9), dict(min_p=0.3, temperature=0.2)):
+        check(z[:3], u[:3], **kw)
+        got = tokens_of(z, u, **kw)
+        assert got[:2] == [-1, V - 3] and UNWRITTEN not in got
+
+
 # ---------------------------------------------------------- misjudged bins
 def groups_row(groups, V, dtype, seed=4):
     """A row of (value, count) groups; the values of each at places of their own, in random order."""
